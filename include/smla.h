@@ -73,13 +73,19 @@ extern "C" {
  *    value = e4m3 * k_scale[slot*4 + c/128] for c < 512 and e4m3 * kpe_scale
  *    for the 64 rope channels (the ckv_scale / kpe_scale split of
  *    flashinfer_mla_sparse_sm90.py, forward_mqa).  Entry points without a
- *    kpe_scale argument use 1.0, the value that page passes. */
+ *    kpe_scale argument use 1.0, the value that page passes.
+ *  SMLA_KV_FP8_E4M3_BLOCK: E4M3 bytes [num_slots, d_qk] with one fp32 scale
+ *    per cache block of tokens (MLA has one latent head, so a block has one
+ *    scale): value = e4m3 * k_scale[block], block = an entry of the block
+ *    table.  Written by smla_cache_append, read by smla_fwd_window; the entry
+ *    points that take slot ids do not serve it (SMLA_ERR_UNSUPPORTED). */
 typedef enum {
   SMLA_KV_BF16 = 0,
   SMLA_KV_FP8_E4M3 = 1,
   SMLA_KV_FP8_E4M3_GROUP128 = 2,
   SMLA_KV_FP8_DS_MLA = 3,
-  SMLA_KV_FP8_E4M3_GROUP4_KPE = 4
+  SMLA_KV_FP8_E4M3_GROUP4_KPE = 4,
+  SMLA_KV_FP8_E4M3_BLOCK = 5
 } smla_kv_dtype;
 
 typedef enum {
@@ -223,6 +229,134 @@ SMLA_API smla_status smla_cache_write_e4m3_group(const void* kv_c, const void* k
                                                  int d_qk, int64_t num_slots,
                                                  void* kv_cache, float* scales,
                                                  cudaStream_t stream);
+
+/*
+ * smla_cache_append — append a step's tokens to a paged cache of any format,
+ * with the rotary position embedding applied on the way, and rotate the
+ * step's queries.  The batch is ragged: request r owns the packed tokens
+ * [query_start[r], query_start[r + 1]) and, once they are appended,
+ * seq_lens[r] positions, so its token i has position
+ *   p = seq_lens[r] - n_r + i,     n_r = query_start[r + 1] - query_start[r]
+ * and belongs in cache row
+ *   slot(p) = block_table[r, p / block_size] * block_stride_rows + p % block_size.
+ * The token's row is [kv_c | rope(k_pe, p)].  rope turns the channel pairs
+ * (a, b) = (2i, 2i + 1) (interleaved) or (i, i + 32) into
+ *   (a cos - b sin, b cos + a sin),   cos, sin = cos_sin[p, i], cos_sin[p, 32 + i]
+ * in fp32; the result is rounded once, to the cache's format:
+ *   SMLA_KV_BF16                 bf16
+ *   SMLA_KV_FP8_E4M3             e4m3(x / k_scale[0]); k_scale is read
+ *   SMLA_KV_FP8_E4M3_GROUP128    as smla_cache_write_e4m3_group; k_scale written
+ *   SMLA_KV_FP8_DS_MLA           four group scales amax / 448 and their codes, bf16 rope
+ *   SMLA_KV_FP8_E4M3_GROUP4_KPE  the same four groups (k_scale [num_slots, 4] written),
+ *                                e4m3(x / kpe_scale) for the rope channels
+ *   SMLA_KV_FP8_E4M3_BLOCK       k_scale[block] = the smallest power of two s >= 2^-64
+ *     with |x| <= 448 s over the finite x that the block receives, or the
+ *     scale it has where that is larger and the block holds older rows (a
+ *     block whose first row is written in this call starts afresh); codes
+ *     e4m3(x * (1 / s)).  Where the scale grows from s0 to s the older rows'
+ *     codes c become e4m3(c * (s0 / s)), so a block's rows share its scale.
+ * All codes are rounded to nearest even and saturate at +-448.
+ *
+ *  kv_c          device bf16, row n at kv_c + n * kv_c_stride, 512 channels
+ *  k_pe          device bf16, row n at k_pe + n * k_pe_stride, 64 channels;
+ *                NULL for d_qk = 512
+ *  cos_sin       device fp32 [cos_sin_rows, 64], 16-byte aligned; NULL for
+ *                d_qk = 512
+ *  q_pe, q_out   device bf16, token n and head p at
+ *                q_pe + n * q_pe_token_stride + p * q_pe_head_stride, 64
+ *                channels, h heads (1..128); q_out may be q_pe (rotation in
+ *                place), otherwise the two must not overlap.  NULL = no
+ *                queries to rotate.
+ *  query_start   device int32 [num_reqs + 1], non-decreasing
+ *  seq_lens      device int32 [num_reqs]
+ *  block_table   device int32 [num_reqs, block_table_stride]; a negative entry
+ *                is an unallocated block (its tokens' rows are not written)
+ *  block_stride_rows  cache rows between consecutive blocks, 0 = block_size
+ *  N             packed tokens; those behind query_start[num_reqs] are left
+ *                alone, in the cache and in q_out
+ *  kv_cache      device, num_slots rows of the format, 16-byte aligned
+ *  k_scale       device fp32 as the format's; SMLA_KV_FP8_E4M3_BLOCK:
+ *                [ceil(num_slots / block_stride_rows)]
+ * Strides are in elements and multiples of 8; bases are 16-byte aligned.  The
+ * rows of one call are distinct: a block that receives rows belongs to one
+ * request.  Tokens at negative positions (seq_lens[r] < n_r) are skipped.  A
+ * position without a cos_sin row (token and query skipped), a position past
+ * the block table or a row past the cache (row skipped) sets the
+ * SMLA_ERR_BAD_INDEX device status.  Asynchronous on `stream`, no allocation.
+ * Errors: SMLA_ERR_INVALID_ARG (N < 0; num_reqs, block_table_stride,
+ * block_size or num_slots < 1; 0 < block_stride_rows < block_size; NULL or
+ * misaligned pointers, bad strides; k_pe or cos_sin given for d_qk = 512 or
+ * missing for 576; q_pe without q_out or with d_qk = 512),
+ * SMLA_ERR_UNSUPPORTED (d_qk not 512 or 576, h > 128, a format that d_qk does
+ * not have), SMLA_ERR_CUDA.  N = 0 is OK.
+ */
+SMLA_API smla_status smla_cache_append(
+    const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
+    const float* cos_sin, int64_t cos_sin_rows, int interleaved, const void* q_pe,
+    int64_t q_pe_token_stride, int64_t q_pe_head_stride, void* q_out,
+    int64_t q_out_token_stride, int64_t q_out_head_stride, int h,
+    const int32_t* query_start, const int32_t* seq_lens, const int32_t* block_table,
+    int num_reqs, int block_table_stride, int block_size, int block_stride_rows, int N,
+    int d_qk, int kv_dtype, int64_t num_slots, void* kv_cache, float* k_scale,
+    float kpe_scale, cudaStream_t stream);
+
+/*
+ * smla_fwd_window — causal attention of a ragged batch over its paged cache,
+ * whole or through a sliding window with first tokens that stay visible (what
+ * a serving stack runs beside the sparse forward: contexts shorter than
+ * top-k, layers without an indexer, prompts, streaming windows).  The batch is
+ * that of smla_cache_append, after the append: token i of request r is at
+ * position p = seq_lens[r] - n_r + i and sees the positions
+ *   e <= p  with  window == 0  or  e > p - window  or  e < sinks
+ * whose block is allocated.  For these, s_e = sm_scale <q, K_e>,
+ *   O = sum softmax(s)_e K_e[0:d_v],   LSE = ln sum exp(s_e),
+ * (0, -inf) for a token that sees no position.  Infinities and NaN in
+ * positions that a token does not see do not reach its row.
+ *  q            device, bf16 [T, h, d_qk] contiguous, 16-byte aligned
+ *  kv_cache     device, [num_slots, d_qk] rows, 16-byte aligned
+ *  kv_dtype     SMLA_KV_BF16, SMLA_KV_FP8_E4M3 or SMLA_KV_FP8_E4M3_BLOCK
+ *  k_scale      device fp32: NULL for bf16, [1], or one per cache block
+ *               [ceil(num_slots / block_stride_rows)]
+ *  query_start, seq_lens, block_table, num_reqs, block_table_stride,
+ *  block_size, block_stride_rows   as for smla_cache_append
+ *  window       positions a token sees, its own included; 0 = all up to it
+ *  sinks        first positions that stay visible (no effect when window = 0)
+ *  max_seq_len  a bound on seq_lens for the split plan, or 0; the result does
+ *               not depend on it being right, only the speed
+ *  T, h         packed tokens (>= 0) and heads (1..128)
+ *  d_v          must be 512
+ *  out          device, bf16 [T, h, d_v], 16-byte aligned
+ *  lse          device fp32 [T, h] or NULL
+ *  workspace    device, caller-owned, 256-byte aligned, at least
+ *               smla_fwd_window_workspace_size(...) bytes; NULL allowed when
+ *               that is 0.  One workspace must not be shared by calls, or by
+ *               captured graphs, that may overlap on the GPU.
+ * Rows of tokens behind query_start[num_reqs] are left alone.  A position past
+ * the block table or a row past the cache is not seen and sets the
+ * SMLA_ERR_BAD_INDEX device status.  Asynchronous on `stream`, no allocation.
+ * Errors: SMLA_ERR_INVALID_ARG (T, window or sinks < 0; h, num_reqs,
+ * block_table_stride, block_size or num_slots < 1; 0 < block_stride_rows <
+ * block_size; NULL or misaligned pointers), SMLA_ERR_UNSUPPORTED (h > 128,
+ * d_qk not 512 or 576, d_v not 512, another format, T * h >= 2^31),
+ * SMLA_ERR_WORKSPACE, SMLA_ERR_CUDA.  T = 0 is OK.
+ */
+SMLA_API smla_status smla_fwd_window(
+    const void* q, const void* kv_cache, int kv_dtype, const float* k_scale,
+    const int32_t* query_start, const int32_t* seq_lens, const int32_t* block_table,
+    int num_reqs, int block_table_stride, int block_size, int block_stride_rows, int window,
+    int sinks, int max_seq_len, int T, int h, int d_qk, int d_v, int64_t num_slots,
+    float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream);
+
+/*
+ * smla_fwd_window_workspace_size — bytes of device workspace smla_fwd_window
+ * needs for these arguments on the current device (0 when the keys of a token
+ * are not split, and for arguments that smla_fwd_window rejects).
+ */
+SMLA_API size_t smla_fwd_window_workspace_size(int num_reqs, int T, int h, int d_qk, int d_v,
+                                               int kv_dtype, int block_table_stride,
+                                               int block_size, int window, int sinks,
+                                               int max_seq_len);
 
 /*
  * smla_fwd_partial — smla_fwd that writes the normalised output in fp32 and

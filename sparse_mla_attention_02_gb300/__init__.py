@@ -23,6 +23,7 @@ SMLA_KV_FP8_E4M3 = 1
 SMLA_KV_FP8_E4M3_GROUP128 = 2
 SMLA_KV_FP8_DS_MLA = 3            # 656-byte rows: 512 E4M3 | 4 fp32 scales | 64 bf16
 SMLA_KV_FP8_E4M3_GROUP4_KPE = 4   # E4M3 [S, 576], k_scale [S, 4], one kpe scale
+SMLA_KV_FP8_E4M3_BLOCK = 5        # E4M3 [S, d_qk], one fp32 scale per cache block
 DS_MLA_ROW_BYTES = 656
 
 SMLA_OK = 0
@@ -63,6 +64,14 @@ def load():
         lib.smla_fwd_ws.restype = I
         lib.smla_cache_write_e4m3_group.argtypes = [P, P, P, I, I, I64, P, P, P]
         lib.smla_cache_write_e4m3_group.restype = I
+        lib.smla_cache_append.argtypes = [P, I64, P, I64, P, I64, I, P, I64, I64, P, I64, I64,
+                                          I, P, P, P, I, I, I, I, I, I, I, I64, P, P, F, P]
+        lib.smla_cache_append.restype = I
+        lib.smla_fwd_window.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I64,
+                                        F, P, P, P, SZ, P]
+        lib.smla_fwd_window.restype = I
+        lib.smla_fwd_window_workspace_size.argtypes = [I] * 11
+        lib.smla_fwd_window_workspace_size.restype = SZ
         lib.smla_fwd_partial.argtypes = fwd_args + [P]
         lib.smla_fwd_partial.restype = I
         lib.smla_fwd_paged.argtypes = [P, P, I, P, P, P, P, I, I, I, I, P, I, I, I,
@@ -267,6 +276,174 @@ def smla_cache_write_e4m3_group(kv_c, k_pe, slot_mapping, kv_cache, scales,
                                            kv_cache.shape[0], _p(kv_cache), _p(scales),
                                            _stream(stream)), "smla_cache_write_e4m3_group")
     return kv_cache, scales
+
+
+def _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, device):
+    """Check a ragged batch's descriptors; return the C arguments."""
+    import torch
+    i32 = torch.int32
+    _require(query_start.dtype == i32 and seq_lens.dtype == i32 and block_table.dtype == i32 and
+             query_start.is_contiguous() and seq_lens.is_contiguous() and
+             block_table.is_contiguous(),
+             "query_start, seq_lens and block_table must be contiguous int32 tensors")
+    _require(query_start.device == device and seq_lens.device == device and
+             block_table.device == device,
+             "query_start, seq_lens and block_table must be on the inputs' device")
+    _require(block_table.dim() == 2, "block_table must be [num_reqs, stride]")
+    R, width = block_table.shape
+    _require(query_start.shape == (R + 1,) and seq_lens.shape == (R,),
+             "query_start must be [num_reqs + 1] and seq_lens [num_reqs]")
+    _require(block_size >= 1 and (block_stride_rows == 0 or block_stride_rows >= block_size),
+             "block_size must be positive and block_stride_rows 0 or at least block_size")
+    return (query_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), R, width,
+            block_size, block_stride_rows)
+
+
+def _on_current_device(t, what):
+    """The library works on the current device: refuse tensors of another."""
+    import torch
+    _require(t.is_cuda and t.get_device() == torch.cuda.current_device(),
+             f"{what} must be on the current CUDA device")
+
+
+def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, device):
+    """Check a paged cache and its scales; return the slot count."""
+    import torch
+    _require(0 <= kv_dtype <= SMLA_KV_FP8_E4M3_BLOCK, "kv_dtype must be an SMLA_KV_* value")
+    row = DS_MLA_ROW_BYTES if kv_dtype == SMLA_KV_FP8_DS_MLA else d_qk
+    _require(kv_cache.dtype == (torch.bfloat16 if kv_dtype == SMLA_KV_BF16 else torch.uint8) and
+             kv_cache.is_contiguous() and kv_cache.device == device,
+             "kv_cache must be a contiguous tensor on the inputs' device, bfloat16 for a bf16 "
+             "cache and uint8 for the E4M3 formats")
+    have = kv_cache.numel() // row
+    S = have if num_slots is None else int(num_slots)
+    _require(S <= have, "num_slots is larger than kv_cache")
+    if kv_dtype == SMLA_KV_BF16 or kv_dtype == SMLA_KV_FP8_DS_MLA:
+        return S
+    need = {SMLA_KV_FP8_E4M3: 1, SMLA_KV_FP8_E4M3_GROUP128: S * ((d_qk + 127) // 128),
+            SMLA_KV_FP8_E4M3_GROUP4_KPE: 4 * S,
+            SMLA_KV_FP8_E4M3_BLOCK: -(-S // rows_per_scale)}[kv_dtype]
+    _require(k_scale is not None and k_scale.dtype == torch.float32 and
+             k_scale.is_contiguous() and k_scale.device == device and k_scale.numel() >= need,
+             "k_scale must be a contiguous fp32 tensor on the inputs' device with a value for "
+             "every scale of the format")
+    return S
+
+
+def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, block_size,
+                      kv_cache, kv_dtype, k_scale=None, kpe_scale=1.0, interleaved=True,
+                      q_pe=None, q_out=None, block_stride_rows=0, num_slots=None, stream=None):
+    """``smla_cache_append``: write a step's rows [kv_c | rope(k_pe)] into the
+    paged cache and rotate the step's queries.
+
+    kv_c bf16 [N,512], k_pe bf16 [N,64] (rows may be strided) or None for
+    512-channel rows; cos_sin fp32 [positions,64] = cos 32 | sin 32;
+    query_start int32 [R+1], seq_lens int32 [R] (lengths after the append),
+    block_table int32 [R,stride]; kv_cache and k_scale as ``kv_dtype`` says
+    (SMLA_KV_FP8_E4M3_BLOCK: fp32, one scale per cache block); q_pe bf16
+    [N,h,64] (strided) or None, q_out likewise (None: in place).
+    Returns (kv_cache, q_out)."""
+    import torch
+    lib = load()
+    bf16 = torch.bfloat16
+    _on_current_device(kv_c, "kv_c")
+    dev = kv_c.device
+    _require(kv_c.dtype == bf16 and kv_c.dim() == 2 and kv_c.shape[1] == 512 and
+             kv_c.stride(1) == 1, "kv_c must be a bf16 tensor [N, 512] with contiguous rows")
+    N = kv_c.shape[0]
+    kv_stride = kv_c.stride(0) if N > 1 else 512
+    pe = cs = None
+    pe_stride = cs_rows = 0
+    if k_pe is not None:
+        _require(k_pe.dtype == bf16 and k_pe.shape == (N, 64) and k_pe.stride(1) == 1 and
+                 k_pe.device == dev, "k_pe must be a bf16 tensor [N, 64] with contiguous rows")
+        _require(cos_sin is not None and cos_sin.dtype == torch.float32 and
+                 cos_sin.dim() == 2 and cos_sin.shape[1] == 64 and cos_sin.is_contiguous() and
+                 cos_sin.device == dev, "cos_sin must be a contiguous fp32 tensor [positions, 64]")
+        pe, pe_stride = k_pe.data_ptr(), k_pe.stride(0) if N > 1 else 64
+        cs, cs_rows = cos_sin.data_ptr(), cos_sin.shape[0]
+    d_qk = 512 if k_pe is None else 576
+    batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, dev)
+    S = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
+                    block_stride_rows or block_size, dev)
+    q_args = (None, 0, 0, None, 0, 0, 0)
+    if q_pe is not None:
+        if q_out is None:
+            q_out = q_pe
+        h = q_pe.shape[1] if q_pe.dim() == 3 else 0
+        for x in (q_pe, q_out):
+            _require(x.dtype == bf16 and x.shape == (N, h, 64) and x.stride(2) == 1 and
+                     x.device == dev, "q_pe and q_out must be bf16 tensors [N, h, 64] with "
+                                      "contiguous channels")
+        q_args = (q_pe.data_ptr(), q_pe.stride(0) if N > 1 else 64,
+                  q_pe.stride(1) if h > 1 else 64, q_out.data_ptr(),
+                  q_out.stride(0) if N > 1 else 64, q_out.stride(1) if h > 1 else 64, h)
+    _check(lib.smla_cache_append(
+        kv_c.data_ptr(), kv_stride, pe, pe_stride, cs, cs_rows, interleaved, *q_args, *batch, N,
+        d_qk, kv_dtype, S, kv_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+        kpe_scale, _stream(stream)), "smla_cache_append")
+    return kv_cache, q_out
+
+
+def smla_fwd_window_workspace_size(num_reqs, T, h, d_qk, kv_dtype, block_table_stride,
+                                   block_size, window=0, sinks=0, max_seq_len=None,
+                                   d_v=512) -> int:
+    return int(load().smla_fwd_window_workspace_size(
+        num_reqs, T, h, d_qk, d_v, kv_dtype, block_table_stride, block_size, window, sinks,
+        max_seq_len or 0))
+
+
+def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table,
+                    block_size, sm_scale, window=0, sinks=0, max_seq_len=None,
+                    block_stride_rows=0, out=None, lse=None, want_lse=True, num_slots=None,
+                    workspace=None, stream=None):
+    """``smla_fwd_window``: causal attention of a ragged batch over its paged
+    cache, through a sliding window (0: none) with ``sinks`` first positions
+    that stay visible.
+
+    q bf16 [T,h,d_qk]; kv_cache bf16 or uint8 [S,d_qk] (SMLA_KV_BF16,
+    SMLA_KV_FP8_E4M3 or SMLA_KV_FP8_E4M3_BLOCK); query_start int32 [R+1],
+    seq_lens int32 [R], block_table int32 [R,stride] as for
+    ``smla_cache_append``; max_seq_len: a bound on seq_lens that sizes the
+    split plan; workspace: a uint8 device tensor of at least
+    smla_fwd_window_workspace_size bytes, or None to allocate one.
+    Returns (out bf16 [T,h,512], lse f32 [T,h] or None); rows behind the last
+    request are not written."""
+    import torch
+    lib = load()
+    _on_current_device(q, "q")
+    dev = q.device
+    _require(q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_contiguous(),
+             "q must be a contiguous bf16 device tensor [T, h, d_qk]")
+    T, h, d_qk = q.shape
+    batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, dev)
+    S = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
+                    block_stride_rows or block_size, dev)
+    if out is None:
+        out = torch.empty((T, h, 512), dtype=torch.bfloat16, device=dev)
+    _require(out.dtype == torch.bfloat16 and out.shape == (T, h, 512) and out.is_contiguous() and
+             out.device == dev, "out must be contiguous bf16 [T, h, 512]")
+    if lse is None and want_lse:
+        lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+    _require(lse is None or (lse.dtype == torch.float32 and lse.shape == (T, h) and
+                             lse.is_contiguous() and lse.device == dev),
+             "lse must be contiguous fp32 [T, h]")
+    limit = max_seq_len or 0
+    if workspace is None:
+        nbytes = lib.smla_fwd_window_workspace_size(batch[3], T, h, d_qk, 512, kv_dtype, batch[4],
+                                                    block_size, window, sinks, limit)
+        if nbytes:
+            with torch.cuda.stream(stream):          # (None: the current stream)
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(lib.smla_fwd_window(
+        q.data_ptr(), kv_cache.data_ptr(), kv_dtype,
+        None if k_scale is None else k_scale.data_ptr(), *batch, window, sinks, limit, T, h, d_qk,
+        512, S, sm_scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream)),
+        "smla_fwd_window")
+    return out, lse
 
 
 def smla_fwd_partial(q, kv_cache, kv_dtype, k_scale, indices, valid_len,

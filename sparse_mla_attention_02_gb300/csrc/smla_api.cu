@@ -89,6 +89,48 @@ smla_status check_args(const void* q, const void* kv, int kv_dtype,
   return SMLA_OK;
 }
 
+// The batch descriptors that smla_cache_append and smla_fwd_window share.
+smla_status make_batch(const int32_t* query_start, const int32_t* seq_lens,
+                       const int32_t* block_table, int num_reqs, int block_table_stride,
+                       int block_size, int block_stride_rows, int N, int64_t num_slots,
+                       smla::PagedBatch* b) {
+  if (N < 0 || num_reqs < 1 || block_table_stride < 1 || block_size < 1 || num_slots < 1 ||
+      (block_stride_rows != 0 && block_stride_rows < block_size))
+    return SMLA_ERR_INVALID_ARG;
+  if (num_slots > 0x7FFFFFFFLL || num_reqs > (1 << 24)) return SMLA_ERR_UNSUPPORTED;
+  if (N == 0) return SMLA_OK;
+  if (!query_start || !seq_lens || !block_table || !aligned(query_start, 4) ||
+      !aligned(seq_lens, 4) || !aligned(block_table, 4))
+    return SMLA_ERR_INVALID_ARG;
+  *b = smla::PagedBatch{query_start, seq_lens, block_table, num_reqs, block_table_stride,
+                        block_size, block_stride_rows ? block_stride_rows : block_size, N,
+                        num_slots};
+  return SMLA_OK;
+}
+
+smla_status check_window_shape(int T, int h, int d_qk, int d_v, int kv_dtype, int window,
+                               int sinks) {
+  if (T < 0 || h < 1 || window < 0 || sinks < 0) return SMLA_ERR_INVALID_ARG;
+  if (h > 128 || (d_qk != 512 && d_qk != 576) || d_v != 512 || (int64_t)T * h > 0x7FFFFFFFLL)
+    return SMLA_ERR_UNSUPPORTED;
+  if (kv_dtype != SMLA_KV_BF16 && kv_dtype != SMLA_KV_FP8_E4M3 &&
+      kv_dtype != SMLA_KV_FP8_E4M3_BLOCK)
+    return SMLA_ERR_UNSUPPORTED;
+  return SMLA_OK;
+}
+
+// The plan of smla_fwd_window: the keys of a request are at most what the
+// block table holds, or the caller's bound where that is smaller.
+smla::WindowPlan window_plan(int num_reqs, int T, int h, int block_table_stride, int block_size,
+                             int window, int sinks, int max_seq_len, int num_sms) {
+  int64_t len = (int64_t)block_table_stride * block_size;
+  if (max_seq_len > 0 && max_seq_len < len) len = max_seq_len;
+  return smla::make_window_plan(T, h, num_reqs, len, window, sinks, num_sms);
+}
+
+// A row stride (in bf16 elements) that keeps 16-byte loads aligned.
+bool row_strides(int64_t stride, int64_t least) { return stride >= least && stride % 8 == 0; }
+
 // Request-local index translation (smla_fwd_paged); table == nullptr for
 // global slot ids.
 struct Paged {
@@ -348,6 +390,141 @@ smla_status smla_cache_write_e4m3_group(const void* kv_c, const void* k_pe,
                                   scales, dev->status, stream) == cudaSuccess
              ? SMLA_OK
              : SMLA_ERR_CUDA;
+}
+
+smla_status smla_cache_append(const void* kv_c, int64_t kv_c_stride, const void* k_pe,
+                              int64_t k_pe_stride, const float* cos_sin,
+                              int64_t cos_sin_rows, int interleaved, const void* q_pe,
+                              int64_t q_pe_token_stride, int64_t q_pe_head_stride,
+                              void* q_out, int64_t q_out_token_stride,
+                              int64_t q_out_head_stride, int h, const int32_t* query_start,
+                              const int32_t* seq_lens, const int32_t* block_table,
+                              int num_reqs, int block_table_stride, int block_size,
+                              int block_stride_rows, int N, int d_qk, int kv_dtype,
+                              int64_t num_slots, void* kv_cache, float* k_scale,
+                              float kpe_scale, cudaStream_t stream) {
+  const bool rope = d_qk == 576;
+  if (d_qk != 512 && d_qk != 576) return SMLA_ERR_UNSUPPORTED;
+  if (kv_dtype < SMLA_KV_BF16 || kv_dtype > SMLA_KV_FP8_E4M3_BLOCK ||
+      ((kv_dtype == SMLA_KV_FP8_DS_MLA || kv_dtype == SMLA_KV_FP8_E4M3_GROUP4_KPE) && !rope))
+    return SMLA_ERR_UNSUPPORTED;
+  smla::PagedBatch b{};
+  smla_status st = make_batch(query_start, seq_lens, block_table, num_reqs,
+                              block_table_stride, block_size, block_stride_rows, N,
+                              num_slots, &b);
+  if (st != SMLA_OK || N == 0) return st;
+  if (!kv_c || !kv_cache || !aligned(kv_c, 16) || !aligned(kv_cache, 16) ||
+      !row_strides(kv_c_stride, 512))
+    return SMLA_ERR_INVALID_ARG;
+  if (rope != (k_pe != nullptr) || rope != (cos_sin != nullptr)) return SMLA_ERR_INVALID_ARG;
+  if (rope && (!aligned(k_pe, 16) || !row_strides(k_pe_stride, 64) || !aligned(cos_sin, 16) ||
+               cos_sin_rows < 1))
+    return SMLA_ERR_INVALID_ARG;
+  const bool scales = kv_dtype != SMLA_KV_BF16 && kv_dtype != SMLA_KV_FP8_DS_MLA;
+  if (scales && (!k_scale || !aligned(k_scale, 4))) return SMLA_ERR_INVALID_ARG;
+  if (q_pe) {
+    if (!rope || !q_out || h < 1 || !aligned(q_pe, 16) || !aligned(q_out, 16) ||
+        !row_strides(q_pe_head_stride, 64) || !row_strides(q_out_head_stride, 64) ||
+        !row_strides(q_pe_token_stride, 64) || !row_strides(q_out_token_stride, 64))
+      return SMLA_ERR_INVALID_ARG;
+    if (h > 128) return SMLA_ERR_UNSUPPORTED;
+  }
+  DeviceInfo* dev = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if ((st = device_info(&dev)) != SMLA_OK) return st;
+  }
+  smla::AppendParams a{};
+  a.b = b;
+  a.kv_c = static_cast<const uint16_t*>(kv_c);
+  a.kv_c_stride = kv_c_stride;
+  a.k_pe = static_cast<const uint16_t*>(k_pe);
+  a.k_pe_stride = k_pe_stride;
+  a.cos_sin = cos_sin;
+  a.cos_sin_rows = cos_sin_rows;
+  a.interleaved = interleaved ? 1 : 0;
+  a.q_pe = static_cast<const uint16_t*>(q_pe);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_tok = q_pe_token_stride;
+  a.q_head = q_pe_head_stride;
+  a.qo_tok = q_out_token_stride;
+  a.qo_head = q_out_head_stride;
+  a.h = h;
+  a.cache = kv_cache;
+  a.k_scale = k_scale;
+  a.kpe_scale = kpe_scale;
+  a.status = dev->status;
+  return smla::launch_append(a, kv_dtype, rope, stream) == cudaSuccess ? SMLA_OK
+                                                                       : SMLA_ERR_CUDA;
+}
+
+smla_status smla_fwd_window(const void* q, const void* kv_cache, int kv_dtype,
+                            const float* k_scale, const int32_t* query_start,
+                            const int32_t* seq_lens, const int32_t* block_table, int num_reqs,
+                            int block_table_stride, int block_size, int block_stride_rows,
+                            int window, int sinks, int max_seq_len, int T, int h, int d_qk,
+                            int d_v, int64_t num_slots, float sm_scale, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  smla_status st = check_window_shape(T, h, d_qk, d_v, kv_dtype, window, sinks);
+  if (st != SMLA_OK) return st;
+  smla::PagedBatch b{};
+  st = make_batch(query_start, seq_lens, block_table, num_reqs, block_table_stride, block_size,
+                  block_stride_rows, T, num_slots, &b);
+  if (st != SMLA_OK || T == 0) return st;
+  if (!q || !kv_cache || !out || (kv_dtype != SMLA_KV_BF16 && !k_scale))
+    return SMLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) ||
+      (k_scale && !aligned(k_scale, 4)) || (lse && !aligned(lse, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  smla::WinParams p{};
+  {
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if ((st = device_info(&dev)) != SMLA_OK) return st;
+    p.inject_stall = dev->stall;
+    p.wait_limit_ns = dev->wait_limit_ns ? dev->wait_limit_ns : smla::kWaitLimitNs;
+  }
+  const smla::WindowPlan plan =
+      window_plan(num_reqs, T, h, block_table_stride, block_size, window, sinks, max_seq_len,
+                  dev->num_sms);
+  if (plan.workspace_bytes > 0) {
+    if (!workspace || workspace_bytes < plan.workspace_bytes) return SMLA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
+    p.o_part = static_cast<float*>(workspace);
+    p.lse_part = p.o_part + (size_t)plan.splits * T * h * 512;
+  }
+  p.b = b;
+  p.q = q;
+  p.kv = kv_cache;
+  p.k_scale = k_scale;
+  p.out = out;
+  p.lse = lse;
+  p.status = dev->status;
+  p.abort_ctr = dev->abort_ctr;
+  p.kv_format = kv_dtype;
+  p.h = h;
+  p.d_qk = d_qk;
+  p.window = window;
+  p.sinks = sinks;
+  p.splits = plan.splits;
+  p.sm_scale = sm_scale;
+  return smla::launch_window(p, stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+size_t smla_fwd_window_workspace_size(int num_reqs, int T, int h, int d_qk, int d_v,
+                                      int kv_dtype, int block_table_stride, int block_size,
+                                      int window, int sinks, int max_seq_len) {
+  if (check_window_shape(T, h, d_qk, d_v, kv_dtype, window, sinks) != SMLA_OK || T == 0 ||
+      num_reqs < 1 || block_table_stride < 1 || block_size < 1)
+    return 0;
+  DeviceInfo* dev = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if (device_info(&dev) != SMLA_OK) return 0;
+  }
+  return window_plan(num_reqs, T, h, block_table_stride, block_size, window, sinks, max_seq_len,
+                     dev->num_sms)
+      .workspace_bytes;
 }
 
 smla_status smla_fwd_partial(const void* q, const void* kv_cache, int kv_dtype,

@@ -1,0 +1,1087 @@
+// smla_tc_win.cu — causal MLA attention over a paged latent cache, whole or
+// through a sliding window with first tokens that stay visible
+// (smla_fwd_window), for bf16 rows and for E4M3 rows with one scale per cache
+// block or per tensor.
+//
+// Mathematics.  The row (token at position p, head) sees the positions
+//   V(p) = { e <= p : window == 0  or  e > p - window  or  e < sinks }
+// whose block is allocated, s_e = sm_scale <q, K_e>, O = sum softmax(s)_e
+// K_e[0:512], LSE = ln sum exp(s_e); no visible position gives (0, -inf).
+// One pass over the keys with a running maximum (raised lazily: O is rescaled
+// only when it grows by more than 2^8) and the running sum in fp32.
+//
+// Tile.  All heads share the key rows, and neighbouring tokens of a request
+// share most of them, so a tile is 128 consecutive rows of the flattened
+// (token, head) list of one request, whatever h is, and a block is 128 key
+// positions.  O [128, 512] in fp32 fills one SM's TMEM by itself, so a tile
+// runs on a pair of SMs as MMAs over both (cta_group::2) with M = 128: a CTA
+// holds 64 rows, whose O takes 256 of its 512 TMEM columns and whose scores
+// take 2 x 64.  The pair's MMAs run at the rate of two single-SM MMAs with
+// M = 128 (measured: 36 QK and 16 PV steps of a block in 2210 cycles, 2176 at
+// the peak rate); no partial score crosses between the SMs, in contrast to
+// the sparse kernels' split over d_qk (smla_tc.cu), which can share one copy
+// of a key row between QK and PV instead.
+//   QK  S[128, 128] = Q . K^T      A = Q rows (64 per CTA, resident),
+//                                  B = K rows: 64 of the 128 keys per CTA
+//   PV  O[128, 256 n ..] += P . V  A = P rows (64 per CTA),
+//                                  B = V^T: 128 of the 256 channels per CTA
+//       for n = 0, 1
+// A key's row is therefore read twice from L2 (as K by one CTA, as V by halves
+// by both), once from HBM.
+//
+// Shared memory (bf16): Q 72 KB, K 72 KB, V 64 KB, P 16 KB.  K and V are one
+// block deep, in rings of 3 channel groups and of 4 (channel half, key half)
+// units; each part is refilled as soon as its MMAs are done, so the loads of
+// block j + 1 run under the MMAs of block j.
+//
+// E4M3 rows.  QK multiplies the codes as they are (kind::f8f6f4, twice the
+// bf16 rate): Q is the sum of two E4M3 terms after a power-of-two scale per
+// row that puts its largest value in [224, 448); a bf16 value has 8 significant bits
+// and an E4M3 value 4, so hi = e4m3(q) and lo = e4m3(q - hi) give q exactly down
+// to 2^-11 of the row's largest value (below, to 2^-19 of it).  The key's
+// scale multiplies its scores in fp32.  PV needs P in 16 bits, so V is
+// converted to bf16 (exact) by four warps on its way to shared memory, and the
+// key's scale multiplies P before it is rounded.
+//
+// Masked positions never reach an MMA as anything but zeros where no row of
+// the tile sees them (unwritten rows, blocks that are not allocated, positions
+// past the last token: the copies read zero fill).  Where a row masks a
+// position that another row of its tile sees, its score is replaced and its
+// weight is 0; an infinity or NaN there would still make 0 * inf, so a row whose
+// output is not finite although its softmax is is computed again from its
+// visible positions alone (slow_row).
+//
+// Few tiles: the keys of a tile are cut into `splits` ranges of blocks, each
+// leaves a normalised fp32 partial and its LSE, and a second kernel merges them.
+//
+// Warp roles: warp 0 issues the MMAs (in the even CTA) and owns TMEM; warps 1
+// and 2 load K and V; warp 3 looks up each block's rows (validity, scales, row
+// ids); warps 4..11 are the softmax: four threads per row (TMEM lane half x
+// column half), 32 keys each; with E4M3 rows warps 12..15 convert V.
+// Every wait is bounded, as in the sparse kernels (tc_common.cuh).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "e4m3_quant.cuh"
+#include "paged_batch.cuh"
+#include "smla_internal.h"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace smla {
+namespace {
+
+using namespace ptx;
+
+constexpr int kBN = 128;                   // key positions per block
+constexpr int kRows = 64;                  // tile rows per CTA
+constexpr uint32_t kAtom = 8192;           // 64 rows x 128 bytes
+constexpr int kKGroups = 3;                // K ring: channel groups
+constexpr int kVUnits = 4;                 // V ring: (channel half n, key half)
+constexpr int kMeta = 4;                   // blocks of lookups ahead
+
+// TMEM columns.
+constexpr uint32_t kColO = 0;              // 2 x 128
+constexpr uint32_t kColS = 256;            // 2 x 64
+constexpr uint32_t kTmemCols = 512;
+
+enum {
+  kBarKFull = 0,                           // [3] even CTA: both CTAs' bytes
+  kBarKEmpty = kBarKFull + kKGroups,       // [3] both
+  kBarVFull = kBarKEmpty + kKGroups,       // [4] even CTA
+  kBarVEmpty = kBarVFull + kVUnits,        // [4] both
+  kBarSFull = kBarVEmpty + kVUnits,        // [2] both
+  kBarSEmpty = kBarSFull + 2,              // [2] even CTA: 16 warps
+  kBarPFull = kBarSEmpty + 2,              // even CTA: 16 warps
+  kBarPEmpty,                              // both
+  kBarQFull,                               // even CTA
+  kBarMFull,                               // [4] own
+  kBarMEmpty = kBarMFull + kMeta,          // [4] own
+  kBarDrain = kBarMEmpty + kMeta,          // even CTA
+  kNumBars
+};
+
+template <bool kFp8>
+struct Cfg {
+  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kElem = kFp8 ? 1 : 2;
+  static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
+  static constexpr int kMaxAtoms = kFp8 ? 5 : 9;        // 128-byte columns of a row
+  static constexpr int kQTerms = kFp8 ? 2 : 1;
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffK = kOffQ + kQTerms * kMaxAtoms * kAtom;
+  static constexpr uint32_t kOffV = kOffK + kMaxAtoms * kAtom;
+  static constexpr uint32_t kOffP = kOffV + kVUnits * 2 * kAtom;
+  static constexpr uint32_t kOffRed = kOffP + 2 * kAtom;             // bf16 [2][4][64]
+  static constexpr uint32_t kOffBar = kOffRed + 1024;
+  static constexpr uint32_t kOffMask = kOffBar + 8 * ((kNumBars + 1) & ~1);   // u32 [kMeta][4]
+  static constexpr uint32_t kOffTmem = kOffMask + kMeta * 16;
+  static constexpr uint32_t kOffAbort = kOffTmem + 4;
+  // E4M3: row ids and scales of a block, the Q rows' scales
+  static constexpr uint32_t kOffIds = (kOffAbort + 4 + 15) & ~15u;
+  static constexpr uint32_t kOffScale = kOffIds + (kFp8 ? kMeta * kBN * 4 : 0);
+  static constexpr uint32_t kOffQScale = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
+  static constexpr uint32_t kSmem = kOffQScale + (kFp8 ? kRows * 4 : 0);
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+// The epilogue's areas: O rows at a stride of 1040 bytes (16-byte row copies,
+// no bank conflicts) over V and the head of P; row sums and flags behind.
+constexpr uint32_t kOStride = 1040;
+constexpr uint32_t kOffSums = 4096;        // from kOffP: float [2][4][64]
+constexpr uint32_t kOffFlag = 4096 + 2048; // from kOffP: int [64]
+static_assert(kRows * kOStride <= kVUnits * 2 * kAtom + 4096, "O staging");
+
+struct WinArgs {
+  CUtensorMap row_map;   // the cache, boxes of one row x 128 bytes (gather4)
+  CUtensorMap box_map;   // the cache, boxes of `box` rows x 128 bytes
+  CUtensorMap q_map;     // bf16 q [T * h, d_qk], boxes of 64 rows x 64 channels
+  WinParams p;
+  int box;               // rows per box, a power of two in 4..64; 0: gather4 alone
+  int atoms;             // 128-byte columns of a row
+  int ksteps;            // 32-byte MMA steps of a row
+  float scale_log2;      // sm_scale * log2(e)
+};
+
+// The tiles of a request are numbered from first_tile on.  h = 128: a tile is
+// a token.  Otherwise n tokens make ceil(n h / 128) <= floor((c + n) h / 128)
+// - floor(c h / 128) + 1 tiles, so floor(start h / 128) + r keeps the requests'
+// numbers apart, and T h / 128 + R of them hold every tile.
+__device__ __forceinline__ int64_t first_tile(const WinParams& p, int r) {
+  const int64_t c = batch_start(p.b, r);
+  return p.h == 128 ? c : c * p.h / 128 + r;
+}
+
+// What a tile sees: positions [lo, hi] and [0, sinks), as key blocks.
+struct Tile {
+  int r;                 // request
+  int64_t row0, row1;    // its rows of the flattened list, row1 exclusive
+  int p_last;            // position of its last token
+  int lo, sinks;         // [lo, p_last] and [0, sinks) are seen by some row
+  int sink_blocks, win_block, n_blocks;
+  __device__ __forceinline__ int block(int i) const {   // i-th block's index
+    return i < sink_blocks ? i : win_block + (i - sink_blocks);
+  }
+};
+
+__device__ __forceinline__ Tile find_tile(const WinParams& p, int64_t u) {
+  Tile t;
+  t.r = warp_last_request(p.b.num_reqs, u, [&](int m) { return first_tile(p, m); });
+  const int c0 = batch_start(p.b, t.r), c1 = batch_start(p.b, t.r + 1);
+  const int64_t k = u - first_tile(p, t.r);
+  t.row0 = (int64_t)c0 * p.h + 128 * k;
+  t.row1 = min(t.row0 + 128, (int64_t)c1 * p.h);
+  if (k < 0) t.row1 = t.row0;
+  t.n_blocks = t.sink_blocks = t.win_block = 0;
+  t.p_last = t.lo = -1;
+  t.sinks = 0;
+  if (t.row1 <= t.row0) return t;
+  const int len = __ldg(p.b.seq_lens + t.r);
+  const int tok0 = (int)(t.row0 / p.h), tok1 = (int)((t.row1 - 1) / p.h);
+  t.p_last = len - (c1 - tok1);
+  if (t.p_last < 0) return t;
+  const int p_first = max(len - (c1 - tok0), 0);
+  t.lo = p.window ? max(p_first - (p.window - 1), 0) : 0;
+  t.sinks = min(p.sinks, t.lo);
+  t.win_block = t.lo / kBN;
+  t.sink_blocks = min((t.sinks + kBN - 1) / kBN, t.win_block);
+  t.n_blocks = t.sink_blocks + t.p_last / kBN + 1 - t.win_block;
+  return t;
+}
+
+// Cache rows of the four positions pos .. pos + 3 (pos a multiple of 4), -1
+// where no row of the tile sees the position or it has no row.
+struct Rows4 {
+  int id[4];
+  int blk[4];
+};
+__device__ __forceinline__ Rows4 lookup4(const WinParams& p, const Tile& t, int pos, bool& bad) {
+  Rows4 o;
+  int page = -1, blk = -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = pos + i;
+    const bool seen = e <= t.p_last && (e >= t.lo || e < t.sinks);
+    o.id[i] = -1;
+    o.blk[i] = -1;
+    if (seen) {
+      const int pg = e / p.b.block_size;
+      if (pg != page) {
+        page = pg;
+        blk = batch_block(p.b, t.r, pg, bad);
+      }
+      o.id[i] = batch_row(p.b, blk, e - pg * p.b.block_size, bad);
+      if (o.id[i] >= 0) o.blk[i] = blk;
+    }
+  }
+  return o;
+}
+
+// A key's scale (E4M3 caches).
+__device__ __forceinline__ float key_scale(const WinParams& p, int blk) {
+  return p.kv_format == kE4m3Block ? __ldg(p.k_scale + blk) : __ldg(p.k_scale);
+}
+
+// One tile row again, from its visible positions alone, by one warp: the
+// positions of blocks [b0, b1) of the tile.  O is written to `out_f32` or
+// `out_bf16` (512 channels).  Lane l holds channels 2 l + 64 i, + 1.
+template <bool kFp8>
+static __device__ __noinline__ void slow_row(const WinParams& p, const Tile& t, int64_t g, int pos,
+                                             int lo, int b0, int b1, float* out_f32,
+                                             __nv_bfloat16* out_bf16) {
+  const int lane = threadIdx.x & 31;
+  const int n2 = p.d_qk / 64;
+  float q[9][2], acc[8][2];
+  const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) +
+                                                         g * p.d_qk) + lane;
+#pragma unroll
+  for (int i = 0; i < 9; ++i) {
+    const uint32_t w = i < n2 ? __ldg(qr + 32 * i) : 0u;
+    q[i][0] = __uint_as_float(w << 16);
+    q[i][1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const int e0 = t.block(b) * kBN;
+    for (int e = e0; e < e0 + kBN && e <= pos; ++e) {
+      if (!(e >= lo || e < p.sinks)) continue;
+      const int page = e / p.b.block_size;
+      const int blk = batch_block(p.b, t.r, page, bad);
+      const int row = batch_row(p.b, blk, e - page * p.b.block_size, bad);
+      if (row < 0) continue;
+      float k[9][2], s = 0.f;
+      const float sc = kFp8 ? key_scale(p, blk) : 1.f;
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        k[i][0] = k[i][1] = 0.f;
+        if (i < n2) {
+          if (kFp8) {
+            const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(
+                                         static_cast<const uint8_t*>(p.kv) +
+                                         (int64_t)row * p.d_qk) + lane + 32 * i);
+            float x, y;
+            e4m3x4_to_f32(w, k[i][0], k[i][1], x, y);
+            k[i][0] *= sc;
+            k[i][1] *= sc;
+          } else {
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(
+                                         static_cast<const uint16_t*>(p.kv) +
+                                         (int64_t)row * p.d_qk) + lane + 32 * i);
+            k[i][0] = __uint_as_float(w << 16);
+            k[i][1] = __uint_as_float(w & 0xFFFF0000u);
+          }
+          s = fmaf(q[i][0], k[i][0], fmaf(q[i][1], k[i][1], s));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      s *= p.sm_scale;
+      if (s > m) {
+        const float a = expf(m - s);
+        l *= a;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[i][0] *= a;
+          acc[i][1] *= a;
+        }
+        m = s;
+      }
+      const float w = s == -INFINITY ? 0.f : expf(s - m);
+      l += w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[i][0] = fmaf(w, k[i][0], acc[i][0]);
+        acc[i][1] = fmaf(w, k[i][1], acc[i][1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = acc[i][0] / l, y = acc[i][1] / l;
+    const int c = 2 * lane + 64 * i;
+    if (out_f32)
+      *reinterpret_cast<float2*>(out_f32 + c) = make_float2(x, y);
+    else
+      *reinterpret_cast<uint32_t*>(out_bf16 + c) = pack_bf16(x, y);
+  }
+}
+
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
+smla_window_kernel(const __grid_constant__ WinArgs a) {
+  using C = Cfg<kFp8>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const WinParams& p = a.p;
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t r = cluster_ctarank();
+
+  // ---- work unit: (tile, range of its key blocks) -------------------------
+  // Tiles are taken from the last: a prompt's later tokens see more keys.
+  const int64_t unit = (int64_t)(blockIdx.x >> 1);
+  const int split = (int)(unit % p.splits);
+  const Tile t = find_tile(p, p.num_tiles - 1 - unit / p.splits);
+  if (t.row1 <= t.row0) return;                      // (both CTAs)
+  const int b0 = (int)((int64_t)t.n_blocks * split / p.splits);
+  const int b1 = (int)((int64_t)t.n_blocks * (split + 1) / p.splits);
+  const int nb = b1 - b0;
+
+  auto bar = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
+  Waiter W{abort_flag, p.status, p.abort_ctr, *reinterpret_cast<volatile int*>(p.abort_ctr),
+           p.wait_limit_ns};
+
+  if (tid == 0) {
+    for (int i = 0; i < kKGroups; ++i) {
+      mbar_init(bar(kBarKFull + i), 1);
+      mbar_init(bar(kBarKEmpty + i), 1);
+    }
+    for (int i = 0; i < kVUnits; ++i) {
+      mbar_init(bar(kBarVFull + i), kFp8 ? 8 : 1);   // E4M3: converter warps of both CTAs
+      mbar_init(bar(kBarVEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarSFull + i), 1);
+      mbar_init(bar(kBarSEmpty + i), 16);
+    }
+    mbar_init(bar(kBarPFull), 16);
+    mbar_init(bar(kBarPEmpty), 1);
+    mbar_init(bar(kBarQFull), kFp8 ? 16 : 1);        // E4M3: the softmax warps write Q
+    for (int i = 0; i < kMeta; ++i) {
+      mbar_init(bar(kBarMFull + i), 1);
+      mbar_init(bar(kBarMEmpty + i), kFp8 ? 12 : 8);
+    }
+    mbar_init(bar(kBarDrain), 1);
+    *abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(sb + C::kOffTmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::kOffTmem);
+  // The even CTA's barriers, as cluster addresses.
+  auto bar0 = [&](int i) { return mapa(bar(i), 0); };
+
+  if (warp == 0) {
+    // ---- MMA issuer (even CTA) ---------------------------------------------
+    if (r == 0 && nb > 0) {
+      const uint32_t id_qk = kFp8 ? idesc_pair_e4m3(128, kBN) : idesc_bf16(128, kBN, false, false);
+      const uint32_t id_pv = idesc_bf16(128, 256, false, true);
+      W.wait_cluster(bar(kBarQFull), 0);
+      auto issue_qk = [&](int j) {
+        if (p.inject_stall && j == 0) return;        // tests: block 0's scores never arrive
+        if (j >= 2) W.wait_cluster(bar(kBarSEmpty + (j & 1)), ((j >> 1) - 1) & 1);
+        const uint32_t dS = tmem + kColS + 64 * (j & 1);
+        for (int g = 0; g * C::kAtomsPerGroup < a.atoms; ++g) {
+          W.wait_cluster(bar(kBarKFull + g), j & 1);
+          __syncwarp();
+          tc_fence_after();
+          const int k0 = g * C::kAtomsPerGroup * 4;
+          const int k1 = min(k0 + C::kAtomsPerGroup * 4, a.ksteps);
+          if (elect_one()) {
+            fence_proxy_async_smem();
+            for (int ks = k0; ks < k1; ++ks) {
+              const uint32_t off = (ks >> 2) * kAtom + (ks & 3) * 32;
+              const uint64_t bd = sdesc(sb + C::kOffK + off, 16, 1024, kLayoutSw128);
+              const uint64_t ad = sdesc(sb + C::kOffQ + off, 16, 1024, kLayoutSw128);
+              if (kFp8) {
+                mma_pair_e4m3(dS, ad, bd, id_qk, ks > 0 ? 1u : 0u);
+                mma_pair_e4m3(dS, sdesc(sb + C::kOffQ + C::kMaxAtoms * kAtom + off, 16, 1024,
+                                        kLayoutSw128), bd, id_qk, 1u);
+              } else {
+                mma_pair_bf16(dS, ad, bd, id_qk, ks > 0 ? 1u : 0u);
+              }
+            }
+            mma_commit_pair(bar(kBarKEmpty + g));
+          }
+          __syncwarp();
+        }
+        if (elect_one()) mma_commit_pair(bar(kBarSFull + (j & 1)));
+        __syncwarp();
+      };
+      auto issue_pv = [&](int j) {
+        W.wait_cluster(bar(kBarPFull), j & 1);
+        for (int v = 0; v < kVUnits; ++v) {          // v = 2 n + key half
+          W.wait_cluster(bar(kBarVFull + v), j & 1);
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+            fence_proxy_async_smem();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint64_t ad = sdesc(sb + C::kOffP + (v & 1) * kAtom + ks * 32, 16, 1024,
+                                        kLayoutSw128);
+              const uint64_t bd = sdesc(sb + C::kOffV + v * 2 * kAtom + ks * 2048, kAtom, 1024,
+                                        kLayoutSw128);
+              mma_pair_bf16(tmem + kColO + 128 * (v >> 1), ad, bd, id_pv,
+                            (j > 0 || (v & 1) || ks > 0) ? 1u : 0u);
+            }
+            mma_commit_pair(bar(kBarVEmpty + v));
+          }
+          __syncwarp();
+        }
+        if (elect_one()) mma_commit_pair(bar(kBarPEmpty));
+        __syncwarp();
+      };
+      issue_qk(0);
+      if (nb > 1) issue_qk(1);
+      for (int j = 0; j < nb; ++j) {
+        issue_pv(j);
+        if (j + 2 < nb) issue_qk(j + 2);
+      }
+    }
+    // Every MMA issued here has completed (also after an abort) before either
+    // CTA frees its TMEM or leaves its tiles.
+    if (r == 0) {
+      __syncwarp();
+      if (elect_one()) mma_commit_pair(bar(kBarDrain));
+      __syncwarp();
+      W.drain(bar(kBarDrain), 0);
+    }
+  } else if (warp == 1) {
+    // ---- K loads: this CTA's 64 of each block's 128 keys --------------------
+    const int groups = (a.atoms + C::kAtomsPerGroup - 1) / C::kAtomsPerGroup;
+    int issued = 0;                                  // channel groups loaded, in order
+    if (!kFp8 && lane == 0) {
+      if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
+      for (int c = 0; c < a.atoms; ++c)
+        tma_load_2d_pair(sb + C::kOffQ + c * kAtom, &a.q_map, 64 * c, (int)(t.row0 + 64 * r),
+                         bar0(kBarQFull));
+    }
+    __syncwarp();
+    const int cols = 128 / C::kElem;                 // channels per atom
+    bool bad = false;
+    Rows4 nx;
+    if (nb > 0) nx = lookup4(p, t, t.block(b0) * kBN + 64 * r + 4 * (lane & 15), bad);
+    for (int j = 0; j < nb; ++j) {
+      const Rows4 cur = nx;
+      if (j + 1 < nb) nx = lookup4(p, t, t.block(b0 + j + 1) * kBN + 64 * r + 4 * (lane & 15), bad);
+      const bool all4 = cur.id[0] >= 0 && cur.id[1] >= 0 && cur.id[2] >= 0 && cur.id[3] >= 0;
+      const uint32_t full = __ballot_sync(0xffffffffu, all4) & 0xFFFFu;
+      // lanes of this lane's box, all seen and allocated: one copy for the box
+      const int per = a.box >> 2;
+      const uint32_t mine = per ? (per == 32 ? ~0u : ((1u << per) - 1u)) << (lane & ~(per - 1)) : 0u;
+      const bool boxed = per && (full & mine) == mine;
+      for (int g = 0; g < groups; ++g) {
+        if (j >= 1) W.wait_cluster(bar(kBarKEmpty + g), (j - 1) & 1);
+        if (*abort_flag) break;
+        const int c0 = g * C::kAtomsPerGroup, c1 = min(c0 + C::kAtomsPerGroup, a.atoms);
+        if (r == 0 && lane == 0)
+          mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * (uint32_t)(c1 - c0) * kAtom);
+        __syncwarp();
+        if (lane < 16 && (!boxed || (lane & (per - 1)) == 0)) {
+          const uint32_t full_bar = bar0(kBarKFull + g);
+          for (int c = c0; c < c1; ++c) {
+            const uint32_t dst = sb + C::kOffK + c * kAtom + 4 * lane * 128;
+            if (boxed)
+              tma_load_2d_pair(dst, &a.box_map, cols * c, cur.id[0], full_bar);
+            else
+              tma_gather4_pair(dst, &a.row_map, cols * c, cur.id[0], cur.id[1], cur.id[2],
+                               cur.id[3], full_bar);
+          }
+        }
+        ++issued;
+        __syncwarp();
+      }
+      if (*abort_flag) break;
+    }
+    // Teardown: the last copies into each part have landed in both CTAs (the
+    // even CTA's barriers count both; earlier ones were consumed).
+    if (r == 0 && lane == 0) {
+      if (!kFp8) W.drain(bar(kBarQFull), 0);
+      for (int g = 0; g < groups && g < issued; ++g)
+        W.drain(bar(kBarKFull + g), ((issued - 1 - g) / groups) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---- V loads (bf16): this CTA's channels of all 128 keys ----------------
+    if (!kFp8) {
+      int issued = 0;
+      bool bad = false;
+      Rows4 nx;
+      if (nb > 0) nx = lookup4(p, t, t.block(b0) * kBN + 4 * lane, bad);
+      for (int j = 0; j < nb; ++j) {
+        const Rows4 cur = nx;
+        if (j + 1 < nb) nx = lookup4(p, t, t.block(b0 + j + 1) * kBN + 4 * lane, bad);
+        const bool all4 = cur.id[0] >= 0 && cur.id[1] >= 0 && cur.id[2] >= 0 && cur.id[3] >= 0;
+        const uint32_t full = __ballot_sync(0xffffffffu, all4);
+        const int per = a.box >> 2;
+        const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
+        const bool boxed = per && (full & mine) == mine;
+        for (int v = 0; v < kVUnits; ++v) {
+          if (j >= 1) W.wait_cluster(bar(kBarVEmpty + v), (j - 1) & 1);
+          if (*abort_flag) break;
+          if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
+          __syncwarp();
+          if ((lane >> 4) == (v & 1) && (!boxed || (lane & (per - 1)) == 0)) {
+            const uint32_t full_bar = bar0(kBarVFull + v);
+            const int ch = 256 * (v >> 1) + 128 * (int)r;
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t dst = sb + C::kOffV + (2 * v + c) * kAtom + 4 * (lane & 15) * 128;
+              if (boxed)
+                tma_load_2d_pair(dst, &a.box_map, ch + 64 * c, cur.id[0], full_bar);
+              else
+                tma_gather4_pair(dst, &a.row_map, ch + 64 * c, cur.id[0], cur.id[1], cur.id[2],
+                                 cur.id[3], full_bar);
+            }
+          }
+          ++issued;
+          __syncwarp();
+        }
+        if (*abort_flag) break;
+      }
+      if (r == 0 && lane == 0)
+        for (int v = 0; v < kVUnits && v < issued; ++v)
+          W.drain(bar(kBarVFull + v), ((issued - 1 - v) / kVUnits) & 1);
+      __syncwarp();
+    }
+  } else if (warp == 3) {
+    // ---- lookups for the softmax (and the E4M3 converters) ------------------
+    uint32_t* words = reinterpret_cast<uint32_t*>(sm + C::kOffMask);
+    bool bad = false;
+    for (int j = 0; j < nb; ++j) {
+      const int m = j % kMeta;
+      const Rows4 x = lookup4(p, t, t.block(b0 + j) * kBN + 4 * lane, bad);
+      float sc[4] = {1.f, 1.f, 1.f, 1.f};
+      if (kFp8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (x.id[i] >= 0) sc[i] = key_scale(p, x.blk[i]);
+      }
+      if (j >= kMeta) W.wait(bar(kBarMEmpty + m), (j / kMeta - 1) & 1);
+      if (*abort_flag) break;
+      __syncwarp();
+      uint32_t nib = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nib |= (x.id[i] >= 0 ? 1u : 0u) << i;
+      nib <<= 4 * (lane & 7);
+#pragma unroll
+      for (int o = 1; o <= 4; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
+      if ((lane & 7) == 0) words[4 * m + (lane >> 3)] = nib;
+      if (kFp8) {
+        reinterpret_cast<int4*>(sm + C::kOffIds)[32 * m + lane] =
+            make_int4(x.id[0], x.id[1], x.id[2], x.id[3]);
+        reinterpret_cast<float4*>(sm + C::kOffScale)[32 * m + lane] =
+            make_float4(sc[0], sc[1], sc[2], sc[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarMFull + m));
+    }
+    if (bad) atomicCAS(p.status, 0, kStatusBadIndex);
+    __syncwarp();
+  } else if (warp < 12) {
+    // ---- softmax --------------------------------------------------------------
+    const int wg = (warp - 4) >> 2;
+    const int i = (warp & 3) * 32 + lane;              // TMEM lane
+    const int row = i & 63, half = i >> 6;             // tile row, key half
+    const int seg = 2 * half + wg;                     // its 32 keys of the block
+    const uint32_t lane_base = ((uint32_t)(warp & 3) * 32u) << 16;
+    const int64_t g = t.row0 + 64 * (int64_t)r + row;
+    const bool live = g < t.row1;
+    const int pos = live ? t.p_last - ((int)((t.row1 - 1) / p.h) - (int)(g / p.h)) : -1;
+    const int lo = p.window ? max(pos - (p.window - 1), 0) : 0;
+    float qs = 1.f;
+    if (kFp8) {
+      // Q rows -> two E4M3 terms under a power-of-two scale; eight lanes a row.
+      const int st = tid - 128, j8 = st & 7;
+      const uint32_t gmask = 0xFFu << (lane & 24);
+      float* qscale = reinterpret_cast<float*>(sm + C::kOffQScale);
+      const int nch = p.d_qk / 64;
+      for (int rr = st >> 3; rr < kRows; rr += 32) {
+        const int64_t gr = t.row0 + 64 * (int64_t)r + rr;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) + (gr < t.row1 ? gr : t.row0) * p.d_qk) + j8;
+        uint4 raw[9];
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < 9; ++c) {
+          raw[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (c < nch && gr < t.row1) raw[c] = __ldg(src + 8 * c);
+        }
+#pragma unroll
+        for (int c = 0; c < 9; ++c) {
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
+                                     fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+        }
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, o));
+        // 2^k with amax 2^k in [224, 448): amax = m 2^e, 1 <= m < 2, k = 8 - e
+        // (m < 1.75) or 7 - e; kept within what 2^-k can hold
+        const uint32_t u = __float_as_uint(amax);
+        int k = 8 - ((int)(u >> 23) - 127) - ((u & 0x7FFFFFu) >= 0x600000u ? 1 : 0);
+        k = amax == 0.f ? 0 : min(max(k, -120), 120);
+        const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+        if (j8 == 0)                                   // (an infinite q: NaN scores)
+          qscale[rr] = amax < INFINITY ? __uint_as_float((uint32_t)(127 - k) << 23) : NAN;
+#pragma unroll
+        for (int c = 0; c < 10; ++c) {                 // 64-channel pieces; the tenth is padding
+          if (c >= 2 * a.atoms) continue;
+          const uint4 v = c < 9 ? raw[c < 9 ? c : 0] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t hi[2], lw[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x[4], y0, y1, y2, y3;
+            x[0] = __uint_as_float(w[2 * e] << 16) * up;
+            x[1] = __uint_as_float(w[2 * e] & 0xFFFF0000u) * up;
+            x[2] = __uint_as_float(w[2 * e + 1] << 16) * up;
+            x[3] = __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * up;
+            hi[e] = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
+            e4m3x4_to_f32(hi[e], y0, y1, y2, y3);
+            lw[e] = e4m3x2(x[0] - y0, x[1] - y1) | (e4m3x2(x[2] - y2, x[3] - y3) << 16);
+          }
+          // channel 64 c + 8 j8: atom c / 2, 16-byte chunk 4 (c % 2) + j8 / 2
+          const uint32_t off = (uint32_t)(c >> 1) * kAtom + (uint32_t)rr * 128u +
+                               (((4u * (c & 1) + (j8 >> 1)) ^ ((uint32_t)rr & 7u)) << 4) +
+                               8u * (j8 & 1);
+          *reinterpret_cast<uint2*>(sm + C::kOffQ + off) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(sm + C::kOffQ + C::kMaxAtoms * kAtom + off) =
+              make_uint2(lw[0], lw[1]);
+        }
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(1, 256);                          // the rows' scales are set
+      if (lane == 0) mbar_arrive_remote(bar0(kBarQFull));
+      qs = qscale[row];
+    }
+    float scale = a.scale_log2 * qs;
+    float m_run = -INFINITY;   // running max (log2 units), the same in a row's four threads
+    float l_run = 0.f;         // this thread's sum of exp2(s - m_run)
+    float lr_run = 0.f;        // the same sum of the bf16-rounded weights
+    __nv_bfloat16* red = reinterpret_cast<__nv_bfloat16*>(sm + C::kOffRed);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(sm + C::kOffMask);
+    const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
+    for (int j = 0; j < nb; ++j) {
+      const int buf = j & 1, m = j % kMeta;
+      const int e0 = t.block(b0 + j) * kBN + 32 * seg;   // this thread's first key
+      W.wait(bar(kBarMFull + m), (j / kMeta) & 1);
+      uint32_t see = words[4 * m + seg];
+      W.wait_cluster(bar(kBarSFull + buf), (j >> 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+      float s[32];
+      {
+        uint32_t w0[16], w1[16];
+        const uint32_t col = tmem + lane_base + kColS + 64 * buf + 32 * wg;
+        tmem_ld16(col, w0);
+        tmem_ld16(col + 16, w1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          s[k] = __uint_as_float(w0[k]);
+          s[16 + k] = __uint_as_float(w1[k]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(sempty + 8u * buf);
+      // The row's view of its 32 keys.
+      {
+        const int up = pos - e0;                         // keys 0 .. up
+        uint32_t v = up >= 31 ? ~0u : up < 0 ? 0u : (2u << up) - 1u;
+        const int dn = lo - e0;                          // keys dn ..
+        const uint32_t win = dn <= 0 ? ~0u : dn > 31 ? 0u : ~0u << dn;
+        const int sk = p.sinks - e0;                     // keys .. sk - 1
+        const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? ~0u : (1u << sk) - 1u;
+        see &= v & (win | snk);
+      }
+      float cl = scale;
+      const float4* ks4 = reinterpret_cast<const float4*>(sm + C::kOffScale) + 32 * m + 8 * seg;
+      if (kFp8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 c = ks4[k];
+          s[4 * k] *= c.x * scale;
+          s[4 * k + 1] *= c.y * scale;
+          s[4 * k + 2] *= c.z * scale;
+          s[4 * k + 3] *= c.w * scale;
+        }
+        cl = 1.f;
+      }
+      if (!__all_sync(0xffffffffu, see == ~0u) || !(scale > 0.f)) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] * cl : -INFINITY;
+        cl = 1.f;
+      }
+      float hm = s[0];
+#pragma unroll
+      for (int k = 1; k < 32; ++k) hm = fmaxf(hm, s[k]);
+      hm *= cl;
+      // The row's reference is the largest of its four (rounded) maxima: all
+      // four threads take the same one, and any value near the maximum serves.
+      __nv_bfloat16* rb = red + 256 * buf;
+      rb[64 * seg + row] = __float2bfloat16(hm);
+      float alpha = 1.f;
+      if (named_bar_or(4, 256, hm > m_run + 8.f)) {      // also true for the first finite max
+        float bm = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) bm = fmaxf(bm, __bfloat162float(rb[64 * k + row]));
+        if (bm > m_run + 7.f) {
+          alpha = ex2_approx(m_run - bm);                // 0 when m_run = -inf
+          m_run = bm;
+        }
+      }
+      uint32_t pk[16];
+      float ls = 0.f, lr = 0.f;
+      if (m_run == -INFINITY) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pk[k] = 0u;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float e0f = ex2_approx(fmaf(s[k], cl, -m_run));
+          const float e1f = ex2_approx(fmaf(s[k + 1], cl, -m_run));
+          ls += e0f + e1f;
+          pk[k / 2] = pack_bf16(e0f, e1f);
+          lr = add_bf16x2_f32(lr, pk[k / 2]);
+        }
+        if (kFp8) {
+          // The key's scale on the rounded weight (exact for powers of two).
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 c = ks4[k];
+            pk[2 * k] = pack_bf16(__uint_as_float(pk[2 * k] << 16) * c.x,
+                                  __uint_as_float(pk[2 * k] & 0xFFFF0000u) * c.y);
+            pk[2 * k + 1] = pack_bf16(__uint_as_float(pk[2 * k + 1] << 16) * c.z,
+                                      __uint_as_float(pk[2 * k + 1] & 0xFFFF0000u) * c.w);
+          }
+        }
+      }
+      l_run = l_run * alpha + ls;
+      lr_run = lr_run * alpha + lr;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));   // the lookups were read
+      if (j >= 1) {
+        W.wait_cluster(bar(kBarPEmpty), (j - 1) & 1);    // PV(j - 1) is done
+        __syncwarp();
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 128 * wg; c < 128 * wg + 128; c += 16) {
+            uint32_t w[16];
+            tmem_ld16(tmem + lane_base + kColO + c, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
+            tmem_st16(tmem + lane_base + kColO + c, w);
+          }
+          tmem_wait_st();
+        }
+      }
+      // P row, keys 64 half + 32 wg .. + 31: chunks 4 wg .. of atom `half`
+      uint8_t* prow = sm + C::kOffP + half * kAtom + row * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(prow + (((uint32_t)(4 * wg + c) ^ ((uint32_t)row & 7u)) << 4)) =
+            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(pfull);
+    }
+
+    // ---- epilogue -------------------------------------------------------------
+    if (nb > 0) {
+      W.wait_cluster(bar(kBarPEmpty), (nb - 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+    }
+    float* sums = reinterpret_cast<float*>(sm + C::kOffP + kOffSums);
+    int* flag = reinterpret_cast<int*>(sm + C::kOffP + kOffFlag);
+    sums[64 * seg + row] = l_run;
+    sums[256 + 64 * seg + row] = lr_run;
+    if (seg == 0) flag[row] = 0;
+    named_bar_sync(4, 256);
+    float l = 0.f, lr = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      l += sums[64 * k + row];
+      lr += sums[256 + 64 * k + row];
+    }
+    const bool empty = l == 0.f;
+    const float inv = empty ? 0.f : __fdividef(1.f, lr);
+    const bool partial = p.o_part != nullptr;
+    const int64_t prow_g = (int64_t)split * p.b.N * p.h + g;   // row of the partials
+    // O columns [128 wg, + 128) are channels 256 wg + 128 half ..
+    const int ch0 = 256 * wg + 128 * half;
+    uint8_t* stage = sm + C::kOffV + row * kOStride;
+    bool odd = false;                                    // an output that is not finite
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 16) {
+      uint32_t w[16];
+      __syncwarp();
+      if (nb > 0) {
+        tmem_ld16(tmem + lane_base + kColO + 128 * wg + c, w);
+        tmem_wait_ld();
+      }
+      float o[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        o[k] = empty ? 0.f : __uint_as_float(w[k]) * inv;
+        odd |= !(fabsf(o[k]) < INFINITY);
+      }
+      if (partial) {
+        if (live && !empty) {
+          float4* dst = reinterpret_cast<float4*>(p.o_part + prow_g * 512 + ch0 + c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      } else {
+        uint32_t b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[k] = pack_bf16(o[2 * k], o[2 * k + 1]);
+        *reinterpret_cast<uint4*>(stage + (ch0 + c) * 2) = make_uint4(b[0], b[1], b[2], b[3]);
+        *reinterpret_cast<uint4*>(stage + (ch0 + c) * 2 + 16) = make_uint4(b[4], b[5], b[6], b[7]);
+      }
+    }
+    if (live && seg == 0) {
+      const float v = empty ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
+      if (partial)
+        p.lse_part[prow_g] = v;
+      else if (p.lse)
+        p.lse[g] = v;
+    }
+    // A softmax that is not finite (a NaN or infinite visible score) is the
+    // answer; a finite one with an output that is not may owe it to a masked
+    // position.
+    odd = odd && live && l < INFINITY && lr < INFINITY;
+    if (odd) flag[row] = 1;
+    fence_proxy_async_smem();
+    const bool any = named_bar_or(4, 256, odd);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+    if (!partial) {
+      const int st = tid - 128;
+      const int64_t gs = t.row0 + 64 * (int64_t)r + st;
+      if (st < kRows && gs < t.row1 && !flag[st]) {
+        bulk_store(out + gs * 512, sb + C::kOffV + st * kOStride, 1024);
+        bulk_commit_group();
+        bulk_wait_read_all();
+      }
+    }
+    if (any) {
+      for (int rr = warp - 4; rr < kRows; rr += 8) {
+        if (!flag[rr]) continue;
+        const int64_t gr = t.row0 + 64 * (int64_t)r + rr;
+        const int pr = t.p_last - ((int)((t.row1 - 1) / p.h) - (int)(gr / p.h));
+        slow_row<kFp8>(p, t, gr, pr, p.window ? max(pr - (p.window - 1), 0) : 0, b0, b1,
+                       partial ? p.o_part + ((int64_t)split * p.b.N * p.h + gr) * 512 : nullptr,
+                       out + gr * 512);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- E4M3 V: rows from global memory, converted to bf16 (exact) ---------
+    // Eight threads per key, 16 channels each; a unit is 64 keys x 128 channels.
+    const int ct = tid - 384, j8 = ct & 7, kr = ct >> 3;     // key row of 16 per pass
+    const uint8_t* kv = static_cast<const uint8_t*>(p.kv);
+    for (int j = 0; j < nb; ++j) {
+      const int m = j % kMeta;
+      W.wait(bar(kBarMFull + m), (j / kMeta) & 1);
+      const int* ids = reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * m;
+      uint4 raw[kVUnits][4];
+#pragma unroll
+      for (int v = 0; v < kVUnits; ++v)
+#pragma unroll
+        for (int ps = 0; ps < 4; ++ps) {
+          const int id = ids[64 * (v & 1) + 16 * ps + kr];
+          raw[v][ps] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                     kv + (int64_t)id * p.d_qk + 256 * (v >> 1) + 128 * r) + j8)
+                               : make_uint4(0u, 0u, 0u, 0u);
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));
+#pragma unroll
+      for (int v = 0; v < kVUnits; ++v) {
+        if (j >= 1) W.wait_cluster(bar(kBarVEmpty + v), (j - 1) & 1);
+        if (!*abort_flag) {
+#pragma unroll
+          for (int ps = 0; ps < 4; ++ps) {
+            const int key = 16 * ps + kr;
+            uint32_t o[8];
+            e4m3x4_to_bf16(raw[v][ps].x, o[0], o[1]);
+            e4m3x4_to_bf16(raw[v][ps].y, o[2], o[3]);
+            e4m3x4_to_bf16(raw[v][ps].z, o[4], o[5]);
+            e4m3x4_to_bf16(raw[v][ps].w, o[6], o[7]);
+            // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1
+            uint8_t* dst = sm + C::kOffV + (2 * v + (j8 >> 2)) * kAtom + key * 128;
+            const uint32_t c0 = 2u * (j8 & 3), sw = (uint32_t)key & 7u;
+            *reinterpret_cast<uint4*>(dst + ((c0 ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + (((c0 + 1u) ^ sw) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(bar0(kBarVFull + v));
+      }
+      if (*abort_flag) break;
+    }
+    __syncwarp();
+  }
+
+  // ---- teardown: both CTAs are done with each other's barriers, tiles and
+  // TMEM (the even CTA drained the MMAs and the pair's copies above).  After an
+  // abort the CTAs may have issued different copies, whose barriers then tell
+  // nothing: 100 us let what is in flight land.
+  if (tid == 0 && *abort_flag) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000u) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ---- merge of the partials -------------------------------------------------
+//   LSE = ln sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s
+// One CTA per row, four channels a thread; a range without a visible key has
+// LSE_s = -inf and its O_s is not read.  Rows of no request are left alone.
+__global__ void __launch_bounds__(128) smla_window_merge_kernel(const WinParams p) {
+  const int64_t row = blockIdx.x;
+  const int tok = (int)(row / p.h);
+  if (tok < batch_start(p.b, 0) || tok >= batch_start(p.b, p.b.num_reqs)) return;
+  const int64_t rows = (int64_t)p.b.N * p.h;
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.lse_part[s * rows + row]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float z = 0.f;
+  const int c = threadIdx.x * 4;
+  if (top != -INFINITY) {
+    for (int s = 0; s < p.splits; ++s) {
+      const float ls = p.lse_part[s * rows + row];
+      if (ls == -INFINITY) continue;
+      const float w = expf(ls - top);
+      const float4 x = *reinterpret_cast<const float4*>(p.o_part + (s * rows + row) * 512 + c);
+      z += w;
+      o.x = fmaf(w, x.x, o.x);
+      o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z);
+      o.w = fmaf(w, x.w, o.w);
+    }
+    const float inv = 1.f / z;
+    o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+  }
+  uint2 packed = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * 512 + c) = packed;
+  if (threadIdx.x == 0 && p.lse) p.lse[row] = top == -INFINITY ? top : top + logf(z);
+}
+
+cudaError_t encode_rows(CUtensorMap* map, bool fp8, const void* base, int d, int64_t rows,
+                        int box_rows) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const int es = fp8 ? 1 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d * es};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <bool kFp8>
+cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
+  using C = Cfg<kFp8>;
+  cudaError_t e = cudaFuncSetAttribute(smla_window_kernel<kFp8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  smla_window_kernel<kFp8><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+int64_t tile_numbers(int T, int h, int num_reqs) {
+  return h == 128 ? T : (int64_t)T * h / 128 + num_reqs;
+}
+
+}  // namespace
+
+// The key ranges per tile.  What is known here are bounds: the tiles are taken
+// as filled (a decode step's requests hold one each), the keys as max_len or
+// the window.  A block takes about 1.3 us on a pair, a unit another 4, and a
+// split writes and reads 4 KB a row at about 3 TB/s besides the merge's launch;
+// the number of ranges with the least sum is taken.
+WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int window, int sinks,
+                            int num_sms) {
+  WindowPlan pl{};
+  pl.tiles = tile_numbers(T, h, num_reqs);
+  const int64_t filled = std::max<int64_t>(std::min(num_reqs, T), ((int64_t)T * h + 127) / 128);
+  int64_t keys = max_len;
+  if (window) keys = std::min<int64_t>(keys, (int64_t)window + (128 + h - 1) / h);
+  int64_t blocks = (keys + kBN - 1) / kBN;
+  if (window && keys < max_len) blocks += 1 + (std::min<int64_t>(sinks, max_len) + kBN - 1) / kBN;
+  const int places = std::max(num_sms / 2, 1);
+  double best = 0;
+  pl.splits = 1;
+  for (int s = 1; s <= 64 && s <= blocks; ++s) {
+    const double waves = (double)((filled * s + places - 1) / places);
+    double us = waves * (1.3 * (double)((blocks + s - 1) / s) + 4.0);
+    if (s > 1) us += 4.0 + (double)s * T * h * 4096.0 / 3e6;
+    if (s == 1 || us < best) {
+      best = us;
+      pl.splits = s;
+    }
+  }
+  pl.workspace_bytes =
+      pl.splits > 1 ? (size_t)pl.splits * T * h * (512 + 1) * sizeof(float) : 0;
+  return pl;
+}
+
+cudaError_t launch_window(WinParams p, cudaStream_t stream) {
+  WinArgs a{};
+  const bool fp8 = p.kv_format != kBf16;
+  const int es = fp8 ? 1 : 2;
+  p.num_tiles = tile_numbers(p.b.N, p.h, p.b.num_reqs);
+  a.atoms = (p.d_qk * es + 127) / 128;
+  a.ksteps = p.d_qk * es / 32;
+  a.scale_log2 = p.sm_scale * 1.4426950408889634f;
+  // Boxes: the largest power of two that divides the block (and 64); blocks of
+  // other sizes than multiples of 4 take gather4 alone.
+  a.box = p.b.block_size & -p.b.block_size;
+  a.box = a.box > 64 ? 64 : a.box < 4 ? 0 : a.box;
+  cudaError_t e = encode_rows(&a.row_map, fp8, p.kv, p.d_qk, p.b.num_slots, 1);
+  if (e == cudaSuccess && a.box)
+    e = encode_rows(&a.box_map, fp8, p.kv, p.d_qk, p.b.num_slots, a.box);
+  if (e == cudaSuccess && !fp8)
+    e = encode_rows(&a.q_map, false, p.q, p.d_qk, (int64_t)p.b.N * p.h, kRows);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = 2 * p.num_tiles * p.splits;
+  if (ctas > 0x7FFFFFFFll || (int64_t)p.b.N * p.h > 0x7FFFFFFFll)
+    return cudaErrorInvalidConfiguration;
+  a.p = p;
+  e = fp8 ? launch<true>(a, (unsigned)ctas, stream) : launch<false>(a, (unsigned)ctas, stream);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  smla_window_merge_kernel<<<(unsigned)(p.b.N * p.h), 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace smla
