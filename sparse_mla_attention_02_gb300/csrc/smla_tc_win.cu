@@ -54,10 +54,12 @@
 // Few tiles: the keys of a tile are cut into `splits` ranges of blocks, each
 // leaves a normalised fp32 partial and its LSE, and a second kernel merges them.
 //
-// Warp roles: warp 0 issues the MMAs (in the even CTA) and owns TMEM; warps 1
-// and 2 load K and V; warp 3 looks up each block's rows (validity, scales, row
-// ids); warps 4..11 are the softmax: four threads per row (TMEM lane half x
-// column half), 32 keys each; with E4M3 rows warps 12..15 convert V.
+// Warp roles: warp 0 issues QK and owns TMEM, another warp issues PV (both in
+// the even CTA; two issuers, so that the waits of one are covered by the MMAs of
+// the other); warps 1 and 2 load K and V; warp 3 looks up each block's rows
+// (validity, scales, row ids); warps 4..11 are the softmax: four threads per
+// row (TMEM lane half x column half), 32 keys each; with E4M3 rows warps
+// 12..15 convert V.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -82,7 +84,7 @@ constexpr int kRows = 64;                  // tile rows per CTA
 constexpr uint32_t kAtom = 8192;           // 64 rows x 128 bytes
 constexpr int kKGroups = 3;                // K ring: channel groups
 constexpr int kVUnits = 4;                 // V ring: (channel half n, key half)
-constexpr int kMeta = 4;                   // blocks of lookups ahead
+constexpr int kMeta = 3;                   // blocks of lookups in flight
 
 // TMEM columns.
 constexpr uint32_t kColO = 0;              // 2 x 128
@@ -99,15 +101,16 @@ enum {
   kBarPFull = kBarSEmpty + 2,              // even CTA: 16 warps
   kBarPEmpty,                              // both
   kBarQFull,                               // even CTA
-  kBarMFull,                               // [4] own
-  kBarMEmpty = kBarMFull + kMeta,          // [4] own
-  kBarDrain = kBarMEmpty + kMeta,          // even CTA
-  kNumBars
+  kBarMFull,                               // [3] own
+  kBarMEmpty = kBarMFull + kMeta,          // [3] own
+  kBarDrain = kBarMEmpty + kMeta,          // [2] even CTA: QK's and PV's last MMAs
+  kNumBars = kBarDrain + 2
 };
 
 template <bool kFp8>
 struct Cfg {
-  static constexpr int kThreads = kFp8 ? 512 : 384;
+  static constexpr int kThreads = kFp8 ? 512 : 416;
+  static constexpr int kWarpPv = kFp8 ? 2 : 12;         // issues PV (warp 2 loads bf16 V)
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
   static constexpr int kMaxAtoms = kFp8 ? 5 : 9;        // 128-byte columns of a row
@@ -121,11 +124,12 @@ struct Cfg {
   static constexpr uint32_t kOffMask = kOffBar + 8 * ((kNumBars + 1) & ~1);   // u32 [kMeta][4]
   static constexpr uint32_t kOffTmem = kOffMask + kMeta * 16;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  // E4M3: row ids and scales of a block, the Q rows' scales
-  static constexpr uint32_t kOffIds = (kOffAbort + 4 + 15) & ~15u;
-  static constexpr uint32_t kOffScale = kOffIds + (kFp8 ? kMeta * kBN * 4 : 0);
+  static constexpr uint32_t kOffIds = (kOffAbort + 4 + 15) & ~15u;   // i32 [kMeta][128] rows
+  // E4M3: the keys' scales of a block, the Q rows' scales
+  static constexpr uint32_t kOffScale = kOffIds + kMeta * kBN * 4;
   static constexpr uint32_t kOffQScale = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
-  static constexpr uint32_t kSmem = kOffQScale + (kFp8 ? kRows * 4 : 0);
+  static constexpr uint32_t kOffPlain = kOffQScale + (kFp8 ? kRows * 4 : 0);
+  static constexpr uint32_t kSmem = kOffPlain + (kFp8 ? kMeta * 4 : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 // The epilogue's areas: O rows at a stride of 1040 bytes (16-byte row copies,
@@ -220,9 +224,42 @@ __device__ __forceinline__ Rows4 lookup4(const WinParams& p, const Tile& t, int 
   return o;
 }
 
+// Slot and phase of the lookups' ring, advanced block by block.
+struct MetaRing {
+  int m = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++m == kMeta) {
+      m = 0;
+      ph ^= 1;
+    }
+  }
+};
+
 // A key's scale (E4M3 caches).
 __device__ __forceinline__ float key_scale(const WinParams& p, int blk) {
   return p.kv_format == kE4m3Block ? __ldg(p.k_scale + blk) : __ldg(p.k_scale);
+}
+
+// The part of a key's scale that its V row takes on the way to bf16, where it
+// costs nothing and is exact: the power of two at or below it, within [2^-100,
+// 2^7] (the conversion multiplies by 2^120 times it).  Its weight takes the rest.
+__device__ __forceinline__ float v_scale(float s) {
+  return fminf(fmaxf(__uint_as_float(__float_as_uint(s) & 0x7F800000u), 0x1p-100f), 128.f);
+}
+__device__ __forceinline__ float p_scale(float s) { return s / v_scale(s); }
+
+// Four E4M3 codes times a power of two, as bf16: the codes' exponent and
+// mantissa bits in bf16's fields read as 2^-120 of their value, one product
+// with k = 2^120 v_scale (both lanes) restores it.  (The NaN code reads as 480:
+// the same row's K makes the score NaN, which is what reaches O.)
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t k, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x = (prmt_sign<0x9180u>(w) << 4) & 0x87F087F0u;
+  const uint32_t y = (prmt_sign<0xB3A2u>(w) << 4) & 0x87F087F0u;
+  const __nv_bfloat162 kk = *reinterpret_cast<const __nv_bfloat162*>(&k);
+  __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), kk);
+  __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), kk);
+  lo = *reinterpret_cast<uint32_t*>(&a);
+  hi = *reinterpret_cast<uint32_t*>(&b);
 }
 
 // One tile row again, from its visible positions alone, by one warp: the
@@ -355,9 +392,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     mbar_init(bar(kBarQFull), kFp8 ? 16 : 1);        // E4M3: the softmax warps write Q
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(bar(kBarMFull + i), 1);
-      mbar_init(bar(kBarMEmpty + i), kFp8 ? 12 : 8);
+      mbar_init(bar(kBarMEmpty + i), kFp8 ? 13 : 10);  // softmax, converters, loaders
     }
     mbar_init(bar(kBarDrain), 1);
+    mbar_init(bar(kBarDrain + 1), 1);
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
@@ -375,81 +413,84 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   // The even CTA's barriers, as cluster addresses.
   auto bar0 = [&](int i) { return mapa(bar(i), 0); };
 
+  // Descriptors advance by constants (16-byte units).
   if (warp == 0) {
-    // ---- MMA issuer (even CTA) ---------------------------------------------
-    if (r == 0 && nb > 0) {
-      const uint32_t id_qk = kFp8 ? idesc_pair_e4m3(128, kBN) : idesc_bf16(128, kBN, false, false);
-      const uint32_t id_pv = idesc_bf16(128, 256, false, true);
-      W.wait_cluster(bar(kBarQFull), 0);
-      auto issue_qk = [&](int j) {
-        if (p.inject_stall && j == 0) return;        // tests: block 0's scores never arrive
-        if (j >= 2) W.wait_cluster(bar(kBarSEmpty + (j & 1)), ((j >> 1) - 1) & 1);
+    // ---- QK issuer (even CTA): runs up to two blocks ahead of the softmax ----
+    if (r == 0) {
+      const uint32_t id = kFp8 ? idesc_pair_e4m3(128, kBN) : idesc_bf16(128, kBN, false, false);
+      const uint64_t dq = sdesc(sb + C::kOffQ, 16, 1024, kLayoutSw128);
+      const uint64_t dk = sdesc(sb + C::kOffK, 16, 1024, kLayoutSw128);
+      if (nb > 0) W.wait_ready(bar(kBarQFull), 0);
+      for (int j = p.inject_stall ? 1 : 0; j < nb; ++j) {   // (tests: block 0's scores never arrive)
+        if (j >= 2) W.wait_ready(bar(kBarSEmpty + (j & 1)), ((j >> 1) - 1) & 1);
         const uint32_t dS = tmem + kColS + 64 * (j & 1);
-        for (int g = 0; g * C::kAtomsPerGroup < a.atoms; ++g) {
-          W.wait_cluster(bar(kBarKFull + g), j & 1);
+#pragma unroll 1
+        for (int g = 0, c = 0; c < a.atoms; ++g) {
+          W.wait_ready(bar(kBarKFull + g), j & 1);
           __syncwarp();
           tc_fence_after();
-          const int k0 = g * C::kAtomsPerGroup * 4;
-          const int k1 = min(k0 + C::kAtomsPerGroup * 4, a.ksteps);
+          const int c1 = min(c + C::kAtomsPerGroup, a.atoms);
           if (elect_one()) {
-            fence_proxy_async_smem();
-            for (int ks = k0; ks < k1; ++ks) {
-              const uint32_t off = (ks >> 2) * kAtom + (ks & 3) * 32;
-              const uint64_t bd = sdesc(sb + C::kOffK + off, 16, 1024, kLayoutSw128);
-              const uint64_t ad = sdesc(sb + C::kOffQ + off, 16, 1024, kLayoutSw128);
-              if (kFp8) {
-                mma_pair_e4m3(dS, ad, bd, id_qk, ks > 0 ? 1u : 0u);
-                mma_pair_e4m3(dS, sdesc(sb + C::kOffQ + C::kMaxAtoms * kAtom + off, 16, 1024,
-                                        kLayoutSw128), bd, id_qk, 1u);
-              } else {
-                mma_pair_bf16(dS, ad, bd, id_qk, ks > 0 ? 1u : 0u);
+#pragma unroll 1
+            for (int cc = c; cc < c1; ++cc) {
+              const uint64_t ad = dq + (uint32_t)cc * (kAtom >> 4);
+              const uint64_t bd = dk + (uint32_t)cc * (kAtom >> 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (kFp8) {
+                  // (the last atom of 576 channels is half padding)
+                  if (4 * cc + i >= a.ksteps) break;
+                  mma_pair_e4m3(dS, ad + 2 * i, bd + 2 * i, id, (cc | i) > 0 ? 1u : 0u);
+                  mma_pair_e4m3(dS, ad + 2 * i + (C::kMaxAtoms * kAtom >> 4), bd + 2 * i, id, 1u);
+                } else {
+                  mma_pair_bf16(dS, ad + 2 * i, bd + 2 * i, id, (cc | i) > 0 ? 1u : 0u);
+                }
               }
             }
             mma_commit_pair(bar(kBarKEmpty + g));
+            if (c1 == a.atoms) mma_commit_pair(bar(kBarSFull + (j & 1)));
           }
+          c = c1;
           __syncwarp();
         }
-        if (elect_one()) mma_commit_pair(bar(kBarSFull + (j & 1)));
-        __syncwarp();
-      };
-      auto issue_pv = [&](int j) {
-        W.wait_cluster(bar(kBarPFull), j & 1);
-        for (int v = 0; v < kVUnits; ++v) {          // v = 2 n + key half
-          W.wait_cluster(bar(kBarVFull + v), j & 1);
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
-            fence_proxy_async_smem();
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t ad = sdesc(sb + C::kOffP + (v & 1) * kAtom + ks * 32, 16, 1024,
-                                        kLayoutSw128);
-              const uint64_t bd = sdesc(sb + C::kOffV + v * 2 * kAtom + ks * 2048, kAtom, 1024,
-                                        kLayoutSw128);
-              mma_pair_bf16(tmem + kColO + 128 * (v >> 1), ad, bd, id_pv,
-                            (j > 0 || (v & 1) || ks > 0) ? 1u : 0u);
-            }
-            mma_commit_pair(bar(kBarVEmpty + v));
-          }
-          __syncwarp();
-        }
-        if (elect_one()) mma_commit_pair(bar(kBarPEmpty));
-        __syncwarp();
-      };
-      issue_qk(0);
-      if (nb > 1) issue_qk(1);
-      for (int j = 0; j < nb; ++j) {
-        issue_pv(j);
-        if (j + 2 < nb) issue_qk(j + 2);
       }
-    }
-    // Every MMA issued here has completed (also after an abort) before either
-    // CTA frees its TMEM or leaves its tiles.
-    if (r == 0) {
+      // Every MMA issued here has completed (also after an abort) before
+      // either CTA frees its TMEM or leaves its tiles.
       __syncwarp();
       if (elect_one()) mma_commit_pair(bar(kBarDrain));
       __syncwarp();
       W.drain(bar(kBarDrain), 0);
+    }
+  } else if (warp == C::kWarpPv) {
+    // ---- PV issuer (even CTA) ------------------------------------------------
+    if (r == 0) {
+      const uint32_t id = idesc_bf16(128, 256, false, true);
+      const uint64_t dp = sdesc(sb + C::kOffP, 16, 1024, kLayoutSw128);
+      const uint64_t dv = sdesc(sb + C::kOffV, kAtom, 1024, kLayoutSw128);
+      for (int j = 0; j < nb; ++j) {
+        W.wait_ready(bar(kBarPFull), j & 1);
+#pragma unroll 1
+        for (int v = 0; v < kVUnits; ++v) {          // v = 2 n + key half
+          W.wait_ready(bar(kBarVFull + v), j & 1);
+          __syncwarp();
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ad = dp + (uint32_t)(v & 1) * (kAtom >> 4);
+            const uint64_t bd = dv + (uint32_t)v * (2 * kAtom >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_pair_bf16(tmem + kColO + 128 * (v >> 1), ad + 2 * ks, bd + 128 * ks, id,
+                            (j > 0 || (v & 1) || ks > 0) ? 1u : 0u);
+            mma_commit_pair(bar(kBarVEmpty + v));
+            if (v == kVUnits - 1) mma_commit_pair(bar(kBarPEmpty));
+          }
+          __syncwarp();
+        }
+      }
+      __syncwarp();
+      if (elect_one()) mma_commit_pair(bar(kBarDrain + 1));
+      __syncwarp();
+      W.drain(bar(kBarDrain + 1), 0);
     }
   } else if (warp == 1) {
     // ---- K loads: this CTA's 64 of each block's 128 keys --------------------
@@ -463,20 +504,21 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     }
     __syncwarp();
     const int cols = 128 / C::kElem;                 // channels per atom
-    bool bad = false;
-    Rows4 nx;
-    if (nb > 0) nx = lookup4(p, t, t.block(b0) * kBN + 64 * r + 4 * (lane & 15), bad);
-    for (int j = 0; j < nb; ++j) {
-      const Rows4 cur = nx;
-      if (j + 1 < nb) nx = lookup4(p, t, t.block(b0 + j + 1) * kBN + 64 * r + 4 * (lane & 15), bad);
-      const bool all4 = cur.id[0] >= 0 && cur.id[1] >= 0 && cur.id[2] >= 0 && cur.id[3] >= 0;
+    MetaRing mr;
+    for (int j = 0; j < nb; ++j, mr.next()) {
+      W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
+      const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + 16 * r +
+                                                                    (lane & 15)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
+      const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
       const uint32_t full = __ballot_sync(0xffffffffu, all4) & 0xFFFFu;
       // lanes of this lane's box, all seen and allocated: one copy for the box
       const int per = a.box >> 2;
       const uint32_t mine = per ? (per == 32 ? ~0u : ((1u << per) - 1u)) << (lane & ~(per - 1)) : 0u;
       const bool boxed = per && (full & mine) == mine;
       for (int g = 0; g < groups; ++g) {
-        if (j >= 1) W.wait_cluster(bar(kBarKEmpty + g), (j - 1) & 1);
+        if (j >= 1) W.wait_ready(bar(kBarKEmpty + g), (j - 1) & 1);
         if (*abort_flag) break;
         const int c0 = g * C::kAtomsPerGroup, c1 = min(c0 + C::kAtomsPerGroup, a.atoms);
         if (r == 0 && lane == 0)
@@ -487,10 +529,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           for (int c = c0; c < c1; ++c) {
             const uint32_t dst = sb + C::kOffK + c * kAtom + 4 * lane * 128;
             if (boxed)
-              tma_load_2d_pair(dst, &a.box_map, cols * c, cur.id[0], full_bar);
+              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, full_bar);
             else
-              tma_gather4_pair(dst, &a.row_map, cols * c, cur.id[0], cur.id[1], cur.id[2],
-                               cur.id[3], full_bar);
+              tma_gather4_pair(dst, &a.row_map, cols * c, id.x, id.y, id.z, id.w, full_bar);
           }
         }
         ++issued;
@@ -506,23 +547,23 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         W.drain(bar(kBarKFull + g), ((issued - 1 - g) / groups) & 1);
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (!kFp8 && warp == 2) {
     // ---- V loads (bf16): this CTA's channels of all 128 keys ----------------
-    if (!kFp8) {
+    {
       int issued = 0;
-      bool bad = false;
-      Rows4 nx;
-      if (nb > 0) nx = lookup4(p, t, t.block(b0) * kBN + 4 * lane, bad);
-      for (int j = 0; j < nb; ++j) {
-        const Rows4 cur = nx;
-        if (j + 1 < nb) nx = lookup4(p, t, t.block(b0 + j + 1) * kBN + 4 * lane, bad);
-        const bool all4 = cur.id[0] >= 0 && cur.id[1] >= 0 && cur.id[2] >= 0 && cur.id[3] >= 0;
+      MetaRing mr;
+      for (int j = 0; j < nb; ++j, mr.next()) {
+        W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
+        const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + lane];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
+        const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
         const uint32_t full = __ballot_sync(0xffffffffu, all4);
         const int per = a.box >> 2;
         const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
         const bool boxed = per && (full & mine) == mine;
         for (int v = 0; v < kVUnits; ++v) {
-          if (j >= 1) W.wait_cluster(bar(kBarVEmpty + v), (j - 1) & 1);
+          if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
           if (*abort_flag) break;
           if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
           __syncwarp();
@@ -532,10 +573,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             for (int c = 0; c < 2; ++c) {
               const uint32_t dst = sb + C::kOffV + (2 * v + c) * kAtom + 4 * (lane & 15) * 128;
               if (boxed)
-                tma_load_2d_pair(dst, &a.box_map, ch + 64 * c, cur.id[0], full_bar);
+                tma_load_2d_pair(dst, &a.box_map, ch + 64 * c, id.x, full_bar);
               else
-                tma_gather4_pair(dst, &a.row_map, ch + 64 * c, cur.id[0], cur.id[1], cur.id[2],
-                                 cur.id[3], full_bar);
+                tma_gather4_pair(dst, &a.row_map, ch + 64 * c, id.x, id.y, id.z, id.w, full_bar);
             }
           }
           ++issued;
@@ -552,16 +592,21 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // ---- lookups for the softmax (and the E4M3 converters) ------------------
     uint32_t* words = reinterpret_cast<uint32_t*>(sm + C::kOffMask);
     bool bad = false;
-    for (int j = 0; j < nb; ++j) {
-      const int m = j % kMeta;
+    MetaRing mr;
+    for (int j = 0; j < nb; ++j, mr.next()) {
+      const int m = mr.m;
       const Rows4 x = lookup4(p, t, t.block(b0 + j) * kBN + 4 * lane, bad);
       float sc[4] = {1.f, 1.f, 1.f, 1.f};
-      if (kFp8) {
+      bool plain = true;                               // scales are powers of two within reach
+      if (kFp8 && p.kv_format == kE4m3Block) {         // (one scale per tensor: at the end)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
           if (x.id[i] >= 0) sc[i] = key_scale(p, x.blk[i]);
+          plain &= v_scale(sc[i]) == sc[i];
+        }
+        plain = __all_sync(0xffffffffu, plain);
       }
-      if (j >= kMeta) W.wait(bar(kBarMEmpty + m), (j / kMeta - 1) & 1);
+      if (j >= kMeta) W.wait_ready(bar(kBarMEmpty + m), mr.ph ^ 1);
       if (*abort_flag) break;
       __syncwarp();
       uint32_t nib = 0;
@@ -571,9 +616,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
       for (int o = 1; o <= 4; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
       if ((lane & 7) == 0) words[4 * m + (lane >> 3)] = nib;
+      reinterpret_cast<int4*>(sm + C::kOffIds)[32 * m + lane] =
+          make_int4(x.id[0], x.id[1], x.id[2], x.id[3]);
       if (kFp8) {
-        reinterpret_cast<int4*>(sm + C::kOffIds)[32 * m + lane] =
-            make_int4(x.id[0], x.id[1], x.id[2], x.id[3]);
+        if (lane == 0) reinterpret_cast<int*>(sm + C::kOffPlain)[m] = plain;
         reinterpret_cast<float4*>(sm + C::kOffScale)[32 * m + lane] =
             make_float4(sc[0], sc[1], sc[2], sc[3]);
       }
@@ -657,22 +703,25 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       fence_proxy_async_smem();
       named_bar_sync(1, 256);                          // the rows' scales are set
-      if (lane == 0) mbar_arrive_remote(bar0(kBarQFull));
+      if (lane == 0) mbar_signal_remote(bar0(kBarQFull));
       qs = qscale[row];
     }
-    float scale = a.scale_log2 * qs;
+    // One scale per tensor multiplies every score and the output.
+    const float kscale = p.kv_format == kE4m3 ? __ldg(p.k_scale) : 1.f;
+    const float scale = a.scale_log2 * qs * kscale;
     float m_run = -INFINITY;   // running max (log2 units), the same in a row's four threads
     float l_run = 0.f;         // this thread's sum of exp2(s - m_run)
     float lr_run = 0.f;        // the same sum of the bf16-rounded weights
     __nv_bfloat16* red = reinterpret_cast<__nv_bfloat16*>(sm + C::kOffRed);
     const uint32_t* words = reinterpret_cast<const uint32_t*>(sm + C::kOffMask);
     const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
-    for (int j = 0; j < nb; ++j) {
-      const int buf = j & 1, m = j % kMeta;
+    MetaRing mr;
+    for (int j = 0; j < nb; ++j, mr.next()) {
+      const int buf = j & 1, m = mr.m;
       const int e0 = t.block(b0 + j) * kBN + 32 * seg;   // this thread's first key
-      W.wait(bar(kBarMFull + m), (j / kMeta) & 1);
+      W.wait_ready(bar(kBarMFull + m), mr.ph);
       uint32_t see = words[4 * m + seg];
-      W.wait_cluster(bar(kBarSFull + buf), (j >> 1) & 1);
+      W.wait_ready(bar(kBarSFull + buf), (j >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       float s[32];
@@ -690,7 +739,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(sempty + 8u * buf);
+      if (lane == 0) mbar_signal_remote(sempty + 8u * buf);
       // The row's view of its 32 keys.
       {
         const int up = pos - e0;                         // keys 0 .. up
@@ -703,7 +752,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       float cl = scale;
       const float4* ks4 = reinterpret_cast<const float4*>(sm + C::kOffScale) + 32 * m + 8 * seg;
-      if (kFp8) {
+      if (kFp8 && p.kv_format == kE4m3Block) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float4 c = ks4[k];
@@ -751,11 +800,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           pk[k / 2] = pack_bf16(e0f, e1f);
           lr = add_bf16x2_f32(lr, pk[k / 2]);
         }
-        if (kFp8) {
-          // The key's scale on the rounded weight (exact for powers of two).
+        if (kFp8 && !reinterpret_cast<const int*>(sm + C::kOffPlain)[m]) {
+          // What V's power of two leaves of the key's scale goes to its weight.
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float4 c = ks4[k];
+            float4 c = ks4[k];
+            c.x = p_scale(c.x); c.y = p_scale(c.y); c.z = p_scale(c.z); c.w = p_scale(c.w);
             pk[2 * k] = pack_bf16(__uint_as_float(pk[2 * k] << 16) * c.x,
                                   __uint_as_float(pk[2 * k] & 0xFFFF0000u) * c.y);
             pk[2 * k + 1] = pack_bf16(__uint_as_float(pk[2 * k + 1] << 16) * c.z,
@@ -768,7 +818,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));   // the lookups were read
       if (j >= 1) {
-        W.wait_cluster(bar(kBarPEmpty), (j - 1) & 1);    // PV(j - 1) is done
+        W.wait_ready(bar(kBarPEmpty), (j - 1) & 1);    // PV(j - 1) is done
         __syncwarp();
         tc_fence_after();
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
@@ -793,12 +843,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(pfull);
+      if (lane == 0) mbar_signal_remote(pfull);
     }
 
     // ---- epilogue -------------------------------------------------------------
     if (nb > 0) {
-      W.wait_cluster(bar(kBarPEmpty), (nb - 1) & 1);
+      W.wait_ready(bar(kBarPEmpty), (nb - 1) & 1);
       __syncwarp();
       tc_fence_after();
     }
@@ -815,7 +865,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       lr += sums[256 + 64 * k + row];
     }
     const bool empty = l == 0.f;
-    const float inv = empty ? 0.f : __fdividef(1.f, lr);
+    const float inv = empty ? 0.f : __fdividef(kscale, lr);
     const bool partial = p.o_part != nullptr;
     const int64_t prow_g = (int64_t)split * p.b.N * p.h + g;   // row of the partials
     // O columns [128 wg, + 128) are channels 256 wg + 128 half ..
@@ -889,47 +939,63 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   } else {
     // ---- E4M3 V: rows from global memory, converted to bf16 (exact) ---------
     // Eight threads per key, 16 channels each; a unit is 64 keys x 128 channels.
+    // A unit's loads for block j + 1 are issued once its registers are free, so
+    // they have a block's time to land.
     const int ct = tid - 384, j8 = ct & 7, kr = ct >> 3;     // key row of 16 per pass
-    const uint8_t* kv = static_cast<const uint8_t*>(p.kv);
-    for (int j = 0; j < nb; ++j) {
-      const int m = j % kMeta;
-      W.wait(bar(kBarMFull + m), (j / kMeta) & 1);
-      const int* ids = reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * m;
-      uint4 raw[kVUnits][4];
+    const uint8_t* kv = static_cast<const uint8_t*>(p.kv) + 128 * r + 16 * j8;
+    uint4 raw[kVUnits][4];
+    uint32_t kk[2][4];                                       // 2^120 v_scale of the keys
+    auto load_unit = [&](int v, const int* ids) {
 #pragma unroll
-      for (int v = 0; v < kVUnits; ++v)
+      for (int ps = 0; ps < 4; ++ps) {
+        const int id = ids[64 * (v & 1) + 16 * ps + kr];
+        raw[v][ps] = make_uint4(0u, 0u, 0u, 0u);
+        if (id >= 0)
+          raw[v][ps] = __ldg(reinterpret_cast<const uint4*>(kv + (int64_t)id * p.d_qk +
+                                                            256 * (v >> 1)));
+      }
+    };
+    auto ids_of = [&](int m) { return reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * m; };
+    MetaRing mr, nx;                                         // this block's and the next one's
+    nx.next();
+    if (nb > 0) {
+      W.wait_ready(bar(kBarMFull), 0);
 #pragma unroll
-        for (int ps = 0; ps < 4; ++ps) {
-          const int id = ids[64 * (v & 1) + 16 * ps + kr];
-          raw[v][ps] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                     kv + (int64_t)id * p.d_qk + 256 * (v >> 1) + 128 * r) + j8)
-                               : make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int v = 0; v < kVUnits; ++v) load_unit(v, ids_of(0));
+    }
+    for (int j = 0; j < nb; ++j, mr.next(), nx.next()) {
+      const float* sc = reinterpret_cast<const float*>(sm + C::kOffScale) + kBN * mr.m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint32_t e = __float_as_uint(v_scale(sc[16 * u + kr]) * 0x1p120f) >> 16;
+        kk[u >> 2][u & 3] = e | (e << 16);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));
+      if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
+      if (j + 1 < nb) W.wait_ready(bar(kBarMFull + nx.m), nx.ph);
 #pragma unroll
       for (int v = 0; v < kVUnits; ++v) {
-        if (j >= 1) W.wait_cluster(bar(kBarVEmpty + v), (j - 1) & 1);
-        if (!*abort_flag) {
+        if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
 #pragma unroll
-          for (int ps = 0; ps < 4; ++ps) {
-            const int key = 16 * ps + kr;
-            uint32_t o[8];
-            e4m3x4_to_bf16(raw[v][ps].x, o[0], o[1]);
-            e4m3x4_to_bf16(raw[v][ps].y, o[2], o[3]);
-            e4m3x4_to_bf16(raw[v][ps].z, o[4], o[5]);
-            e4m3x4_to_bf16(raw[v][ps].w, o[6], o[7]);
-            // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1
-            uint8_t* dst = sm + C::kOffV + (2 * v + (j8 >> 2)) * kAtom + key * 128;
-            const uint32_t c0 = 2u * (j8 & 3), sw = (uint32_t)key & 7u;
-            *reinterpret_cast<uint4*>(dst + ((c0 ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + (((c0 + 1u) ^ sw) << 4)) =
-                make_uint4(o[4], o[5], o[6], o[7]);
-          }
+        for (int ps = 0; ps < 4; ++ps) {
+          const int key = 16 * ps + kr;
+          const uint32_t k = kk[v & 1][ps];
+          uint32_t o[8];
+          codes_to_bf16(raw[v][ps].x, k, o[0], o[1]);
+          codes_to_bf16(raw[v][ps].y, k, o[2], o[3]);
+          codes_to_bf16(raw[v][ps].z, k, o[4], o[5]);
+          codes_to_bf16(raw[v][ps].w, k, o[6], o[7]);
+          // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1
+          uint8_t* dst = sm + C::kOffV + (2 * v + (j8 >> 2)) * kAtom + key * 128;
+          const uint32_t c0 = 2u * (j8 & 3), sw = (uint32_t)key & 7u;
+          *reinterpret_cast<uint4*>(dst + ((c0 ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(dst + (((c0 + 1u) ^ sw) << 4)) =
+              make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(bar0(kBarVFull + v));
+        if (lane == 0) mbar_signal_remote(bar0(kBarVFull + v));
+        if (j + 1 < nb) load_unit(v, ids_of(nx.m));
       }
       if (*abort_flag) break;
     }
