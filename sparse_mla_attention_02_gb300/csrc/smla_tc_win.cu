@@ -127,7 +127,8 @@ struct Cfg {
   static constexpr uint32_t kOffIds = (kOffAbort + 4 + 15) & ~15u;   // i32 [kMeta][128] rows
   // E4M3: the keys' scales of a block, the Q rows' scales
   static constexpr uint32_t kOffScale = kOffIds + kMeta * kBN * 4;
-  static constexpr uint32_t kOffQScale = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
+  static constexpr uint32_t kOffMul = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
+  static constexpr uint32_t kOffQScale = kOffMul + (kFp8 ? kMeta * kBN * 4 : 0);
   static constexpr uint32_t kOffPlain = kOffQScale + (kFp8 ? kRows * 4 : 0);
   static constexpr uint32_t kSmem = kOffPlain + (kFp8 ? kMeta * 4 : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -142,6 +143,8 @@ static_assert(kRows * kOStride <= kVUnits * 2 * kAtom + 4096, "O staging");
 struct WinArgs {
   CUtensorMap row_map;   // the cache, boxes of one row x 128 bytes (gather4)
   CUtensorMap box_map;   // the cache, boxes of `box` rows x 128 bytes
+  CUtensorMap k_map;     // the cache as (128-byte column, row, column index): boxes of 64 rows
+  CUtensorMap v_map;     // x one K group's columns, and x two columns (bf16, whole boxes)
   CUtensorMap q_map;     // bf16 q [T * h, d_qk], boxes of 64 rows x 64 channels
   WinParams p;
   int box;               // rows per box, a power of two in 4..64; 0: gather4 alone
@@ -504,6 +507,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     }
     __syncwarp();
     const int cols = 128 / C::kElem;                 // channels per atom
+    const uint32_t kfull0 = bar0(kBarKFull);
     MetaRing mr;
     for (int j = 0; j < nb; ++j, mr.next()) {
       W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
@@ -513,9 +517,31 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
       const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
       const uint32_t full = __ballot_sync(0xffffffffu, all4) & 0xFFFFu;
+      if (a.box == 64 && full == 0xFFFFu) {            // the 64 rows of one block, all seen
+        if (lane == 0) {
+          for (int g = 0; g < groups; ++g) {
+            if (j >= 1) W.wait_ready(bar(kBarKEmpty + g), (j - 1) & 1);
+            if (*abort_flag) break;
+            const int c0 = g * C::kAtomsPerGroup;
+            const uint32_t bytes = (uint32_t)min(C::kAtomsPerGroup, a.atoms - c0) * kAtom;
+            if (r == 0) mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * bytes);
+            const uint32_t dst = sb + C::kOffK + c0 * kAtom;
+            if (bytes == C::kAtomsPerGroup * kAtom)
+              tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * g);
+            else
+              for (int c = c0; c < a.atoms; ++c)
+                tma_load_2d_pair(dst + (c - c0) * kAtom, &a.box_map, cols * c, id.x,
+                                 kfull0 + 8u * g);
+            ++issued;
+          }
+        }
+        __syncwarp();
+        if (*abort_flag) break;
+        continue;
+      }
       // lanes of this lane's box, all seen and allocated: one copy for the box
       const int per = a.box >> 2;
-      const uint32_t mine = per ? (per == 32 ? ~0u : ((1u << per) - 1u)) << (lane & ~(per - 1)) : 0u;
+      const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
       const bool boxed = per && (full & mine) == mine;
       for (int g = 0; g < groups; ++g) {
         if (j >= 1) W.wait_ready(bar(kBarKEmpty + g), (j - 1) & 1);
@@ -525,13 +551,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * (uint32_t)(c1 - c0) * kAtom);
         __syncwarp();
         if (lane < 16 && (!boxed || (lane & (per - 1)) == 0)) {
-          const uint32_t full_bar = bar0(kBarKFull + g);
           for (int c = c0; c < c1; ++c) {
             const uint32_t dst = sb + C::kOffK + c * kAtom + 4 * lane * 128;
             if (boxed)
-              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, full_bar);
+              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, kfull0 + 8u * g);
             else
-              tma_gather4_pair(dst, &a.row_map, cols * c, id.x, id.y, id.z, id.w, full_bar);
+              tma_gather4_pair(dst, &a.row_map, cols * c, id.x, id.y, id.z, id.w,
+                               kfull0 + 8u * g);
           }
         }
         ++issued;
@@ -550,6 +576,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   } else if (!kFp8 && warp == 2) {
     // ---- V loads (bf16): this CTA's channels of all 128 keys ----------------
     {
+      const uint32_t vfull0 = bar0(kBarVFull);
       int issued = 0;
       MetaRing mr;
       for (int j = 0; j < nb; ++j, mr.next()) {
@@ -559,6 +586,22 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
         const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
         const uint32_t full = __ballot_sync(0xffffffffu, all4);
+        if (a.box == 64 && full == ~0u) {              // two whole blocks
+          const int y1 = __shfl_sync(0xffffffffu, id.x, 16);
+          if (lane == 0) {
+            for (int v = 0; v < kVUnits; ++v) {
+              if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
+              if (*abort_flag) break;
+              if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
+              tma_load_3d_pair(sb + C::kOffV + 2 * v * kAtom, &a.v_map, 0, v & 1 ? y1 : id.x,
+                               4 * (v >> 1) + 2 * (int)r, vfull0 + 8u * v);
+              ++issued;
+            }
+          }
+          __syncwarp();
+          if (*abort_flag) break;
+          continue;
+        }
         const int per = a.box >> 2;
         const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
         const bool boxed = per && (full & mine) == mine;
@@ -568,7 +611,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
           __syncwarp();
           if ((lane >> 4) == (v & 1) && (!boxed || (lane & (per - 1)) == 0)) {
-            const uint32_t full_bar = bar0(kBarVFull + v);
+            const uint32_t full_bar = vfull0 + 8u * v;
             const int ch = 256 * (v >> 1) + 128 * (int)r;
             for (int c = 0; c < 2; ++c) {
               const uint32_t dst = sb + C::kOffV + (2 * v + c) * kAtom + 4 * (lane & 15) * 128;
@@ -622,6 +665,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (lane == 0) reinterpret_cast<int*>(sm + C::kOffPlain)[m] = plain;
         reinterpret_cast<float4*>(sm + C::kOffScale)[32 * m + lane] =
             make_float4(sc[0], sc[1], sc[2], sc[3]);
+        uint32_t mul[4];                               // 2^120 v_scale, twice in bf16
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mul[i] = __byte_perm(__float_as_uint(v_scale(sc[i]) * 0x1p120f), 0u, 0x3232);
+        reinterpret_cast<uint4*>(sm + C::kOffMul)[32 * m + lane] =
+            make_uint4(mul[0], mul[1], mul[2], mul[3]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarMFull + m));
@@ -939,63 +988,67 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   } else {
     // ---- E4M3 V: rows from global memory, converted to bf16 (exact) ---------
     // Eight threads per key, 16 channels each; a unit is 64 keys x 128 channels.
-    // A unit's loads for block j + 1 are issued once its registers are free, so
-    // they have a block's time to land.
+    // A unit's loads are issued two units ahead, into the registers that the
+    // unit before it in the same key half has left.
     const int ct = tid - 384, j8 = ct & 7, kr = ct >> 3;     // key row of 16 per pass
     const uint8_t* kv = static_cast<const uint8_t*>(p.kv) + 128 * r + 16 * j8;
-    uint4 raw[kVUnits][4];
-    uint32_t kk[2][4];                                       // 2^120 v_scale of the keys
-    auto load_unit = [&](int v, const int* ids) {
-#pragma unroll
-      for (int ps = 0; ps < 4; ++ps) {
-        const int id = ids[64 * (v & 1) + 16 * ps + kr];
-        raw[v][ps] = make_uint4(0u, 0u, 0u, 0u);
-        if (id >= 0)
-          raw[v][ps] = __ldg(reinterpret_cast<const uint4*>(kv + (int64_t)id * p.d_qk +
-                                                            256 * (v >> 1)));
-      }
-    };
-    auto ids_of = [&](int m) { return reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * m; };
+    // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1; rows kr + 16 ps have kr's swizzle
+    const uint32_t off0 = (uint32_t)(j8 >> 2) * kAtom + kr * 128 +
+                          (((2u * (j8 & 3)) ^ ((uint32_t)kr & 7u)) << 4);
+    const uint32_t off1 = off0 ^ 16u;
+    const uint32_t vfull0 = bar0(kBarVFull);
     MetaRing mr, nx;                                         // this block's and the next one's
     nx.next();
+    uint4 raw[2][4];
+    auto load_unit = [&](uint4 (&x)[4], int m, int half, int n) {
+      const int* ids = reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * m + 64 * half + kr;
+#pragma unroll
+      for (int ps = 0; ps < 4; ++ps) {
+        const int id = ids[16 * ps];
+        x[ps] = make_uint4(0u, 0u, 0u, 0u);
+        if (id >= 0)
+          x[ps] = __ldg(reinterpret_cast<const uint4*>(kv + (int64_t)id * p.d_qk + 256 * n));
+      }
+    };
     if (nb > 0) {
       W.wait_ready(bar(kBarMFull), 0);
-#pragma unroll
-      for (int v = 0; v < kVUnits; ++v) load_unit(v, ids_of(0));
+      load_unit(raw[0], 0, 0, 0);
+      load_unit(raw[1], 0, 1, 0);
     }
     for (int j = 0; j < nb; ++j, mr.next(), nx.next()) {
-      const float* sc = reinterpret_cast<const float*>(sm + C::kOffScale) + kBN * mr.m;
+#pragma unroll 1
+      for (int n = 0; n < 2; ++n) {
+        if (n == 1 && j + 1 < nb) W.wait_ready(bar(kBarMFull + nx.m), nx.ph);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t e = __float_as_uint(v_scale(sc[16 * u + kr]) * 0x1p120f) >> 16;
-        kk[u >> 2][u & 3] = e | (e << 16);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
-      if (j + 1 < nb) W.wait_ready(bar(kBarMFull + nx.m), nx.ph);
+        for (int half = 0; half < 2; ++half) {
+          const int v = 2 * n + half;
+          const uint32_t* mul = reinterpret_cast<const uint32_t*>(sm + C::kOffMul) + kBN * mr.m +
+                                64 * half + kr;
+          if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
+          uint8_t* dst = sm + C::kOffV + 2 * v * kAtom;
 #pragma unroll
-      for (int v = 0; v < kVUnits; ++v) {
-        if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
-#pragma unroll
-        for (int ps = 0; ps < 4; ++ps) {
-          const int key = 16 * ps + kr;
-          const uint32_t k = kk[v & 1][ps];
-          uint32_t o[8];
-          codes_to_bf16(raw[v][ps].x, k, o[0], o[1]);
-          codes_to_bf16(raw[v][ps].y, k, o[2], o[3]);
-          codes_to_bf16(raw[v][ps].z, k, o[4], o[5]);
-          codes_to_bf16(raw[v][ps].w, k, o[6], o[7]);
-          // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1
-          uint8_t* dst = sm + C::kOffV + (2 * v + (j8 >> 2)) * kAtom + key * 128;
-          const uint32_t c0 = 2u * (j8 & 3), sw = (uint32_t)key & 7u;
-          *reinterpret_cast<uint4*>(dst + ((c0 ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(dst + (((c0 + 1u) ^ sw) << 4)) =
-              make_uint4(o[4], o[5], o[6], o[7]);
+          for (int ps = 0; ps < 4; ++ps) {
+            const uint4 x = raw[half][ps];
+            const uint32_t k = mul[16 * ps];
+            uint32_t o[8];
+            codes_to_bf16(x.x, k, o[0], o[1]);
+            codes_to_bf16(x.y, k, o[2], o[3]);
+            codes_to_bf16(x.z, k, o[4], o[5]);
+            codes_to_bf16(x.w, k, o[6], o[7]);
+            *reinterpret_cast<uint4*>(dst + off0 + 2048 * ps) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + off1 + 2048 * ps) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          if (n == 0)
+            load_unit(raw[half], mr.m, half, 1);
+          else if (j + 1 < nb)
+            load_unit(raw[half], nx.m, half, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_signal_remote(vfull0 + 8u * v);
+            if (v == 3) mbar_arrive(bar(kBarMEmpty + mr.m));
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_signal_remote(bar0(kBarVFull + v));
-        if (j + 1 < nb) load_unit(v, ids_of(nx.m));
       }
       if (*abort_flag) break;
     }
@@ -1075,6 +1128,27 @@ cudaError_t encode_rows(CUtensorMap* map, bool fp8, const void* base, int d, int
              : cudaErrorInvalidValue;
 }
 
+// The cache as (128-byte column, row, column index): one copy brings several
+// columns of 64 rows, each as a tile of its own.  The column count is that of
+// whole columns.
+cudaError_t encode_columns(CUtensorMap* map, bool fp8, const void* base, int d, int64_t rows,
+                           int box_columns) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const int es = fp8 ? 1 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)(128 / es), (cuuint64_t)rows, (cuuint64_t)(d * es / 128)};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * es, 128};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), 64, (cuuint32_t)box_columns};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 template <bool kFp8>
 cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   using C = Cfg<kFp8>;
@@ -1137,6 +1211,10 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   cudaError_t e = encode_rows(&a.row_map, fp8, p.kv, p.d_qk, p.b.num_slots, 1);
   if (e == cudaSuccess && a.box)
     e = encode_rows(&a.box_map, fp8, p.kv, p.d_qk, p.b.num_slots, a.box);
+  if (e == cudaSuccess && a.box == 64)
+    e = encode_columns(&a.k_map, fp8, p.kv, p.d_qk, p.b.num_slots, fp8 ? 2 : 3);
+  if (e == cudaSuccess && a.box == 64 && !fp8)
+    e = encode_columns(&a.v_map, fp8, p.kv, p.d_qk, p.b.num_slots, 2);
   if (e == cudaSuccess && !fp8)
     e = encode_rows(&a.q_map, false, p.q, p.d_qk, (int64_t)p.b.N * p.h, kRows);
   if (e != cudaSuccess) return e;
