@@ -40,7 +40,7 @@
 // and an E4M3 value 4, so hi = e4m3(q) and lo = e4m3(q - hi) give q exactly down
 // to 2^-11 of the row's largest value (below, to 2^-19 of it).  The key's
 // scale multiplies its scores in fp32.  PV needs P in 16 bits, so V is
-// converted to bf16 (exact) by four warps on its way to shared memory, and the
+// converted to bf16 (exact) by eight warps on its way to shared memory, and the
 // key's scale multiplies P before it is rounded.
 //
 // Masked positions never reach an MMA as anything but zeros where no row of
@@ -59,7 +59,7 @@
 // the other); warps 1 and 2 load K and V; warp 3 looks up each block's rows
 // (validity, scales, row ids); warps 4..11 are the softmax: four threads per
 // row (TMEM lane half x column half), 32 keys each; with E4M3 rows warps
-// 12..15 convert V.
+// 12..19 convert V.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -109,7 +109,7 @@ enum {
 
 template <bool kFp8>
 struct Cfg {
-  static constexpr int kThreads = kFp8 ? 512 : 416;
+  static constexpr int kThreads = kFp8 ? 640 : 416;
   static constexpr int kWarpPv = kFp8 ? 2 : 12;         // issues PV (warp 2 loads bf16 V)
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
@@ -130,7 +130,8 @@ struct Cfg {
   static constexpr uint32_t kOffMul = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
   static constexpr uint32_t kOffQScale = kOffMul + (kFp8 ? kMeta * kBN * 4 : 0);
   static constexpr uint32_t kOffPlain = kOffQScale + (kFp8 ? kRows * 4 : 0);
-  static constexpr uint32_t kSmem = kOffPlain + (kFp8 ? kMeta * 4 : 0);
+  static constexpr uint32_t kOffSeg = kOffPlain + (kFp8 ? kMeta * 4 : 0);   // f32 [kMeta][4]
+  static constexpr uint32_t kSmem = kOffSeg + (kFp8 ? kMeta * 16 : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 // The epilogue's areas: O rows at a stride of 1040 bytes (16-byte row copies,
@@ -383,7 +384,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       mbar_init(bar(kBarKEmpty + i), 1);
     }
     for (int i = 0; i < kVUnits; ++i) {
-      mbar_init(bar(kBarVFull + i), kFp8 ? 8 : 1);   // E4M3: converter warps of both CTAs
+      mbar_init(bar(kBarVFull + i), kFp8 ? 16 : 1);  // E4M3: converter warps of both CTAs
       mbar_init(bar(kBarVEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -395,7 +396,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     mbar_init(bar(kBarQFull), kFp8 ? 16 : 1);        // E4M3: the softmax warps write Q
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(bar(kBarMFull + i), 1);
-      mbar_init(bar(kBarMEmpty + i), kFp8 ? 13 : 10);  // softmax, converters, loaders
+      mbar_init(bar(kBarMEmpty + i), kFp8 ? 17 : 10);  // softmax, converters, loaders
     }
     mbar_init(bar(kBarDrain), 1);
     mbar_init(bar(kBarDrain + 1), 1);
@@ -640,6 +641,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const int m = mr.m;
       const Rows4 x = lookup4(p, t, t.block(b0 + j) * kBN + 4 * lane, bad);
       float sc[4] = {1.f, 1.f, 1.f, 1.f};
+      float own = 1.f;                                 // the segment's scale, 0: several
       bool plain = true;                               // scales are powers of two within reach
       if (kFp8 && p.kv_format == kE4m3Block) {         // (one scale per tensor: at the end)
 #pragma unroll
@@ -648,7 +650,28 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           plain &= v_scale(sc[i]) == sc[i];
         }
         plain = __all_sync(0xffffffffu, plain);
+        // (a segment: the 32 keys of eight lanes; keys that no row sees agree
+        // with any scale)
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (x.id[i] >= 0) top = fmaxf(top, sc[i]);
+#pragma unroll
+        for (int o = 1; o <= 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        bool same = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (x.id[i] < 0) sc[i] = top > 0.f ? top : 1.f;
+          same &= sc[i] == top;
+        }
+        const uint32_t votes = __ballot_sync(0xffffffffu, same) >> (lane & 24);
+        own = (votes & 0xFFu) == 0xFFu ? top : 0.f;
       }
+      // The block's rows on their way into L2, two to three blocks before their
+      // copies: a copy then waits for L2, not for HBM.
+      if (a.box == 64 && (lane & 15) == 0 && x.id[0] >= 0 && (lane >> 4) == (int)r)
+        for (int c = 0; c < p.d_qk * C::kElem / 128; c += C::kAtomsPerGroup)
+          tma_prefetch_3d(&a.k_map, 0, x.id[0], c);
       if (j >= kMeta) W.wait_ready(bar(kBarMEmpty + m), mr.ph ^ 1);
       if (*abort_flag) break;
       __syncwarp();
@@ -663,6 +686,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           make_int4(x.id[0], x.id[1], x.id[2], x.id[3]);
       if (kFp8) {
         if (lane == 0) reinterpret_cast<int*>(sm + C::kOffPlain)[m] = plain;
+        if ((lane & 7) == 0) reinterpret_cast<float*>(sm + C::kOffSeg)[4 * m + (lane >> 3)] = own;
         reinterpret_cast<float4*>(sm + C::kOffScale)[32 * m + lane] =
             make_float4(sc[0], sc[1], sc[2], sc[3]);
         uint32_t mul[4];                               // 2^120 v_scale, twice in bf16
@@ -773,6 +797,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       W.wait_ready(bar(kBarSFull + buf), (j >> 1) & 1);
       __syncwarp();
       tc_fence_after();
+      // The row's view of its 32 keys.
+      {
+        const int up = pos - e0;                         // keys 0 .. up
+        uint32_t v = up >= 31 ? ~0u : up < 0 ? 0u : (2u << up) - 1u;
+        const int dn = lo - e0;                          // keys dn ..
+        const uint32_t win = dn <= 0 ? ~0u : dn > 31 ? 0u : ~0u << dn;
+        const int sk = p.sinks - e0;                     // keys .. sk - 1
+        const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? ~0u : (1u << sk) - 1u;
+        see &= v & (win | snk);
+      }
       float s[32];
       {
         uint32_t w0[16], w1[16];
@@ -789,37 +823,35 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_signal_remote(sempty + 8u * buf);
-      // The row's view of its 32 keys.
-      {
-        const int up = pos - e0;                         // keys 0 .. up
-        uint32_t v = up >= 31 ? ~0u : up < 0 ? 0u : (2u << up) - 1u;
-        const int dn = lo - e0;                          // keys dn ..
-        const uint32_t win = dn <= 0 ? ~0u : dn > 31 ? 0u : ~0u << dn;
-        const int sk = p.sinks - e0;                     // keys .. sk - 1
-        const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? ~0u : (1u << sk) - 1u;
-        see &= v & (win | snk);
-      }
+      // Scores in log2 units are s * cl: where nothing is masked and the 32
+      // keys share their scale they stay as the MMA left them (the factor is
+      // positive and keeps their order).
       float cl = scale;
       const float4* ks4 = reinterpret_cast<const float4*>(sm + C::kOffScale) + 32 * m + 8 * seg;
-      if (kFp8 && p.kv_format == kE4m3Block) {
+      if (kFp8) {
+        const float own = reinterpret_cast<const float*>(sm + C::kOffSeg)[4 * m + seg];
+        if (own > 0.f) {
+          cl *= own;
+        } else {                                         // several scales in the segment
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 c = ks4[k];
-          s[4 * k] *= c.x * scale;
-          s[4 * k + 1] *= c.y * scale;
-          s[4 * k + 2] *= c.z * scale;
-          s[4 * k + 3] *= c.w * scale;
+          for (int k = 0; k < 8; ++k) {
+            const float4 c = ks4[k];
+            s[4 * k] *= c.x * scale;
+            s[4 * k + 1] *= c.y * scale;
+            s[4 * k + 2] *= c.z * scale;
+            s[4 * k + 3] *= c.w * scale;
+          }
+          cl = 1.f;
         }
-        cl = 1.f;
       }
-      if (!__all_sync(0xffffffffu, see == ~0u) || !(scale > 0.f)) {
+      if (!__all_sync(0xffffffffu, see == ~0u && cl > 0.f)) {
 #pragma unroll
         for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] * cl : -INFINITY;
         cl = 1.f;
       }
-      float hm = s[0];
+      float hm = fmaxf(s[0], s[1]);
 #pragma unroll
-      for (int k = 1; k < 32; ++k) hm = fmaxf(hm, s[k]);
+      for (int k = 2; k < 32; k += 2) hm = max3(hm, s[k], s[k + 1]);
       hm *= cl;
       // The row's reference is the largest of its four (rounded) maxima: all
       // four threads take the same one, and any value near the maximum serves.
@@ -836,30 +868,28 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         }
       }
       uint32_t pk[16];
-      float ls = 0.f, lr = 0.f;
-      if (m_run == -INFINITY) {
+      float ls = 0.f, ls1 = 0.f, lr = 0.f, lr1 = 0.f;
+      const float mm = m_run == -INFINITY ? 0.f : m_run; // (no score yet: every weight is 0)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) pk[k] = 0u;
-      } else {
+      for (int k = 0; k < 32; k += 2) {
+        fma2_bcast(s[k], s[k + 1], cl, -mm);
+        const float w0 = ex2_approx(s[k]), w1 = ex2_approx(s[k + 1]);
+        add2(ls, ls1, w0, w1);
+        pk[k / 2] = pack_bf16(w0, w1);
+        add_bf16x2_f32x2(lr, lr1, pk[k / 2]);
+      }
+      ls += ls1;
+      lr += lr1;
+      if (kFp8 && !reinterpret_cast<const int*>(sm + C::kOffPlain)[m]) {
+        // What V's power of two leaves of the key's scale goes to its weight.
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float e0f = ex2_approx(fmaf(s[k], cl, -m_run));
-          const float e1f = ex2_approx(fmaf(s[k + 1], cl, -m_run));
-          ls += e0f + e1f;
-          pk[k / 2] = pack_bf16(e0f, e1f);
-          lr = add_bf16x2_f32(lr, pk[k / 2]);
-        }
-        if (kFp8 && !reinterpret_cast<const int*>(sm + C::kOffPlain)[m]) {
-          // What V's power of two leaves of the key's scale goes to its weight.
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float4 c = ks4[k];
-            c.x = p_scale(c.x); c.y = p_scale(c.y); c.z = p_scale(c.z); c.w = p_scale(c.w);
-            pk[2 * k] = pack_bf16(__uint_as_float(pk[2 * k] << 16) * c.x,
-                                  __uint_as_float(pk[2 * k] & 0xFFFF0000u) * c.y);
-            pk[2 * k + 1] = pack_bf16(__uint_as_float(pk[2 * k + 1] << 16) * c.z,
-                                      __uint_as_float(pk[2 * k + 1] & 0xFFFF0000u) * c.w);
-          }
+        for (int k = 0; k < 8; ++k) {
+          float4 c = ks4[k];
+          c.x = p_scale(c.x); c.y = p_scale(c.y); c.z = p_scale(c.z); c.w = p_scale(c.w);
+          pk[2 * k] = pack_bf16(__uint_as_float(pk[2 * k] << 16) * c.x,
+                                __uint_as_float(pk[2 * k] & 0xFFFF0000u) * c.y);
+          pk[2 * k + 1] = pack_bf16(__uint_as_float(pk[2 * k + 1] << 16) * c.z,
+                                    __uint_as_float(pk[2 * k + 1] & 0xFFFF0000u) * c.w);
         }
       }
       l_run = l_run * alpha + ls;
@@ -990,21 +1020,21 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // Eight threads per key, 16 channels each; a unit is 64 keys x 128 channels.
     // A unit's loads are issued two units ahead, into the registers that the
     // unit before it in the same key half has left.
-    const int ct = tid - 384, j8 = ct & 7, kr = ct >> 3;     // key row of 16 per pass
+    const int ct = tid - 384, j8 = ct & 7, kr = ct >> 3;     // key row of 32 per pass
     const uint8_t* kv = static_cast<const uint8_t*>(p.kv) + 128 * r + 16 * j8;
-    // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1; rows kr + 16 ps have kr's swizzle
+    // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1; rows kr + 32 ps have kr's swizzle
     const uint32_t off0 = (uint32_t)(j8 >> 2) * kAtom + kr * 128 +
                           (((2u * (j8 & 3)) ^ ((uint32_t)kr & 7u)) << 4);
     const uint32_t off1 = off0 ^ 16u;
     const uint32_t vfull0 = bar0(kBarVFull);
     MetaRing mr, nx;                                         // this block's and the next one's
     nx.next();
-    uint4 raw[2][4];
-    auto load_unit = [&](uint4 (&x)[4], int m, int half, int n) {
+    uint4 raw[2][2];
+    auto load_unit = [&](uint4 (&x)[2], int m, int half, int n) {
       const int* ids = reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * m + 64 * half + kr;
 #pragma unroll
-      for (int ps = 0; ps < 4; ++ps) {
-        const int id = ids[16 * ps];
+      for (int ps = 0; ps < 2; ++ps) {
+        const int id = ids[32 * ps];
         x[ps] = make_uint4(0u, 0u, 0u, 0u);
         if (id >= 0)
           x[ps] = __ldg(reinterpret_cast<const uint4*>(kv + (int64_t)id * p.d_qk + 256 * n));
@@ -1027,16 +1057,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
           uint8_t* dst = sm + C::kOffV + 2 * v * kAtom;
 #pragma unroll
-          for (int ps = 0; ps < 4; ++ps) {
+          for (int ps = 0; ps < 2; ++ps) {
             const uint4 x = raw[half][ps];
-            const uint32_t k = mul[16 * ps];
+            const uint32_t k = mul[32 * ps];
             uint32_t o[8];
             codes_to_bf16(x.x, k, o[0], o[1]);
             codes_to_bf16(x.y, k, o[2], o[3]);
             codes_to_bf16(x.z, k, o[4], o[5]);
             codes_to_bf16(x.w, k, o[6], o[7]);
-            *reinterpret_cast<uint4*>(dst + off0 + 2048 * ps) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + off1 + 2048 * ps) = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(dst + off0 + 4096 * ps) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + off1 + 4096 * ps) = make_uint4(o[4], o[5], o[6], o[7]);
           }
           if (n == 0)
             load_unit(raw[half], mr.m, half, 1);

@@ -144,6 +144,13 @@ __device__ __forceinline__ float add_bf16x2_f32(float acc, uint32_t pk) {
   return acc;
 }
 
+// The same into two sums, one per half.
+__device__ __forceinline__ void add_bf16x2_f32x2(float& a, float& b, uint32_t pk) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(a), "+f"(b) : "r"(pk));
+}
+
 // The slot ids at top-k positions [k0, k0 + n) of one index row into
 // slots[0, n) (n a multiple of 4), -1 where masked: at or past k1, negative,
 // or >= num_slots (the last makes the return value true).  The nthr threads
