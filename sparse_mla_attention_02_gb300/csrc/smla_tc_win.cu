@@ -54,10 +54,15 @@
 // Few tiles: the keys of a tile are cut into `splits` ranges of blocks, each
 // leaves a normalised fp32 partial and its LSE, and a second kernel merges them.
 //
+// Scheduling.  A unit is (tile, range).  The grid has one cluster per unit, but
+// a running cluster takes over units that have not started
+// (clusterlaunchcontrol) and keeps its barriers, TMEM and loaders going, so the
+// next unit's first loads and QK run under the epilogue of the last one.
+//
 // Warp roles: warp 0 issues QK and owns TMEM, another warp issues PV (both in
 // the even CTA; two issuers, so that the waits of one are covered by the MMAs of
-// the other); warps 1 and 2 load K and V; warp 3 looks up each block's rows
-// (validity, scales, row ids); warps 4..11 are the softmax: four threads per
+// the other); warps 1 and 2 load K and V; warp 3 takes units and looks up
+// each block's rows (validity, scales, row ids); warps 4..11 are the softmax: four threads per
 // row (TMEM lane half x column half), 32 keys each; with E4M3 rows warps
 // 12..19 convert V.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
@@ -101,11 +106,30 @@ enum {
   kBarPFull = kBarSEmpty + 2,              // even CTA: 16 warps
   kBarPEmpty,                              // both
   kBarQFull,                               // even CTA
+  kBarQEmpty,                              // both
   kBarMFull,                               // [3] own
   kBarMEmpty = kBarMFull + kMeta,          // [3] own
-  kBarDrain = kBarMEmpty + kMeta,          // [2] even CTA: QK's and PV's last MMAs
+  kBarTFull = kBarMEmpty + kMeta,          // [2] own: a unit's description
+  kBarTEmpty = kBarTFull + 2,              // [2] own
+  kBarCFull = kBarTEmpty + 2,              // [2] own: an answer of the launch control
+  kBarCEmpty = kBarCFull + 2,              // [2] even CTA: both have read it
+  kBarDrain = kBarCEmpty + 2,              // [2] even CTA: QK's and PV's last MMAs
   kNumBars = kBarDrain + 2
 };
+
+// A unit as its warps need it: rows [row0, row1) of the flattened (token, head)
+// list, of request r, whose last token has position p_last; positions
+// [lo, p_last] and [0, sinks) are seen by some row; its key blocks are numbers
+// [b0, b0 + nb) of the tile's list (block()).
+struct Unit {
+  int row0, row1, p_last, r;
+  int lo, sinks, sink_blocks, win_block;
+  int b0, nb, split, live;                 // live 0: no more units
+  __device__ __forceinline__ int block(int i) const {   // i-th block's index
+    return i < sink_blocks ? i : win_block + (i - sink_blocks);
+  }
+};
+static_assert(sizeof(Unit) == 48, "three 16-byte words");
 
 template <bool kFp8>
 struct Cfg {
@@ -122,11 +146,13 @@ struct Cfg {
   static constexpr uint32_t kOffRed = kOffP + 2 * kAtom;             // bf16 [2][4][64]
   static constexpr uint32_t kOffBar = kOffRed + 1024;
   static constexpr uint32_t kOffMask = kOffBar + 8 * ((kNumBars + 1) & ~1);   // u32 [kMeta][4]
-  static constexpr uint32_t kOffTmem = kOffMask + kMeta * 16;
-  static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  static constexpr uint32_t kOffIds = (kOffAbort + 4 + 15) & ~15u;   // i32 [kMeta][128] rows
+  static constexpr uint32_t kOffUnit = kOffMask + kMeta * 16;         // Unit [2]
+  static constexpr uint32_t kOffAnswer = kOffUnit + 2 * 48;           // 16 bytes [2]
+  static constexpr uint32_t kOffIds = kOffAnswer + 32;                // i32 [kMeta][128] rows
   // E4M3: the keys' scales of a block, the Q rows' scales
-  static constexpr uint32_t kOffScale = kOffIds + kMeta * kBN * 4;
+  static constexpr uint32_t kOffTmem = kOffIds + kMeta * kBN * 4;
+  static constexpr uint32_t kOffAbort = kOffTmem + 4;
+  static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 4 + 15) & ~15u : kOffAbort + 4;
   static constexpr uint32_t kOffMul = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
   static constexpr uint32_t kOffQScale = kOffMul + (kFp8 ? kMeta * kBN * 4 : 0);
   static constexpr uint32_t kOffPlain = kOffQScale + (kFp8 ? kRows * 4 : 0);
@@ -134,12 +160,9 @@ struct Cfg {
   static constexpr uint32_t kSmem = kOffSeg + (kFp8 ? kMeta * 16 : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
-// The epilogue's areas: O rows at a stride of 1040 bytes (16-byte row copies,
-// no bank conflicts) over V and the head of P; row sums and flags behind.
-constexpr uint32_t kOStride = 1040;
-constexpr uint32_t kOffSums = 4096;        // from kOffP: float [2][4][64]
-constexpr uint32_t kOffFlag = 4096 + 2048; // from kOffP: int [64]
-static_assert(kRows * kOStride <= kVUnits * 2 * kAtom + 4096, "O staging");
+// The epilogue's areas in P: row sums and flags.
+constexpr uint32_t kOffSums = 4096;        // float [2][4][64]
+constexpr uint32_t kOffFlag = 4096 + 2048; // int [64]
 
 struct WinArgs {
   CUtensorMap row_map;   // the cache, boxes of one row x 128 bytes (gather4)
@@ -149,6 +172,9 @@ struct WinArgs {
   CUtensorMap q_map;     // bf16 q [T * h, d_qk], boxes of 64 rows x 64 channels
   WinParams p;
   int box;               // rows per box, a power of two in 4..64; 0: gather4 alone
+  int quad;              // blocks are multiples of 4 rows: 4 positions share one
+  int shift;             // log2 of the block size, -1 if it is no power of two
+  int wide;              // out is 32-byte aligned
   int atoms;             // 128-byte columns of a row
   int ksteps;            // 32-byte MMA steps of a row
   float scale_log2;      // sm_scale * log2(e)
@@ -163,32 +189,26 @@ __device__ __forceinline__ int64_t first_tile(const WinParams& p, int r) {
   return p.h == 128 ? c : c * p.h / 128 + r;
 }
 
-// What a tile sees: positions [lo, hi] and [0, sinks), as key blocks.
-struct Tile {
-  int r;                 // request
-  int64_t row0, row1;    // its rows of the flattened list, row1 exclusive
-  int p_last;            // position of its last token
-  int lo, sinks;         // [lo, p_last] and [0, sinks) are seen by some row
-  int sink_blocks, win_block, n_blocks;
-  __device__ __forceinline__ int block(int i) const {   // i-th block's index
-    return i < sink_blocks ? i : win_block + (i - sink_blocks);
-  }
-};
-
-__device__ __forceinline__ Tile find_tile(const WinParams& p, int64_t u) {
-  Tile t;
-  t.r = warp_last_request(p.b.num_reqs, u, [&](int m) { return first_tile(p, m); });
+// Unit number u (tile * splits + range, the tiles from the last: a prompt's
+// later tokens see more keys); row1 = row0 when the tile number is not used.
+__device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
+  Unit t;
+  t.split = (int)(u % p.splits);
+  const int64_t tile = p.num_tiles - 1 - u / p.splits;
+  t.r = warp_last_request(p.b.num_reqs, tile, [&](int m) { return first_tile(p, m); });
   const int c0 = batch_start(p.b, t.r), c1 = batch_start(p.b, t.r + 1);
-  const int64_t k = u - first_tile(p, t.r);
-  t.row0 = (int64_t)c0 * p.h + 128 * k;
-  t.row1 = min(t.row0 + 128, (int64_t)c1 * p.h);
-  if (k < 0) t.row1 = t.row0;
-  t.n_blocks = t.sink_blocks = t.win_block = 0;
+  const int64_t k = tile - first_tile(p, t.r);
+  const int64_t r0 = (int64_t)c0 * p.h + 128 * k, r1 = min(r0 + 128, (int64_t)c1 * p.h);
+  const bool used = k >= 0 && r1 > r0;
+  t.row0 = used ? (int)r0 : 0;
+  t.row1 = used ? (int)r1 : 0;
+  t.b0 = t.nb = t.sink_blocks = t.win_block = 0;
   t.p_last = t.lo = -1;
   t.sinks = 0;
-  if (t.row1 <= t.row0) return t;
+  t.live = 1;
+  if (!used) return t;
   const int len = __ldg(p.b.seq_lens + t.r);
-  const int tok0 = (int)(t.row0 / p.h), tok1 = (int)((t.row1 - 1) / p.h);
+  const int tok0 = (int)(r0 / p.h), tok1 = (int)((r1 - 1) / p.h);
   t.p_last = len - (c1 - tok1);
   if (t.p_last < 0) return t;
   const int p_first = max(len - (c1 - tok0), 0);
@@ -196,7 +216,9 @@ __device__ __forceinline__ Tile find_tile(const WinParams& p, int64_t u) {
   t.sinks = min(p.sinks, t.lo);
   t.win_block = t.lo / kBN;
   t.sink_blocks = min((t.sinks + kBN - 1) / kBN, t.win_block);
-  t.n_blocks = t.sink_blocks + t.p_last / kBN + 1 - t.win_block;
+  const int64_t n = t.sink_blocks + t.p_last / kBN + 1 - t.win_block;
+  t.b0 = (int)(n * t.split / p.splits);
+  t.nb = (int)(n * (t.split + 1) / p.splits) - t.b0;
   return t;
 }
 
@@ -206,7 +228,7 @@ struct Rows4 {
   int id[4];
   int blk[4];
 };
-__device__ __forceinline__ Rows4 lookup4(const WinParams& p, const Tile& t, int pos, bool& bad) {
+__device__ __forceinline__ Rows4 lookup4(const WinParams& p, const Unit& t, int pos, bool& bad) {
   Rows4 o;
   int page = -1, blk = -1;
 #pragma unroll
@@ -266,12 +288,12 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t k, uint32_t& 
   hi = *reinterpret_cast<uint32_t*>(&b);
 }
 
-// One tile row again, from its visible positions alone, by one warp: the
-// positions of blocks [b0, b1) of the tile.  O is written to `out_f32` or
+// One row again, from its visible positions in the unit's blocks alone, by one
+// warp.  O is written to `out_f32` or
 // `out_bf16` (512 channels).  Lane l holds channels 2 l + 64 i, + 1.
 template <bool kFp8>
-static __device__ __noinline__ void slow_row(const WinParams& p, const Tile& t, int64_t g, int pos,
-                                             int lo, int b0, int b1, float* out_f32,
+__device__ __forceinline__ void slow_row(const WinParams& p, const Unit& t, int64_t g, int pos,
+                                             int lo, float* out_f32,
                                              __nv_bfloat16* out_bf16) {
   const int lane = threadIdx.x & 31;
   const int n2 = p.d_qk / 64;
@@ -288,7 +310,7 @@ static __device__ __noinline__ void slow_row(const WinParams& p, const Tile& t, 
   for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0.f;
   float m = -INFINITY, l = 0.f;
   bool bad = false;
-  for (int b = b0; b < b1; ++b) {
+  for (int b = t.b0; b < t.b0 + t.nb; ++b) {
     const int e0 = t.block(b) * kBN;
     for (int e = e0; e < e0 + kBN && e <= pos; ++e) {
       if (!(e >= lo || e < p.sinks)) continue;
@@ -363,16 +385,6 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t r = cluster_ctarank();
 
-  // ---- work unit: (tile, range of its key blocks) -------------------------
-  // Tiles are taken from the last: a prompt's later tokens see more keys.
-  const int64_t unit = (int64_t)(blockIdx.x >> 1);
-  const int split = (int)(unit % p.splits);
-  const Tile t = find_tile(p, p.num_tiles - 1 - unit / p.splits);
-  if (t.row1 <= t.row0) return;                      // (both CTAs)
-  const int b0 = (int)((int64_t)t.n_blocks * split / p.splits);
-  const int b1 = (int)((int64_t)t.n_blocks * (split + 1) / p.splits);
-  const int nb = b1 - b0;
-
   auto bar = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
   Waiter W{abort_flag, p.status, p.abort_ctr, *reinterpret_cast<volatile int*>(p.abort_ctr),
@@ -398,6 +410,14 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       mbar_init(bar(kBarMFull + i), 1);
       mbar_init(bar(kBarMEmpty + i), kFp8 ? 17 : 10);  // softmax, converters, loaders
     }
+    mbar_init(bar(kBarQEmpty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarTFull + i), 1);
+      // softmax, K loads, V loads or conversion, the even CTA's issuers
+      mbar_init(bar(kBarTEmpty + i), (kFp8 ? 17 : 10) + (r == 0 ? 2 : 0));
+      mbar_init(bar(kBarCFull + i), 1);
+      mbar_init(bar(kBarCEmpty + i), 2);
+    }
     mbar_init(bar(kBarDrain), 1);
     mbar_init(bar(kBarDrain + 1), 1);
     *abort_flag = 0;
@@ -416,6 +436,25 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::kOffTmem);
   // The even CTA's barriers, as cluster addresses.
   auto bar0 = [&](int i) { return mapa(bar(i), 0); };
+  // The i-th unit's description, copied by the calling warp, which then lets it
+  // go; false behind the last one (or after an abort).
+  auto take_unit = [&](int i, Unit& u) {
+    W.wait_ready(bar(kBarTFull + (i & 1)), (i >> 1) & 1);
+    const int4* src = reinterpret_cast<const int4*>(sm + C::kOffUnit + 48 * (i & 1));
+    const int4 x = src[0], y = src[1], z = src[2];
+    u.row0 = x.x; u.row1 = x.y; u.p_last = x.z; u.r = x.w;
+    u.lo = y.x; u.sinks = y.y; u.sink_blocks = y.z; u.win_block = y.w;
+    u.b0 = z.x; u.nb = z.y; u.split = z.z; u.live = z.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
+    return u.live != 0 && *abort_flag == 0;
+  };
+  // The same in place, for a warp that lets it go itself, at the unit's end.
+  auto peek_unit = [&](int i) {
+    W.wait_ready(bar(kBarTFull + (i & 1)), (i >> 1) & 1);
+    return reinterpret_cast<const Unit*>(sm + C::kOffUnit + 48 * (i & 1));
+  };
+  // Blocks are counted across units (J): a barrier's n-th phase is block n's.
 
   // Descriptors advance by constants (16-byte units).
   if (warp == 0) {
@@ -424,13 +463,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const uint32_t id = kFp8 ? idesc_pair_e4m3(128, kBN) : idesc_bf16(128, kBN, false, false);
       const uint64_t dq = sdesc(sb + C::kOffQ, 16, 1024, kLayoutSw128);
       const uint64_t dk = sdesc(sb + C::kOffK, 16, 1024, kLayoutSw128);
-      if (nb > 0) W.wait_ready(bar(kBarQFull), 0);
-      for (int j = p.inject_stall ? 1 : 0; j < nb; ++j) {   // (tests: block 0's scores never arrive)
-        if (j >= 2) W.wait_ready(bar(kBarSEmpty + (j & 1)), ((j >> 1) - 1) & 1);
-        const uint32_t dS = tmem + kColS + 64 * (j & 1);
+      Unit u;
+      for (int i = 0, q = 0, J = 0; take_unit(i, u); ++i) {
+       if (u.nb > 0) W.wait_ready(bar(kBarQFull), q++ & 1);
+       for (int j = 0; j < u.nb; ++j, ++J) {
+        if (p.inject_stall && j == 0) continue;      // tests: these scores never arrive
+        if (J >= 2) W.wait_ready(bar(kBarSEmpty + (J & 1)), ((J >> 1) - 1) & 1);
+        const uint32_t dS = tmem + kColS + 64 * (J & 1);
 #pragma unroll 1
         for (int g = 0, c = 0; c < a.atoms; ++g) {
-          W.wait_ready(bar(kBarKFull + g), j & 1);
+          W.wait_ready(bar(kBarKFull + g), J & 1);
           __syncwarp();
           tc_fence_after();
           const int c1 = min(c + C::kAtomsPerGroup, a.atoms);
@@ -452,11 +494,15 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
               }
             }
             mma_commit_pair(bar(kBarKEmpty + g));
-            if (c1 == a.atoms) mma_commit_pair(bar(kBarSFull + (j & 1)));
+            if (c1 == a.atoms) {
+              mma_commit_pair(bar(kBarSFull + (J & 1)));
+              if (j == u.nb - 1) mma_commit_pair(bar(kBarQEmpty));
+            }
           }
           c = c1;
           __syncwarp();
         }
+       }
       }
       // Every MMA issued here has completed (also after an abort) before
       // either CTA frees its TMEM or leaves its tiles.
@@ -471,11 +517,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const uint32_t id = idesc_bf16(128, 256, false, true);
       const uint64_t dp = sdesc(sb + C::kOffP, 16, 1024, kLayoutSw128);
       const uint64_t dv = sdesc(sb + C::kOffV, kAtom, 1024, kLayoutSw128);
-      for (int j = 0; j < nb; ++j) {
-        W.wait_ready(bar(kBarPFull), j & 1);
+      Unit u;
+      for (int i = 0, J = 0; take_unit(i, u); ++i) {
+       for (int j = 0; j < u.nb; ++j, ++J) {
+        W.wait_ready(bar(kBarPFull), J & 1);
 #pragma unroll 1
         for (int v = 0; v < kVUnits; ++v) {          // v = 2 n + key half
-          W.wait_ready(bar(kBarVFull + v), j & 1);
+          W.wait_ready(bar(kBarVFull + v), J & 1);
           __syncwarp();
           tc_fence_after();
           if (elect_one()) {
@@ -490,6 +538,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           }
           __syncwarp();
         }
+       }
       }
       __syncwarp();
       if (elect_one()) mma_commit_pair(bar(kBarDrain + 1));
@@ -500,17 +549,25 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // ---- K loads: this CTA's 64 of each block's 128 keys --------------------
     const int groups = (a.atoms + C::kAtomsPerGroup - 1) / C::kAtomsPerGroup;
     int issued = 0;                                  // channel groups loaded, in order
-    if (!kFp8 && lane == 0) {
-      if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
-      for (int c = 0; c < a.atoms; ++c)
-        tma_load_2d_pair(sb + C::kOffQ + c * kAtom, &a.q_map, 64 * c, (int)(t.row0 + 64 * r),
-                         bar0(kBarQFull));
-    }
-    __syncwarp();
     const int cols = 128 / C::kElem;                 // channels per atom
     const uint32_t kfull0 = bar0(kBarKFull);
     MetaRing mr;
-    for (int j = 0; j < nb; ++j, mr.next()) {
+    Unit u;
+    int q = 0, J = 0;
+    for (int i = 0; take_unit(i, u); ++i) {
+     if (!kFp8 && u.nb > 0) {
+      if (q >= 1) W.wait_ready(bar(kBarQEmpty), (q - 1) & 1);
+      if (*abort_flag) break;
+      if (lane == 0) {
+        if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
+        for (int c = 0; c < a.atoms; ++c)
+          tma_load_2d_pair(sb + C::kOffQ + c * kAtom, &a.q_map, 64 * c, u.row0 + 64 * (int)r,
+                           bar0(kBarQFull));
+      }
+      ++q;
+      __syncwarp();
+     }
+     for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
       W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
       const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + 16 * r +
                                                                     (lane & 15)];
@@ -521,7 +578,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       if (a.box == 64 && full == 0xFFFFu) {            // the 64 rows of one block, all seen
         if (lane == 0) {
           for (int g = 0; g < groups; ++g) {
-            if (j >= 1) W.wait_ready(bar(kBarKEmpty + g), (j - 1) & 1);
+            if (J >= 1) W.wait_ready(bar(kBarKEmpty + g), (J - 1) & 1);
             if (*abort_flag) break;
             const int c0 = g * C::kAtomsPerGroup;
             const uint32_t bytes = (uint32_t)min(C::kAtomsPerGroup, a.atoms - c0) * kAtom;
@@ -545,7 +602,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
       const bool boxed = per && (full & mine) == mine;
       for (int g = 0; g < groups; ++g) {
-        if (j >= 1) W.wait_ready(bar(kBarKEmpty + g), (j - 1) & 1);
+        if (J >= 1) W.wait_ready(bar(kBarKEmpty + g), (J - 1) & 1);
         if (*abort_flag) break;
         const int c0 = g * C::kAtomsPerGroup, c1 = min(c0 + C::kAtomsPerGroup, a.atoms);
         if (r == 0 && lane == 0)
@@ -565,11 +622,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         __syncwarp();
       }
       if (*abort_flag) break;
+     }
     }
     // Teardown: the last copies into each part have landed in both CTAs (the
     // even CTA's barriers count both; earlier ones were consumed).
     if (r == 0 && lane == 0) {
-      if (!kFp8) W.drain(bar(kBarQFull), 0);
+      if (q > 0) W.drain(bar(kBarQFull), (q - 1) & 1);
       for (int g = 0; g < groups && g < issued; ++g)
         W.drain(bar(kBarKFull + g), ((issued - 1 - g) / groups) & 1);
     }
@@ -578,9 +636,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // ---- V loads (bf16): this CTA's channels of all 128 keys ----------------
     {
       const uint32_t vfull0 = bar0(kBarVFull);
-      int issued = 0;
+      int issued = 0, J = 0;
       MetaRing mr;
-      for (int j = 0; j < nb; ++j, mr.next()) {
+      Unit u;
+      for (int i = 0; take_unit(i, u); ++i) {
+       for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
         W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
         const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + lane];
         __syncwarp();
@@ -591,7 +651,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           const int y1 = __shfl_sync(0xffffffffu, id.x, 16);
           if (lane == 0) {
             for (int v = 0; v < kVUnits; ++v) {
-              if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
+              if (J >= 1) W.wait_ready(bar(kBarVEmpty + v), (J - 1) & 1);
               if (*abort_flag) break;
               if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
               tma_load_3d_pair(sb + C::kOffV + 2 * v * kAtom, &a.v_map, 0, v & 1 ? y1 : id.x,
@@ -607,7 +667,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
         const bool boxed = per && (full & mine) == mine;
         for (int v = 0; v < kVUnits; ++v) {
-          if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
+          if (J >= 1) W.wait_ready(bar(kBarVEmpty + v), (J - 1) & 1);
           if (*abort_flag) break;
           if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
           __syncwarp();
@@ -626,6 +686,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           __syncwarp();
         }
         if (*abort_flag) break;
+       }
       }
       if (r == 0 && lane == 0)
         for (int v = 0; v < kVUnits && v < issued; ++v)
@@ -633,110 +694,235 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
     }
   } else if (warp == 3) {
-    // ---- lookups for the softmax (and the E4M3 converters) ------------------
+    // ---- units, and lookups: each block's rows, validity bits and scales ------
+    // This cluster's own unit comes first, then those it takes over.  Both CTAs
+    // decode the same answers and read the same batch, so they agree.
+    // Lane l looks up positions 4 l .. 4 l + 3.  Where these share a cache block
+    // (quad), the table entry of block j + 2 and the scale of block j + 1 are
+    // on their way while block j is written down.
     uint32_t* words = reinterpret_cast<uint32_t*>(sm + C::kOffMask);
+    const bool keyed = kFp8 && p.kv_format == kE4m3Block;   // (one scale per tensor: at the end)
     bool bad = false;
     MetaRing mr;
-    for (int j = 0; j < nb; ++j, mr.next()) {
-      const int m = mr.m;
-      const Rows4 x = lookup4(p, t, t.block(b0 + j) * kBN + 4 * lane, bad);
-      float sc[4] = {1.f, 1.f, 1.f, 1.f};
-      float own = 1.f;                                 // the segment's scale, 0: several
-      bool plain = true;                               // scales are powers of two within reach
-      if (kFp8 && p.kv_format == kE4m3Block) {         // (one scale per tensor: at the end)
+    Unit u{};
+    int J = 0;
+    struct Entry {
+      int off, blk;                                    // row within the block, table entry
+      uint32_t seen;                                   // bits of the four positions
+    };
+    auto entry = [&](int j) {
+      Entry e{0, -1, 0u};
+      if (j >= u.nb) return e;
+      const int pos = u.block(u.b0 + j) * kBN + 4 * lane;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (x.id[i] >= 0) sc[i] = key_scale(p, x.blk[i]);
-          plain &= v_scale(sc[i]) == sc[i];
-        }
-        plain = __all_sync(0xffffffffu, plain);
-        // (a segment: the 32 keys of eight lanes; keys that no row sees agree
-        // with any scale)
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (x.id[i] >= 0) top = fmaxf(top, sc[i]);
-#pragma unroll
-        for (int o = 1; o <= 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        bool same = true;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (x.id[i] < 0) sc[i] = top > 0.f ? top : 1.f;
-          same &= sc[i] == top;
-        }
-        const uint32_t votes = __ballot_sync(0xffffffffu, same) >> (lane & 24);
-        own = (votes & 0xFFu) == 0xFFu ? top : 0.f;
+      for (int i = 0; i < 4; ++i)
+        e.seen |= (pos + i <= u.p_last && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
+      if (e.seen) {
+        const int page = a.shift >= 0 ? pos >> a.shift : pos / p.b.block_size;
+        e.off = pos - page * p.b.block_size;
+        e.blk = batch_block(p.b, u.r, page, bad);
       }
-      // The block's rows on their way into L2, two to three blocks before their
-      // copies: a copy then waits for L2, not for HBM.
-      if (a.box == 64 && (lane & 15) == 0 && x.id[0] >= 0 && (lane >> 4) == (int)r)
-        for (int c = 0; c < p.d_qk * C::kElem / 128; c += C::kAtomsPerGroup)
-          tma_prefetch_3d(&a.k_map, 0, x.id[0], c);
-      if (j >= kMeta) W.wait_ready(bar(kBarMEmpty + m), mr.ph ^ 1);
+      return e;
+    };
+    struct Found {
+      int id[4];
+      float sc;
+    };
+    auto found = [&](const Entry& e) {
+      Found f;
+      f.sc = 1.f;
+      const int64_t row = (int64_t)e.blk * p.b.block_stride_rows + e.off;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = e.blk >= 0 && (e.seen >> i & 1u);
+        bad |= in && row + i >= p.b.num_slots;
+        f.id[i] = in && row + i < p.b.num_slots ? (int)row + i : -1;
+      }
+      if (keyed && f.id[0] >= 0) f.sc = __ldg(p.k_scale + e.blk);
+      if (keyed && f.id[0] < 0 && (f.id[1] & f.id[2] & f.id[3]) >= 0)
+        f.sc = __ldg(p.k_scale + e.blk);
+      return f;
+    };
+    int i = 0;                                         // units described
+    auto publish = [&](const Unit& x) {
+      if (i >= 2) W.wait_ready(bar(kBarTEmpty + (i & 1)), ((i >> 1) - 1) & 1);
+      int4* dst = reinterpret_cast<int4*>(sm + C::kOffUnit + 48 * (i & 1));
+      if (lane == 0) {
+        dst[0] = make_int4(x.row0, x.row1, x.p_last, x.r);
+        dst[1] = make_int4(x.lo, x.sinks, x.sink_blocks, x.win_block);
+        dst[2] = make_int4(x.b0, x.nb, x.split, x.live);
+        mbar_arrive(bar(kBarTFull + (i & 1)));
+      }
+      __syncwarp();
+      ++i;
+    };
+    int64_t unit = (int64_t)(blockIdx.x >> 1);
+    bool pending = false;                              // an answer is on its way
+    int n = 0;                                         // answers read
+    while (!*abort_flag) {
+      // Ask for the next unit before this one is worked on.
+      const uint32_t cfull = bar(kBarCFull + (n & 1));
+      const uint32_t answer = sb + C::kOffAnswer + 16 * (n & 1);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(cfull, 16);
+        if (r == 0) {
+          if (n >= 2) W.wait(bar(kBarCEmpty + (n & 1)), ((n >> 1) - 1) & 1);
+          cluster_take_over(answer, cfull);
+        }
+      }
+      pending = true;
+      __syncwarp();
+      u = find_unit(p, unit);
+      if (u.row1 > u.row0) publish(u);
+      Entry e1{}, e2{};
+      Found f{};
+      if (a.quad) {
+        f = found(entry(0));
+        e1 = entry(1);
+        e2 = entry(2);
+      }
+      for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
+        const int m = mr.m;
+        int id[4];
+        float sc[4] = {1.f, 1.f, 1.f, 1.f};
+        if (a.quad) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            id[k] = f.id[k];
+            sc[k] = f.sc;
+          }
+          f = found(e1);
+          e1 = e2;
+          e2 = entry(j + 3);
+        } else {
+          const Rows4 x = lookup4(p, u, u.block(u.b0 + j) * kBN + 4 * lane, bad);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            id[k] = x.id[k];
+            if (keyed && id[k] >= 0) sc[k] = key_scale(p, x.blk[k]);
+          }
+        }
+        float own = 1.f;                               // the segment's scale, 0: several
+        bool plain = true;                             // scales are powers of two within reach
+        if (keyed) {
+          // (a segment: the 32 keys of eight lanes; keys that no row sees agree
+          // with any scale)
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (id[k] >= 0) {
+              plain &= v_scale(sc[k]) == sc[k];
+              top = fmaxf(top, sc[k]);
+            }
+#pragma unroll
+          for (int o = 1; o <= 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          bool same = true;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (id[k] < 0) sc[k] = top > 0.f ? top : 1.f;
+            same &= sc[k] == top;
+          }
+          const uint32_t votes = __ballot_sync(0xffffffffu, same) >> (lane & 24);
+          own = (votes & 0xFFu) == 0xFFu ? top : 0.f;
+          plain = __all_sync(0xffffffffu, plain);
+        }
+        // The block's rows on their way into L2, two to three blocks before
+        // their copies: a copy then waits for L2, not for HBM.
+        if (a.box == 64 && (lane & 15) == 0 && id[0] >= 0 && (lane >> 4) == (int)r)
+          for (int c = 0; c < p.d_qk * C::kElem / 128; c += C::kAtomsPerGroup)
+            tma_prefetch_3d(&a.k_map, 0, id[0], c);
+        if (J >= kMeta) W.wait_ready(bar(kBarMEmpty + m), mr.ph ^ 1);
+        if (*abort_flag) break;
+        __syncwarp();
+        uint32_t nib = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) nib |= (id[k] >= 0 ? 1u : 0u) << k;
+        nib <<= 4 * (lane & 7);
+#pragma unroll
+        for (int o = 1; o <= 4; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
+        if ((lane & 7) == 0) words[4 * m + (lane >> 3)] = nib;
+        reinterpret_cast<int4*>(sm + C::kOffIds)[32 * m + lane] =
+            make_int4(id[0], id[1], id[2], id[3]);
+        if (kFp8) {
+          if (lane == 0) reinterpret_cast<int*>(sm + C::kOffPlain)[m] = plain;
+          if ((lane & 7) == 0)
+            reinterpret_cast<float*>(sm + C::kOffSeg)[4 * m + (lane >> 3)] = own;
+          reinterpret_cast<float4*>(sm + C::kOffScale)[32 * m + lane] =
+              make_float4(sc[0], sc[1], sc[2], sc[3]);
+          uint32_t mul[4];                             // 2^120 v_scale, twice in bf16
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mul[k] = __byte_perm(__float_as_uint(v_scale(sc[k]) * 0x1p120f), 0u, 0x3232);
+          reinterpret_cast<uint4*>(sm + C::kOffMul)[32 * m + lane] =
+              make_uint4(mul[0], mul[1], mul[2], mul[3]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarMFull + m));
+      }
+      W.wait(cfull, (n >> 1) & 1);
       if (*abort_flag) break;
+      pending = false;
+      int first;
+      const bool taken = cluster_taken(answer, first);
+      fence_proxy_async_smem();                        // the answer was read
       __syncwarp();
-      uint32_t nib = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) nib |= (x.id[i] >= 0 ? 1u : 0u) << i;
-      nib <<= 4 * (lane & 7);
-#pragma unroll
-      for (int o = 1; o <= 4; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
-      if ((lane & 7) == 0) words[4 * m + (lane >> 3)] = nib;
-      reinterpret_cast<int4*>(sm + C::kOffIds)[32 * m + lane] =
-          make_int4(x.id[0], x.id[1], x.id[2], x.id[3]);
-      if (kFp8) {
-        if (lane == 0) reinterpret_cast<int*>(sm + C::kOffPlain)[m] = plain;
-        if ((lane & 7) == 0) reinterpret_cast<float*>(sm + C::kOffSeg)[4 * m + (lane >> 3)] = own;
-        reinterpret_cast<float4*>(sm + C::kOffScale)[32 * m + lane] =
-            make_float4(sc[0], sc[1], sc[2], sc[3]);
-        uint32_t mul[4];                               // 2^120 v_scale, twice in bf16
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mul[i] = __byte_perm(__float_as_uint(v_scale(sc[i]) * 0x1p120f), 0u, 0x3232);
-        reinterpret_cast<uint4*>(sm + C::kOffMul)[32 * m + lane] =
-            make_uint4(mul[0], mul[1], mul[2], mul[3]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarMFull + m));
+      if (lane == 0) mbar_signal_remote(bar0(kBarCEmpty + (n & 1)));
+      if (!taken) break;
+      unit = (int64_t)(first >> 1);
+      ++n;
     }
+    // (after an abort: an answer on its way still writes to shared memory)
+    if (pending && lane == 0) W.drain(bar(kBarCFull + (n & 1)), (n >> 1) & 1);
+    __syncwarp();
+    u.live = 0;
+    publish(u);
     if (bad) atomicCAS(p.status, 0, kStatusBadIndex);
     __syncwarp();
   } else if (warp < 12) {
     // ---- softmax --------------------------------------------------------------
     const int wg = (warp - 4) >> 2;
-    const int i = (warp & 3) * 32 + lane;              // TMEM lane
-    const int row = i & 63, half = i >> 6;             // tile row, key half
+    const int tl = (warp & 3) * 32 + lane;             // TMEM lane
+    const int row = tl & 63, half = tl >> 6;           // tile row, key half
     const int seg = 2 * half + wg;                     // its 32 keys of the block
     const uint32_t lane_base = ((uint32_t)(warp & 3) * 32u) << 16;
-    const int64_t g = t.row0 + 64 * (int64_t)r + row;
-    const bool live = g < t.row1;
-    const int pos = live ? t.p_last - ((int)((t.row1 - 1) / p.h) - (int)(g / p.h)) : -1;
-    const int lo = p.window ? max(pos - (p.window - 1), 0) : 0;
+    __nv_bfloat16* red = reinterpret_cast<__nv_bfloat16*>(sm + C::kOffRed);
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(sm + C::kOffMask);
+    const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
+    // One scale per tensor multiplies every score and the output.
+    const float kscale = p.kv_format == kE4m3 ? __ldg(p.k_scale) : 1.f;
+    MetaRing mr;
+    int J = 0;
+    for (int i = 0;; ++i) {
+    const Unit* t = peek_unit(i);
+    if (!t->live || *abort_flag) break;
+    int pos = -1, lo = 0;                              // the row's token sees [lo, pos], sinks
+    {
+      const int g = t->row0 + 64 * (int)r + row;
+      if (g < t->row1) pos = t->p_last - ((t->row1 - 1) / p.h - g / p.h);
+      if (p.window) lo = max(pos - (p.window - 1), 0);
+    }
+    const int nb = t->nb;
     float qs = 1.f;
-    if (kFp8) {
+    if (kFp8 && nb > 0) {
       // Q rows -> two E4M3 terms under a power-of-two scale; eight lanes a row.
       const int st = tid - 128, j8 = st & 7;
       const uint32_t gmask = 0xFFu << (lane & 24);
       float* qscale = reinterpret_cast<float*>(sm + C::kOffQScale);
       const int nch = p.d_qk / 64;
       for (int rr = st >> 3; rr < kRows; rr += 32) {
-        const int64_t gr = t.row0 + 64 * (int64_t)r + rr;
+        const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
         const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) + (gr < t.row1 ? gr : t.row0) * p.d_qk) + j8;
-        uint4 raw[9];
+            static_cast<const uint16_t*>(p.q) + (gr < t->row1 ? gr : t->row0) * p.d_qk) + j8;
+        // (read twice, for the largest value and for the codes: registers)
         float amax = 0.f;
-#pragma unroll
-        for (int c = 0; c < 9; ++c) {
-          raw[c] = make_uint4(0u, 0u, 0u, 0u);
-          if (c < nch && gr < t.row1) raw[c] = __ldg(src + 8 * c);
-        }
-#pragma unroll
-        for (int c = 0; c < 9; ++c) {
-          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll 3
+        for (int c = 0; c < nch; ++c) {
+          const uint4 v = gr < t->row1 ? __ldg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
-                                     fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+            amax = max3(amax, fabsf(__uint_as_float(w[e] << 16)),
+                        fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
         }
 #pragma unroll
         for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, o));
@@ -748,10 +934,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         const float up = __uint_as_float((uint32_t)(k + 127) << 23);
         if (j8 == 0)                                   // (an infinite q: NaN scores)
           qscale[rr] = amax < INFINITY ? __uint_as_float((uint32_t)(127 - k) << 23) : NAN;
-#pragma unroll
-        for (int c = 0; c < 10; ++c) {                 // 64-channel pieces; the tenth is padding
-          if (c >= 2 * a.atoms) continue;
-          const uint4 v = c < 9 ? raw[c < 9 ? c : 0] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 3
+        for (int c = 0; c < 2 * a.atoms; ++c) {        // 64-channel pieces; a tenth is padding
+          const uint4 v = c < nch && gr < t->row1 ? __ldg(src + 8 * c)
+                                                 : make_uint4(0u, 0u, 0u, 0u);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t hi[2], lw[2];
 #pragma unroll
@@ -779,22 +965,19 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       if (lane == 0) mbar_signal_remote(bar0(kBarQFull));
       qs = qscale[row];
     }
-    // One scale per tensor multiplies every score and the output.
-    const float kscale = p.kv_format == kE4m3 ? __ldg(p.k_scale) : 1.f;
     const float scale = a.scale_log2 * qs * kscale;
     float m_run = -INFINITY;   // running max (log2 units), the same in a row's four threads
     float l_run = 0.f;         // this thread's sum of exp2(s - m_run)
     float lr_run = 0.f;        // the same sum of the bf16-rounded weights
-    __nv_bfloat16* red = reinterpret_cast<__nv_bfloat16*>(sm + C::kOffRed);
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(sm + C::kOffMask);
-    const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
-    MetaRing mr;
-    for (int j = 0; j < nb; ++j, mr.next()) {
-      const int buf = j & 1, m = mr.m;
-      const int e0 = t.block(b0 + j) * kBN + 32 * seg;   // this thread's first key
+    int blk = nb > 0 ? t->block(t->b0) : 0;
+    const int jump = t->sink_blocks - t->b0;             // the block behind the sinks'
+    for (int j = 0; j < nb; ++j, ++J, mr.next()) {
+      const int buf = J & 1, m = mr.m;
+      const int e0 = blk * kBN + 32 * seg;               // this thread's first key
+      blk = j + 1 == jump ? t->win_block : blk + 1;
       W.wait_ready(bar(kBarMFull + m), mr.ph);
       uint32_t see = words[4 * m + seg];
-      W.wait_ready(bar(kBarSFull + buf), (j >> 1) & 1);
+      W.wait_ready(bar(kBarSFull + buf), (J >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       // The row's view of its 32 keys.
@@ -897,7 +1080,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));   // the lookups were read
       if (j >= 1) {
-        W.wait_ready(bar(kBarPEmpty), (j - 1) & 1);    // PV(j - 1) is done
+        W.wait_ready(bar(kBarPEmpty), (J - 1) & 1);    // PV(j - 1) is done
         __syncwarp();
         tc_fence_after();
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
@@ -927,7 +1110,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 
     // ---- epilogue -------------------------------------------------------------
     if (nb > 0) {
-      W.wait_ready(bar(kBarPEmpty), (nb - 1) & 1);
+      W.wait_ready(bar(kBarPEmpty), (J - 1) & 1);
       __syncwarp();
       tc_fence_after();
     }
@@ -946,10 +1129,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const bool empty = l == 0.f;
     const float inv = empty ? 0.f : __fdividef(kscale, lr);
     const bool partial = p.o_part != nullptr;
-    const int64_t prow_g = (int64_t)split * p.b.N * p.h + g;   // row of the partials
-    // O columns [128 wg, + 128) are channels 256 wg + 128 half ..
+    const int64_t g = (int64_t)t->row0 + 64 * (int)r + row;
+    const bool live = g < t->row1;
+    const int64_t prow_g = (int64_t)t->split * p.b.N * p.h + g; // row of the partials
+    // O columns [128 wg, + 128) are channels 256 wg + 128 half ..; a thread's
+    // stores fill whole 32-byte sectors, straight from registers.
     const int ch0 = 256 * wg + 128 * half;
-    uint8_t* stage = sm + C::kOffV + row * kOStride;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
     bool odd = false;                                    // an output that is not finite
 #pragma unroll 1
     for (int c = 0; c < 128; c += 16) {
@@ -959,25 +1145,31 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         tmem_ld16(tmem + lane_base + kColO + 128 * wg + c, w);
         tmem_wait_ld();
       }
-      float o[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        o[k] = empty ? 0.f : __uint_as_float(w[k]) * inv;
-        odd |= !(fabsf(o[k]) < INFINITY);
+        const float o = empty ? 0.f : __uint_as_float(w[k]) * inv;
+        odd |= !(fabsf(o) < INFINITY);
+        w[k] = __float_as_uint(o);
       }
+      if (!live) continue;
       if (partial) {
-        if (live && !empty) {
-          float4* dst = reinterpret_cast<float4*>(p.o_part + prow_g * 512 + ch0 + c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        if (!empty) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.o_part + prow_g * 512 + ch0 + c);
+          st_global_32(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+          st_global_32(dst + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
         }
       } else {
         uint32_t b[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) b[k] = pack_bf16(o[2 * k], o[2 * k + 1]);
-        *reinterpret_cast<uint4*>(stage + (ch0 + c) * 2) = make_uint4(b[0], b[1], b[2], b[3]);
-        *reinterpret_cast<uint4*>(stage + (ch0 + c) * 2 + 16) = make_uint4(b[4], b[5], b[6], b[7]);
+        for (int k = 0; k < 8; ++k)
+          b[k] = pack_bf16(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+        uint32_t* dst = reinterpret_cast<uint32_t*>(out + g * 512 + ch0 + c);
+        if (a.wide) {
+          st_global_32(dst, b[0], b[1], b[2], b[3], b[4], b[5], b[6], b[7]);
+        } else {
+          reinterpret_cast<uint4*>(dst)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+          reinterpret_cast<uint4*>(dst)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+        }
       }
     }
     if (live && seg == 0) {
@@ -989,30 +1181,24 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     }
     // A softmax that is not finite (a NaN or infinite visible score) is the
     // answer; a finite one with an output that is not may owe it to a masked
-    // position.
+    // position: the row is computed again and written over.
     odd = odd && live && l < INFINITY && lr < INFINITY;
     if (odd) flag[row] = 1;
-    fence_proxy_async_smem();
-    const bool any = named_bar_or(4, 256, odd);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-    if (!partial) {
-      const int st = tid - 128;
-      const int64_t gs = t.row0 + 64 * (int64_t)r + st;
-      if (st < kRows && gs < t.row1 && !flag[st]) {
-        bulk_store(out + gs * 512, sb + C::kOffV + st * kOStride, 1024);
-        bulk_commit_group();
-        bulk_wait_read_all();
-      }
-    }
-    if (any) {
+    if (named_bar_or(4, 256, odd)) {                     // (also orders the stores before)
       for (int rr = warp - 4; rr < kRows; rr += 8) {
         if (!flag[rr]) continue;
-        const int64_t gr = t.row0 + 64 * (int64_t)r + rr;
-        const int pr = t.p_last - ((int)((t.row1 - 1) / p.h) - (int)(gr / p.h));
-        slow_row<kFp8>(p, t, gr, pr, p.window ? max(pr - (p.window - 1), 0) : 0, b0, b1,
-                       partial ? p.o_part + ((int64_t)split * p.b.N * p.h + gr) * 512 : nullptr,
+        const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
+        const int pr = t->p_last - ((t->row1 - 1) / p.h - (int)gr / p.h);
+        slow_row<kFp8>(p, *t, gr, pr, p.window ? max(pr - (p.window - 1), 0) : 0,
+                       partial ? p.o_part + ((int64_t)t->split * p.b.N * p.h + gr) * 512 : nullptr,
                        out + gr * 512);
       }
+      named_bar_sync(4, 256);                            // the flags were read
+    }
+    // (the next unit's first weights are signalled behind these TMEM loads)
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
     }
     __syncwarp();
   } else {
@@ -1040,21 +1226,24 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           x[ps] = __ldg(reinterpret_cast<const uint4*>(kv + (int64_t)id * p.d_qk + 256 * n));
       }
     };
-    if (nb > 0) {
-      W.wait_ready(bar(kBarMFull), 0);
-      load_unit(raw[0], 0, 0, 0);
-      load_unit(raw[1], 0, 1, 0);
+    Unit t;
+    int J = 0;
+    for (int i = 0; take_unit(i, t); ++i) {
+    if (t.nb > 0) {
+      W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
+      load_unit(raw[0], mr.m, 0, 0);
+      load_unit(raw[1], mr.m, 1, 0);
     }
-    for (int j = 0; j < nb; ++j, mr.next(), nx.next()) {
+    for (int j = 0; j < t.nb; ++j, ++J, mr.next(), nx.next()) {
 #pragma unroll 1
       for (int n = 0; n < 2; ++n) {
-        if (n == 1 && j + 1 < nb) W.wait_ready(bar(kBarMFull + nx.m), nx.ph);
+        if (n == 1 && j + 1 < t.nb) W.wait_ready(bar(kBarMFull + nx.m), nx.ph);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int v = 2 * n + half;
           const uint32_t* mul = reinterpret_cast<const uint32_t*>(sm + C::kOffMul) + kBN * mr.m +
                                 64 * half + kr;
-          if (j >= 1) W.wait_ready(bar(kBarVEmpty + v), (j - 1) & 1);
+          if (J >= 1) W.wait_ready(bar(kBarVEmpty + v), (J - 1) & 1);
           uint8_t* dst = sm + C::kOffV + 2 * v * kAtom;
 #pragma unroll
           for (int ps = 0; ps < 2; ++ps) {
@@ -1070,7 +1259,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           }
           if (n == 0)
             load_unit(raw[half], mr.m, half, 1);
-          else if (j + 1 < nb)
+          else if (j + 1 < t.nb)
             load_unit(raw[half], nx.m, half, 0);
           fence_proxy_async_smem();
           __syncwarp();
@@ -1081,6 +1270,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         }
       }
       if (*abort_flag) break;
+    }
     }
     __syncwarp();
   }
@@ -1238,6 +1428,11 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   // other sizes than multiples of 4 take gather4 alone.
   a.box = p.b.block_size & -p.b.block_size;
   a.box = a.box > 64 ? 64 : a.box < 4 ? 0 : a.box;
+  a.quad = p.b.block_size % 4 == 0;
+  a.shift = -1;
+  for (int k = 0; k < 31; ++k)
+    if (p.b.block_size == 1 << k) a.shift = k;
+  a.wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
   cudaError_t e = encode_rows(&a.row_map, fp8, p.kv, p.d_qk, p.b.num_slots, 1);
   if (e == cudaSuccess && a.box)
     e = encode_rows(&a.box_map, fp8, p.kv, p.d_qk, p.b.num_slots, a.box);

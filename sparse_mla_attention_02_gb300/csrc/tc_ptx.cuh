@@ -221,6 +221,41 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
+// Cluster launch control: ask to take over the work of a cluster of this grid
+// that has not started.  The 16-byte answer is written to the same offset in
+// every CTA of the cluster and counted on the same mbarrier of each.
+__device__ __forceinline__ void cluster_take_over(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes."
+      "multicast::cluster::all.b128 [%0], [%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+// Whether the answer hands over a cluster, and its first CTA's index (x).
+__device__ __forceinline__ bool cluster_taken(uint32_t answer, int& first) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  first = (int)x;
+  return ok != 0;
+}
+
+// 32 bytes to global memory (32-byte aligned): one whole sector.
+__device__ __forceinline__ void st_global_32(void* dst, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d, uint32_t e, uint32_t f, uint32_t g,
+                                             uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a),
+               "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+
 // 2^x on the SFU (approximate; flushes subnormal results to zero).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
