@@ -117,6 +117,40 @@ enum {
   kNumBars = kBarDrain + 2
 };
 
+// The bounded waits of tc_common.cuh with everything but the first try out of
+// line: the roles' loops then stay small, and they have to share one
+// instruction cache (waits in line cost this kernel 1.2x).
+struct PairWaiter {
+  uint32_t flags;                          // shared address: abort flag, abort counter at the start
+  const WinParams* p;
+  __device__ __forceinline__ volatile int* shared(int i) const {
+    return static_cast<volatile int*>(__cvta_shared_to_generic(flags)) + i;
+  }
+  __device__ __forceinline__ bool aborted() const {
+    int v;
+    asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(flags) : "memory");
+    return v != 0;
+  }
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) const;
+  __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const;
+};
+
+static __device__ __noinline__ void pair_wait_slow(uint32_t bar, uint32_t parity, uint32_t flags,
+                                                   const WinParams* p, bool drain) {
+  const PairWaiter w{flags, p};
+  Waiter slow{w.shared(0), p->status, p->abort_ctr, *w.shared(1), p->wait_limit_ns};
+  if (drain)
+    slow.drain(bar, parity);
+  else
+    slow.wait(bar, parity);
+}
+__device__ __forceinline__ void PairWaiter::wait(uint32_t bar, uint32_t parity) const {
+  if (__builtin_expect(!mbar_try_wait(bar, parity), 0)) pair_wait_slow(bar, parity, flags, p, false);
+}
+__device__ __forceinline__ void PairWaiter::drain(uint32_t bar, uint32_t parity) const {
+  pair_wait_slow(bar, parity, flags, p, true);
+}
+
 // A unit as its warps need it: rows [row0, row1) of the flattened (token, head)
 // list, of request r, whose last token has position p_last; positions
 // [lo, p_last] and [0, sinks) are seen by some row; its key blocks are numbers
@@ -152,7 +186,7 @@ struct Cfg {
   // E4M3: the keys' scales of a block, the Q rows' scales
   static constexpr uint32_t kOffTmem = kOffIds + kMeta * kBN * 4;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
-  static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 4 + 15) & ~15u : kOffAbort + 4;
+  static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 8 + 15) & ~15u : kOffAbort + 8;
   static constexpr uint32_t kOffMul = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
   static constexpr uint32_t kOffQScale = kOffMul + (kFp8 ? kMeta * kBN * 4 : 0);
   static constexpr uint32_t kOffPlain = kOffQScale + (kFp8 ? kRows * 4 : 0);
@@ -228,7 +262,7 @@ struct Rows4 {
   int id[4];
   int blk[4];
 };
-__device__ __forceinline__ Rows4 lookup4(const WinParams& p, const Unit& t, int pos, bool& bad) {
+static __device__ __noinline__ Rows4 lookup4(const WinParams& p, const Unit& t, int pos, bool& bad) {
   Rows4 o;
   int page = -1, blk = -1;
 #pragma unroll
@@ -272,7 +306,9 @@ __device__ __forceinline__ float key_scale(const WinParams& p, int blk) {
 __device__ __forceinline__ float v_scale(float s) {
   return fminf(fmaxf(__uint_as_float(__float_as_uint(s) & 0x7F800000u), 0x1p-100f), 128.f);
 }
-__device__ __forceinline__ float p_scale(float s) { return s / v_scale(s); }
+__device__ __forceinline__ float p_scale(float s) {   // s / v_scale(s): a power of two
+  return s * __uint_as_float(0x7F000000u - __float_as_uint(v_scale(s)));
+}
 
 // Four E4M3 codes times a power of two, as bf16: the codes' exponent and
 // mantissa bits in bf16's fields read as 2^-120 of their value, one product
@@ -386,9 +422,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   const uint32_t r = cluster_ctarank();
 
   auto bar = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kOffAbort);
-  Waiter W{abort_flag, p.status, p.abort_ctr, *reinterpret_cast<volatile int*>(p.abort_ctr),
-           p.wait_limit_ns};
+  const PairWaiter W{sb + C::kOffAbort, &p};
 
   if (tid == 0) {
     for (int i = 0; i < kKGroups; ++i) {
@@ -420,7 +454,8 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     }
     mbar_init(bar(kBarDrain), 1);
     mbar_init(bar(kBarDrain + 1), 1);
-    *abort_flag = 0;
+    *W.shared(0) = 0;
+    *W.shared(1) = *reinterpret_cast<volatile int*>(p.abort_ctr);
     fence_mbar_init_cluster();
   }
   if (warp == 0) {
@@ -439,7 +474,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   // The i-th unit's description, copied by the calling warp, which then lets it
   // go; false behind the last one (or after an abort).
   auto take_unit = [&](int i, Unit& u) {
-    W.wait_ready(bar(kBarTFull + (i & 1)), (i >> 1) & 1);
+    W.wait(bar(kBarTFull + (i & 1)), (i >> 1) & 1);
     const int4* src = reinterpret_cast<const int4*>(sm + C::kOffUnit + 48 * (i & 1));
     const int4 x = src[0], y = src[1], z = src[2];
     u.row0 = x.x; u.row1 = x.y; u.p_last = x.z; u.r = x.w;
@@ -447,11 +482,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     u.b0 = z.x; u.nb = z.y; u.split = z.z; u.live = z.w;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
-    return u.live != 0 && *abort_flag == 0;
+    return u.live != 0 && !W.aborted();
   };
   // The same in place, for a warp that lets it go itself, at the unit's end.
   auto peek_unit = [&](int i) {
-    W.wait_ready(bar(kBarTFull + (i & 1)), (i >> 1) & 1);
+    W.wait(bar(kBarTFull + (i & 1)), (i >> 1) & 1);
     return reinterpret_cast<const Unit*>(sm + C::kOffUnit + 48 * (i & 1));
   };
   // Blocks are counted across units (J): a barrier's n-th phase is block n's.
@@ -465,14 +500,14 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const uint64_t dk = sdesc(sb + C::kOffK, 16, 1024, kLayoutSw128);
       Unit u;
       for (int i = 0, q = 0, J = 0; take_unit(i, u); ++i) {
-       if (u.nb > 0) W.wait_ready(bar(kBarQFull), q++ & 1);
+       if (u.nb > 0) W.wait(bar(kBarQFull), q++ & 1);
        for (int j = 0; j < u.nb; ++j, ++J) {
         if (p.inject_stall && j == 0) continue;      // tests: these scores never arrive
-        if (J >= 2) W.wait_ready(bar(kBarSEmpty + (J & 1)), ((J >> 1) - 1) & 1);
+        if (J >= 2) W.wait(bar(kBarSEmpty + (J & 1)), ((J >> 1) - 1) & 1);
         const uint32_t dS = tmem + kColS + 64 * (J & 1);
 #pragma unroll 1
         for (int g = 0, c = 0; c < a.atoms; ++g) {
-          W.wait_ready(bar(kBarKFull + g), J & 1);
+          W.wait(bar(kBarKFull + g), J & 1);
           __syncwarp();
           tc_fence_after();
           const int c1 = min(c + C::kAtomsPerGroup, a.atoms);
@@ -520,10 +555,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       Unit u;
       for (int i = 0, J = 0; take_unit(i, u); ++i) {
        for (int j = 0; j < u.nb; ++j, ++J) {
-        W.wait_ready(bar(kBarPFull), J & 1);
+        W.wait(bar(kBarPFull), J & 1);
 #pragma unroll 1
         for (int v = 0; v < kVUnits; ++v) {          // v = 2 n + key half
-          W.wait_ready(bar(kBarVFull + v), J & 1);
+          W.wait(bar(kBarVFull + v), J & 1);
           __syncwarp();
           tc_fence_after();
           if (elect_one()) {
@@ -556,10 +591,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     int q = 0, J = 0;
     for (int i = 0; take_unit(i, u); ++i) {
      if (!kFp8 && u.nb > 0) {
-      if (q >= 1) W.wait_ready(bar(kBarQEmpty), (q - 1) & 1);
-      if (*abort_flag) break;
+      if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
+      if (W.aborted()) break;
       if (lane == 0) {
         if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
+#pragma unroll 1
         for (int c = 0; c < a.atoms; ++c)
           tma_load_2d_pair(sb + C::kOffQ + c * kAtom, &a.q_map, 64 * c, u.row0 + 64 * (int)r,
                            bar0(kBarQFull));
@@ -568,7 +604,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
      }
      for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
-      W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
+      W.wait(bar(kBarMFull + mr.m), mr.ph);
       const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + 16 * r +
                                                                     (lane & 15)];
       __syncwarp();
@@ -577,9 +613,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const uint32_t full = __ballot_sync(0xffffffffu, all4) & 0xFFFFu;
       if (a.box == 64 && full == 0xFFFFu) {            // the 64 rows of one block, all seen
         if (lane == 0) {
+#pragma unroll 1
           for (int g = 0; g < groups; ++g) {
-            if (J >= 1) W.wait_ready(bar(kBarKEmpty + g), (J - 1) & 1);
-            if (*abort_flag) break;
+            if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
+            if (W.aborted()) break;
             const int c0 = g * C::kAtomsPerGroup;
             const uint32_t bytes = (uint32_t)min(C::kAtomsPerGroup, a.atoms - c0) * kAtom;
             if (r == 0) mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * bytes);
@@ -587,6 +624,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             if (bytes == C::kAtomsPerGroup * kAtom)
               tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * g);
             else
+#pragma unroll 1
               for (int c = c0; c < a.atoms; ++c)
                 tma_load_2d_pair(dst + (c - c0) * kAtom, &a.box_map, cols * c, id.x,
                                  kfull0 + 8u * g);
@@ -594,21 +632,23 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           }
         }
         __syncwarp();
-        if (*abort_flag) break;
+        if (W.aborted()) break;
         continue;
       }
       // lanes of this lane's box, all seen and allocated: one copy for the box
       const int per = a.box >> 2;
       const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
       const bool boxed = per && (full & mine) == mine;
+#pragma unroll 1
       for (int g = 0; g < groups; ++g) {
-        if (J >= 1) W.wait_ready(bar(kBarKEmpty + g), (J - 1) & 1);
-        if (*abort_flag) break;
+        if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
+        if (W.aborted()) break;
         const int c0 = g * C::kAtomsPerGroup, c1 = min(c0 + C::kAtomsPerGroup, a.atoms);
         if (r == 0 && lane == 0)
           mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * (uint32_t)(c1 - c0) * kAtom);
         __syncwarp();
         if (lane < 16 && (!boxed || (lane & (per - 1)) == 0)) {
+#pragma unroll 1
           for (int c = c0; c < c1; ++c) {
             const uint32_t dst = sb + C::kOffK + c * kAtom + 4 * lane * 128;
             if (boxed)
@@ -621,13 +661,14 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         ++issued;
         __syncwarp();
       }
-      if (*abort_flag) break;
+      if (W.aborted()) break;
      }
     }
     // Teardown: the last copies into each part have landed in both CTAs (the
     // even CTA's barriers count both; earlier ones were consumed).
     if (r == 0 && lane == 0) {
       if (q > 0) W.drain(bar(kBarQFull), (q - 1) & 1);
+#pragma unroll 1
       for (int g = 0; g < groups && g < issued; ++g)
         W.drain(bar(kBarKFull + g), ((issued - 1 - g) / groups) & 1);
     }
@@ -641,7 +682,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       Unit u;
       for (int i = 0; take_unit(i, u); ++i) {
        for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
-        W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
+        W.wait(bar(kBarMFull + mr.m), mr.ph);
         const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
@@ -650,9 +691,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (a.box == 64 && full == ~0u) {              // two whole blocks
           const int y1 = __shfl_sync(0xffffffffu, id.x, 16);
           if (lane == 0) {
+#pragma unroll 1
             for (int v = 0; v < kVUnits; ++v) {
-              if (J >= 1) W.wait_ready(bar(kBarVEmpty + v), (J - 1) & 1);
-              if (*abort_flag) break;
+              if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
+              if (W.aborted()) break;
               if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
               tma_load_3d_pair(sb + C::kOffV + 2 * v * kAtom, &a.v_map, 0, v & 1 ? y1 : id.x,
                                4 * (v >> 1) + 2 * (int)r, vfull0 + 8u * v);
@@ -660,20 +702,22 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             }
           }
           __syncwarp();
-          if (*abort_flag) break;
+          if (W.aborted()) break;
           continue;
         }
         const int per = a.box >> 2;
         const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
         const bool boxed = per && (full & mine) == mine;
+#pragma unroll 1
         for (int v = 0; v < kVUnits; ++v) {
-          if (J >= 1) W.wait_ready(bar(kBarVEmpty + v), (J - 1) & 1);
-          if (*abort_flag) break;
+          if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
+          if (W.aborted()) break;
           if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
           __syncwarp();
           if ((lane >> 4) == (v & 1) && (!boxed || (lane & (per - 1)) == 0)) {
             const uint32_t full_bar = vfull0 + 8u * v;
             const int ch = 256 * (v >> 1) + 128 * (int)r;
+#pragma unroll 1
             for (int c = 0; c < 2; ++c) {
               const uint32_t dst = sb + C::kOffV + (2 * v + c) * kAtom + 4 * (lane & 15) * 128;
               if (boxed)
@@ -685,10 +729,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           ++issued;
           __syncwarp();
         }
-        if (*abort_flag) break;
+        if (W.aborted()) break;
        }
       }
       if (r == 0 && lane == 0)
+#pragma unroll 1
         for (int v = 0; v < kVUnits && v < issued; ++v)
           W.drain(bar(kBarVFull + v), ((issued - 1 - v) / kVUnits) & 1);
       __syncwarp();
@@ -745,7 +790,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     };
     int i = 0;                                         // units described
     auto publish = [&](const Unit& x) {
-      if (i >= 2) W.wait_ready(bar(kBarTEmpty + (i & 1)), ((i >> 1) - 1) & 1);
+      if (i >= 2) W.wait(bar(kBarTEmpty + (i & 1)), ((i >> 1) - 1) & 1);
       int4* dst = reinterpret_cast<int4*>(sm + C::kOffUnit + 48 * (i & 1));
       if (lane == 0) {
         dst[0] = make_int4(x.row0, x.row1, x.p_last, x.r);
@@ -759,7 +804,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     int64_t unit = (int64_t)(blockIdx.x >> 1);
     bool pending = false;                              // an answer is on its way
     int n = 0;                                         // answers read
-    while (!*abort_flag) {
+    while (!W.aborted()) {
       // Ask for the next unit before this one is worked on.
       const uint32_t cfull = bar(kBarCFull + (n & 1));
       const uint32_t answer = sb + C::kOffAnswer + 16 * (n & 1);
@@ -829,10 +874,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         // The block's rows on their way into L2, two to three blocks before
         // their copies: a copy then waits for L2, not for HBM.
         if (a.box == 64 && (lane & 15) == 0 && id[0] >= 0 && (lane >> 4) == (int)r)
+#pragma unroll 1
           for (int c = 0; c < p.d_qk * C::kElem / 128; c += C::kAtomsPerGroup)
             tma_prefetch_3d(&a.k_map, 0, id[0], c);
-        if (J >= kMeta) W.wait_ready(bar(kBarMEmpty + m), mr.ph ^ 1);
-        if (*abort_flag) break;
+        if (J >= kMeta) W.wait(bar(kBarMEmpty + m), mr.ph ^ 1);
+        if (W.aborted()) break;
         __syncwarp();
         uint32_t nib = 0;
 #pragma unroll
@@ -860,7 +906,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (lane == 0) mbar_arrive(bar(kBarMFull + m));
       }
       W.wait(cfull, (n >> 1) & 1);
-      if (*abort_flag) break;
+      if (W.aborted()) break;
       pending = false;
       int first;
       const bool taken = cluster_taken(answer, first);
@@ -894,7 +940,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     int J = 0;
     for (int i = 0;; ++i) {
     const Unit* t = peek_unit(i);
-    if (!t->live || *abort_flag) break;
+    if (!t->live || W.aborted()) break;
     int pos = -1, lo = 0;                              // the row's token sees [lo, pos], sinks
     {
       const int g = t->row0 + 64 * (int)r + row;
@@ -975,9 +1021,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const int buf = J & 1, m = mr.m;
       const int e0 = blk * kBN + 32 * seg;               // this thread's first key
       blk = j + 1 == jump ? t->win_block : blk + 1;
-      W.wait_ready(bar(kBarMFull + m), mr.ph);
+      W.wait(bar(kBarMFull + m), mr.ph);
       uint32_t see = words[4 * m + seg];
-      W.wait_ready(bar(kBarSFull + buf), (J >> 1) & 1);
+      W.wait(bar(kBarSFull + buf), (J >> 1) & 1);
       __syncwarp();
       tc_fence_after();
       // The row's view of its 32 keys.
@@ -1013,7 +1059,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const float4* ks4 = reinterpret_cast<const float4*>(sm + C::kOffScale) + 32 * m + 8 * seg;
       if (kFp8) {
         const float own = reinterpret_cast<const float*>(sm + C::kOffSeg)[4 * m + seg];
-        if (own > 0.f) {
+        if (__builtin_expect(own > 0.f, 1)) {
           cl *= own;
         } else {                                         // several scales in the segment
 #pragma unroll
@@ -1027,7 +1073,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           cl = 1.f;
         }
       }
-      if (!__all_sync(0xffffffffu, see == ~0u && cl > 0.f)) {
+      if (__builtin_expect(!__all_sync(0xffffffffu, see == ~0u && cl > 0.f), 0)) {
 #pragma unroll
         for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] * cl : -INFINITY;
         cl = 1.f;
@@ -1063,7 +1109,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       ls += ls1;
       lr += lr1;
-      if (kFp8 && !reinterpret_cast<const int*>(sm + C::kOffPlain)[m]) {
+      if (kFp8 && __builtin_expect(!reinterpret_cast<const int*>(sm + C::kOffPlain)[m], 0)) {
         // What V's power of two leaves of the key's scale goes to its weight.
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -1080,7 +1126,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));   // the lookups were read
       if (j >= 1) {
-        W.wait_ready(bar(kBarPEmpty), (J - 1) & 1);    // PV(j - 1) is done
+        W.wait(bar(kBarPEmpty), (J - 1) & 1);    // PV(j - 1) is done
         __syncwarp();
         tc_fence_after();
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
@@ -1110,7 +1156,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 
     // ---- epilogue -------------------------------------------------------------
     if (nb > 0) {
-      W.wait_ready(bar(kBarPEmpty), (J - 1) & 1);
+      W.wait(bar(kBarPEmpty), (J - 1) & 1);
       __syncwarp();
       tc_fence_after();
     }
@@ -1184,7 +1230,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // position: the row is computed again and written over.
     odd = odd && live && l < INFINITY && lr < INFINITY;
     if (odd) flag[row] = 1;
-    if (named_bar_or(4, 256, odd)) {                     // (also orders the stores before)
+    if (__builtin_expect(named_bar_or(4, 256, odd), 0)) {                     // (also orders the stores before)
       for (int rr = warp - 4; rr < kRows; rr += 8) {
         if (!flag[rr]) continue;
         const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
@@ -1230,20 +1276,20 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     int J = 0;
     for (int i = 0; take_unit(i, t); ++i) {
     if (t.nb > 0) {
-      W.wait_ready(bar(kBarMFull + mr.m), mr.ph);
+      W.wait(bar(kBarMFull + mr.m), mr.ph);
       load_unit(raw[0], mr.m, 0, 0);
       load_unit(raw[1], mr.m, 1, 0);
     }
     for (int j = 0; j < t.nb; ++j, ++J, mr.next(), nx.next()) {
 #pragma unroll 1
       for (int n = 0; n < 2; ++n) {
-        if (n == 1 && j + 1 < t.nb) W.wait_ready(bar(kBarMFull + nx.m), nx.ph);
+        if (n == 1 && j + 1 < t.nb) W.wait(bar(kBarMFull + nx.m), nx.ph);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int v = 2 * n + half;
           const uint32_t* mul = reinterpret_cast<const uint32_t*>(sm + C::kOffMul) + kBN * mr.m +
                                 64 * half + kr;
-          if (J >= 1) W.wait_ready(bar(kBarVEmpty + v), (J - 1) & 1);
+          if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
           uint8_t* dst = sm + C::kOffV + 2 * v * kAtom;
 #pragma unroll
           for (int ps = 0; ps < 2; ++ps) {
@@ -1269,7 +1315,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           }
         }
       }
-      if (*abort_flag) break;
+      if (W.aborted()) break;
     }
     }
     __syncwarp();
@@ -1279,7 +1325,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   // TMEM (the even CTA drained the MMAs and the pair's copies above).  After an
   // abort the CTAs may have issued different copies, whose barriers then tell
   // nothing: 100 us let what is in flight land.
-  if (tid == 0 && *abort_flag) {
+  if (tid == 0 && W.aborted()) {
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 100000u) {
     }
