@@ -32,16 +32,23 @@
 // Shared memory (bf16): Q 72 KB, K 72 KB, V 64 KB, P 16 KB.  K and V are one
 // block deep, in rings of 3 channel groups and of 4 (channel half, key half)
 // units; each part is refilled as soon as its MMAs are done, so the loads of
-// block j + 1 run under the MMAs of block j.
+// block j + 1 run under the MMAs of block j.  E4M3: Q 80 KB (two terms), K two
+// blocks of 40 KB, V 32 KB, P 24 KB (three terms).
 //
-// E4M3 rows.  QK multiplies the codes as they are (kind::f8f6f4, twice the
-// bf16 rate): Q is the sum of two E4M3 terms after a power-of-two scale per
-// row that puts its largest value in [224, 448); a bf16 value has 8 significant bits
-// and an E4M3 value 4, so hi = e4m3(q) and lo = e4m3(q - hi) give q exactly down
-// to 2^-11 of the row's largest value (below, to 2^-19 of it).  The key's
-// scale multiplies its scores in fp32.  PV needs P in 16 bits, so V is
-// converted to bf16 (exact) by eight warps on its way to shared memory, and the
-// key's scale multiplies P before it is rounded.
+// E4M3 rows.  Both products take the codes as they are (kind::f8f6f4, twice the
+// bf16 rate for each pass).  QK: Q is the sum of two E4M3 terms after a
+// power-of-two scale per row that puts its largest value in [224, 448); a bf16
+// value has 8 significant bits and an E4M3 value 4, so hi = e4m3(q) and
+// lo = e4m3(q - hi) give q exactly down to 2^-11 of the row's largest value
+// (below, to 2^-19 of it).  The key's scale multiplies its scores in fp32.
+// PV: a weight is the sum of three E5M2 terms.  E5M2 is the upper byte of f16 and
+// holds 3 significant bits, so a weight rounded to 9 of f16's 11 bits is exactly
+// its upper byte + that of the rest + that of what then remains (one bit more
+// than bf16 keeps); what falls below E5M2's grid is less than 2^-23 of a weight of
+// 1.  The key's scale belongs to its weight: with t = s + log2(scale) the running
+// maximum is taken over t, the weights are 2^(t - m) = scale 2^(s - m), and the
+// sums that divide add weight / scale.  So blocks of any scales share one range,
+// and nothing is converted on V's way to the tensor core.
 //
 // Masked positions never reach an MMA as anything but zeros where no row of
 // the tile sees them (unwritten rows, blocks that are not allocated, positions
@@ -63,8 +70,7 @@
 // the even CTA; two issuers, so that the waits of one are covered by the MMAs of
 // the other); warps 1 and 2 load K and V; warp 3 takes units and looks up
 // each block's rows (validity, scales, row ids); warps 4..11 are the softmax: four threads per
-// row (TMEM lane half x column half), 32 keys each; with E4M3 rows warps
-// 12..19 convert V.
+// row (TMEM lane half x column half), 32 keys each.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -72,6 +78,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "e4m3_quant.cuh"
 #include "paged_batch.cuh"
@@ -114,7 +121,8 @@ enum {
   kBarCFull = kBarTEmpty + 2,              // [2] own: an answer of the launch control
   kBarCEmpty = kBarCFull + 2,              // [2] even CTA: both have read it
   kBarDrain = kBarCEmpty + 2,              // [2] even CTA: QK's and PV's last MMAs
-  kNumBars = kBarDrain + 2
+  kBarK1 = kBarDrain + 2,                  // KFull and KEmpty of a second K block
+  kNumBars = kBarK1 + 2 * kKGroups
 };
 
 // The bounded waits of tc_common.cuh with everything but the first try out of
@@ -165,33 +173,39 @@ struct Unit {
 };
 static_assert(sizeof(Unit) == 48, "three 16-byte words");
 
+constexpr int kThreads = 416;              // 13 warps
+constexpr int kWarpPv = 12;                // issues PV
+
 template <bool kFp8>
 struct Cfg {
-  static constexpr int kThreads = kFp8 ? 640 : 416;
-  static constexpr int kWarpPv = kFp8 ? 2 : 12;         // issues PV (warp 2 loads bf16 V)
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
   static constexpr int kMaxAtoms = kFp8 ? 5 : 9;        // 128-byte columns of a row
+  static constexpr int kKStages = kFp8 ? 2 : 1;         // K blocks in shared memory
   static constexpr int kQTerms = kFp8 ? 2 : 1;
+  static constexpr int kPTerms = kFp8 ? 3 : 1;
+  static constexpr uint32_t kVUnit = kFp8 ? kAtom : 2 * kAtom;     // 64 keys x 128 channels
+  static constexpr uint32_t kPTerm = kFp8 ? kAtom : 2 * kAtom;     // 64 rows x 128 keys
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kOffQ + kQTerms * kMaxAtoms * kAtom;
-  static constexpr uint32_t kOffV = kOffK + kMaxAtoms * kAtom;
-  static constexpr uint32_t kOffP = kOffV + kVUnits * 2 * kAtom;
-  static constexpr uint32_t kOffRed = kOffP + 2 * kAtom;             // bf16 [2][4][64]
-  static constexpr uint32_t kOffBar = kOffRed + 1024;
-  static constexpr uint32_t kOffMask = kOffBar + 8 * ((kNumBars + 1) & ~1);   // u32 [kMeta][4]
+  static constexpr uint32_t kOffV = kOffK + kKStages * kMaxAtoms * kAtom;
+  static constexpr uint32_t kOffP = kOffV + kVUnits * kVUnit;
+  // row maxima [2][4][64]: bf16 (the room that is left), or fp32
+  static constexpr uint32_t kOffRed = kOffP + kPTerms * kPTerm;
+  static constexpr uint32_t kOffBar = kOffRed + (kFp8 ? 2048 : 1024);
+  static constexpr uint32_t kOffMask = kOffBar + 8 * (((kFp8 ? kNumBars : kBarK1) + 1) & ~1);
+                                                                      // u32 [kMeta][4]
   static constexpr uint32_t kOffUnit = kOffMask + kMeta * 16;         // Unit [2]
   static constexpr uint32_t kOffAnswer = kOffUnit + 2 * 48;           // 16 bytes [2]
   static constexpr uint32_t kOffIds = kOffAnswer + 32;                // i32 [kMeta][128] rows
-  // E4M3: the keys' scales of a block, the Q rows' scales
   static constexpr uint32_t kOffTmem = kOffIds + kMeta * kBN * 4;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
+  // E4M3: the keys' scales, each 32 keys' common scale (0: several), its log2
+  // and its reciprocal, the Q rows' scales
   static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 8 + 15) & ~15u : kOffAbort + 8;
-  static constexpr uint32_t kOffMul = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);
-  static constexpr uint32_t kOffQScale = kOffMul + (kFp8 ? kMeta * kBN * 4 : 0);
-  static constexpr uint32_t kOffPlain = kOffQScale + (kFp8 ? kRows * 4 : 0);
-  static constexpr uint32_t kOffSeg = kOffPlain + (kFp8 ? kMeta * 4 : 0);   // f32 [kMeta][4]
-  static constexpr uint32_t kSmem = kOffSeg + (kFp8 ? kMeta * 16 : 0);
+  static constexpr uint32_t kOffSeg = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);   // float4 [kMeta][4]
+  static constexpr uint32_t kOffQScale = kOffSeg + (kFp8 ? kMeta * 64 : 0);
+  static constexpr uint32_t kSmem = kOffQScale + (kFp8 ? kRows * 4 : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 // The epilogue's areas in P: row sums and flags.
@@ -300,30 +314,6 @@ __device__ __forceinline__ float key_scale(const WinParams& p, int blk) {
   return p.kv_format == kE4m3Block ? __ldg(p.k_scale + blk) : __ldg(p.k_scale);
 }
 
-// The part of a key's scale that its V row takes on the way to bf16, where it
-// costs nothing and is exact: the power of two at or below it, within [2^-100,
-// 2^7] (the conversion multiplies by 2^120 times it).  Its weight takes the rest.
-__device__ __forceinline__ float v_scale(float s) {
-  return fminf(fmaxf(__uint_as_float(__float_as_uint(s) & 0x7F800000u), 0x1p-100f), 128.f);
-}
-__device__ __forceinline__ float p_scale(float s) {   // s / v_scale(s): a power of two
-  return s * __uint_as_float(0x7F000000u - __float_as_uint(v_scale(s)));
-}
-
-// Four E4M3 codes times a power of two, as bf16: the codes' exponent and
-// mantissa bits in bf16's fields read as 2^-120 of their value, one product
-// with k = 2^120 v_scale (both lanes) restores it.  (The NaN code reads as 480:
-// the same row's K makes the score NaN, which is what reaches O.)
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t k, uint32_t& lo, uint32_t& hi) {
-  const uint32_t x = (prmt_sign<0x9180u>(w) << 4) & 0x87F087F0u;
-  const uint32_t y = (prmt_sign<0xB3A2u>(w) << 4) & 0x87F087F0u;
-  const __nv_bfloat162 kk = *reinterpret_cast<const __nv_bfloat162*>(&k);
-  __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), kk);
-  __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), kk);
-  lo = *reinterpret_cast<uint32_t*>(&a);
-  hi = *reinterpret_cast<uint32_t*>(&b);
-}
-
 // One row again, from its visible positions in the unit's blocks alone, by one
 // warp.  O is written to `out_f32` or
 // `out_bf16` (512 channels).  Lane l holds channels 2 l + 64 i, + 1.
@@ -412,7 +402,7 @@ __device__ __forceinline__ void slow_row(const WinParams& p, const Unit& t, int6
 }
 
 template <bool kFp8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 smla_window_kernel(const __grid_constant__ WinArgs a) {
   using C = Cfg<kFp8>;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -425,12 +415,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   const PairWaiter W{sb + C::kOffAbort, &p};
 
   if (tid == 0) {
-    for (int i = 0; i < kKGroups; ++i) {
+    for (int i = 0; i < 2 * kKGroups; ++i) {             // KFull and KEmpty
       mbar_init(bar(kBarKFull + i), 1);
-      mbar_init(bar(kBarKEmpty + i), 1);
+      if (kFp8) mbar_init(bar(kBarK1 + i), 1);
     }
     for (int i = 0; i < kVUnits; ++i) {
-      mbar_init(bar(kBarVFull + i), kFp8 ? 16 : 1);  // E4M3: converter warps of both CTAs
+      mbar_init(bar(kBarVFull + i), 1);
       mbar_init(bar(kBarVEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -442,13 +432,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     mbar_init(bar(kBarQFull), kFp8 ? 16 : 1);        // E4M3: the softmax warps write Q
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(bar(kBarMFull + i), 1);
-      mbar_init(bar(kBarMEmpty + i), kFp8 ? 17 : 10);  // softmax, converters, loaders
+      mbar_init(bar(kBarMEmpty + i), 10);              // softmax, loaders
     }
     mbar_init(bar(kBarQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarTFull + i), 1);
-      // softmax, K loads, V loads or conversion, the even CTA's issuers
-      mbar_init(bar(kBarTEmpty + i), (kFp8 ? 17 : 10) + (r == 0 ? 2 : 0));
+      mbar_init(bar(kBarTEmpty + i), 10 + (r == 0 ? 2 : 0));   // those, the even CTA's issuers
       mbar_init(bar(kBarCFull + i), 1);
       mbar_init(bar(kBarCEmpty + i), 2);
     }
@@ -505,9 +494,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (p.inject_stall && j == 0) continue;      // tests: these scores never arrive
         if (J >= 2) W.wait(bar(kBarSEmpty + (J & 1)), ((J >> 1) - 1) & 1);
         const uint32_t dS = tmem + kColS + 64 * (J & 1);
+        const int st = J % C::kKStages, kph = (J / C::kKStages) & 1;
 #pragma unroll 1
-        for (int g = 0, c = 0; c < a.atoms; ++g) {
-          W.wait(bar(kBarKFull + g), J & 1);
+        for (int g = kBarK1 * st, c = 0; c < a.atoms; ++g) {
+          W.wait(bar(kBarKFull + g), kph);
           __syncwarp();
           tc_fence_after();
           const int c1 = min(c + C::kAtomsPerGroup, a.atoms);
@@ -515,7 +505,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll 1
             for (int cc = c; cc < c1; ++cc) {
               const uint64_t ad = dq + (uint32_t)cc * (kAtom >> 4);
-              const uint64_t bd = dk + (uint32_t)cc * (kAtom >> 4);
+              const uint64_t bd = dk + (uint32_t)(cc + st * C::kMaxAtoms) * (kAtom >> 4);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (kFp8) {
@@ -546,10 +536,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
       W.drain(bar(kBarDrain), 0);
     }
-  } else if (warp == C::kWarpPv) {
+  } else if (warp == kWarpPv) {
     // ---- PV issuer (even CTA) ------------------------------------------------
     if (r == 0) {
-      const uint32_t id = idesc_bf16(128, 256, false, true);
+      const uint32_t id = kFp8 ? idesc_pair_e5m2_e4m3(128, 256) : idesc_bf16(128, 256, false, true);
       const uint64_t dp = sdesc(sb + C::kOffP, 16, 1024, kLayoutSw128);
       const uint64_t dv = sdesc(sb + C::kOffV, kAtom, 1024, kLayoutSw128);
       Unit u;
@@ -562,12 +552,23 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           __syncwarp();
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t ad = dp + (uint32_t)(v & 1) * (kAtom >> 4);
-            const uint64_t bd = dv + (uint32_t)v * (2 * kAtom >> 4);
+            const uint32_t dO = tmem + kColO + 128 * (v >> 1);
+            const uint64_t bd = dv + (uint32_t)v * (C::kVUnit >> 4);
+            const uint32_t keep = (j > 0 || (v & 1)) ? 1u : 0u;
+            if (kFp8) {
+              const uint64_t ad = dp + (uint32_t)(v & 1) * 4;    // 64 keys = 64 bytes
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_pair_bf16(tmem + kColO + 128 * (v >> 1), ad + 2 * ks, bd + 128 * ks, id,
-                            (j > 0 || (v & 1) || ks > 0) ? 1u : 0u);
+              for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int x = 0; x < 3; ++x)
+                  mma_pair_e4m3(dO, ad + 2 * ks + x * (C::kPTerm >> 4), bd + 256 * ks, id,
+                                (keep || ks > 0 || x > 0) ? 1u : 0u);
+            } else {
+              const uint64_t ad = dp + (uint32_t)(v & 1) * (kAtom >> 4);
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_pair_bf16(dO, ad + 2 * ks, bd + 128 * ks, id, (keep || ks > 0) ? 1u : 0u);
+            }
             mma_commit_pair(bar(kBarVEmpty + v));
             if (v == kVUnits - 1) mma_commit_pair(bar(kBarPEmpty));
           }
@@ -611,23 +612,25 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
       const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
       const uint32_t full = __ballot_sync(0xffffffffu, all4) & 0xFFFFu;
+      const int st = J % C::kKStages, kph = (J / C::kKStages) & 1, g0 = kBarK1 * st;
+      const uint32_t ktile = sb + C::kOffK + st * C::kMaxAtoms * kAtom;
       if (a.box == 64 && full == 0xFFFFu) {            // the 64 rows of one block, all seen
         if (lane == 0) {
 #pragma unroll 1
           for (int g = 0; g < groups; ++g) {
-            if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
+            if (J >= C::kKStages) W.wait(bar(kBarKEmpty + g0 + g), kph ^ 1);
             if (W.aborted()) break;
             const int c0 = g * C::kAtomsPerGroup;
             const uint32_t bytes = (uint32_t)min(C::kAtomsPerGroup, a.atoms - c0) * kAtom;
-            if (r == 0) mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * bytes);
-            const uint32_t dst = sb + C::kOffK + c0 * kAtom;
+            if (r == 0) mbar_arrive_expect_tx(bar(kBarKFull + g0 + g), 2u * bytes);
+            const uint32_t dst = ktile + c0 * kAtom;
             if (bytes == C::kAtomsPerGroup * kAtom)
-              tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * g);
+              tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * (g0 + g));
             else
 #pragma unroll 1
               for (int c = c0; c < a.atoms; ++c)
                 tma_load_2d_pair(dst + (c - c0) * kAtom, &a.box_map, cols * c, id.x,
-                                 kfull0 + 8u * g);
+                                 kfull0 + 8u * (g0 + g));
             ++issued;
           }
         }
@@ -641,21 +644,21 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const bool boxed = per && (full & mine) == mine;
 #pragma unroll 1
       for (int g = 0; g < groups; ++g) {
-        if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
+        if (J >= C::kKStages) W.wait(bar(kBarKEmpty + g0 + g), kph ^ 1);
         if (W.aborted()) break;
         const int c0 = g * C::kAtomsPerGroup, c1 = min(c0 + C::kAtomsPerGroup, a.atoms);
         if (r == 0 && lane == 0)
-          mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * (uint32_t)(c1 - c0) * kAtom);
+          mbar_arrive_expect_tx(bar(kBarKFull + g0 + g), 2u * (uint32_t)(c1 - c0) * kAtom);
         __syncwarp();
         if (lane < 16 && (!boxed || (lane & (per - 1)) == 0)) {
 #pragma unroll 1
           for (int c = c0; c < c1; ++c) {
-            const uint32_t dst = sb + C::kOffK + c * kAtom + 4 * lane * 128;
+            const uint32_t dst = ktile + c * kAtom + 4 * lane * 128;
             if (boxed)
-              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, kfull0 + 8u * g);
+              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, kfull0 + 8u * (g0 + g));
             else
               tma_gather4_pair(dst, &a.row_map, cols * c, id.x, id.y, id.z, id.w,
-                               kfull0 + 8u * g);
+                               kfull0 + 8u * (g0 + g));
           }
         }
         ++issued;
@@ -668,13 +671,17 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // even CTA's barriers count both; earlier ones were consumed).
     if (r == 0 && lane == 0) {
       if (q > 0) W.drain(bar(kBarQFull), (q - 1) & 1);
+      // (copy number x went to group x % groups of block x / groups)
 #pragma unroll 1
-      for (int g = 0; g < groups && g < issued; ++g)
-        W.drain(bar(kBarKFull + g), ((issued - 1 - g) / groups) & 1);
+      for (int x = max(issued - C::kKStages * groups, 0); x < issued; ++x) {
+        const int blk = x / groups;
+        W.drain(bar(kBarKFull + kBarK1 * (blk % C::kKStages) + x % groups),
+                (blk / C::kKStages) & 1);
+      }
     }
     __syncwarp();
-  } else if (!kFp8 && warp == 2) {
-    // ---- V loads (bf16): this CTA's channels of all 128 keys ----------------
+  } else if (warp == 2) {
+    // ---- V loads: this CTA's channels of all 128 keys -------------------------
     {
       const uint32_t vfull0 = bar0(kBarVFull);
       int issued = 0, J = 0;
@@ -695,9 +702,14 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             for (int v = 0; v < kVUnits; ++v) {
               if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
               if (W.aborted()) break;
-              if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
-              tma_load_3d_pair(sb + C::kOffV + 2 * v * kAtom, &a.v_map, 0, v & 1 ? y1 : id.x,
-                               4 * (v >> 1) + 2 * (int)r, vfull0 + 8u * v);
+              if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
+              if (kFp8)
+                tma_load_2d_pair(sb + C::kOffV + v * C::kVUnit, &a.box_map,
+                                 256 * (v >> 1) + 128 * (int)r, v & 1 ? y1 : id.x,
+                                 vfull0 + 8u * v);
+              else
+                tma_load_3d_pair(sb + C::kOffV + v * C::kVUnit, &a.v_map, 0, v & 1 ? y1 : id.x,
+                                 4 * (v >> 1) + 2 * (int)r, vfull0 + 8u * v);
               ++issued;
             }
           }
@@ -712,14 +724,15 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         for (int v = 0; v < kVUnits; ++v) {
           if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
           if (W.aborted()) break;
-          if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 4u * kAtom);
+          if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
           __syncwarp();
           if ((lane >> 4) == (v & 1) && (!boxed || (lane & (per - 1)) == 0)) {
             const uint32_t full_bar = vfull0 + 8u * v;
             const int ch = 256 * (v >> 1) + 128 * (int)r;
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t dst = sb + C::kOffV + (2 * v + c) * kAtom + 4 * (lane & 15) * 128;
+            for (int c = 0; c < (int)(C::kVUnit / kAtom); ++c) {
+              const uint32_t dst = sb + C::kOffV + v * C::kVUnit + c * kAtom +
+                                   4 * (lane & 15) * 128;
               if (boxed)
                 tma_load_2d_pair(dst, &a.box_map, ch + 64 * c, id.x, full_bar);
               else
@@ -848,17 +861,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           }
         }
         float own = 1.f;                               // the segment's scale, 0: several
-        bool plain = true;                             // scales are powers of two within reach
         if (keyed) {
           // (a segment: the 32 keys of eight lanes; keys that no row sees agree
           // with any scale)
           float top = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (id[k] >= 0) {
-              plain &= v_scale(sc[k]) == sc[k];
-              top = fmaxf(top, sc[k]);
-            }
+            if (id[k] >= 0) top = fmaxf(top, sc[k]);
 #pragma unroll
           for (int o = 1; o <= 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           bool same = true;
@@ -869,7 +878,6 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           }
           const uint32_t votes = __ballot_sync(0xffffffffu, same) >> (lane & 24);
           own = (votes & 0xFFu) == 0xFFu ? top : 0.f;
-          plain = __all_sync(0xffffffffu, plain);
         }
         // The block's rows on their way into L2, two to three blocks before
         // their copies: a copy then waits for L2, not for HBM.
@@ -890,17 +898,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         reinterpret_cast<int4*>(sm + C::kOffIds)[32 * m + lane] =
             make_int4(id[0], id[1], id[2], id[3]);
         if (kFp8) {
-          if (lane == 0) reinterpret_cast<int*>(sm + C::kOffPlain)[m] = plain;
           if ((lane & 7) == 0)
-            reinterpret_cast<float*>(sm + C::kOffSeg)[4 * m + (lane >> 3)] = own;
+            reinterpret_cast<float4*>(sm + C::kOffSeg)[4 * m + (lane >> 3)] =
+                make_float4(own, own > 0.f ? log2f(own) : 0.f, own > 0.f ? 1.f / own : 0.f, 0.f);
           reinterpret_cast<float4*>(sm + C::kOffScale)[32 * m + lane] =
               make_float4(sc[0], sc[1], sc[2], sc[3]);
-          uint32_t mul[4];                             // 2^120 v_scale, twice in bf16
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mul[k] = __byte_perm(__float_as_uint(v_scale(sc[k]) * 0x1p120f), 0u, 0x3232);
-          reinterpret_cast<uint4*>(sm + C::kOffMul)[32 * m + lane] =
-              make_uint4(mul[0], mul[1], mul[2], mul[3]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarMFull + m));
@@ -931,7 +933,8 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const int row = tl & 63, half = tl >> 6;           // tile row, key half
     const int seg = 2 * half + wg;                     // its 32 keys of the block
     const uint32_t lane_base = ((uint32_t)(warp & 3) * 32u) << 16;
-    __nv_bfloat16* red = reinterpret_cast<__nv_bfloat16*>(sm + C::kOffRed);
+    using Red = std::conditional_t<kFp8, float, __nv_bfloat16>;
+    Red* red = reinterpret_cast<Red*>(sm + C::kOffRed);
     const uint32_t* words = reinterpret_cast<const uint32_t*>(sm + C::kOffMask);
     const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
     // One scale per tensor multiplies every score and the output.
@@ -1056,21 +1059,22 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       // keys share their scale they stay as the MMA left them (the factor is
       // positive and keeps their order).
       float cl = scale;
-      const float4* ks4 = reinterpret_cast<const float4*>(sm + C::kOffScale) + 32 * m + 8 * seg;
+      // E4M3: the weights are 2^(t - m), t = s + log2(key's scale); `shift` is
+      // that log2 and `back` the reciprocal for the 32 keys' common scale.
+      float shift = 0.f, back = 1.f;
+      bool several = false;
+      const float* ks = reinterpret_cast<const float*>(sm + C::kOffScale) + kBN * m + 32 * seg;
       if (kFp8) {
-        const float own = reinterpret_cast<const float*>(sm + C::kOffSeg)[4 * m + seg];
-        if (__builtin_expect(own > 0.f, 1)) {
-          cl *= own;
-        } else {                                         // several scales in the segment
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 c = ks4[k];
-            s[4 * k] *= c.x * scale;
-            s[4 * k + 1] *= c.y * scale;
-            s[4 * k + 2] *= c.z * scale;
-            s[4 * k + 3] *= c.w * scale;
-          }
+        const float4 own = reinterpret_cast<const float4*>(sm + C::kOffSeg)[4 * m + seg];
+        cl *= own.x;
+        shift = own.y;
+        back = own.z;
+        several = !(own.x > 0.f);
+        if (__builtin_expect(several, 0)) {
           cl = 1.f;
+          back = 0.f;                                    // (their sums are taken below)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[k] = s[k] * (ks[k] * scale) + __log2f(ks[k]);
         }
       }
       if (__builtin_expect(!__all_sync(0xffffffffu, see == ~0u && cl > 0.f), 0)) {
@@ -1081,45 +1085,78 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       float hm = fmaxf(s[0], s[1]);
 #pragma unroll
       for (int k = 2; k < 32; k += 2) hm = max3(hm, s[k], s[k + 1]);
-      hm *= cl;
-      // The row's reference is the largest of its four (rounded) maxima: all
-      // four threads take the same one, and any value near the maximum serves.
-      __nv_bfloat16* rb = red + 256 * buf;
-      rb[64 * seg + row] = __float2bfloat16(hm);
+      hm = fmaf(hm, cl, shift);
+      // The row's reference is the largest of its four maxima (bf16 rows: rounded
+      // to bf16, any value near the maximum serves): all four threads take the
+      // same one.
+      Red* rb = red + 256 * buf;
+      if constexpr (kFp8)
+        rb[64 * seg + row] = hm;
+      else
+        rb[64 * seg + row] = __float2bfloat16(hm);
       float alpha = 1.f;
       if (named_bar_or(4, 256, hm > m_run + 8.f)) {      // also true for the first finite max
         float bm = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) bm = fmaxf(bm, __bfloat162float(rb[64 * k + row]));
+        for (int k = 0; k < 4; ++k) bm = fmaxf(bm, static_cast<float>(rb[64 * k + row]));
         if (bm > m_run + 7.f) {
           alpha = ex2_approx(m_run - bm);                // 0 when m_run = -inf
           m_run = bm;
         }
       }
-      uint32_t pk[16];
+      // bf16: 16 pairs of weights.  E4M3: three terms of four weights a word.
+      uint32_t pk[kFp8 ? 24 : 16];
       float ls = 0.f, ls1 = 0.f, lr = 0.f, lr1 = 0.f;
-      const float mm = m_run == -INFINITY ? 0.f : m_run; // (no score yet: every weight is 0)
+      const float mm = (m_run == -INFINITY ? 0.f : m_run) - shift;  // (no score: weights are 0)
+      if constexpr (kFp8) {
+        // 2^(t - m + 7) <= 2^15: within E5M2's range, its grid 2^-23 of a weight
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        fma2_bcast(s[k], s[k + 1], cl, -mm);
-        const float w0 = ex2_approx(s[k]), w1 = ex2_approx(s[k + 1]);
-        add2(ls, ls1, w0, w1);
-        pk[k / 2] = pack_bf16(w0, w1);
-        add_bf16x2_f32x2(lr, lr1, pk[k / 2]);
-      }
-      ls += ls1;
-      lr += lr1;
-      if (kFp8 && __builtin_expect(!reinterpret_cast<const int*>(sm + C::kOffPlain)[m], 0)) {
-        // What V's power of two leaves of the key's scale goes to its weight.
+        for (int k = 0; k < 32; k += 4) {
+          uint32_t h[2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float4 c = ks4[k];
-          c.x = p_scale(c.x); c.y = p_scale(c.y); c.z = p_scale(c.z); c.w = p_scale(c.w);
-          pk[2 * k] = pack_bf16(__uint_as_float(pk[2 * k] << 16) * c.x,
-                                __uint_as_float(pk[2 * k] & 0xFFFF0000u) * c.y);
-          pk[2 * k + 1] = pack_bf16(__uint_as_float(pk[2 * k + 1] << 16) * c.z,
-                                    __uint_as_float(pk[2 * k + 1] & 0xFFFF0000u) * c.w);
+          for (int e = 0; e < 2; ++e) {
+            float& s0 = s[k + 2 * e];
+            float& s1 = s[k + 2 * e + 1];
+            fma2_bcast(s0, s1, cl, 7.f - mm);
+            const float w0 = ex2_approx(s0), w1 = ex2_approx(s1);
+            add2(ls, ls1, w0, w1);
+            h[e] = (pack_f16(w0, w1) + 0x00020002u) & 0xFFFCFFFCu;   // 9 significant bits
+            add_f16x2_f32x2(lr, lr1, h[e]);
+            s0 = w0;
+            s1 = w1;
+          }
+#pragma unroll
+          for (int x = 0; x < 3; ++x) {
+            pk[8 * x + k / 4] = __byte_perm(h[0], h[1], 0x7531);     // the four upper bytes
+            if (x < 2) {
+              h[0] = sub_f16x2(h[0], h[0] & 0xFF00FF00u);
+              h[1] = sub_f16x2(h[1], h[1] & 0xFF00FF00u);
+            }
+          }
         }
+        back *= 0x1p-7f;
+        ls = (ls + ls1) * back;
+        lr = (lr + lr1) * back;
+        if (__builtin_expect(several, 0)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) ls += ks[k] > 0.f ? __fdividef(s[k] * 0x1p-7f, ks[k]) : 0.f;
+          // (a zero scale: key and value are zero, its weight is 2^(0 - m))
+#pragma unroll 1
+          for (int k = 0; k < 32; ++k)
+            if (ks[k] == 0.f && (see >> k & 1u)) ls += ex2_approx(-mm);
+          lr = ls;                                       // (9 bits: 2^-9 of a weight at most)
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          fma2_bcast(s[k], s[k + 1], cl, -mm);
+          const float w0 = ex2_approx(s[k]), w1 = ex2_approx(s[k + 1]);
+          add2(ls, ls1, w0, w1);
+          pk[k / 2] = pack_bf16(w0, w1);
+          add_bf16x2_f32x2(lr, lr1, pk[k / 2]);
+        }
+        ls += ls1;
+        lr += lr1;
       }
       l_run = l_run * alpha + ls;
       lr_run = lr_run * alpha + lr;
@@ -1142,12 +1179,24 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           tmem_wait_st();
         }
       }
-      // P row, keys 64 half + 32 wg .. + 31: chunks 4 wg .. of atom `half`
-      uint8_t* prow = sm + C::kOffP + half * kAtom + row * 128;
+      // P row: bf16, keys 64 half + 32 wg .. + 31 as chunks 4 wg .. of atom `half`;
+      // E4M3, bytes 32 seg .. + 31 of each term's row.
+      uint8_t* prow = sm + C::kOffP + row * 128;
+      const uint32_t sw = (uint32_t)row & 7u;
+      if constexpr (kFp8) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<uint4*>(prow + (((uint32_t)(4 * wg + c) ^ ((uint32_t)row & 7u)) << 4)) =
-            make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(prow + x * C::kPTerm + (((uint32_t)(2 * seg + c) ^ sw) << 4)) =
+                make_uint4(pk[8 * x + 4 * c], pk[8 * x + 4 * c + 1], pk[8 * x + 4 * c + 2],
+                           pk[8 * x + 4 * c + 3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(prow + half * kAtom + (((uint32_t)(4 * wg + c) ^ sw) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+      }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -1173,7 +1222,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       lr += sums[256 + 64 * k + row];
     }
     const bool empty = l == 0.f;
-    const float inv = empty ? 0.f : __fdividef(kscale, lr);
+    // (a sum that is not finite: NaN, whatever the weights' terms became)
+    const float inv = empty ? 0.f : l < INFINITY ? __fdividef(kFp8 ? kscale * 0x1p-7f : kscale, lr)
+                                                 : NAN;
     const bool partial = p.o_part != nullptr;
     const int64_t g = (int64_t)t->row0 + 64 * (int)r + row;
     const bool live = g < t->row1;
@@ -1245,78 +1296,6 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
-    }
-    __syncwarp();
-  } else {
-    // ---- E4M3 V: rows from global memory, converted to bf16 (exact) ---------
-    // Eight threads per key, 16 channels each; a unit is 64 keys x 128 channels.
-    // A unit's loads are issued two units ahead, into the registers that the
-    // unit before it in the same key half has left.
-    const int ct = tid - 384, j8 = ct & 7, kr = ct >> 3;     // key row of 32 per pass
-    const uint8_t* kv = static_cast<const uint8_t*>(p.kv) + 128 * r + 16 * j8;
-    // channels 16 j8 ..: atom j8 / 4, chunks 2 (j8 % 4), + 1; rows kr + 32 ps have kr's swizzle
-    const uint32_t off0 = (uint32_t)(j8 >> 2) * kAtom + kr * 128 +
-                          (((2u * (j8 & 3)) ^ ((uint32_t)kr & 7u)) << 4);
-    const uint32_t off1 = off0 ^ 16u;
-    const uint32_t vfull0 = bar0(kBarVFull);
-    MetaRing mr, nx;                                         // this block's and the next one's
-    nx.next();
-    uint4 raw[2][2];
-    auto load_unit = [&](uint4 (&x)[2], int m, int half, int n) {
-      const int* ids = reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * m + 64 * half + kr;
-#pragma unroll
-      for (int ps = 0; ps < 2; ++ps) {
-        const int id = ids[32 * ps];
-        x[ps] = make_uint4(0u, 0u, 0u, 0u);
-        if (id >= 0)
-          x[ps] = __ldg(reinterpret_cast<const uint4*>(kv + (int64_t)id * p.d_qk + 256 * n));
-      }
-    };
-    Unit t;
-    int J = 0;
-    for (int i = 0; take_unit(i, t); ++i) {
-    if (t.nb > 0) {
-      W.wait(bar(kBarMFull + mr.m), mr.ph);
-      load_unit(raw[0], mr.m, 0, 0);
-      load_unit(raw[1], mr.m, 1, 0);
-    }
-    for (int j = 0; j < t.nb; ++j, ++J, mr.next(), nx.next()) {
-#pragma unroll 1
-      for (int n = 0; n < 2; ++n) {
-        if (n == 1 && j + 1 < t.nb) W.wait(bar(kBarMFull + nx.m), nx.ph);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int v = 2 * n + half;
-          const uint32_t* mul = reinterpret_cast<const uint32_t*>(sm + C::kOffMul) + kBN * mr.m +
-                                64 * half + kr;
-          if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
-          uint8_t* dst = sm + C::kOffV + 2 * v * kAtom;
-#pragma unroll
-          for (int ps = 0; ps < 2; ++ps) {
-            const uint4 x = raw[half][ps];
-            const uint32_t k = mul[32 * ps];
-            uint32_t o[8];
-            codes_to_bf16(x.x, k, o[0], o[1]);
-            codes_to_bf16(x.y, k, o[2], o[3]);
-            codes_to_bf16(x.z, k, o[4], o[5]);
-            codes_to_bf16(x.w, k, o[6], o[7]);
-            *reinterpret_cast<uint4*>(dst + off0 + 4096 * ps) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + off1 + 4096 * ps) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          if (n == 0)
-            load_unit(raw[half], mr.m, half, 1);
-          else if (j + 1 < t.nb)
-            load_unit(raw[half], nx.m, half, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_signal_remote(vfull0 + 8u * v);
-            if (v == 3) mbar_arrive(bar(kBarMEmpty + mr.m));
-          }
-        }
-      }
-      if (W.aborted()) break;
-    }
     }
     __syncwarp();
   }
@@ -1421,7 +1400,7 @@ cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(smla_window_kernel<kFp8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  smla_window_kernel<kFp8><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
+  smla_window_kernel<kFp8><<<ctas, kThreads, C::kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 

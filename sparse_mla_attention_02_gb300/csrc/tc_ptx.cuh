@@ -442,7 +442,7 @@ __device__ __forceinline__ void mma_pair_bf16(uint32_t d_tmem, uint64_t a_desc, 
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The same with E4M3 operands (32 values of K per instruction).
+// The same with 8-bit operands (32 values of K per instruction).
 __device__ __forceinline__ void mma_pair_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -455,6 +455,10 @@ __device__ __forceinline__ void mma_pair_e4m3(uint32_t d_tmem, uint64_t a_desc, 
 // Instruction descriptor for .kind::f8f6f4 with E4M3 A/B (K-major) and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_pair_e4m3(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// The same with E5M2 A (K-major) and E4M3 B (MN-major).
+__host__ __device__ constexpr uint32_t idesc_pair_e5m2_e4m3(int M, int N) {
+  return idesc_pair_e4m3(M, N) | (1u << 7) | (1u << 16);
 }
 // Arrive on the same mbarrier of both CTAs when all prior MMAs end.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {

@@ -57,23 +57,29 @@ class Batch:
 
 
 def dequant(cache, fmt, scale, batch):
-    """fp64 rows [S, d] of a bf16, per-tensor or per-block cache."""
+    """fp64 rows [S, d] of a bf16, per-tensor or per-block cache (and each
+    row's scale as batch.row_scale, for the tolerances)."""
+    S = cache.shape[0]
     if fmt == BF16:
+        batch.row_scale = torch.ones(S, dtype=torch.float64)
         return cache.double()
     x = cache.view(torch.float8_e4m3fn).double()
     if fmt == E4M3:
-        return x * scale.double()
-    step = batch.stride_rows or batch.block
-    return x * scale.double().repeat_interleave(step)[:x.shape[0], None]
+        batch.row_scale = scale.double().expand(S)
+    else:
+        batch.row_scale = scale.double().repeat_interleave(batch.stride_rows or batch.block)[:S]
+    return x * batch.row_scale[:, None]
 
 
 def attend(q, rows, batch, sm_scale, window, sinks):
-    """fp64 reference: (O, LSE, A, D, K) with A = sum softmax |V|, D the largest
-    sum |q k| and K the largest sum |k| of a visible key, for the tolerances."""
+    """fp64 reference: (O, LSE, A, D, K, G) with A = sum softmax |V|, D the largest
+    sum |q k| and K the largest sum |k| of a visible key, G = the largest scale
+    times the sum of the visible keys' |V| / scale, for the tolerances."""
     T, h, d = q.shape
     O = torch.zeros((T, h, 512), dtype=torch.float64)
     L = torch.full((T, h), -float("inf"), dtype=torch.float64)
-    A, D, K = torch.zeros_like(O), torch.zeros_like(L), torch.zeros_like(L)
+    A, D, K, G = torch.zeros_like(O), torch.zeros_like(L), torch.zeros_like(L), torch.zeros_like(O)
+    unit = getattr(batch, "row_scale", torch.ones(rows.shape[0], dtype=torch.float64))
     qd = q.double()
     slots = {}
     for n, r, pos in batch.tokens():
@@ -90,7 +96,8 @@ def attend(q, rows, batch, sm_scale, window, sinks):
         A[n] = w @ k[:, :512].abs()
         D[n] = (qd[n].abs() @ k.abs().T).amax(-1)
         K[n] = k.abs().sum(1).max()
-    return O, L, A, D, K
+        G[n] = (k[:, :512].abs() / unit[at][:, None]).sum(0) * unit[at].max()
+    return O, L, A, D, K, G
 
 
 def check_attention(out, lse, ref, q, fmt, sm_scale, batch, pow2=True):
@@ -100,8 +107,12 @@ def check_attention(out, lse, ref, q, fmt, sm_scale, batch, pow2=True):
     2^-10, where the row's largest value is 224 or more: 2^-17.8 of it per
     channel.  Weights: bf16 (2^-8 each, numerator and the sum that
     divides), a second rounding where the key's scale is no power of two; O is
-    rounded to bf16 once (2^-8); 2^-16 for exponentials and sums."""
-    O, L, A, D, K = ref
+    rounded to bf16 once (2^-8); 2^-16 for exponentials and sums.
+    E4M3 rows: a weight is cut to a grid of 2^-23 of 2^(t - m), t = s + log2(scale)
+    and m at most the row's largest t, so the row's sum of weight / scale is at
+    least 1 / (that key's scale) and each key's share of O is off by at most
+    2^-23 |V| / scale times that scale: together 2^-23 G."""
+    O, L, A, D, K, G = ref
     ds = 40 * 2.0 ** -23 * D * abs(sm_scale)
     if fmt != BF16:
         ds = ds + 2.0 ** -17.8 * q.double().abs().amax(-1) * K * abs(sm_scale)
@@ -115,6 +126,8 @@ def check_attention(out, lse, ref, q, fmt, sm_scale, batch, pow2=True):
     assert bool((dl <= tl).all()), f"LSE off by {float((dl - tl).max())} over its bound"
     do = (out[:n] - O[:n]).abs()
     to = 2.0 ** -8 * O[:n].abs() + (wt + 2 * ds[:n, :, None]) * A[:n]
+    if fmt != BF16:
+        to = to + 2.0 ** -23 * G[:n]
     assert bool(torch.isfinite(out[:n]).all())
     assert bool((do <= to).all()), f"O off by {float((do - to).max())} over its bound"
 
