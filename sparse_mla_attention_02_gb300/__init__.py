@@ -282,52 +282,61 @@ def _batch_args(query_start, seq_lens, block_table, block_size, block_stride_row
     """Check a ragged batch's descriptors; return the C arguments."""
     import torch
     i32 = torch.int32
-    _require(query_start.dtype == i32 and seq_lens.dtype == i32 and block_table.dtype == i32 and
-             query_start.is_contiguous() and seq_lens.is_contiguous() and
-             block_table.is_contiguous(),
-             "query_start, seq_lens and block_table must be contiguous int32 tensors")
-    _require(query_start.device == device and seq_lens.device == device and
-             block_table.device == device,
-             "query_start, seq_lens and block_table must be on the inputs' device")
-    _require(block_table.dim() == 2, "block_table must be [num_reqs, stride]")
+    if not (query_start.dtype is i32 and seq_lens.dtype is i32 and block_table.dtype is i32 and
+            query_start.is_contiguous() and seq_lens.is_contiguous() and
+            block_table.is_contiguous()):
+        raise ValueError("query_start, seq_lens and block_table must be contiguous int32 tensors")
+    if not (query_start.device == device and seq_lens.device == device and
+            block_table.device == device):
+        raise ValueError("query_start, seq_lens and block_table must be on the inputs' device")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_reqs, stride]")
     R, width = block_table.shape
-    _require(query_start.shape == (R + 1,) and seq_lens.shape == (R,),
-             "query_start must be [num_reqs + 1] and seq_lens [num_reqs]")
-    _require(block_size >= 1 and (block_stride_rows == 0 or block_stride_rows >= block_size),
-             "block_size must be positive and block_stride_rows 0 or at least block_size")
+    if query_start.shape != (R + 1,) or seq_lens.shape != (R,):
+        raise ValueError("query_start must be [num_reqs + 1] and seq_lens [num_reqs]")
+    if block_size < 1 or (block_stride_rows != 0 and block_stride_rows < block_size):
+        raise ValueError("block_size must be positive and block_stride_rows 0 or at least "
+                         "block_size")
     return (query_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), R, width,
             block_size, block_stride_rows)
 
 
-def _on_current_device(t, what):
-    """The library works on the current device: refuse tensors of another."""
+def _device_stream(t, what, stream):
+    """The raw stream of a call on tensor ``t``.  The library works on the
+    current device: tensors of another are refused."""
     import torch
-    _require(t.is_cuda and t.get_device() == torch.cuda.current_device(),
-             f"{what} must be on the current CUDA device")
+    index = t.get_device()
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError(what + " must be on the current CUDA device")
+    # (torch.cuda.current_stream() builds a Stream object, 3 us a call)
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, device):
-    """Check a paged cache and its scales; return the slot count."""
+    """Check a paged cache and its scales; return (slots, k_scale's address)."""
     import torch
-    _require(0 <= kv_dtype <= SMLA_KV_FP8_E4M3_BLOCK, "kv_dtype must be an SMLA_KV_* value")
+    if not 0 <= kv_dtype <= SMLA_KV_FP8_E4M3_BLOCK:
+        raise ValueError("kv_dtype must be an SMLA_KV_* value")
     row = DS_MLA_ROW_BYTES if kv_dtype == SMLA_KV_FP8_DS_MLA else d_qk
-    _require(kv_cache.dtype == (torch.bfloat16 if kv_dtype == SMLA_KV_BF16 else torch.uint8) and
-             kv_cache.is_contiguous() and kv_cache.device == device,
-             "kv_cache must be a contiguous tensor on the inputs' device, bfloat16 for a bf16 "
-             "cache and uint8 for the E4M3 formats")
-    have = kv_cache.numel() // row
-    S = have if num_slots is None else int(num_slots)
-    _require(S <= have, "num_slots is larger than kv_cache")
+    if not (kv_cache.dtype is (torch.bfloat16 if kv_dtype == SMLA_KV_BF16 else torch.uint8) and
+            kv_cache.is_contiguous() and kv_cache.device == device):
+        raise ValueError("kv_cache must be a contiguous tensor on the inputs' device, bfloat16 "
+                         "for a bf16 cache and uint8 for the E4M3 formats")
+    S = kv_cache.numel() // row
+    if num_slots is not None:
+        if num_slots > S:
+            raise ValueError("num_slots is larger than kv_cache")
+        S = int(num_slots)
     if kv_dtype == SMLA_KV_BF16 or kv_dtype == SMLA_KV_FP8_DS_MLA:
-        return S
-    need = {SMLA_KV_FP8_E4M3: 1, SMLA_KV_FP8_E4M3_GROUP128: S * ((d_qk + 127) // 128),
-            SMLA_KV_FP8_E4M3_GROUP4_KPE: 4 * S,
-            SMLA_KV_FP8_E4M3_BLOCK: -(-S // rows_per_scale)}[kv_dtype]
-    _require(k_scale is not None and k_scale.dtype == torch.float32 and
-             k_scale.is_contiguous() and k_scale.device == device and k_scale.numel() >= need,
-             "k_scale must be a contiguous fp32 tensor on the inputs' device with a value for "
-             "every scale of the format")
-    return S
+        return S, None
+    need = (1 if kv_dtype == SMLA_KV_FP8_E4M3 else
+            -(-S // rows_per_scale) if kv_dtype == SMLA_KV_FP8_E4M3_BLOCK else
+            4 * S if kv_dtype == SMLA_KV_FP8_E4M3_GROUP4_KPE else S * ((d_qk + 127) // 128))
+    if not (k_scale is not None and k_scale.dtype is torch.float32 and
+            k_scale.is_contiguous() and k_scale.device == device and k_scale.numel() >= need):
+        raise ValueError("k_scale must be a contiguous fp32 tensor on the inputs' device with a "
+                         "value for every scale of the format")
+    return S, k_scale.data_ptr()
 
 
 def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, block_size,
@@ -344,44 +353,50 @@ def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, b
     [N,h,64] (strided) or None, q_out likewise (None: in place).
     Returns (kv_cache, q_out)."""
     import torch
-    lib = load()
+    lib = _lib or load()
     bf16 = torch.bfloat16
-    _on_current_device(kv_c, "kv_c")
+    raw_stream = _device_stream(kv_c, "kv_c", stream)
     dev = kv_c.device
-    _require(kv_c.dtype == bf16 and kv_c.dim() == 2 and kv_c.shape[1] == 512 and
-             kv_c.stride(1) == 1, "kv_c must be a bf16 tensor [N, 512] with contiguous rows")
+    if not (kv_c.dtype is bf16 and kv_c.dim() == 2 and kv_c.shape[1] == 512 and
+            kv_c.stride(1) == 1):
+        raise ValueError("kv_c must be a bf16 tensor [N, 512] with contiguous rows")
     N = kv_c.shape[0]
-    kv_stride = kv_c.stride(0) if N > 1 else 512
+    one = N < 2                               # a single token's stride says nothing
     pe = cs = None
     pe_stride = cs_rows = 0
+    d_qk = 512
     if k_pe is not None:
-        _require(k_pe.dtype == bf16 and k_pe.shape == (N, 64) and k_pe.stride(1) == 1 and
-                 k_pe.device == dev, "k_pe must be a bf16 tensor [N, 64] with contiguous rows")
-        _require(cos_sin is not None and cos_sin.dtype == torch.float32 and
-                 cos_sin.dim() == 2 and cos_sin.shape[1] == 64 and cos_sin.is_contiguous() and
-                 cos_sin.device == dev, "cos_sin must be a contiguous fp32 tensor [positions, 64]")
-        pe, pe_stride = k_pe.data_ptr(), k_pe.stride(0) if N > 1 else 64
+        if not (k_pe.dtype is bf16 and k_pe.shape == (N, 64) and k_pe.stride(1) == 1 and
+                k_pe.device == dev):
+            raise ValueError("k_pe must be a bf16 tensor [N, 64] with contiguous rows")
+        if not (cos_sin is not None and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and
+                cos_sin.shape[1] == 64 and cos_sin.is_contiguous() and cos_sin.device == dev):
+            raise ValueError("cos_sin must be a contiguous fp32 tensor [positions, 64]")
+        d_qk = 576
+        pe, pe_stride = k_pe.data_ptr(), 64 if one else k_pe.stride(0)
         cs, cs_rows = cos_sin.data_ptr(), cos_sin.shape[0]
-    d_qk = 512 if k_pe is None else 576
     batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, dev)
-    S = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
-                    block_stride_rows or block_size, dev)
+    S, scale = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
+                           block_stride_rows or block_size, dev)
     q_args = (None, 0, 0, None, 0, 0, 0)
     if q_pe is not None:
         if q_out is None:
             q_out = q_pe
         h = q_pe.shape[1] if q_pe.dim() == 3 else 0
+        strides = []
         for x in (q_pe, q_out):
-            _require(x.dtype == bf16 and x.shape == (N, h, 64) and x.stride(2) == 1 and
-                     x.device == dev, "q_pe and q_out must be bf16 tensors [N, h, 64] with "
-                                      "contiguous channels")
-        q_args = (q_pe.data_ptr(), q_pe.stride(0) if N > 1 else 64,
-                  q_pe.stride(1) if h > 1 else 64, q_out.data_ptr(),
-                  q_out.stride(0) if N > 1 else 64, q_out.stride(1) if h > 1 else 64, h)
-    _check(lib.smla_cache_append(
-        kv_c.data_ptr(), kv_stride, pe, pe_stride, cs, cs_rows, interleaved, *q_args, *batch, N,
-        d_qk, kv_dtype, S, kv_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
-        kpe_scale, _stream(stream)), "smla_cache_append")
+            if not (x.dtype is bf16 and x.shape == (N, h, 64) and x.device == dev):
+                raise ValueError("q_pe and q_out must be bf16 tensors [N, h, 64]")
+            s0, s1, s2 = x.stride()
+            if s2 != 1:
+                raise ValueError("q_pe and q_out must have contiguous channels")
+            strides.append((x.data_ptr(), 64 if one else s0, 64 if h < 2 else s1))
+        q_args = (*strides[0], *strides[1], h)
+    code = lib.smla_cache_append(
+        kv_c.data_ptr(), 512 if one else kv_c.stride(0), pe, pe_stride, cs, cs_rows, interleaved,
+        *q_args, *batch, N, d_qk, kv_dtype, S, kv_cache.data_ptr(), scale, kpe_scale, raw_stream)
+    if code:
+        raise SmlaError(code, "smla_cache_append")
     return kv_cache, q_out
 
 
@@ -410,39 +425,48 @@ def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block
     Returns (out bf16 [T,h,512], lse f32 [T,h] or None); rows behind the last
     request are not written."""
     import torch
-    lib = load()
-    _on_current_device(q, "q")
+    lib = _lib or load()
+    raw_stream = _device_stream(q, "q", stream)
     dev = q.device
-    _require(q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_contiguous(),
-             "q must be a contiguous bf16 device tensor [T, h, d_qk]")
+    bf16 = torch.bfloat16
+    if not (q.dtype is bf16 and q.dim() == 3 and q.is_contiguous()):
+        raise ValueError("q must be a contiguous bf16 device tensor [T, h, d_qk]")
     T, h, d_qk = q.shape
     batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, dev)
-    S = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
-                    block_stride_rows or block_size, dev)
+    S, scale = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
+                           block_stride_rows or block_size, dev)
     if out is None:
-        out = torch.empty((T, h, 512), dtype=torch.bfloat16, device=dev)
-    _require(out.dtype == torch.bfloat16 and out.shape == (T, h, 512) and out.is_contiguous() and
-             out.device == dev, "out must be contiguous bf16 [T, h, 512]")
-    if lse is None and want_lse:
-        lse = torch.empty((T, h), dtype=torch.float32, device=dev)
-    _require(lse is None or (lse.dtype == torch.float32 and lse.shape == (T, h) and
-                             lse.is_contiguous() and lse.device == dev),
-             "lse must be contiguous fp32 [T, h]")
+        out = torch.empty((T, h, 512), dtype=bf16, device=dev)
+    elif not (out.dtype is bf16 and out.shape == (T, h, 512) and out.is_contiguous() and
+              out.device == dev):
+        raise ValueError("out must be contiguous bf16 [T, h, 512]")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+    elif not (lse.dtype is torch.float32 and lse.shape == (T, h) and lse.is_contiguous() and
+              lse.device == dev):
+        raise ValueError("lse must be contiguous fp32 [T, h]")
     limit = max_seq_len or 0
     if workspace is None:
+        ws = None
         nbytes = lib.smla_fwd_window_workspace_size(batch[3], T, h, d_qk, 512, kv_dtype, batch[4],
                                                     block_size, window, sinks, limit)
         if nbytes:
-            with torch.cuda.stream(stream):          # (None: the current stream)
+            if stream is None:
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            else:
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
     else:
         nbytes = workspace.numel() * workspace.element_size()
-    _check(lib.smla_fwd_window(
-        q.data_ptr(), kv_cache.data_ptr(), kv_dtype,
-        None if k_scale is None else k_scale.data_ptr(), *batch, window, sinks, limit, T, h, d_qk,
-        512, S, sm_scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream)),
-        "smla_fwd_window")
+        ws = workspace.data_ptr()
+    code = lib.smla_fwd_window(
+        q.data_ptr(), kv_cache.data_ptr(), kv_dtype, scale, *batch, window, sinks, limit, T, h,
+        d_qk, 512, S, sm_scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
+        nbytes, raw_stream)
+    if code:
+        raise SmlaError(code, "smla_fwd_window")
     return out, lse
 
 

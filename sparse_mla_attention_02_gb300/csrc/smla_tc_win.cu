@@ -32,8 +32,9 @@
 // Shared memory (bf16): Q 72 KB, K 72 KB, V 64 KB, P 16 KB.  K and V are one
 // block deep, in rings of 3 channel groups and of 4 (channel half, key half)
 // units; each part is refilled as soon as its MMAs are done, so the loads of
-// block j + 1 run under the MMAs of block j.  E4M3: Q 80 KB (two terms), K two
-// blocks of 40 KB, V 32 KB, P 24 KB (three terms).
+// block j + 1 run under the MMAs of block j.  E4M3: Q 80 KB (two terms), K 40 KB,
+// V 32 KB, P 2 x 24 KB (three terms): the weights of block j + 1 are written while
+// PV of block j runs (a second bf16 P in place of a V unit: 2 % slower).
 //
 // E4M3 rows.  Both products take the codes as they are (kind::f8f6f4, twice the
 // bf16 rate for each pass).  QK: Q is the sum of two E4M3 terms after a
@@ -78,6 +79,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "e4m3_quant.cuh"
@@ -95,7 +97,7 @@ constexpr int kBN = 128;                   // key positions per block
 constexpr int kRows = 64;                  // tile rows per CTA
 constexpr uint32_t kAtom = 8192;           // 64 rows x 128 bytes
 constexpr int kKGroups = 3;                // K ring: channel groups
-constexpr int kVUnits = 4;                 // V ring: (channel half n, key half)
+constexpr int kVUnits = 4;                 // V of a block: (channel half n, key half)
 constexpr int kMeta = 3;                   // blocks of lookups in flight
 
 // TMEM columns.
@@ -106,13 +108,13 @@ constexpr uint32_t kTmemCols = 512;
 enum {
   kBarKFull = 0,                           // [3] even CTA: both CTAs' bytes
   kBarKEmpty = kBarKFull + kKGroups,       // [3] both
-  kBarVFull = kBarKEmpty + kKGroups,       // [4] even CTA
+  kBarVFull = kBarKEmpty + kKGroups,       // [4] even CTA (a slot each)
   kBarVEmpty = kBarVFull + kVUnits,        // [4] both
   kBarSFull = kBarVEmpty + kVUnits,        // [2] both
   kBarSEmpty = kBarSFull + 2,              // [2] even CTA: 16 warps
-  kBarPFull = kBarSEmpty + 2,              // even CTA: 16 warps
-  kBarPEmpty,                              // both
-  kBarQFull,                               // even CTA
+  kBarPFull = kBarSEmpty + 2,              // [2] even CTA: 16 warps
+  kBarPEmpty = kBarPFull + 2,              // [2] both
+  kBarQFull = kBarPEmpty + 2,              // even CTA
   kBarQEmpty,                              // both
   kBarMFull,                               // [3] own
   kBarMEmpty = kBarMFull + kMeta,          // [3] own
@@ -121,8 +123,7 @@ enum {
   kBarCFull = kBarTEmpty + 2,              // [2] own: an answer of the launch control
   kBarCEmpty = kBarCFull + 2,              // [2] even CTA: both have read it
   kBarDrain = kBarCEmpty + 2,              // [2] even CTA: QK's and PV's last MMAs
-  kBarK1 = kBarDrain + 2,                  // KFull and KEmpty of a second K block
-  kNumBars = kBarK1 + 2 * kKGroups
+  kNumBars = kBarDrain + 2
 };
 
 // The bounded waits of tc_common.cuh with everything but the first try out of
@@ -181,20 +182,19 @@ struct Cfg {
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
   static constexpr int kMaxAtoms = kFp8 ? 5 : 9;        // 128-byte columns of a row
-  static constexpr int kKStages = kFp8 ? 2 : 1;         // K blocks in shared memory
+  static constexpr int kPBufs = kFp8 ? 2 : 1;
   static constexpr int kQTerms = kFp8 ? 2 : 1;
   static constexpr int kPTerms = kFp8 ? 3 : 1;
   static constexpr uint32_t kVUnit = kFp8 ? kAtom : 2 * kAtom;     // 64 keys x 128 channels
   static constexpr uint32_t kPTerm = kFp8 ? kAtom : 2 * kAtom;     // 64 rows x 128 keys
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kOffQ + kQTerms * kMaxAtoms * kAtom;
-  static constexpr uint32_t kOffV = kOffK + kKStages * kMaxAtoms * kAtom;
+  static constexpr uint32_t kOffV = kOffK + kMaxAtoms * kAtom;
   static constexpr uint32_t kOffP = kOffV + kVUnits * kVUnit;
   // row maxima [2][4][64]: bf16 (the room that is left), or fp32
-  static constexpr uint32_t kOffRed = kOffP + kPTerms * kPTerm;
+  static constexpr uint32_t kOffRed = kOffP + kPBufs * kPTerms * kPTerm;
   static constexpr uint32_t kOffBar = kOffRed + (kFp8 ? 2048 : 1024);
-  static constexpr uint32_t kOffMask = kOffBar + 8 * (((kFp8 ? kNumBars : kBarK1) + 1) & ~1);
-                                                                      // u32 [kMeta][4]
+  static constexpr uint32_t kOffMask = kOffBar + 8 * ((kNumBars + 1) & ~1);   // u32 [kMeta][4]
   static constexpr uint32_t kOffUnit = kOffMask + kMeta * 16;         // Unit [2]
   static constexpr uint32_t kOffAnswer = kOffUnit + 2 * 48;           // 16 bytes [2]
   static constexpr uint32_t kOffIds = kOffAnswer + 32;                // i32 [kMeta][128] rows
@@ -415,9 +415,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   const PairWaiter W{sb + C::kOffAbort, &p};
 
   if (tid == 0) {
-    for (int i = 0; i < 2 * kKGroups; ++i) {             // KFull and KEmpty
+    for (int i = 0; i < kKGroups; ++i) {
       mbar_init(bar(kBarKFull + i), 1);
-      if (kFp8) mbar_init(bar(kBarK1 + i), 1);
+      mbar_init(bar(kBarKEmpty + i), 1);
     }
     for (int i = 0; i < kVUnits; ++i) {
       mbar_init(bar(kBarVFull + i), 1);
@@ -426,9 +426,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarSFull + i), 1);
       mbar_init(bar(kBarSEmpty + i), 16);
+      mbar_init(bar(kBarPFull + i), 16);
+      mbar_init(bar(kBarPEmpty + i), 1);
     }
-    mbar_init(bar(kBarPFull), 16);
-    mbar_init(bar(kBarPEmpty), 1);
     mbar_init(bar(kBarQFull), kFp8 ? 16 : 1);        // E4M3: the softmax warps write Q
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(bar(kBarMFull + i), 1);
@@ -460,6 +460,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::kOffTmem);
   // The even CTA's barriers, as cluster addresses.
   auto bar0 = [&](int i) { return mapa(bar(i), 0); };
+  // Whether the block gave up, the same answer for the whole warp: lanes leave a
+  // wait at different times, and a warp that splits here would take the
+  // warp-wide instructions below apart.
+  auto stopped = [&] { return __any_sync(0xffffffffu, W.aborted()) != 0; };
   // The i-th unit's description, copied by the calling warp, which then lets it
   // go; false behind the last one (or after an abort).
   auto take_unit = [&](int i, Unit& u) {
@@ -471,7 +475,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     u.b0 = z.x; u.nb = z.y; u.split = z.z; u.live = z.w;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
-    return u.live != 0 && !W.aborted();
+    return __all_sync(0xffffffffu, u.live != 0 && !W.aborted()) != 0;
   };
   // The same in place, for a warp that lets it go itself, at the unit's end.
   auto peek_unit = [&](int i) {
@@ -483,7 +487,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   // Descriptors advance by constants (16-byte units).
   if (warp == 0) {
     // ---- QK issuer (even CTA): runs up to two blocks ahead of the softmax ----
-    if (r == 0) {
+    // (Tests that stall it: no scores arrive at all.  Leaving out one block's alone
+    // would let the next one's wait pass on the phase before its own.)
+    if (r == 0 && !p.inject_stall) {
       const uint32_t id = kFp8 ? idesc_pair_e4m3(128, kBN) : idesc_bf16(128, kBN, false, false);
       const uint64_t dq = sdesc(sb + C::kOffQ, 16, 1024, kLayoutSw128);
       const uint64_t dk = sdesc(sb + C::kOffK, 16, 1024, kLayoutSw128);
@@ -491,13 +497,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       for (int i = 0, q = 0, J = 0; take_unit(i, u); ++i) {
        if (u.nb > 0) W.wait(bar(kBarQFull), q++ & 1);
        for (int j = 0; j < u.nb; ++j, ++J) {
-        if (p.inject_stall && j == 0) continue;      // tests: these scores never arrive
         if (J >= 2) W.wait(bar(kBarSEmpty + (J & 1)), ((J >> 1) - 1) & 1);
+        if (stopped()) break;
         const uint32_t dS = tmem + kColS + 64 * (J & 1);
-        const int st = J % C::kKStages, kph = (J / C::kKStages) & 1;
 #pragma unroll 1
-        for (int g = kBarK1 * st, c = 0; c < a.atoms; ++g) {
-          W.wait(bar(kBarKFull + g), kph);
+        for (int g = 0, c = 0; c < a.atoms; ++g) {
+          W.wait(bar(kBarKFull + g), J & 1);
           __syncwarp();
           tc_fence_after();
           const int c1 = min(c + C::kAtomsPerGroup, a.atoms);
@@ -505,7 +510,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll 1
             for (int cc = c; cc < c1; ++cc) {
               const uint64_t ad = dq + (uint32_t)cc * (kAtom >> 4);
-              const uint64_t bd = dk + (uint32_t)(cc + st * C::kMaxAtoms) * (kAtom >> 4);
+              const uint64_t bd = dk + (uint32_t)cc * (kAtom >> 4);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 if (kFp8) {
@@ -530,9 +535,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
        }
       }
       // Every MMA issued here has completed (also after an abort) before
-      // either CTA frees its TMEM or leaves its tiles.
+      // either CTA frees its TMEM or leaves its tiles.  (Signalled to this CTA
+      // alone: nothing may be on its way to the other when it leaves.)
       __syncwarp();
-      if (elect_one()) mma_commit_pair(bar(kBarDrain));
+      if (elect_one()) mma_commit_pair(bar(kBarDrain), 1);
       __syncwarp();
       W.drain(bar(kBarDrain), 0);
     }
@@ -545,7 +551,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       Unit u;
       for (int i = 0, J = 0; take_unit(i, u); ++i) {
        for (int j = 0; j < u.nb; ++j, ++J) {
-        W.wait(bar(kBarPFull), J & 1);
+        const int pb = J % C::kPBufs;
+        W.wait(bar(kBarPFull + pb), (J / C::kPBufs) & 1);
+        if (stopped()) break;
+        const uint64_t dpj = dp + (uint32_t)pb * (C::kPTerms * C::kPTerm >> 4);
 #pragma unroll 1
         for (int v = 0; v < kVUnits; ++v) {          // v = 2 n + key half
           W.wait(bar(kBarVFull + v), J & 1);
@@ -556,7 +565,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             const uint64_t bd = dv + (uint32_t)v * (C::kVUnit >> 4);
             const uint32_t keep = (j > 0 || (v & 1)) ? 1u : 0u;
             if (kFp8) {
-              const uint64_t ad = dp + (uint32_t)(v & 1) * 4;    // 64 keys = 64 bytes
+              const uint64_t ad = dpj + (uint32_t)(v & 1) * 4;    // 64 keys = 64 bytes
 #pragma unroll
               for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -564,20 +573,20 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
                   mma_pair_e4m3(dO, ad + 2 * ks + x * (C::kPTerm >> 4), bd + 256 * ks, id,
                                 (keep || ks > 0 || x > 0) ? 1u : 0u);
             } else {
-              const uint64_t ad = dp + (uint32_t)(v & 1) * (kAtom >> 4);
+              const uint64_t ad = dpj + (uint32_t)(v & 1) * (kAtom >> 4);
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 mma_pair_bf16(dO, ad + 2 * ks, bd + 128 * ks, id, (keep || ks > 0) ? 1u : 0u);
             }
             mma_commit_pair(bar(kBarVEmpty + v));
-            if (v == kVUnits - 1) mma_commit_pair(bar(kBarPEmpty));
+            if (v == kVUnits - 1) mma_commit_pair(bar(kBarPEmpty + pb));
           }
           __syncwarp();
         }
        }
       }
       __syncwarp();
-      if (elect_one()) mma_commit_pair(bar(kBarDrain + 1));
+      if (elect_one()) mma_commit_pair(bar(kBarDrain + 1), 1);
       __syncwarp();
       W.drain(bar(kBarDrain + 1), 0);
     }
@@ -593,7 +602,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     for (int i = 0; take_unit(i, u); ++i) {
      if (!kFp8 && u.nb > 0) {
       if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
-      if (W.aborted()) break;
+      if (stopped()) break;
       if (lane == 0) {
         if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
 #pragma unroll 1
@@ -612,30 +621,31 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
       const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
       const uint32_t full = __ballot_sync(0xffffffffu, all4) & 0xFFFFu;
-      const int st = J % C::kKStages, kph = (J / C::kKStages) & 1, g0 = kBarK1 * st;
-      const uint32_t ktile = sb + C::kOffK + st * C::kMaxAtoms * kAtom;
+      const uint32_t ktile = sb + C::kOffK;
       if (a.box == 64 && full == 0xFFFFu) {            // the 64 rows of one block, all seen
         if (lane == 0) {
 #pragma unroll 1
           for (int g = 0; g < groups; ++g) {
-            if (J >= C::kKStages) W.wait(bar(kBarKEmpty + g0 + g), kph ^ 1);
-            if (W.aborted()) break;
+            if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
+            if (W.aborted()) break;                    // (one lane)
             const int c0 = g * C::kAtomsPerGroup;
-            const uint32_t bytes = (uint32_t)min(C::kAtomsPerGroup, a.atoms - c0) * kAtom;
-            if (r == 0) mbar_arrive_expect_tx(bar(kBarKFull + g0 + g), 2u * bytes);
             const uint32_t dst = ktile + c0 * kAtom;
-            if (bytes == C::kAtomsPerGroup * kAtom)
-              tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * (g0 + g));
+            // E4M3 rows of 576 end in half a column, which the map of whole
+            // columns leaves out.  bf16: a column past a row of 512 reads zeros
+            // into the tile's spare atom.
+            const bool half = kFp8 && c0 + 1 == a.atoms;
+            if (r == 0)
+              mbar_arrive_expect_tx(bar(kBarKFull + g),
+                                    2u * (half ? 1u : (uint32_t)C::kAtomsPerGroup) * kAtom);
+            if (half)
+              tma_load_2d_pair(dst, &a.box_map, cols * c0, id.x, kfull0 + 8u * g);
             else
-#pragma unroll 1
-              for (int c = c0; c < a.atoms; ++c)
-                tma_load_2d_pair(dst + (c - c0) * kAtom, &a.box_map, cols * c, id.x,
-                                 kfull0 + 8u * (g0 + g));
+              tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * g);
             ++issued;
           }
         }
         __syncwarp();
-        if (W.aborted()) break;
+        if (stopped()) break;
         continue;
       }
       // lanes of this lane's box, all seen and allocated: one copy for the box
@@ -644,47 +654,45 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const bool boxed = per && (full & mine) == mine;
 #pragma unroll 1
       for (int g = 0; g < groups; ++g) {
-        if (J >= C::kKStages) W.wait(bar(kBarKEmpty + g0 + g), kph ^ 1);
-        if (W.aborted()) break;
-        const int c0 = g * C::kAtomsPerGroup, c1 = min(c0 + C::kAtomsPerGroup, a.atoms);
+        if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
+        if (stopped()) break;
+        const int c0 = g * C::kAtomsPerGroup;
+        // (as many columns as the other CTA's whole groups have)
+        const int c1 = kFp8 ? min(c0 + C::kAtomsPerGroup, a.atoms) : c0 + C::kAtomsPerGroup;
         if (r == 0 && lane == 0)
-          mbar_arrive_expect_tx(bar(kBarKFull + g0 + g), 2u * (uint32_t)(c1 - c0) * kAtom);
+          mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * (uint32_t)(c1 - c0) * kAtom);
         __syncwarp();
         if (lane < 16 && (!boxed || (lane & (per - 1)) == 0)) {
 #pragma unroll 1
           for (int c = c0; c < c1; ++c) {
             const uint32_t dst = ktile + c * kAtom + 4 * lane * 128;
             if (boxed)
-              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, kfull0 + 8u * (g0 + g));
+              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, kfull0 + 8u * g);
             else
               tma_gather4_pair(dst, &a.row_map, cols * c, id.x, id.y, id.z, id.w,
-                               kfull0 + 8u * (g0 + g));
+                               kfull0 + 8u * g);
           }
         }
         ++issued;
         __syncwarp();
       }
-      if (W.aborted()) break;
+      if (stopped()) break;
      }
     }
     // Teardown: the last copies into each part have landed in both CTAs (the
     // even CTA's barriers count both; earlier ones were consumed).
     if (r == 0 && lane == 0) {
       if (q > 0) W.drain(bar(kBarQFull), (q - 1) & 1);
-      // (copy number x went to group x % groups of block x / groups)
 #pragma unroll 1
-      for (int x = max(issued - C::kKStages * groups, 0); x < issued; ++x) {
-        const int blk = x / groups;
-        W.drain(bar(kBarKFull + kBarK1 * (blk % C::kKStages) + x % groups),
-                (blk / C::kKStages) & 1);
-      }
+      for (int g = 0; g < groups && g < issued; ++g)
+        W.drain(bar(kBarKFull + g), ((issued - 1 - g) / groups) & 1);
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---- V loads: this CTA's channels of all 128 keys -------------------------
     {
       const uint32_t vfull0 = bar0(kBarVFull);
-      int issued = 0, J = 0;
+      int issued = 0, J = 0;                         // (units loaded, in order)
       MetaRing mr;
       Unit u;
       for (int i = 0; take_unit(i, u); ++i) {
@@ -695,44 +703,27 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
         const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
         const uint32_t full = __ballot_sync(0xffffffffu, all4);
-        if (a.box == 64 && full == ~0u) {              // two whole blocks
-          const int y1 = __shfl_sync(0xffffffffu, id.x, 16);
-          if (lane == 0) {
-#pragma unroll 1
-            for (int v = 0; v < kVUnits; ++v) {
-              if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
-              if (W.aborted()) break;
-              if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
-              if (kFp8)
-                tma_load_2d_pair(sb + C::kOffV + v * C::kVUnit, &a.box_map,
-                                 256 * (v >> 1) + 128 * (int)r, v & 1 ? y1 : id.x,
-                                 vfull0 + 8u * v);
-              else
-                tma_load_3d_pair(sb + C::kOffV + v * C::kVUnit, &a.v_map, 0, v & 1 ? y1 : id.x,
-                                 4 * (v >> 1) + 2 * (int)r, vfull0 + 8u * v);
-              ++issued;
-            }
-          }
-          __syncwarp();
-          if (W.aborted()) break;
-          continue;
-        }
+        // The 16 lanes of a key half: one copy by its first lane where the half is
+        // one piece of a cache block, a box per lane group, or four rows per lane.
         const int per = a.box >> 2;
         const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
         const bool boxed = per && (full & mine) == mine;
 #pragma unroll 1
         for (int v = 0; v < kVUnits; ++v) {
           if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
-          if (W.aborted()) break;
+          if (stopped()) break;
           if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
           __syncwarp();
+          const uint32_t full_bar = vfull0 + 8u * v;
+          const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
           if ((lane >> 4) == (v & 1) && (!boxed || (lane & (per - 1)) == 0)) {
-            const uint32_t full_bar = vfull0 + 8u * v;
             const int ch = 256 * (v >> 1) + 128 * (int)r;
+            const bool one = !kFp8 && boxed && per == 16;
+            if (one)
+              tma_load_3d_pair(slot, &a.v_map, 0, id.x, ch / 64, full_bar);
 #pragma unroll 1
-            for (int c = 0; c < (int)(C::kVUnit / kAtom); ++c) {
-              const uint32_t dst = sb + C::kOffV + v * C::kVUnit + c * kAtom +
-                                   4 * (lane & 15) * 128;
+            for (int c = 0; !one && c < (int)(C::kVUnit / kAtom); ++c) {
+              const uint32_t dst = slot + c * kAtom + 4 * (lane & 15) * 128;
               if (boxed)
                 tma_load_2d_pair(dst, &a.box_map, ch + 64 * c, id.x, full_bar);
               else
@@ -742,7 +733,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           ++issued;
           __syncwarp();
         }
-        if (W.aborted()) break;
+        if (stopped()) break;
        }
       }
       if (r == 0 && lane == 0)
@@ -804,6 +795,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     int i = 0;                                         // units described
     auto publish = [&](const Unit& x) {
       if (i >= 2) W.wait(bar(kBarTEmpty + (i & 1)), ((i >> 1) - 1) & 1);
+      if (stopped()) return;                           // (the slot may still be in use)
       int4* dst = reinterpret_cast<int4*>(sm + C::kOffUnit + 48 * (i & 1));
       if (lane == 0) {
         dst[0] = make_int4(x.row0, x.row1, x.p_last, x.r);
@@ -817,7 +809,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     int64_t unit = (int64_t)(blockIdx.x >> 1);
     bool pending = false;                              // an answer is on its way
     int n = 0;                                         // answers read
-    while (!W.aborted()) {
+    while (!stopped()) {
       // Ask for the next unit before this one is worked on.
       const uint32_t cfull = bar(kBarCFull + (n & 1));
       const uint32_t answer = sb + C::kOffAnswer + 16 * (n & 1);
@@ -886,7 +878,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           for (int c = 0; c < p.d_qk * C::kElem / 128; c += C::kAtomsPerGroup)
             tma_prefetch_3d(&a.k_map, 0, id[0], c);
         if (J >= kMeta) W.wait(bar(kBarMEmpty + m), mr.ph ^ 1);
-        if (W.aborted()) break;
+        if (stopped()) break;
         __syncwarp();
         uint32_t nib = 0;
 #pragma unroll
@@ -908,7 +900,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (lane == 0) mbar_arrive(bar(kBarMFull + m));
       }
       W.wait(cfull, (n >> 1) & 1);
-      if (W.aborted()) break;
+      if (stopped()) break;
       pending = false;
       int first;
       const bool taken = cluster_taken(answer, first);
@@ -943,7 +935,8 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     int J = 0;
     for (int i = 0;; ++i) {
     const Unit* t = peek_unit(i);
-    if (!t->live || W.aborted()) break;
+    // (all eight warps leave together: they share the named barriers below)
+    if (named_bar_or(4, 256, !t->live || W.aborted())) break;
     int pos = -1, lo = 0;                              // the row's token sees [lo, pos], sinks
     {
       const int g = t->row0 + 64 * (int)r + row;
@@ -1162,26 +1155,27 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       lr_run = lr_run * alpha + lr;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));   // the lookups were read
-      if (j >= 1) {
-        W.wait(bar(kBarPEmpty), (J - 1) & 1);    // PV(j - 1) is done
+      if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);  // PV(j - 1)
         __syncwarp();
         tc_fence_after();
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 128 * wg; c < 128 * wg + 128; c += 16) {
-            uint32_t w[16];
-            tmem_ld16(tmem + lane_base + kColO + c, w);
-            tmem_wait_ld();
+        for (int c = 128 * wg; c < 128 * wg + 128; c += 16) {
+          uint32_t w[16];
+          tmem_ld16(tmem + lane_base + kColO + c, w);
+          tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
-            tmem_st16(tmem + lane_base + kColO + c, w);
-          }
-          tmem_wait_st();
+          for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
+          tmem_st16(tmem + lane_base + kColO + c, w);
         }
+        tmem_wait_st();
       }
+      const int pb = J % C::kPBufs;
+      if (J >= C::kPBufs)                                // the buffer was read
+        W.wait(bar(kBarPEmpty + pb), (J / C::kPBufs - 1) & 1);
       // P row: bf16, keys 64 half + 32 wg .. + 31 as chunks 4 wg .. of atom `half`;
       // E4M3, bytes 32 seg .. + 31 of each term's row.
-      uint8_t* prow = sm + C::kOffP + row * 128;
+      uint8_t* prow = sm + C::kOffP + pb * (C::kPTerms * C::kPTerm) + row * 128;
       const uint32_t sw = (uint32_t)row & 7u;
       if constexpr (kFp8) {
 #pragma unroll
@@ -1200,12 +1194,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_signal_remote(pfull);
+      if (lane == 0) mbar_signal_remote(pfull + 8u * pb);
     }
 
     // ---- epilogue -------------------------------------------------------------
     if (nb > 0) {
-      W.wait(bar(kBarPEmpty), (J - 1) & 1);
+      W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);
       __syncwarp();
       tc_fence_after();
     }
@@ -1301,19 +1295,25 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   }
 
   // ---- teardown: both CTAs are done with each other's barriers, tiles and
-  // TMEM (the even CTA drained the MMAs and the pair's copies above).  After an
-  // abort the CTAs may have issued different copies, whose barriers then tell
-  // nothing: 100 us let what is in flight land.
-  if (tid == 0 && W.aborted()) {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 100000u) {
-    }
-  }
+  // TMEM (the even CTA drained the MMAs and the pair's copies above).  Where one
+  // gave up, the two may have issued different copies (the signals of an aborted
+  // issuer let the other CTA's loaders go on), whose barriers then tell nothing,
+  // and a copy must not outlive the CTA that holds its barrier: a CTA that gave up
+  // says so to the other, and both wait 100 us for what is in flight.
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && W.aborted()) st_cluster_s32(mapa(sb + C::kOffAbort, r ^ 1u), 1);
   __syncwarp();
   cluster_arrive();
   cluster_wait();
+  if (W.aborted()) {                                   // (the same in both CTAs)
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000u) {
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == 0) {
     __syncwarp();
     tc_fence_after();
@@ -1397,9 +1397,17 @@ cudaError_t encode_columns(CUtensorMap* map, bool fp8, const void* base, int d, 
 template <bool kFp8>
 cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   using C = Cfg<kFp8>;
-  cudaError_t e = cudaFuncSetAttribute(smla_window_kernel<kFp8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  // (once per device: the attribute call costs as much as a launch)
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+    e = cudaFuncSetAttribute(smla_window_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   smla_window_kernel<kFp8><<<ctas, kThreads, C::kSmem, stream>>>(a);
   return cudaGetLastError();
 }
@@ -1459,7 +1467,7 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
     if (p.b.block_size == 1 << k) a.shift = k;
   a.wide = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
   cudaError_t e = encode_rows(&a.row_map, fp8, p.kv, p.d_qk, p.b.num_slots, 1);
-  if (e == cudaSuccess && a.box)
+  if (e == cudaSuccess && a.box && (fp8 || a.box < 64))
     e = encode_rows(&a.box_map, fp8, p.kv, p.d_qk, p.b.num_slots, a.box);
   if (e == cudaSuccess && a.box == 64)
     e = encode_columns(&a.k_map, fp8, p.kv, p.d_qk, p.b.num_slots, fp8 ? 2 : 3);

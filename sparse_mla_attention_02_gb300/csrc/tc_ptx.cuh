@@ -119,6 +119,11 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   return r;
 }
 
+// Write a word of a cluster's shared memory (address from mapa).
+__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // TMA gather: four rows (y0..y3) of a 2-D tensor map, one box of columns
 // starting at x each, into four consecutive 128-byte rows at dst; the bytes
 // are counted on the mbarrier (complete_tx).  Out-of-range rows read zeros.
@@ -460,13 +465,13 @@ __host__ __device__ constexpr uint32_t idesc_pair_e4m3(int M, int N) {
 __host__ __device__ constexpr uint32_t idesc_pair_e5m2_e4m3(int M, int N) {
   return idesc_pair_e4m3(M, N) | (1u << 7) | (1u << 16);
 }
-// Arrive on the same mbarrier of both CTAs when all prior MMAs end.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  const uint16_t both = 3;
+// Arrive on the same mbarrier of the CTAs in `mask` (default: both) when all
+// prior MMAs end.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(bar),
-      "h"(both)
+      "h"(mask)
       : "memory");
 }
 // TMA loads into this CTA's shared memory whose bytes are counted on an
