@@ -71,7 +71,8 @@
 // the even CTA; two issuers, so that the waits of one are covered by the MMAs of
 // the other); warps 1 and 2 load K and V; warp 3 takes units and looks up
 // each block's rows (validity, scales, row ids); warps 4..11 are the softmax: four threads per
-// row (TMEM lane half x column half), 32 keys each.
+// row (TMEM lane half x column half), 32 keys each; with E4M3 rows warps 13..15
+// split Q.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -123,7 +124,8 @@ enum {
   kBarCFull = kBarTEmpty + 2,              // [2] own: an answer of the launch control
   kBarCEmpty = kBarCFull + 2,              // [2] even CTA: both have read it
   kBarDrain = kBarCEmpty + 2,              // [2] even CTA: QK's and PV's last MMAs
-  kNumBars = kBarDrain + 2
+  kBarQScale = kBarDrain + 2,              // own, E4M3: the Q rows' scales are written
+  kNumBars
 };
 
 // The bounded waits of tc_common.cuh with everything but the first try out of
@@ -174,11 +176,11 @@ struct Unit {
 };
 static_assert(sizeof(Unit) == 48, "three 16-byte words");
 
-constexpr int kThreads = 416;              // 13 warps
 constexpr int kWarpPv = 12;                // issues PV
 
 template <bool kFp8>
 struct Cfg {
+  static constexpr int kThreads = kFp8 ? 512 : 416;
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
   static constexpr int kMaxAtoms = kFp8 ? 5 : 9;        // 128-byte columns of a row
@@ -194,18 +196,19 @@ struct Cfg {
   // row maxima [2][4][64]: bf16 (the room that is left), or fp32
   static constexpr uint32_t kOffRed = kOffP + kPBufs * kPTerms * kPTerm;
   static constexpr uint32_t kOffBar = kOffRed + (kFp8 ? 2048 : 1024);
-  static constexpr uint32_t kOffMask = kOffBar + 8 * ((kNumBars + 1) & ~1);   // u32 [kMeta][4]
+  static constexpr uint32_t kOffMask = kOffBar + 8 * (((kFp8 ? kNumBars : kBarQScale) + 1) & ~1);
+                                                                      // u32 [kMeta][4]
   static constexpr uint32_t kOffUnit = kOffMask + kMeta * 16;         // Unit [2]
   static constexpr uint32_t kOffAnswer = kOffUnit + 2 * 48;           // 16 bytes [2]
   static constexpr uint32_t kOffIds = kOffAnswer + 32;                // i32 [kMeta][128] rows
   static constexpr uint32_t kOffTmem = kOffIds + kMeta * kBN * 4;
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
   // E4M3: the keys' scales, each 32 keys' common scale (0: several), its log2
-  // and its reciprocal, the Q rows' scales
+  // and its reciprocal, the Q rows' scales (two units')
   static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 8 + 15) & ~15u : kOffAbort + 8;
   static constexpr uint32_t kOffSeg = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);   // float4 [kMeta][4]
   static constexpr uint32_t kOffQScale = kOffSeg + (kFp8 ? kMeta * 64 : 0);
-  static constexpr uint32_t kSmem = kOffQScale + (kFp8 ? kRows * 4 : 0);
+  static constexpr uint32_t kSmem = kOffQScale + (kFp8 ? 2 * kRows * 4 : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 // The epilogue's areas in P: row sums and flags.
@@ -402,7 +405,7 @@ __device__ __forceinline__ void slow_row(const WinParams& p, const Unit& t, int6
 }
 
 template <bool kFp8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
 smla_window_kernel(const __grid_constant__ WinArgs a) {
   using C = Cfg<kFp8>;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -429,7 +432,8 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       mbar_init(bar(kBarPFull + i), 16);
       mbar_init(bar(kBarPEmpty + i), 1);
     }
-    mbar_init(bar(kBarQFull), kFp8 ? 16 : 1);        // E4M3: the softmax warps write Q
+    mbar_init(bar(kBarQFull), kFp8 ? 6 : 1);         // E4M3: three warps of both CTAs write Q
+    if (kFp8) mbar_init(bar(kBarQScale), 3);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(bar(kBarMFull + i), 1);
       mbar_init(bar(kBarMEmpty + i), 10);              // softmax, loaders
@@ -437,7 +441,8 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     mbar_init(bar(kBarQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarTFull + i), 1);
-      mbar_init(bar(kBarTEmpty + i), 10 + (r == 0 ? 2 : 0));   // those, the even CTA's issuers
+      // those, the even CTA's issuers, E4M3: the warps that split Q
+      mbar_init(bar(kBarTEmpty + i), 10 + (r == 0 ? 2 : 0) + (kFp8 ? 3 : 0));
       mbar_init(bar(kBarCFull + i), 1);
       mbar_init(bar(kBarCEmpty + i), 2);
     }
@@ -932,7 +937,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // One scale per tensor multiplies every score and the output.
     const float kscale = p.kv_format == kE4m3 ? __ldg(p.k_scale) : 1.f;
     MetaRing mr;
-    int J = 0;
+    int J = 0, q = 0;                                  // blocks, units with blocks
     for (int i = 0;; ++i) {
     const Unit* t = peek_unit(i);
     // (all eight warps leave together: they share the named barriers below)
@@ -946,66 +951,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const int nb = t->nb;
     float qs = 1.f;
     if (kFp8 && nb > 0) {
-      // Q rows -> two E4M3 terms under a power-of-two scale; eight lanes a row.
-      const int st = tid - 128, j8 = st & 7;
-      const uint32_t gmask = 0xFFu << (lane & 24);
-      float* qscale = reinterpret_cast<float*>(sm + C::kOffQScale);
-      const int nch = p.d_qk / 64;
-      for (int rr = st >> 3; rr < kRows; rr += 32) {
-        const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) + (gr < t->row1 ? gr : t->row0) * p.d_qk) + j8;
-        // (read twice, for the largest value and for the codes: registers)
-        float amax = 0.f;
-#pragma unroll 3
-        for (int c = 0; c < nch; ++c) {
-          const uint4 v = gr < t->row1 ? __ldg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = max3(amax, fabsf(__uint_as_float(w[e] << 16)),
-                        fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
-        }
-#pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, o));
-        // 2^k with amax 2^k in [224, 448): amax = m 2^e, 1 <= m < 2, k = 8 - e
-        // (m < 1.75) or 7 - e; kept within what 2^-k can hold
-        const uint32_t u = __float_as_uint(amax);
-        int k = 8 - ((int)(u >> 23) - 127) - ((u & 0x7FFFFFu) >= 0x600000u ? 1 : 0);
-        k = amax == 0.f ? 0 : min(max(k, -120), 120);
-        const float up = __uint_as_float((uint32_t)(k + 127) << 23);
-        if (j8 == 0)                                   // (an infinite q: NaN scores)
-          qscale[rr] = amax < INFINITY ? __uint_as_float((uint32_t)(127 - k) << 23) : NAN;
-#pragma unroll 3
-        for (int c = 0; c < 2 * a.atoms; ++c) {        // 64-channel pieces; a tenth is padding
-          const uint4 v = c < nch && gr < t->row1 ? __ldg(src + 8 * c)
-                                                 : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t hi[2], lw[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x[4], y0, y1, y2, y3;
-            x[0] = __uint_as_float(w[2 * e] << 16) * up;
-            x[1] = __uint_as_float(w[2 * e] & 0xFFFF0000u) * up;
-            x[2] = __uint_as_float(w[2 * e + 1] << 16) * up;
-            x[3] = __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * up;
-            hi[e] = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
-            e4m3x4_to_f32(hi[e], y0, y1, y2, y3);
-            lw[e] = e4m3x2(x[0] - y0, x[1] - y1) | (e4m3x2(x[2] - y2, x[3] - y3) << 16);
-          }
-          // channel 64 c + 8 j8: atom c / 2, 16-byte chunk 4 (c % 2) + j8 / 2
-          const uint32_t off = (uint32_t)(c >> 1) * kAtom + (uint32_t)rr * 128u +
-                               (((4u * (c & 1) + (j8 >> 1)) ^ ((uint32_t)rr & 7u)) << 4) +
-                               8u * (j8 & 1);
-          *reinterpret_cast<uint2*>(sm + C::kOffQ + off) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(sm + C::kOffQ + C::kMaxAtoms * kAtom + off) =
-              make_uint2(lw[0], lw[1]);
-        }
-      }
-      fence_proxy_async_smem();
-      named_bar_sync(1, 256);                          // the rows' scales are set
-      if (lane == 0) mbar_signal_remote(bar0(kBarQFull));
-      qs = qscale[row];
+      W.wait(bar(kBarQScale), q & 1);
+      qs = reinterpret_cast<const float*>(sm + C::kOffQScale)[kRows * (q & 1) + row];
+      ++q;
     }
     const float scale = a.scale_log2 * qs * kscale;
     float m_run = -INFINITY;   // running max (log2 units), the same in a row's four threads
@@ -1229,37 +1177,42 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
     bool odd = false;                                    // an output that is not finite
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 16) {
-      uint32_t w[16];
+    for (int c4 = 0; c4 < 128; c4 += 32) {               // (32 columns per TMEM wait)
+      uint32_t wide[2][16];
       __syncwarp();
       if (nb > 0) {
-        tmem_ld16(tmem + lane_base + kColO + 128 * wg + c, w);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          tmem_ld16(tmem + lane_base + kColO + 128 * wg + c4 + 16 * x, wide[x]);
         tmem_wait_ld();
       }
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float o = empty ? 0.f : __uint_as_float(w[k]) * inv;
-        odd |= !(fabsf(o) < INFINITY);
-        w[k] = __float_as_uint(o);
-      }
-      if (!live) continue;
-      if (partial) {
-        if (!empty) {
+      for (int x = 0; x < 2; ++x) {
+        uint32_t (&w)[16] = wide[x];
+        const int c = c4 + 16 * x;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float o = empty ? 0.f : __uint_as_float(w[k]) * inv;
+          odd |= !(fabsf(o) < INFINITY);
+          w[k] = __float_as_uint(o);
+        }
+        if (live && partial && !empty) {
           uint32_t* dst = reinterpret_cast<uint32_t*>(p.o_part + prow_g * 512 + ch0 + c);
           st_global_32(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
           st_global_32(dst + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
         }
-      } else {
-        uint32_t b[8];
+        if (live && !partial) {
+          uint32_t b[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          b[k] = pack_bf16(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
-        uint32_t* dst = reinterpret_cast<uint32_t*>(out + g * 512 + ch0 + c);
-        if (a.wide) {
-          st_global_32(dst, b[0], b[1], b[2], b[3], b[4], b[5], b[6], b[7]);
-        } else {
-          reinterpret_cast<uint4*>(dst)[0] = make_uint4(b[0], b[1], b[2], b[3]);
-          reinterpret_cast<uint4*>(dst)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+          for (int k = 0; k < 8; ++k)
+            b[k] = pack_bf16(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+          uint32_t* dst = reinterpret_cast<uint32_t*>(out + g * 512 + ch0 + c);
+          if (a.wide) {
+            st_global_32(dst, b[0], b[1], b[2], b[3], b[4], b[5], b[6], b[7]);
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+          }
         }
       }
     }
@@ -1290,6 +1243,83 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
+    }
+    __syncwarp();
+  } else if (kFp8) {
+    // ---- Q rows -> two E4M3 terms under a power-of-two scale ------------------
+    // Eight lanes a row; the next unit's rows are split while the last blocks of
+    // the one before are still in the softmax.
+    const int j8 = lane & 7, g0 = 4 * (warp - 13) + (lane >> 3);   // of 12 groups
+    const uint32_t gmask = 0xFFu << (lane & 24);
+    const int nch = p.d_qk / 64;
+    Unit u;
+    for (int i = 0, q = 0; take_unit(i, u); ++i) {
+      if (u.nb <= 0) continue;
+      if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
+      __syncwarp();
+      float* qscale = reinterpret_cast<float*>(sm + C::kOffQScale) + kRows * (q & 1);
+#pragma unroll 1
+      for (int rr = g0; rr < kRows; rr += 12) {
+        const int64_t gr = (int64_t)u.row0 + 64 * (int)r + rr;
+        const bool have = gr < u.row1;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) + (have ? gr : u.row0) * p.d_qk) + j8;
+        uint4 raw[9];
+#pragma unroll
+        for (int c = 0; c < 9; ++c)
+          raw[c] = have && c < nch ? __ldg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < 9; ++c) {
+          const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            amax = max3(amax, fabsf(__uint_as_float(w[e] << 16)),
+                        fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
+        }
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, o));
+        // 2^k with amax 2^k in [224, 448): amax = m 2^e, 1 <= m < 2, k = 8 - e
+        // (m < 1.75) or 7 - e; kept within what 2^-k can hold
+        const uint32_t bits = __float_as_uint(amax);
+        int k = 8 - ((int)(bits >> 23) - 127) - ((bits & 0x7FFFFFu) >= 0x600000u ? 1 : 0);
+        k = amax == 0.f ? 0 : min(max(k, -120), 120);
+        const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+        if (j8 == 0)                                   // (an infinite q: NaN scores)
+          qscale[rr] = amax < INFINITY ? __uint_as_float((uint32_t)(127 - k) << 23) : NAN;
+#pragma unroll
+        for (int c = 0; c < 10; ++c) {                 // 64-channel pieces; a tenth is padding
+          if (c >= 2 * a.atoms) break;
+          const uint4 v = c < 9 ? raw[c < 9 ? c : 0] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t hi[2], lw[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x[4], y0, y1, y2, y3;
+            x[0] = __uint_as_float(w[2 * e] << 16) * up;
+            x[1] = __uint_as_float(w[2 * e] & 0xFFFF0000u) * up;
+            x[2] = __uint_as_float(w[2 * e + 1] << 16) * up;
+            x[3] = __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * up;
+            hi[e] = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
+            e4m3x4_to_f32(hi[e], y0, y1, y2, y3);
+            lw[e] = e4m3x2(x[0] - y0, x[1] - y1) | (e4m3x2(x[2] - y2, x[3] - y3) << 16);
+          }
+          // channel 64 c + 8 j8: atom c / 2, 16-byte chunk 4 (c % 2) + j8 / 2
+          const uint32_t off = (uint32_t)(c >> 1) * kAtom + (uint32_t)rr * 128u +
+                               (((4u * (c & 1) + (j8 >> 1)) ^ ((uint32_t)rr & 7u)) << 4) +
+                               8u * (j8 & 1);
+          *reinterpret_cast<uint2*>(sm + C::kOffQ + off) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(sm + C::kOffQ + C::kMaxAtoms * kAtom + off) =
+              make_uint2(lw[0], lw[1]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kBarQScale));
+        mbar_signal_remote(bar0(kBarQFull));
+      }
+      ++q;
     }
     __syncwarp();
   }
@@ -1408,7 +1438,7 @@ cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  smla_window_kernel<kFp8><<<ctas, kThreads, C::kSmem, stream>>>(a);
+  smla_window_kernel<kFp8><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
