@@ -142,7 +142,9 @@ struct PairWaiter {
     asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(flags) : "memory");
     return v != 0;
   }
-  __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) const;
+  // false: gave up (the block is aborting).  A lane whose wait came true need not
+  // look at the flag.
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const;
   __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const;
 };
 
@@ -155,8 +157,10 @@ static __device__ __noinline__ void pair_wait_slow(uint32_t bar, uint32_t parity
   else
     slow.wait(bar, parity);
 }
-__device__ __forceinline__ void PairWaiter::wait(uint32_t bar, uint32_t parity) const {
-  if (__builtin_expect(!mbar_try_wait(bar, parity), 0)) pair_wait_slow(bar, parity, flags, p, false);
+__device__ __forceinline__ bool PairWaiter::wait(uint32_t bar, uint32_t parity) const {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  pair_wait_slow(bar, parity, flags, p, false);
+  return !aborted();
 }
 __device__ __forceinline__ void PairWaiter::drain(uint32_t bar, uint32_t parity) const {
   pair_wait_slow(bar, parity, flags, p, true);
@@ -169,7 +173,7 @@ __device__ __forceinline__ void PairWaiter::drain(uint32_t bar, uint32_t parity)
 struct Unit {
   int row0, row1, p_last, r;
   int lo, sinks, sink_blocks, win_block;
-  int b0, nb, split, live;                 // live 0: no more units
+  int b0, nb, split, live;                 // live: 1 + the request's length; 0: no more units
   __device__ __forceinline__ int block(int i) const {   // i-th block's index
     return i < sink_blocks ? i : win_block + (i - sink_blocks);
   }
@@ -256,9 +260,9 @@ __device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
   t.b0 = t.nb = t.sink_blocks = t.win_block = 0;
   t.p_last = t.lo = -1;
   t.sinks = 0;
-  t.live = 1;
-  if (!used) return t;
   const int len = __ldg(p.b.seq_lens + t.r);
+  t.live = 1 + min(max(len, 0), 0x7FFFFFFE);
+  if (!used) return t;
   const int tok0 = (int)(r0 / p.h), tok1 = (int)((r1 - 1) / p.h);
   t.p_last = len - (c1 - tok1);
   if (t.p_last < 0) return t;
@@ -417,7 +421,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   auto bar = [&](int i) { return sb + C::kOffBar + 8u * (uint32_t)i; };
   const PairWaiter W{sb + C::kOffAbort, &p};
 
-  if (tid == 0) {
+  // Setup, spread over the warps: barriers, TMEM, the abort flag and the tensor
+  // maps; the lookups' warp meanwhile finds the first unit and its table entries.
+  if (tid == 32) {
     for (int i = 0; i < kKGroups; ++i) {
       mbar_init(bar(kBarKFull + i), 1);
       mbar_init(bar(kBarKEmpty + i), 1);
@@ -448,13 +454,56 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     }
     mbar_init(bar(kBarDrain), 1);
     mbar_init(bar(kBarDrain + 1), 1);
+    fence_mbar_init_cluster();
+  }
+  if (tid == 64) {
     *W.shared(0) = 0;
     *W.shared(1) = *reinterpret_cast<volatile int*>(p.abort_ctr);
-    fence_mbar_init_cluster();
+  }
+  if (tid == 128) {
+    tma_prefetch_map(&a.row_map);
+    if (a.box && (kFp8 || a.box < 64)) tma_prefetch_map(&a.box_map);
+    if (a.box == 64) tma_prefetch_map(&a.k_map);
+    if (a.box == 64 && !kFp8) tma_prefetch_map(&a.v_map);
+    if (!kFp8) tma_prefetch_map(&a.q_map);
   }
   if (warp == 0) {
     tmem_alloc_pair(sb + C::kOffTmem, kTmemCols);
     tmem_relinquish_pair();
+  }
+  Unit next{};                                         // (warp 3's)
+  bool bad = false;
+  // Lane l of the lookups' warp has positions 4 l .. 4 l + 3 of a block, which
+  // share a table entry where cache blocks are multiples of four rows (quad).
+  struct Entry {
+    int off, blk;                                      // row within the block, table entry
+    uint32_t seen;                                     // bits of the four positions
+  };
+  const int per = a.box >> 2;                          // lanes whose rows one copy can bring
+  const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 1u << lane;
+  auto entry = [&](const Unit& u, int j) {
+    Entry e{0, -1, 0u};
+    if (j >= u.nb) return e;
+    const int pos = u.block(u.b0 + j) * kBN + 4 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      e.seen |= (pos + i <= u.p_last && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
+    // (a copy brings its rows whole where a row of the tile sees one of them)
+    if (__ballot_sync(0xffffffffu, e.seen != 0) & mine) {
+      const int page = a.shift >= 0 ? pos >> a.shift : pos / p.b.block_size;
+      e.off = pos - page * p.b.block_size;
+      e.blk = batch_block(p.b, u.r, page, bad);
+    }
+    return e;
+  };
+  Entry e0{0, -1, 0u}, e1 = e0, e2 = e0;
+  if (warp == 3) {
+    next = find_unit(p, (int64_t)(blockIdx.x >> 1));
+    if (a.quad) {
+      e0 = entry(next, 0);
+      e1 = entry(next, 1);
+      e2 = entry(next, 2);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -486,6 +535,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   auto peek_unit = [&](int i) {
     W.wait(bar(kBarTFull + (i & 1)), (i >> 1) & 1);
     return reinterpret_cast<const Unit*>(sm + C::kOffUnit + 48 * (i & 1));
+  };
+  // Whether this lane's four rows come with one copy of their box: all of the box's
+  // rows are there, or all are absent, which a box before the cache's first row
+  // reads as zeros.
+  auto whole_box = [&](int4& id) {
+    const uint32_t there = __ballot_sync(0xffffffffu, (id.x | id.y | id.z | id.w) >= 0);
+    const uint32_t absent = __ballot_sync(0xffffffffu, (id.x & id.y & id.z & id.w) < 0);
+    if (per == 0) return false;
+    if ((absent & mine) == mine) id.x = -64;
+    return (there & mine) == mine || (absent & mine) == mine;
   };
   // Blocks are counted across units (J): a barrier's n-th phase is block n's.
 
@@ -620,19 +679,18 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
      }
      for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
       W.wait(bar(kBarMFull + mr.m), mr.ph);
-      const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + 16 * r +
-                                                                    (lane & 15)];
+      int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + 16 * r + (lane & 15)];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
-      const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
-      const uint32_t full = __ballot_sync(0xffffffffu, all4) & 0xFFFFu;
+      // (rows of a block that no row of the tile sees come along: their scores
+      // are replaced)
+      const bool boxed = whole_box(id);
       const uint32_t ktile = sb + C::kOffK;
-      if (a.box == 64 && full == 0xFFFFu) {            // the 64 rows of one block, all seen
-        if (lane == 0) {
+      if (a.box == 64 && __all_sync(0xffffffffu, boxed)) {   // the 64 rows as one box
+        if (elect_one()) {
 #pragma unroll 1
           for (int g = 0; g < groups; ++g) {
-            if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
-            if (W.aborted()) break;                    // (one lane)
+            if (J >= 1 && !W.wait(bar(kBarKEmpty + g), (J - 1) & 1)) break;
             const int c0 = g * C::kAtomsPerGroup;
             const uint32_t dst = ktile + c0 * kAtom;
             // E4M3 rows of 576 end in half a column, which the map of whole
@@ -653,10 +711,6 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (stopped()) break;
         continue;
       }
-      // lanes of this lane's box, all seen and allocated: one copy for the box
-      const int per = a.box >> 2;
-      const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
-      const bool boxed = per && (full & mine) == mine;
 #pragma unroll 1
       for (int g = 0; g < groups; ++g) {
         if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
@@ -703,16 +757,44 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       for (int i = 0; take_unit(i, u); ++i) {
        for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
         W.wait(bar(kBarMFull + mr.m), mr.ph);
-        const int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + lane];
+        int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
-        const bool all4 = (id.x | id.y | id.z | id.w) >= 0;
-        const uint32_t full = __ballot_sync(0xffffffffu, all4);
+        // Rows behind the last token may never have been written, and a weight of
+        // 0 times NaN is NaN: they are read as zeros.  (The other rows of a block
+        // were written; one that is not finite costs the tile slow_row.)
+        const int up = u.live - 2 - (u.block(u.b0 + j) * kBN + 4 * lane);
+        if (up < 0) id.x = -1;
+        if (up < 1) id.y = -1;
+        if (up < 2) id.z = -1;
+        if (up < 3) id.w = -1;
+        const bool boxed = whole_box(id);
+        if (!kFp8 && a.box == 64 && __all_sync(0xffffffffu, boxed)) {   // two whole boxes
+          const int far = __shfl_sync(0xffffffffu, id.x, 16);
+          bool on = true;
+          if (elect_one()) {
+#pragma unroll 1
+            for (int v = 0; v < kVUnits; ++v) {
+              if (J >= 1 && !W.wait(bar(kBarVEmpty + v), (J - 1) & 1)) {
+                on = false;
+                break;
+              }
+              if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
+              const int ch = 256 * (v >> 1) + 128 * (int)r, row = v & 1 ? far : id.x;
+              const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
+              if (kFp8)
+                tma_load_2d_pair(slot, &a.box_map, ch, row, vfull0 + 8u * v);
+              else
+                tma_load_3d_pair(slot, &a.v_map, 0, row, ch / 64, vfull0 + 8u * v);
+              ++issued;
+            }
+          }
+          __syncwarp();
+          if (__any_sync(0xffffffffu, !on)) break;
+          continue;
+        }
         // The 16 lanes of a key half: one copy by its first lane where the half is
         // one piece of a cache block, a box per lane group, or four rows per lane.
-        const int per = a.box >> 2;
-        const uint32_t mine = per ? ((1u << per) - 1u) << (lane & ~(per - 1)) : 0u;
-        const bool boxed = per && (full & mine) == mine;
 #pragma unroll 1
         for (int v = 0; v < kVUnits; ++v) {
           if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
@@ -740,6 +822,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         }
         if (stopped()) break;
        }
+       if (stopped()) break;
       }
       if (r == 0 && lane == 0)
 #pragma unroll 1
@@ -756,45 +839,26 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // on their way while block j is written down.
     uint32_t* words = reinterpret_cast<uint32_t*>(sm + C::kOffMask);
     const bool keyed = kFp8 && p.kv_format == kE4m3Block;   // (one scale per tensor: at the end)
-    bool bad = false;
     MetaRing mr;
-    Unit u{};
     int J = 0;
-    struct Entry {
-      int off, blk;                                    // row within the block, table entry
-      uint32_t seen;                                   // bits of the four positions
-    };
-    auto entry = [&](int j) {
-      Entry e{0, -1, 0u};
-      if (j >= u.nb) return e;
-      const int pos = u.block(u.b0 + j) * kBN + 4 * lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        e.seen |= (pos + i <= u.p_last && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
-      if (e.seen) {
-        const int page = a.shift >= 0 ? pos >> a.shift : pos / p.b.block_size;
-        e.off = pos - page * p.b.block_size;
-        e.blk = batch_block(p.b, u.r, page, bad);
-      }
-      return e;
-    };
     struct Found {
       int id[4];
+      uint32_t seen;                                   // of those that have a row
       float sc;
     };
     auto found = [&](const Entry& e) {
       Found f;
       f.sc = 1.f;
+      f.seen = 0;
       const int64_t row = (int64_t)e.blk * p.b.block_stride_rows + e.off;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool in = e.blk >= 0 && (e.seen >> i & 1u);
-        bad |= in && row + i >= p.b.num_slots;
-        f.id[i] = in && row + i < p.b.num_slots ? (int)row + i : -1;
+        const bool in = e.blk >= 0 && row + i < p.b.num_slots;
+        bad |= e.blk >= 0 && !in && (e.seen >> i & 1u);
+        f.id[i] = in ? (int)row + i : -1;
+        f.seen |= in ? e.seen & 1u << i : 0u;
       }
       if (keyed && f.id[0] >= 0) f.sc = __ldg(p.k_scale + e.blk);
-      if (keyed && f.id[0] < 0 && (f.id[1] & f.id[2] & f.id[3]) >= 0)
-        f.sc = __ldg(p.k_scale + e.blk);
       return f;
     };
     int i = 0;                                         // units described
@@ -811,7 +875,6 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
       ++i;
     };
-    int64_t unit = (int64_t)(blockIdx.x >> 1);
     bool pending = false;                              // an answer is on its way
     int n = 0;                                         // answers read
     while (!stopped()) {
@@ -827,18 +890,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       pending = true;
       __syncwarp();
-      u = find_unit(p, unit);
+      const Unit u = next;
       if (u.row1 > u.row0) publish(u);
-      Entry e1{}, e2{};
-      Found f{};
-      if (a.quad) {
-        f = found(entry(0));
-        e1 = entry(1);
-        e2 = entry(2);
-      }
+      Found f = found(e0);
       for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
         const int m = mr.m;
         int id[4];
+        uint32_t seen = 0;
         float sc[4] = {1.f, 1.f, 1.f, 1.f};
         if (a.quad) {
 #pragma unroll
@@ -846,14 +904,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             id[k] = f.id[k];
             sc[k] = f.sc;
           }
+          seen = f.seen;
           f = found(e1);
           e1 = e2;
-          e2 = entry(j + 3);
+          e2 = entry(u, j + 3);
         } else {
           const Rows4 x = lookup4(p, u, u.block(u.b0 + j) * kBN + 4 * lane, bad);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             id[k] = x.id[k];
+            seen |= (id[k] >= 0 ? 1u : 0u) << k;
             if (keyed && id[k] >= 0) sc[k] = key_scale(p, x.blk[k]);
           }
         }
@@ -885,10 +945,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         if (J >= kMeta) W.wait(bar(kBarMEmpty + m), mr.ph ^ 1);
         if (stopped()) break;
         __syncwarp();
-        uint32_t nib = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) nib |= (id[k] >= 0 ? 1u : 0u) << k;
-        nib <<= 4 * (lane & 7);
+        uint32_t nib = seen << 4 * (lane & 7);
 #pragma unroll
         for (int o = 1; o <= 4; o <<= 1) nib |= __shfl_xor_sync(0xffffffffu, nib, o);
         if ((lane & 7) == 0) words[4 * m + (lane >> 3)] = nib;
@@ -913,14 +970,19 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
       if (lane == 0) mbar_signal_remote(bar0(kBarCEmpty + (n & 1)));
       if (!taken) break;
-      unit = (int64_t)(first >> 1);
+      next = find_unit(p, (int64_t)(first >> 1));
+      if (a.quad) {
+        e0 = entry(next, 0);
+        e1 = entry(next, 1);
+        e2 = entry(next, 2);
+      }
       ++n;
     }
     // (after an abort: an answer on its way still writes to shared memory)
     if (pending && lane == 0) W.drain(bar(kBarCFull + (n & 1)), (n >> 1) & 1);
     __syncwarp();
-    u.live = 0;
-    publish(u);
+    next.live = 0;
+    publish(next);
     if (bad) atomicCAS(p.status, 0, kStatusBadIndex);
     __syncwarp();
   } else if (warp < 12) {
