@@ -490,8 +490,10 @@ smla_status smla_fwd_window(const void* q, const void* kv_cache, int kv_dtype,
   if (plan.workspace_bytes > 0) {
     if (!workspace || workspace_bytes < plan.workspace_bytes) return SMLA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
-    p.o_part = static_cast<float*>(workspace);
-    p.lse_part = p.o_part + (size_t)plan.splits * T * h * 512;
+    p.parts = static_cast<int*>(workspace);
+    p.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        ((size_t)T * h * sizeof(int) + 255) / 256 * 256);
+    p.lse_part = p.o_part + (size_t)plan.workers * 2 * 128 * 512;
   }
   p.b = b;
   p.q = q;
@@ -506,7 +508,8 @@ smla_status smla_fwd_window(const void* q, const void* kv_cache, int kv_dtype,
   p.d_qk = d_qk;
   p.window = window;
   p.sinks = sinks;
-  p.splits = plan.splits;
+  p.workers = plan.workers;
+  p.merge_groups = plan.merge_groups;
   p.sm_scale = sm_scale;
   return smla::launch_window(p, stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }

@@ -147,22 +147,26 @@ struct WinParams {
   const float* k_scale;        // E4M3: [1] or one per cache block
   void* out;                   // bf16 [N, h, 512]
   float* lse;                  // [N, h] or nullptr
-  float* o_part;               // splits > 1: [splits, N, h, 512], else nullptr
-  float* lse_part;             // [splits, N, h]
+  // workers > 0: the key blocks of all tiles are cut into that many ranges, and
+  // tiles in parts leave partials: two per range, of up to 128 rows
+  int workers;
+  float* o_part;               // [2 workers, 128, 512]
+  float* lse_part;             // [2 workers, 128]
+  int* parts;                  // [N, h] the ranges that hold the row's tile, its row
+  int merge_groups;            // thread groups of the merge
   int* status;
   int* abort_ctr;
   uint64_t wait_limit_ns;
   int inject_stall;            // see FwdParams
   int kv_format, h, d_qk;
   int window, sinks;           // window 0: every position up to the token's own
-  int splits;
   int64_t num_tiles;           // set by launch_window
   float sm_scale;
 };
 
 struct WindowPlan {
   int64_t tiles;
-  int splits;
+  int workers, merge_groups;
   size_t workspace_bytes;
 };
 WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int window, int sinks,

@@ -59,13 +59,16 @@
 // output is not finite although its softmax is is computed again from its
 // visible positions alone (slow_row).
 //
-// Few tiles: the keys of a tile are cut into `splits` ranges of blocks, each
-// leaves a normalised fp32 partial and its LSE, and a second kernel merges them.
-//
-// Scheduling.  A unit is (tile, range).  The grid has one cluster per unit, but
-// a running cluster takes over units that have not started
-// (clusterlaunchcontrol) and keeps its barriers, TMEM and loaders going, so the
-// next unit's first loads and QK run under the epilogue of the last one.
+// Scheduling.  A unit is a tile with some of its key blocks.  Many tiles: a unit
+// is a tile; the grid has one cluster per tile, and a running cluster takes over
+// tiles that have not started (clusterlaunchcontrol).  Few tiles: the blocks of
+// all tiles, tile after tile, are cut into as many equal ranges as there are
+// places for a pair; a cluster works on the tiles, or parts of tiles, in its
+// range.  A part leaves a normalised fp32 partial and its LSE, and a second
+// kernel merges a tile's parts in their order.  (Against equal numbers of ranges
+// per tile, 32 E4M3 requests of 8 to 16 thousand keys with 128 heads: @EVEN@.)
+// Either way a cluster keeps its barriers, TMEM and loaders going, so the next
+// unit's first loads and QK run under the epilogue of the last one.
 //
 // Warp roles: warp 0 issues QK and owns TMEM, another warp issues PV (both in
 // the even CTA; two issuers, so that the waits of one are covered by the MMAs of
@@ -173,7 +176,7 @@ __device__ __forceinline__ void PairWaiter::drain(uint32_t bar, uint32_t parity)
 struct Unit {
   int row0, row1, p_last, r;
   int lo, sinks, sink_blocks, win_block;
-  int b0, nb, split, live;                 // live: 1 + the request's length; 0: no more units
+  int b0, nb, slot, live;                  // slot: of its partial, -1: the tile's only part; live: 1 + the request's length; 0: no more units
   __device__ __forceinline__ int block(int i) const {   // i-th block's index
     return i < sink_blocks ? i : win_block + (i - sink_blocks);
   }
@@ -244,15 +247,13 @@ __device__ __forceinline__ int64_t first_tile(const WinParams& p, int r) {
   return p.h == 128 ? c : c * p.h / 128 + r;
 }
 
-// Unit number u (tile * splits + range, the tiles from the last: a prompt's
-// later tokens see more keys); row1 = row0 when the tile number is not used.
-__device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
+// The k-th tile of request r, whose tokens are [c0, c1) and whose length is len,
+// with all of its key blocks; row1 = row0 where there is no such tile.
+__device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int c1, int len,
+                                          int64_t k) {
   Unit t;
-  t.split = (int)(u % p.splits);
-  const int64_t tile = p.num_tiles - 1 - u / p.splits;
-  t.r = warp_last_request(p.b.num_reqs, tile, [&](int m) { return first_tile(p, m); });
-  const int c0 = batch_start(p.b, t.r), c1 = batch_start(p.b, t.r + 1);
-  const int64_t k = tile - first_tile(p, t.r);
+  t.r = r;
+  t.slot = -1;
   const int64_t r0 = (int64_t)c0 * p.h + 128 * k, r1 = min(r0 + 128, (int64_t)c1 * p.h);
   const bool used = k >= 0 && r1 > r0;
   t.row0 = used ? (int)r0 : 0;
@@ -260,10 +261,9 @@ __device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
   t.b0 = t.nb = t.sink_blocks = t.win_block = 0;
   t.p_last = t.lo = -1;
   t.sinks = 0;
-  const int len = __ldg(p.b.seq_lens + t.r);
   t.live = 1 + min(max(len, 0), 0x7FFFFFFE);
   if (!used) return t;
-  const int tok0 = (int)(r0 / p.h), tok1 = (int)((r1 - 1) / p.h);
+  const int tok0 = t.row0 / p.h, tok1 = (t.row1 - 1) / p.h;
   t.p_last = len - (c1 - tok1);
   if (t.p_last < 0) return t;
   const int p_first = max(len - (c1 - tok0), 0);
@@ -271,10 +271,140 @@ __device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
   t.sinks = min(p.sinks, t.lo);
   t.win_block = t.lo / kBN;
   t.sink_blocks = min((t.sinks + kBN - 1) / kBN, t.win_block);
-  const int64_t n = t.sink_blocks + t.p_last / kBN + 1 - t.win_block;
-  t.b0 = (int)(n * t.split / p.splits);
-  t.nb = (int)(n * (t.split + 1) / p.splits) - t.b0;
+  t.nb = t.sink_blocks + t.p_last / kBN + 1 - t.win_block;
   return t;
+}
+
+// Unit number u where a unit is a tile: the tiles from the last, as a prompt's
+// later tokens see more keys.
+__device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
+  const int64_t tile = p.num_tiles - 1 - u;
+  const int r = warp_last_request(p.b.num_reqs, tile, [&](int m) { return first_tile(p, m); });
+  return tile_unit(p, r, batch_start(p.b, r), batch_start(p.b, r + 1), __ldg(p.b.seq_lens + r),
+                   tile - first_tile(p, r));
+}
+
+// A cluster's range of the list of all tiles' blocks (a tile without one counts
+// one), where it stands, and the request that it stands in.  Beginning a second
+// tile costs a range about as much as 5 blocks (its Q, its first loads, another
+// epilogue: 7 us with bf16 rows, 12 with E4M3), so every tile but the list's
+// first counts that much more, before its blocks.
+constexpr int kTileCost = 5;
+struct Walk {
+  int64_t pos, end, total;
+  int64_t base;                            // the request's first block in the list
+  int r;
+  int ranges;                              // no more than there are blocks: none is empty
+};
+__device__ __forceinline__ int request_tiles(const WinParams& p, int c0, int c1) {
+  return c1 > c0 ? (int)(((int64_t)(c1 - c0) * p.h + 127) / 128) : 0;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if ((int)(threadIdx.x & 31) >= o) x += y;
+  }
+  return x;
+}
+// x / y for x >= 0 and y > 0, in 32 bits where they hold it.
+static __device__ __noinline__ int64_t divide_wide(int64_t x, int64_t y) { return x / y; }
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+  return x < 0x7FFFFFFF && y < 0x7FFFFFFF ? (int64_t)((uint32_t)x / (uint32_t)y) : divide_wide(x, y);
+}
+// The w-th range.  First the list's length, then the range's place.
+__device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
+  const int lane = threadIdx.x & 31;
+  Walk k{0, 0, 0, 0, 0, 0};
+  int64_t n = 0, upto = 0, all = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t acc = 0;
+#pragma unroll 1
+    for (int first = 0; first < p.b.num_reqs; first += 32) {
+      if (pass == 0 || p.b.num_reqs > 32) {
+        const int r = min(first + lane, p.b.num_reqs - 1);
+        const int c0 = batch_start(p.b, r), c1 = batch_start(p.b, r + 1);
+        const int len = __ldg(p.b.seq_lens + r);
+        const int tiles = first + lane < p.b.num_reqs ? request_tiles(p, c0, c1) : 0;
+        n = 0;
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t) n += kTileCost + max(tile_unit(p, r, c0, c1, len, t).nb, 1);
+        upto = warp_scan(n);
+        all = __shfl_sync(0xffffffffu, upto, 31);
+      }
+      if (pass == 1 && k.pos < acc + all) {
+        const int src = __ffs(__ballot_sync(0xffffffffu, k.pos < acc + upto)) - 1;
+        k.r = first + src;
+        k.base = acc + __shfl_sync(0xffffffffu, upto - n, src);
+        return k;
+      }
+      acc += all;
+    }
+    if (pass == 0) {
+      k.total = acc - kTileCost;
+      k.ranges = (int)min((int64_t)p.workers, k.total);
+      if (w >= k.ranges) return k;
+      k.pos = kTileCost + divide(k.total * w, k.ranges);
+      k.end = kTileCost + divide(k.total * (w + 1), k.ranges);
+    }
+  }
+  return k;
+}
+// The next part of a tile in the range; its row1 = row0 behind the last.  `note`:
+// this CTA writes down which ranges hold the tile, for the merge.
+__device__ __forceinline__ Unit next_part(const WinParams& p, Walk& k, int w, bool note) {
+  const int lane = threadIdx.x & 31;
+  Unit u{};
+#pragma unroll 1
+  while (k.pos < k.end && k.r < p.b.num_reqs) {
+    const int c0 = batch_start(p.b, k.r), c1 = batch_start(p.b, k.r + 1);
+    const int len = __ldg(p.b.seq_lens + k.r);
+    const int tiles = request_tiles(p, c0, c1);
+    // The request's tile that holds the place: number t, its blocks from t0 on.
+    int t = 0;
+    int64_t t0 = k.base;
+#pragma unroll 1
+    for (; tiles > 1 && t < tiles; t += 32) {
+      const int64_t n =
+          t + lane < tiles ? kTileCost + max(tile_unit(p, k.r, c0, c1, len, t + lane).nb, 1) : 0;
+      const int64_t upto = warp_scan(n), all = __shfl_sync(0xffffffffu, upto, 31);
+      if (k.pos < t0 + all) {
+        const int src = __ffs(__ballot_sync(0xffffffffu, k.pos < t0 + upto)) - 1;
+        t0 += __shfl_sync(0xffffffffu, upto - n, src);
+        t += src;
+        break;
+      }
+      t0 += all;
+    }
+    if (t < tiles) {
+      u = tile_unit(p, k.r, c0, c1, len, t);
+      const int blocks = max(u.nb, 1);
+      t0 += kTileCost;                                 // its first block
+      if (k.pos < t0 + blocks) {
+        u.b0 = (int)max(k.pos - t0, (int64_t)0);
+        const int take = (int)(min(t0 + blocks, k.end) - t0) - u.b0;
+        if (take <= 0) return Unit{};                  // (the range ends before it)
+        // (a range ends in at most one tile that goes on and begins in at most one
+        // that went before: two partials)
+        u.slot = take == blocks ? -1 : 2 * w + (u.b0 + take < blocks ? 1 : 0);
+        if (u.nb > 0) u.nb = take;
+        if (note && u.b0 == 0) {
+          const int64_t upto = t0 + blocks - kTileCost;
+          const int last = (int)divide(upto * k.ranges - 1, k.total);
+          for (int g = u.row0 + lane; g < u.row1; g += 32)
+            p.parts[g] = w << 19 | last << 7 | (g - u.row0);
+        }
+        k.pos = t0 + u.b0 + take;
+        return u;
+      }
+      t0 += blocks;                                    // (the request's only tile: done)
+    }
+    k.base = t0;
+    ++k.r;
+    u = Unit{};
+  }
+  return u;
 }
 
 // Cache rows of the four positions pos .. pos + 3 (pos a multiple of 4), -1
@@ -472,6 +602,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     tmem_relinquish_pair();
   }
   Unit next{};                                         // (warp 3's)
+  Walk walk{};
   bool bad = false;
   // Lane l of the lookups' warp has positions 4 l .. 4 l + 3 of a block, which
   // share a table entry where cache blocks are multiples of four rows (quad).
@@ -498,7 +629,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   };
   Entry e0{0, -1, 0u}, e1 = e0, e2 = e0;
   if (warp == 3) {
-    next = find_unit(p, (int64_t)(blockIdx.x >> 1));
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.workers > 0) {
+      walk = start_walk(p, (int)(blockIdx.x >> 1));
+      next = next_part(p, walk, (int)(blockIdx.x >> 1), r == 0);
+    } else {
+      next = find_unit(p, (int64_t)(blockIdx.x >> 1));
+    }
     if (a.quad) {
       e0 = entry(next, 0);
       e1 = entry(next, 1);
@@ -526,7 +663,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const int4 x = src[0], y = src[1], z = src[2];
     u.row0 = x.x; u.row1 = x.y; u.p_last = x.z; u.r = x.w;
     u.lo = y.x; u.sinks = y.y; u.sink_blocks = y.z; u.win_block = y.w;
-    u.b0 = z.x; u.nb = z.y; u.split = z.z; u.live = z.w;
+    u.b0 = z.x; u.nb = z.y; u.slot = z.z; u.live = z.w;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
     return __all_sync(0xffffffffu, u.live != 0 && !W.aborted()) != 0;
@@ -869,7 +1006,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       if (lane == 0) {
         dst[0] = make_int4(x.row0, x.row1, x.p_last, x.r);
         dst[1] = make_int4(x.lo, x.sinks, x.sink_blocks, x.win_block);
-        dst[2] = make_int4(x.b0, x.nb, x.split, x.live);
+        dst[2] = make_int4(x.b0, x.nb, x.slot, x.live);
         mbar_arrive(bar(kBarTFull + (i & 1)));
       }
       __syncwarp();
@@ -878,18 +1015,20 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     bool pending = false;                              // an answer is on its way
     int n = 0;                                         // answers read
     while (!stopped()) {
-      // Ask for the next unit before this one is worked on.
+      // Ask for the next tile before this one is worked on.
       const uint32_t cfull = bar(kBarCFull + (n & 1));
       const uint32_t answer = sb + C::kOffAnswer + 16 * (n & 1);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(cfull, 16);
-        if (r == 0) {
-          if (n >= 2) W.wait(bar(kBarCEmpty + (n & 1)), ((n >> 1) - 1) & 1);
-          cluster_take_over(answer, cfull);
+      if (p.workers == 0) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(cfull, 16);
+          if (r == 0) {
+            if (n >= 2) W.wait(bar(kBarCEmpty + (n & 1)), ((n >> 1) - 1) & 1);
+            cluster_take_over(answer, cfull);
+          }
         }
+        pending = true;
+        __syncwarp();
       }
-      pending = true;
-      __syncwarp();
       const Unit u = next;
       if (u.row1 > u.row0) publish(u);
       Found f = found(e0);
@@ -961,22 +1100,28 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarMFull + m));
       }
-      W.wait(cfull, (n >> 1) & 1);
       if (stopped()) break;
-      pending = false;
-      int first;
-      const bool taken = cluster_taken(answer, first);
-      fence_proxy_async_smem();                        // the answer was read
-      __syncwarp();
-      if (lane == 0) mbar_signal_remote(bar0(kBarCEmpty + (n & 1)));
-      if (!taken) break;
-      next = find_unit(p, (int64_t)(first >> 1));
+      if (p.workers > 0) {
+        next = next_part(p, walk, (int)(blockIdx.x >> 1), r == 0);
+        if (next.row1 <= next.row0) break;
+      } else {
+        W.wait(cfull, (n >> 1) & 1);
+        if (stopped()) break;
+        pending = false;
+        int first;
+        const bool taken = cluster_taken(answer, first);
+        fence_proxy_async_smem();                        // the answer was read
+        __syncwarp();
+        if (lane == 0) mbar_signal_remote(bar0(kBarCEmpty + (n & 1)));
+        if (!taken) break;
+        next = find_unit(p, (int64_t)(first >> 1));
+        ++n;
+      }
       if (a.quad) {
         e0 = entry(next, 0);
         e1 = entry(next, 1);
         e2 = entry(next, 2);
       }
-      ++n;
     }
     // (after an abort: an answer on its way still writes to shared memory)
     if (pending && lane == 0) W.drain(bar(kBarCFull + (n & 1)), (n >> 1) & 1);
@@ -1229,10 +1374,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     // (a sum that is not finite: NaN, whatever the weights' terms became)
     const float inv = empty ? 0.f : l < INFINITY ? __fdividef(kFp8 ? kscale * 0x1p-7f : kscale, lr)
                                                  : NAN;
-    const bool partial = p.o_part != nullptr;
+    const bool partial = t->slot >= 0;
     const int64_t g = (int64_t)t->row0 + 64 * (int)r + row;
     const bool live = g < t->row1;
-    const int64_t prow_g = (int64_t)t->split * p.b.N * p.h + g; // row of the partials
+    const int64_t prow_g = (int64_t)t->slot * 128 + 64 * (int)r + row;  // row of the partials
     // O columns [128 wg, + 128) are channels 256 wg + 128 half ..; a thread's
     // stores fill whole 32-byte sectors, straight from registers.
     const int ch0 = 256 * wg + 128 * half;
@@ -1296,7 +1441,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
         const int pr = t->p_last - ((t->row1 - 1) / p.h - (int)gr / p.h);
         slow_row<kFp8>(p, *t, gr, pr, p.window ? max(pr - (p.window - 1), 0) : 0,
-                       partial ? p.o_part + ((int64_t)t->split * p.b.N * p.h + gr) * 512 : nullptr,
+                       partial ? p.o_part + ((int64_t)t->slot * 128 + 64 * (int)r + rr) * 512 : nullptr,
                        out + gr * 512);
       }
       named_bar_sync(4, 256);                            // the flags were read
@@ -1415,36 +1560,83 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 
 // ---- merge of the partials -------------------------------------------------
 //   LSE = ln sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s
-// One CTA per row, four channels a thread; a range without a visible key has
-// LSE_s = -inf and its O_s is not read.  Rows of no request are left alone.
-__global__ void __launch_bounds__(128) smla_window_merge_kernel(const WinParams p) {
+// One CTA per row, four channels a thread, and where a tile may have more than 16
+// parts four groups of threads that share them; the ranges first .. last hold the
+// row's tile (one: it is written already), the last as its first part and the
+// others as their last.  A part without a visible key has LSE_s = -inf and its
+// O_s is not read.  Rows of no request are left alone.  Launched under the end of
+// the kernel before (its launch took 3 us of a short call); it waits for it here.
+constexpr int kMaxParts = 128;
+constexpr int kMergeGroups = 4;
+__global__ void __launch_bounds__(128 * kMergeGroups)
+smla_window_merge_kernel(const WinParams p) {
+  __shared__ float weight[kMaxParts];
+  __shared__ float red[2][4];
+  __shared__ float4 sums[kMergeGroups][128];
+  const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, groups = blockDim.x >> 7;
   const int64_t row = blockIdx.x;
   const int tok = (int)(row / p.h);
-  if (tok < batch_start(p.b, 0) || tok >= batch_start(p.b, p.b.num_reqs)) return;
-  const int64_t rows = (int64_t)p.b.N * p.h;
-  float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.lse_part[s * rows + row]);
+  const bool owned = tok >= batch_start(p.b, 0) && tok < batch_start(p.b, p.b.num_reqs);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!owned) return;
+  const int part = p.parts[row];
+  const int first = part >> 19, last = (part >> 7) & 0xFFF, off = part & 127;
+  // (starts that do not ascend leave rows without a tile, and this word as it was)
+  if (part < 0 || first >= last || last >= p.workers) return;
+  const int n = last - first + 1;
+  auto at = [&](int s) {
+    return (int64_t)(2 * (first + s) + (first + s < last ? 1 : 0)) * 128 + off;
+  };
+  const float ls = tid < n ? p.lse_part[at(tid)] : -INFINITY;   // (every group alike)
+  float top = ls;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (group == 0 && (tid & 31) == 0) red[0][tid >> 5] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  // (fmaxf passes over a NaN; its weight is NaN and so is the row)
+  const float e = ls == -INFINITY ? 0.f : expf(ls - top);
+  float z = e;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  if (group == 0 && (tid & 31) == 0) red[1][tid >> 5] = z;
+  if (group == 0) weight[tid] = e;
+  __syncthreads();
+  z = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float z = 0.f;
-  const int c = threadIdx.x * 4;
-  if (top != -INFINITY) {
-    for (int s = 0; s < p.splits; ++s) {
-      const float ls = p.lse_part[s * rows + row];
-      if (ls == -INFINITY) continue;
-      const float w = expf(ls - top);
-      const float4 x = *reinterpret_cast<const float4*>(p.o_part + (s * rows + row) * 512 + c);
-      z += w;
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
+  const int c = tid * 4;
+  for (int s0 = group; s0 < n; s0 += 8 * groups) {     // eight parts on their way at once
+    float4 x[8];
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i * groups;
+      w[i] = s < n ? weight[s] : 0.f;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (w[i] != 0.f) x[i] = *reinterpret_cast<const float4*>(p.o_part + at(s) * 512 + c);
     }
-    const float inv = 1.f / z;
-    o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      o.x = fmaf(w[i], x[i].x, o.x);
+      o.y = fmaf(w[i], x[i].y, o.y);
+      o.z = fmaf(w[i], x[i].z, o.z);
+      o.w = fmaf(w[i], x[i].w, o.w);
+    }
   }
-  uint2 packed = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+  if (groups > 1) {
+    sums[group][tid] = o;
+    __syncthreads();
+    if (group > 0) return;
+    for (int g = 1; g < groups; ++g) {
+      const float4 x = sums[g][tid];
+      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+    }
+  }
+  const bool none = z == 0.f;
+  const float inv = none ? 0.f : 1.f / z;
+  uint2 packed = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * 512 + c) = packed;
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = top == -INFINITY ? top : top + logf(z);
+  if (tid == 0 && p.lse) p.lse[row] = none ? -INFINITY : top + logf(z);
 }
 
 cudaError_t encode_rows(CUtensorMap* map, bool fp8, const void* base, int d, int64_t rows,
@@ -1510,11 +1702,12 @@ int64_t tile_numbers(int T, int h, int num_reqs) {
 
 }  // namespace
 
-// The key ranges per tile.  What is known here are bounds: the tiles are taken
-// as filled (a decode step's requests hold one each), the keys as max_len or
-// the window.  A block takes about 1.3 us on a pair, a unit another 4, and a
-// split writes and reads 4 KB a row at about 3 TB/s besides the merge's launch;
-// the number of ranges with the least sum is taken.
+// One unit per tile, or equal ranges of all tiles' blocks (WinParams::workers).
+// What is known here are bounds: the tiles are taken as filled (a decode step's
+// requests hold one each), the keys as max_len or the window.  A block takes about
+// 1.6 us on a pair, a unit another 4; ranges cost the merge (4) and write and read
+// the partials, 4 KB a row, at about 9 TB/s (L2).  The smaller sum is taken.
+// Ranges need the list's length, which every cluster counts: up to 1024 tiles.
 WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int window, int sinks,
                             int num_sms) {
   WindowPlan pl{};
@@ -1524,20 +1717,19 @@ WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int win
   if (window) keys = std::min<int64_t>(keys, (int64_t)window + (128 + h - 1) / h);
   int64_t blocks = (keys + kBN - 1) / kBN;
   if (window && keys < max_len) blocks += 1 + (std::min<int64_t>(sinks, max_len) + kBN - 1) / kBN;
-  const int places = std::max(num_sms / 2, 1);
-  double best = 0;
-  pl.splits = 1;
-  for (int s = 1; s <= 64 && s <= blocks; ++s) {
-    const double waves = (double)((filled * s + places - 1) / places);
-    double us = waves * (1.3 * (double)((blocks + s - 1) / s) + 4.0);
-    if (s > 1) us += 4.0 + (double)s * T * h * 4096.0 / 3e6;
-    if (s == 1 || us < best) {
-      best = us;
-      pl.splits = s;
-    }
-  }
-  pl.workspace_bytes =
-      pl.splits > 1 ? (size_t)pl.splits * T * h * (512 + 1) * sizeof(float) : 0;
+  blocks = std::max<int64_t>(blocks, 1);
+  const int64_t places = std::min(std::max(num_sms / 2, 1), kMaxParts);
+  const double one = (double)((filled + places - 1) / places) * (1.6 * (double)blocks + 4.0);
+  const int64_t list = filled * (blocks + kTileCost) - kTileCost;
+  const int64_t workers = std::min<int64_t>(places, filled * blocks);
+  const double rows = (double)T * h / (double)filled;
+  const double ranges = 1.6 * (double)((list + workers - 1) / workers) + 4.0 + 4.0 +
+                        (double)(workers + std::min(filled, workers)) * rows * 4096.0 / 9e6;
+  if (workers > 1 && pl.tiles <= 1024 && ranges < one) pl.workers = (int)workers;
+  pl.merge_groups = workers > 16 * filled ? kMergeGroups : 1;
+  if (pl.workers > 0)
+    pl.workspace_bytes = ((size_t)T * h * sizeof(int) + 255) / 256 * 256 +
+                         (size_t)pl.workers * 2 * 128 * (512 + 1) * sizeof(float);
   return pl;
 }
 
@@ -1568,14 +1760,22 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   if (e == cudaSuccess && !fp8)
     e = encode_rows(&a.q_map, false, p.q, p.d_qk, (int64_t)p.b.N * p.h, kRows);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = 2 * p.num_tiles * p.splits;
+  const int64_t ctas = 2 * (p.workers > 0 ? p.workers : p.num_tiles);
   if (ctas > 0x7FFFFFFFll || (int64_t)p.b.N * p.h > 0x7FFFFFFFll)
     return cudaErrorInvalidConfiguration;
   a.p = p;
   e = fp8 ? launch<true>(a, (unsigned)ctas, stream) : launch<false>(a, (unsigned)ctas, stream);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  smla_window_merge_kernel<<<(unsigned)(p.b.N * p.h), 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (e != cudaSuccess || p.workers == 0) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(p.b.N * p.h));
+  cfg.blockDim = dim3(128 * p.merge_groups);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, smla_window_merge_kernel, p);
 }
 
 }  // namespace smla
