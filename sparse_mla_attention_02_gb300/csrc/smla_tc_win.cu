@@ -65,8 +65,9 @@
 // all tiles, tile after tile, are cut into as many equal ranges as there are
 // places for a pair; a cluster works on the tiles, or parts of tiles, in its
 // range.  A part leaves a normalised fp32 partial and its LSE, and a second
-// kernel merges a tile's parts in their order.  (Against equal numbers of ranges
-// per tile, 32 E4M3 requests of 8 to 16 thousand keys with 128 heads: @EVEN@.)
+// kernel merges a tile's parts in their order.  (Equal numbers of ranges per
+// tile took 137 us for 32 E4M3 requests of 8 to 16 thousand keys with 128 heads,
+// this 110 us.)
 // Either way a cluster keeps its barriers, TMEM and loaders going, so the next
 // unit's first loads and QK run under the epilogue of the last one.
 //
@@ -1156,6 +1157,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       if (p.window) lo = max(pos - (p.window - 1), 0);
     }
     const int nb = t->nb;
+    // A warp whose 32 rows lie behind the tile's last only keeps step: nothing reads
+    // the O that its weights, whatever is in P, make (a mixed batch with 16 heads:
+    // 263 -> 258 us).
+    const bool idle = t->row0 + 64 * (int)r + (row & 32) >= t->row1;
     float qs = 1.f;
     if (kFp8 && nb > 0) {
       W.wait(bar(kBarQScale), q & 1);
@@ -1176,6 +1181,17 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       uint32_t see = words[4 * m + seg];
       W.wait(bar(kBarSFull + buf), (J >> 1) & 1);
       __syncwarp();
+      if (idle) {
+        if (lane == 0) {
+          mbar_signal_remote(sempty + 8u * buf);
+          mbar_arrive(bar(kBarMEmpty + m));
+        }
+        named_bar_or(4, 256, false);
+        if (J >= C::kPBufs) W.wait(bar(kBarPEmpty + J % C::kPBufs), (J / C::kPBufs - 1) & 1);
+        __syncwarp();
+        if (lane == 0) mbar_signal_remote(pfull + 8u * (J % C::kPBufs));
+        continue;
+      }
       tc_fence_after();
       // The row's view of its 32 keys.
       {
@@ -1384,7 +1400,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
     bool odd = false;                                    // an output that is not finite
 #pragma unroll 1
-    for (int c4 = 0; c4 < 128; c4 += 32) {               // (32 columns per TMEM wait)
+    for (int c4 = idle ? 128 : 0; c4 < 128; c4 += 32) {  // (32 columns per TMEM wait)
       uint32_t wide[2][16];
       __syncwarp();
       if (nb > 0) {
@@ -1468,6 +1484,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll 1
       for (int rr = g0; rr < kRows; rr += 12) {
         const int64_t gr = (int64_t)u.row0 + 64 * (int)r + rr;
+        if (gr - (rr & 31) >= u.row1) break;           // (rows of an idle softmax warp)
         const bool have = gr < u.row1;
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(p.q) + (have ? gr : u.row0) * p.d_qk) + j8;
