@@ -321,8 +321,9 @@ SMLA_API smla_status smla_cache_append(
  *  block_size, block_stride_rows   as for smla_cache_append
  *  window       positions a token sees, its own included; 0 = all up to it
  *  sinks        first positions that stay visible (no effect when window = 0)
- *  max_seq_len  a bound on seq_lens for the split plan, or 0; the result does
- *               not depend on it being right, only the speed
+ *  max_seq_len  a bound on seq_lens, or 0: how the keys are shared out follows
+ *               it (and T, h, num_reqs, the table's width), so sums may be
+ *               rounded differently under another; it need not be right
  *  T, h         packed tokens (>= 0) and heads (1..128)
  *  d_v          must be 512
  *  out          device, bf16 [T, h, d_v], 16-byte aligned
@@ -350,8 +351,9 @@ SMLA_API smla_status smla_fwd_window(
 
 /*
  * smla_fwd_window_workspace_size — bytes of device workspace smla_fwd_window
- * needs for these arguments on the current device (0 when the keys of a token
- * are not split, and for arguments that smla_fwd_window rejects).
+ * needs for these arguments on the current device (0 when the plan does not
+ * share a token's keys out, and for arguments that smla_fwd_window rejects).
+ * At most T * h words and, on 152 SMs, 40 MB.
  */
 SMLA_API size_t smla_fwd_window_workspace_size(int num_reqs, int T, int h, int d_qk, int d_v,
                                                int kv_dtype, int block_table_stride,
@@ -558,8 +560,9 @@ SMLA_API smla_status smla_get_device_status(int* status_out, int clear);
  *
  *  stall          nonzero: later tensor-core launches on the current device
  *                 leave out the first batch of score MMAs of every work
- *                 unit, so the wait for those scores cannot complete and
- *                 runs out; 0: normal launches.
+ *                 unit (smla_fwd_window: all of them), so the wait for
+ *                 those scores cannot complete and runs out; 0: normal
+ *                 launches.
  *  wait_limit_us  the time limit of one bounded wait in later launches on
  *                 the current device, in microseconds; 0 = the default
  *                 (500 ms).

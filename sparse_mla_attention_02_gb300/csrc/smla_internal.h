@@ -161,6 +161,7 @@ struct WinParams {
   int kv_format, h, d_qk;
   int window, sinks;           // window 0: every position up to the token's own
   int64_t num_tiles;           // set by launch_window
+  int table_end;               // the last position a block table can hold (launch_window)
   float sm_scale;
 };
 

@@ -51,13 +51,14 @@
 // sums that divide add weight / scale.  So blocks of any scales share one range,
 // and nothing is converted on V's way to the tensor core.
 //
-// Masked positions never reach an MMA as anything but zeros where no row of
-// the tile sees them (unwritten rows, blocks that are not allocated, positions
-// past the last token: the copies read zero fill).  Where a row masks a
-// position that another row of its tile sees, its score is replaced and its
-// weight is 0; an infinity or NaN there would still make 0 * inf, so a row whose
-// output is not finite although its softmax is is computed again from its
-// visible positions alone (slow_row).
+// Masked positions.  A cache block of which a row of the tile sees some position
+// is loaded whole: three columns of 64 rows arrive in 700 cycles as one copy, in
+// 3400 as 48 gathers of four rows.  K needs no zeros: a masked score is replaced,
+// its weight is 0.  V does, as 0 times NaN is NaN: rows behind the request's last
+// token, which may never have been written, and blocks that are not allocated are
+// read as zeros.  Any other masked position was written; should it hold an infinity
+// or NaN, a row whose output is not finite although its softmax is is computed
+// again from its visible positions alone (slow_row).
 //
 // Scheduling.  A unit is a tile with some of its key blocks.  Many tiles: a unit
 // is a tile; the grid has one cluster per tile, and a running cluster takes over
@@ -74,9 +75,9 @@
 // Warp roles: warp 0 issues QK and owns TMEM, another warp issues PV (both in
 // the even CTA; two issuers, so that the waits of one are covered by the MMAs of
 // the other); warps 1 and 2 load K and V; warp 3 takes units and looks up
-// each block's rows (validity, scales, row ids); warps 4..11 are the softmax: four threads per
-// row (TMEM lane half x column half), 32 keys each; with E4M3 rows warps 13..15
-// split Q.
+// each block's rows (validity, scales, row ids); warps 4..11 are the softmax: four
+// threads per row (TMEM lane half x column half), 32 keys each; with E4M3 rows
+// warps 13..15 split Q.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -177,7 +178,9 @@ __device__ __forceinline__ void PairWaiter::drain(uint32_t bar, uint32_t parity)
 struct Unit {
   int row0, row1, p_last, r;
   int lo, sinks, sink_blocks, win_block;
-  int b0, nb, slot, live;                  // slot: of its partial, -1: the tile's only part; live: 1 + the request's length; 0: no more units
+  int b0, nb;
+  int slot;                                // of its partial; -1: the tile's only part
+  int live;                                // 1 + the request's length; 0: no more units
   __device__ __forceinline__ int block(int i) const {   // i-th block's index
     return i < sink_blocks ? i : win_block + (i - sink_blocks);
   }
@@ -214,7 +217,7 @@ struct Cfg {
   // E4M3: the keys' scales, each 32 keys' common scale (0: several), its log2
   // and its reciprocal, the Q rows' scales (two units')
   static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 8 + 15) & ~15u : kOffAbort + 8;
-  static constexpr uint32_t kOffSeg = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0);   // float4 [kMeta][4]
+  static constexpr uint32_t kOffSeg = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0); // float4 [kMeta][4]
   static constexpr uint32_t kOffQScale = kOffSeg + (kFp8 ? kMeta * 64 : 0);
   static constexpr uint32_t kSmem = kOffQScale + (kFp8 ? 2 * kRows * 4 : 0);
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -271,8 +274,10 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
   t.lo = p.window ? max(p_first - (p.window - 1), 0) : 0;
   t.sinks = min(p.sinks, t.lo);
   t.win_block = t.lo / kBN;
-  t.sink_blocks = min((t.sinks + kBN - 1) / kBN, t.win_block);
-  t.nb = t.sink_blocks + t.p_last / kBN + 1 - t.win_block;
+  // (blocks past the table hold nothing, whatever a length says)
+  const int end = min(t.p_last, p.table_end) / kBN + 1;
+  t.sink_blocks = min(min((t.sinks + kBN - 1) / kBN, t.win_block), end);
+  t.nb = t.sink_blocks + max(end - t.win_block, 0);
   return t;
 }
 
@@ -311,7 +316,8 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x) {
 // x / y for x >= 0 and y > 0, in 32 bits where they hold it.
 static __device__ __noinline__ int64_t divide_wide(int64_t x, int64_t y) { return x / y; }
 __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
-  return x < 0x7FFFFFFF && y < 0x7FFFFFFF ? (int64_t)((uint32_t)x / (uint32_t)y) : divide_wide(x, y);
+  if (x < 0x7FFFFFFF && y < 0x7FFFFFFF) return (uint32_t)x / (uint32_t)y;
+  return divide_wide(x, y);
 }
 // The w-th range.  First the list's length, then the range's place.
 __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
@@ -328,9 +334,20 @@ __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
         const int c0 = batch_start(p.b, r), c1 = batch_start(p.b, r + 1);
         const int len = __ldg(p.b.seq_lens + r);
         const int tiles = first + lane < p.b.num_reqs ? request_tiles(p, c0, c1) : 0;
-        n = 0;
+        // One tile: its lane counts it.  More: the warp counts the request together.
+        n = tiles == 1 ? kTileCost + max(tile_unit(p, r, c0, c1, len, 0).nb, 1) : 0;
+        for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 1); many; many &= many - 1) {
+          const int src = __ffs(many) - 1;
+          const int s0 = __shfl_sync(0xffffffffu, c0, src), s1 = __shfl_sync(0xffffffffu, c1, src);
+          const int sl = __shfl_sync(0xffffffffu, len, src);
+          const int st = __shfl_sync(0xffffffffu, tiles, src);
+          int64_t sum = 0;
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t) n += kTileCost + max(tile_unit(p, r, c0, c1, len, t).nb, 1);
+          for (int t = lane; t < st; t += 32)
+            sum += kTileCost + max(tile_unit(p, 0, s0, s1, sl, t).nb, 1);
+          sum = __shfl_sync(0xffffffffu, warp_scan(sum), 31);
+          if (lane == src) n = sum;
+        }
         upto = warp_scan(n);
         all = __shfl_sync(0xffffffffu, upto, 31);
       }
@@ -414,7 +431,8 @@ struct Rows4 {
   int id[4];
   int blk[4];
 };
-static __device__ __noinline__ Rows4 lookup4(const WinParams& p, const Unit& t, int pos, bool& bad) {
+static __device__ __noinline__ Rows4 lookup4(const WinParams& p, const Unit& t, int pos,
+                                             bool& bad) {
   Rows4 o;
   int page = -1, blk = -1;
 #pragma unroll
@@ -697,44 +715,44 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const uint64_t dk = sdesc(sb + C::kOffK, 16, 1024, kLayoutSw128);
       Unit u;
       for (int i = 0, q = 0, J = 0; take_unit(i, u); ++i) {
-       if (u.nb > 0) W.wait(bar(kBarQFull), q++ & 1);
-       for (int j = 0; j < u.nb; ++j, ++J) {
-        if (J >= 2) W.wait(bar(kBarSEmpty + (J & 1)), ((J >> 1) - 1) & 1);
-        if (stopped()) break;
-        const uint32_t dS = tmem + kColS + 64 * (J & 1);
+        if (u.nb > 0) W.wait(bar(kBarQFull), q++ & 1);
+        for (int j = 0; j < u.nb; ++j, ++J) {
+          if (J >= 2) W.wait(bar(kBarSEmpty + (J & 1)), ((J >> 1) - 1) & 1);
+          if (stopped()) break;
+          const uint32_t dS = tmem + kColS + 64 * (J & 1);
 #pragma unroll 1
-        for (int g = 0, c = 0; c < a.atoms; ++g) {
-          W.wait(bar(kBarKFull + g), J & 1);
-          __syncwarp();
-          tc_fence_after();
-          const int c1 = min(c + C::kAtomsPerGroup, a.atoms);
-          if (elect_one()) {
+          for (int g = 0, c = 0; c < a.atoms; ++g) {
+            W.wait(bar(kBarKFull + g), J & 1);
+            __syncwarp();
+            tc_fence_after();
+            const int c1 = min(c + C::kAtomsPerGroup, a.atoms);
+            if (elect_one()) {
 #pragma unroll 1
-            for (int cc = c; cc < c1; ++cc) {
-              const uint64_t ad = dq + (uint32_t)cc * (kAtom >> 4);
-              const uint64_t bd = dk + (uint32_t)cc * (kAtom >> 4);
+              for (int cc = c; cc < c1; ++cc) {
+                const uint64_t ad = dq + (uint32_t)cc * (kAtom >> 4);
+                const uint64_t bd = dk + (uint32_t)cc * (kAtom >> 4);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if (kFp8) {
-                  // (the last atom of 576 channels is half padding)
-                  if (4 * cc + i >= a.ksteps) break;
-                  mma_pair_e4m3(dS, ad + 2 * i, bd + 2 * i, id, (cc | i) > 0 ? 1u : 0u);
-                  mma_pair_e4m3(dS, ad + 2 * i + (C::kMaxAtoms * kAtom >> 4), bd + 2 * i, id, 1u);
-                } else {
-                  mma_pair_bf16(dS, ad + 2 * i, bd + 2 * i, id, (cc | i) > 0 ? 1u : 0u);
+                for (int i = 0; i < 4; ++i) {
+                  if (kFp8) {
+                    // (the last atom of 576 channels is half padding)
+                    if (4 * cc + i >= a.ksteps) break;
+                    mma_pair_e4m3(dS, ad + 2 * i, bd + 2 * i, id, (cc | i) > 0 ? 1u : 0u);
+                    mma_pair_e4m3(dS, ad + 2 * i + (C::kMaxAtoms * kAtom >> 4), bd + 2 * i, id, 1u);
+                  } else {
+                    mma_pair_bf16(dS, ad + 2 * i, bd + 2 * i, id, (cc | i) > 0 ? 1u : 0u);
+                  }
                 }
               }
+              mma_commit_pair(bar(kBarKEmpty + g));
+              if (c1 == a.atoms) {
+                mma_commit_pair(bar(kBarSFull + (J & 1)));
+                if (j == u.nb - 1) mma_commit_pair(bar(kBarQEmpty));
+              }
             }
-            mma_commit_pair(bar(kBarKEmpty + g));
-            if (c1 == a.atoms) {
-              mma_commit_pair(bar(kBarSFull + (J & 1)));
-              if (j == u.nb - 1) mma_commit_pair(bar(kBarQEmpty));
-            }
+            c = c1;
+            __syncwarp();
           }
-          c = c1;
-          __syncwarp();
         }
-       }
       }
       // Every MMA issued here has completed (also after an abort) before
       // either CTA frees its TMEM or leaves its tiles.  (Signalled to this CTA
@@ -752,40 +770,40 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const uint64_t dv = sdesc(sb + C::kOffV, kAtom, 1024, kLayoutSw128);
       Unit u;
       for (int i = 0, J = 0; take_unit(i, u); ++i) {
-       for (int j = 0; j < u.nb; ++j, ++J) {
-        const int pb = J % C::kPBufs;
-        W.wait(bar(kBarPFull + pb), (J / C::kPBufs) & 1);
-        if (stopped()) break;
-        const uint64_t dpj = dp + (uint32_t)pb * (C::kPTerms * C::kPTerm >> 4);
+        for (int j = 0; j < u.nb; ++j, ++J) {
+          const int pb = J % C::kPBufs;
+          W.wait(bar(kBarPFull + pb), (J / C::kPBufs) & 1);
+          if (stopped()) break;
+          const uint64_t dpj = dp + (uint32_t)pb * (C::kPTerms * C::kPTerm >> 4);
 #pragma unroll 1
-        for (int v = 0; v < kVUnits; ++v) {          // v = 2 n + key half
-          W.wait(bar(kBarVFull + v), J & 1);
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t dO = tmem + kColO + 128 * (v >> 1);
-            const uint64_t bd = dv + (uint32_t)v * (C::kVUnit >> 4);
-            const uint32_t keep = (j > 0 || (v & 1)) ? 1u : 0u;
-            if (kFp8) {
-              const uint64_t ad = dpj + (uint32_t)(v & 1) * 4;    // 64 keys = 64 bytes
+          for (int v = 0; v < kVUnits; ++v) {        // v = 2 n + key half
+            W.wait(bar(kBarVFull + v), J & 1);
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t dO = tmem + kColO + 128 * (v >> 1);
+              const uint64_t bd = dv + (uint32_t)v * (C::kVUnit >> 4);
+              const uint32_t keep = (j > 0 || (v & 1)) ? 1u : 0u;
+              if (kFp8) {
+                const uint64_t ad = dpj + (uint32_t)(v & 1) * 4;  // 64 keys = 64 bytes
 #pragma unroll
-              for (int ks = 0; ks < 2; ++ks)
+                for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int x = 0; x < 3; ++x)
-                  mma_pair_e4m3(dO, ad + 2 * ks + x * (C::kPTerm >> 4), bd + 256 * ks, id,
-                                (keep || ks > 0 || x > 0) ? 1u : 0u);
-            } else {
-              const uint64_t ad = dpj + (uint32_t)(v & 1) * (kAtom >> 4);
+                  for (int x = 0; x < 3; ++x)
+                    mma_pair_e4m3(dO, ad + 2 * ks + x * (C::kPTerm >> 4), bd + 256 * ks, id,
+                                  (keep || ks > 0 || x > 0) ? 1u : 0u);
+              } else {
+                const uint64_t ad = dpj + (uint32_t)(v & 1) * (kAtom >> 4);
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_pair_bf16(dO, ad + 2 * ks, bd + 128 * ks, id, (keep || ks > 0) ? 1u : 0u);
+                for (int ks = 0; ks < 4; ++ks)
+                  mma_pair_bf16(dO, ad + 2 * ks, bd + 128 * ks, id, (keep || ks > 0) ? 1u : 0u);
+              }
+              mma_commit_pair(bar(kBarVEmpty + v));
+              if (v == kVUnits - 1) mma_commit_pair(bar(kBarPEmpty + pb));
             }
-            mma_commit_pair(bar(kBarVEmpty + v));
-            if (v == kVUnits - 1) mma_commit_pair(bar(kBarPEmpty + pb));
+            __syncwarp();
           }
-          __syncwarp();
         }
-       }
       }
       __syncwarp();
       if (elect_one()) mma_commit_pair(bar(kBarDrain + 1), 1);
@@ -802,79 +820,79 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     Unit u;
     int q = 0, J = 0;
     for (int i = 0; take_unit(i, u); ++i) {
-     if (!kFp8 && u.nb > 0) {
-      if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
-      if (stopped()) break;
-      if (lane == 0) {
-        if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
-#pragma unroll 1
-        for (int c = 0; c < a.atoms; ++c)
-          tma_load_2d_pair(sb + C::kOffQ + c * kAtom, &a.q_map, 64 * c, u.row0 + 64 * (int)r,
-                           bar0(kBarQFull));
-      }
-      ++q;
-      __syncwarp();
-     }
-     for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
-      W.wait(bar(kBarMFull + mr.m), mr.ph);
-      int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + 16 * r + (lane & 15)];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
-      // (rows of a block that no row of the tile sees come along: their scores
-      // are replaced)
-      const bool boxed = whole_box(id);
-      const uint32_t ktile = sb + C::kOffK;
-      if (a.box == 64 && __all_sync(0xffffffffu, boxed)) {   // the 64 rows as one box
-        if (elect_one()) {
-#pragma unroll 1
-          for (int g = 0; g < groups; ++g) {
-            if (J >= 1 && !W.wait(bar(kBarKEmpty + g), (J - 1) & 1)) break;
-            const int c0 = g * C::kAtomsPerGroup;
-            const uint32_t dst = ktile + c0 * kAtom;
-            // E4M3 rows of 576 end in half a column, which the map of whole
-            // columns leaves out.  bf16: a column past a row of 512 reads zeros
-            // into the tile's spare atom.
-            const bool half = kFp8 && c0 + 1 == a.atoms;
-            if (r == 0)
-              mbar_arrive_expect_tx(bar(kBarKFull + g),
-                                    2u * (half ? 1u : (uint32_t)C::kAtomsPerGroup) * kAtom);
-            if (half)
-              tma_load_2d_pair(dst, &a.box_map, cols * c0, id.x, kfull0 + 8u * g);
-            else
-              tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * g);
-            ++issued;
-          }
-        }
-        __syncwarp();
+      if (!kFp8 && u.nb > 0) {
+        if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
         if (stopped()) break;
-        continue;
-      }
+        if (lane == 0) {
+          if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
 #pragma unroll 1
-      for (int g = 0; g < groups; ++g) {
-        if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
-        if (stopped()) break;
-        const int c0 = g * C::kAtomsPerGroup;
-        // (as many columns as the other CTA's whole groups have)
-        const int c1 = kFp8 ? min(c0 + C::kAtomsPerGroup, a.atoms) : c0 + C::kAtomsPerGroup;
-        if (r == 0 && lane == 0)
-          mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * (uint32_t)(c1 - c0) * kAtom);
-        __syncwarp();
-        if (lane < 16 && (!boxed || (lane & (per - 1)) == 0)) {
-#pragma unroll 1
-          for (int c = c0; c < c1; ++c) {
-            const uint32_t dst = ktile + c * kAtom + 4 * lane * 128;
-            if (boxed)
-              tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, kfull0 + 8u * g);
-            else
-              tma_gather4_pair(dst, &a.row_map, cols * c, id.x, id.y, id.z, id.w,
-                               kfull0 + 8u * g);
-          }
+          for (int c = 0; c < a.atoms; ++c)
+            tma_load_2d_pair(sb + C::kOffQ + c * kAtom, &a.q_map, 64 * c, u.row0 + 64 * (int)r,
+                             bar0(kBarQFull));
         }
-        ++issued;
+        ++q;
         __syncwarp();
       }
-      if (stopped()) break;
-     }
+      for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
+        W.wait(bar(kBarMFull + mr.m), mr.ph);
+        int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + 16 * r + (lane & 15)];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
+        // (rows of a block that no row of the tile sees come along: their scores
+        // are replaced)
+        const bool boxed = whole_box(id);
+        const uint32_t ktile = sb + C::kOffK;
+        if (a.box == 64 && __all_sync(0xffffffffu, boxed)) {  // the 64 rows as one box
+          if (elect_one()) {
+#pragma unroll 1
+            for (int g = 0; g < groups; ++g) {
+              if (J >= 1 && !W.wait(bar(kBarKEmpty + g), (J - 1) & 1)) break;
+              const int c0 = g * C::kAtomsPerGroup;
+              const uint32_t dst = ktile + c0 * kAtom;
+              // E4M3 rows of 576 end in half a column, which the map of whole
+              // columns leaves out.  bf16: a column past a row of 512 reads zeros
+              // into the tile's spare atom.
+              const bool half = kFp8 && c0 + 1 == a.atoms;
+              if (r == 0)
+                mbar_arrive_expect_tx(bar(kBarKFull + g),
+                                      2u * (half ? 1u : (uint32_t)C::kAtomsPerGroup) * kAtom);
+              if (half)
+                tma_load_2d_pair(dst, &a.box_map, cols * c0, id.x, kfull0 + 8u * g);
+              else
+                tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * g);
+              ++issued;
+            }
+          }
+          issued = __reduce_max_sync(0xffffffffu, issued);     // (the elected lane's)
+          if (stopped()) break;
+          continue;
+        }
+#pragma unroll 1
+        for (int g = 0; g < groups; ++g) {
+          if (J >= 1) W.wait(bar(kBarKEmpty + g), (J - 1) & 1);
+          if (stopped()) break;
+          const int c0 = g * C::kAtomsPerGroup;
+          // (as many columns as the other CTA's whole groups have)
+          const int c1 = kFp8 ? min(c0 + C::kAtomsPerGroup, a.atoms) : c0 + C::kAtomsPerGroup;
+          if (r == 0 && lane == 0)
+            mbar_arrive_expect_tx(bar(kBarKFull + g), 2u * (uint32_t)(c1 - c0) * kAtom);
+          __syncwarp();
+          if (lane < 16 && (!boxed || (lane & (per - 1)) == 0)) {
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+              const uint32_t dst = ktile + c * kAtom + 4 * lane * 128;
+              if (boxed)
+                tma_load_2d_pair(dst, &a.box_map, cols * c, id.x, kfull0 + 8u * g);
+              else
+                tma_gather4_pair(dst, &a.row_map, cols * c, id.x, id.y, id.z, id.w,
+                                 kfull0 + 8u * g);
+            }
+          }
+          ++issued;
+          __syncwarp();
+        }
+        if (stopped()) break;
+      }
     }
     // Teardown: the last copies into each part have landed in both CTAs (the
     // even CTA's barriers count both; earlier ones were consumed).
@@ -893,74 +911,74 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       MetaRing mr;
       Unit u;
       for (int i = 0; take_unit(i, u); ++i) {
-       for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
-        W.wait(bar(kBarMFull + mr.m), mr.ph);
-        int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + lane];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
-        // Rows behind the last token may never have been written, and a weight of
-        // 0 times NaN is NaN: they are read as zeros.  (The other rows of a block
-        // were written; one that is not finite costs the tile slow_row.)
-        const int up = u.live - 2 - (u.block(u.b0 + j) * kBN + 4 * lane);
-        if (up < 0) id.x = -1;
-        if (up < 1) id.y = -1;
-        if (up < 2) id.z = -1;
-        if (up < 3) id.w = -1;
-        const bool boxed = whole_box(id);
-        if (!kFp8 && a.box == 64 && __all_sync(0xffffffffu, boxed)) {   // two whole boxes
-          const int far = __shfl_sync(0xffffffffu, id.x, 16);
-          bool on = true;
-          if (elect_one()) {
+        for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
+          W.wait(bar(kBarMFull + mr.m), mr.ph);
+          int4 id = reinterpret_cast<const int4*>(sm + C::kOffIds)[32 * mr.m + lane];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
+          // Rows behind the last token may never have been written, and a weight of
+          // 0 times NaN is NaN: they are read as zeros.  (The other rows of a block
+          // were written; one that is not finite costs the tile slow_row.)
+          const int up = u.live - 2 - (u.block(u.b0 + j) * kBN + 4 * lane);
+          if (up < 0) id.x = -1;
+          if (up < 1) id.y = -1;
+          if (up < 2) id.z = -1;
+          if (up < 3) id.w = -1;
+          const bool boxed = whole_box(id);
+          if (!kFp8 && a.box == 64 && __all_sync(0xffffffffu, boxed)) {  // two whole boxes
+            const int far = __shfl_sync(0xffffffffu, id.x, 16);
+            bool on = true;
+            if (elect_one()) {
 #pragma unroll 1
-            for (int v = 0; v < kVUnits; ++v) {
-              if (J >= 1 && !W.wait(bar(kBarVEmpty + v), (J - 1) & 1)) {
-                on = false;
-                break;
+              for (int v = 0; v < kVUnits; ++v) {
+                if (J >= 1 && !W.wait(bar(kBarVEmpty + v), (J - 1) & 1)) {
+                  on = false;
+                  break;
+                }
+                if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
+                const int ch = 256 * (v >> 1) + 128 * (int)r, row = v & 1 ? far : id.x;
+                const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
+                if (kFp8)
+                  tma_load_2d_pair(slot, &a.box_map, ch, row, vfull0 + 8u * v);
+                else
+                  tma_load_3d_pair(slot, &a.v_map, 0, row, ch / 64, vfull0 + 8u * v);
+                ++issued;
               }
-              if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
-              const int ch = 256 * (v >> 1) + 128 * (int)r, row = v & 1 ? far : id.x;
-              const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
-              if (kFp8)
-                tma_load_2d_pair(slot, &a.box_map, ch, row, vfull0 + 8u * v);
-              else
-                tma_load_3d_pair(slot, &a.v_map, 0, row, ch / 64, vfull0 + 8u * v);
-              ++issued;
             }
+            issued = __reduce_max_sync(0xffffffffu, issued);   // (the elected lane's)
+            if (__any_sync(0xffffffffu, !on)) break;
+            continue;
           }
-          __syncwarp();
-          if (__any_sync(0xffffffffu, !on)) break;
-          continue;
-        }
-        // The 16 lanes of a key half: one copy by its first lane where the half is
-        // one piece of a cache block, a box per lane group, or four rows per lane.
+          // The 16 lanes of a key half: one copy by its first lane where the half is
+          // one piece of a cache block, a box per lane group, or four rows per lane.
 #pragma unroll 1
-        for (int v = 0; v < kVUnits; ++v) {
-          if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
+          for (int v = 0; v < kVUnits; ++v) {
+            if (J >= 1) W.wait(bar(kBarVEmpty + v), (J - 1) & 1);
+            if (stopped()) break;
+            if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
+            __syncwarp();
+            const uint32_t full_bar = vfull0 + 8u * v;
+            const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
+            if ((lane >> 4) == (v & 1) && (!boxed || (lane & (per - 1)) == 0)) {
+              const int ch = 256 * (v >> 1) + 128 * (int)r;
+              const bool one = !kFp8 && boxed && per == 16;
+              if (one)
+                tma_load_3d_pair(slot, &a.v_map, 0, id.x, ch / 64, full_bar);
+#pragma unroll 1
+              for (int c = 0; !one && c < (int)(C::kVUnit / kAtom); ++c) {
+                const uint32_t dst = slot + c * kAtom + 4 * (lane & 15) * 128;
+                if (boxed)
+                  tma_load_2d_pair(dst, &a.box_map, ch + 64 * c, id.x, full_bar);
+                else
+                  tma_gather4_pair(dst, &a.row_map, ch + 64 * c, id.x, id.y, id.z, id.w, full_bar);
+              }
+            }
+            ++issued;
+            __syncwarp();
+          }
           if (stopped()) break;
-          if (r == 0 && lane == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
-          __syncwarp();
-          const uint32_t full_bar = vfull0 + 8u * v;
-          const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
-          if ((lane >> 4) == (v & 1) && (!boxed || (lane & (per - 1)) == 0)) {
-            const int ch = 256 * (v >> 1) + 128 * (int)r;
-            const bool one = !kFp8 && boxed && per == 16;
-            if (one)
-              tma_load_3d_pair(slot, &a.v_map, 0, id.x, ch / 64, full_bar);
-#pragma unroll 1
-            for (int c = 0; !one && c < (int)(C::kVUnit / kAtom); ++c) {
-              const uint32_t dst = slot + c * kAtom + 4 * (lane & 15) * 128;
-              if (boxed)
-                tma_load_2d_pair(dst, &a.box_map, ch + 64 * c, id.x, full_bar);
-              else
-                tma_gather4_pair(dst, &a.row_map, ch + 64 * c, id.x, id.y, id.z, id.w, full_bar);
-            }
-          }
-          ++issued;
-          __syncwarp();
         }
         if (stopped()) break;
-       }
-       if (stopped()) break;
       }
       if (r == 0 && lane == 0)
 #pragma unroll 1
@@ -1031,6 +1049,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         __syncwarp();
       }
       const Unit u = next;
+      bad |= u.row1 > u.row0 && u.p_last > p.table_end;
       if (u.row1 > u.row0) publish(u);
       Found f = found(e0);
       for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
@@ -1147,325 +1166,328 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     MetaRing mr;
     int J = 0, q = 0;                                  // blocks, units with blocks
     for (int i = 0;; ++i) {
-    const Unit* t = peek_unit(i);
-    // (all eight warps leave together: they share the named barriers below)
-    if (named_bar_or(4, 256, !t->live || W.aborted())) break;
-    int pos = -1, lo = 0;                              // the row's token sees [lo, pos], sinks
-    {
-      const int g = t->row0 + 64 * (int)r + row;
-      if (g < t->row1) pos = t->p_last - ((t->row1 - 1) / p.h - g / p.h);
-      if (p.window) lo = max(pos - (p.window - 1), 0);
-    }
-    const int nb = t->nb;
-    // A warp whose 32 rows lie behind the tile's last only keeps step: nothing reads
-    // the O that its weights, whatever is in P, make (a mixed batch with 16 heads:
-    // 263 -> 258 us).
-    const bool idle = t->row0 + 64 * (int)r + (row & 32) >= t->row1;
-    float qs = 1.f;
-    if (kFp8 && nb > 0) {
-      W.wait(bar(kBarQScale), q & 1);
-      qs = reinterpret_cast<const float*>(sm + C::kOffQScale)[kRows * (q & 1) + row];
-      ++q;
-    }
-    const float scale = a.scale_log2 * qs * kscale;
-    float m_run = -INFINITY;   // running max (log2 units), the same in a row's four threads
-    float l_run = 0.f;         // this thread's sum of exp2(s - m_run)
-    float lr_run = 0.f;        // the same sum of the bf16-rounded weights
-    int blk = nb > 0 ? t->block(t->b0) : 0;
-    const int jump = t->sink_blocks - t->b0;             // the block behind the sinks'
-    for (int j = 0; j < nb; ++j, ++J, mr.next()) {
-      const int buf = J & 1, m = mr.m;
-      const int e0 = blk * kBN + 32 * seg;               // this thread's first key
-      blk = j + 1 == jump ? t->win_block : blk + 1;
-      W.wait(bar(kBarMFull + m), mr.ph);
-      uint32_t see = words[4 * m + seg];
-      W.wait(bar(kBarSFull + buf), (J >> 1) & 1);
-      __syncwarp();
-      if (idle) {
-        if (lane == 0) {
-          mbar_signal_remote(sempty + 8u * buf);
-          mbar_arrive(bar(kBarMEmpty + m));
-        }
-        named_bar_or(4, 256, false);
-        if (J >= C::kPBufs) W.wait(bar(kBarPEmpty + J % C::kPBufs), (J / C::kPBufs - 1) & 1);
+      const Unit* t = peek_unit(i);
+      // (all eight warps leave together: they share the named barriers below)
+      if (named_bar_or(4, 256, !t->live || W.aborted())) break;
+      int pos = -1, lo = 0;                            // the row's token sees [lo, pos], sinks
+      {
+        const int g = t->row0 + 64 * (int)r + row;
+        if (g < t->row1) pos = t->p_last - ((t->row1 - 1) / p.h - g / p.h);
+        if (p.window) lo = max(pos - (p.window - 1), 0);
+      }
+      const int nb = t->nb;
+      // A warp whose 32 rows lie behind the tile's last only keeps step: nothing reads
+      // the O that its weights, whatever is in P, make (a mixed batch with 16 heads:
+      // 263 -> 258 us).
+      const bool idle = t->row0 + 64 * (int)r + (row & 32) >= t->row1;
+      float qs = 1.f;
+      if (kFp8 && nb > 0) {
+        W.wait(bar(kBarQScale), q & 1);
+        qs = reinterpret_cast<const float*>(sm + C::kOffQScale)[kRows * (q & 1) + row];
+        ++q;
+      }
+      const float scale = a.scale_log2 * qs * kscale;
+      float m_run = -INFINITY;  // running max (log2 units), the same in a row's four threads
+      float l_run = 0.f;       // this thread's sum of exp2(s - m_run)
+      float lr_run = 0.f;      // the same sum of the bf16-rounded weights
+      int blk = nb > 0 ? t->block(t->b0) : 0;
+      const int jump = t->sink_blocks - t->b0;           // the block behind the sinks'
+      for (int j = 0; j < nb; ++j, ++J, mr.next()) {
+        const int buf = J & 1, m = mr.m;
+        const int e0 = blk * kBN + 32 * seg;             // this thread's first key
+        blk = j + 1 == jump ? t->win_block : blk + 1;
+        W.wait(bar(kBarMFull + m), mr.ph);
+        uint32_t see = words[4 * m + seg];
+        W.wait(bar(kBarSFull + buf), (J >> 1) & 1);
         __syncwarp();
-        if (lane == 0) mbar_signal_remote(pfull + 8u * (J % C::kPBufs));
-        continue;
-      }
-      tc_fence_after();
-      // The row's view of its 32 keys.
-      {
-        const int up = pos - e0;                         // keys 0 .. up
-        uint32_t v = up >= 31 ? ~0u : up < 0 ? 0u : (2u << up) - 1u;
-        const int dn = lo - e0;                          // keys dn ..
-        const uint32_t win = dn <= 0 ? ~0u : dn > 31 ? 0u : ~0u << dn;
-        const int sk = p.sinks - e0;                     // keys .. sk - 1
-        const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? ~0u : (1u << sk) - 1u;
-        see &= v & (win | snk);
-      }
-      float s[32];
-      {
-        uint32_t w0[16], w1[16];
-        const uint32_t col = tmem + lane_base + kColS + 64 * buf + 32 * wg;
-        tmem_ld16(col, w0);
-        tmem_ld16(col + 16, w1);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          s[k] = __uint_as_float(w0[k]);
-          s[16 + k] = __uint_as_float(w1[k]);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_signal_remote(sempty + 8u * buf);
-      // Scores in log2 units are s * cl: where nothing is masked and the 32
-      // keys share their scale they stay as the MMA left them (the factor is
-      // positive and keeps their order).
-      float cl = scale;
-      // E4M3: the weights are 2^(t - m), t = s + log2(key's scale); `shift` is
-      // that log2 and `back` the reciprocal for the 32 keys' common scale.
-      float shift = 0.f, back = 1.f;
-      bool several = false;
-      const float* ks = reinterpret_cast<const float*>(sm + C::kOffScale) + kBN * m + 32 * seg;
-      if (kFp8) {
-        const float4 own = reinterpret_cast<const float4*>(sm + C::kOffSeg)[4 * m + seg];
-        cl *= own.x;
-        shift = own.y;
-        back = own.z;
-        several = !(own.x > 0.f);
-        if (__builtin_expect(several, 0)) {
-          cl = 1.f;
-          back = 0.f;                                    // (their sums are taken below)
-#pragma unroll
-          for (int k = 0; k < 32; ++k) s[k] = s[k] * (ks[k] * scale) + __log2f(ks[k]);
-        }
-      }
-      if (__builtin_expect(!__all_sync(0xffffffffu, see == ~0u && cl > 0.f), 0)) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] * cl : -INFINITY;
-        cl = 1.f;
-      }
-      float hm = fmaxf(s[0], s[1]);
-#pragma unroll
-      for (int k = 2; k < 32; k += 2) hm = max3(hm, s[k], s[k + 1]);
-      hm = fmaf(hm, cl, shift);
-      // The row's reference is the largest of its four maxima (bf16 rows: rounded
-      // to bf16, any value near the maximum serves): all four threads take the
-      // same one.
-      Red* rb = red + 256 * buf;
-      if constexpr (kFp8)
-        rb[64 * seg + row] = hm;
-      else
-        rb[64 * seg + row] = __float2bfloat16(hm);
-      float alpha = 1.f;
-      if (named_bar_or(4, 256, hm > m_run + 8.f)) {      // also true for the first finite max
-        float bm = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) bm = fmaxf(bm, static_cast<float>(rb[64 * k + row]));
-        if (bm > m_run + 7.f) {
-          alpha = ex2_approx(m_run - bm);                // 0 when m_run = -inf
-          m_run = bm;
-        }
-      }
-      // bf16: 16 pairs of weights.  E4M3: three terms of four weights a word.
-      uint32_t pk[kFp8 ? 24 : 16];
-      float ls = 0.f, ls1 = 0.f, lr = 0.f, lr1 = 0.f;
-      const float mm = (m_run == -INFINITY ? 0.f : m_run) - shift;  // (no score: weights are 0)
-      if constexpr (kFp8) {
-        // 2^(t - m + 7) <= 2^15: within E5M2's range, its grid 2^-23 of a weight
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          uint32_t h[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& s0 = s[k + 2 * e];
-            float& s1 = s[k + 2 * e + 1];
-            fma2_bcast(s0, s1, cl, 7.f - mm);
-            const float w0 = ex2_approx(s0), w1 = ex2_approx(s1);
-            add2(ls, ls1, w0, w1);
-            h[e] = (pack_f16(w0, w1) + 0x00020002u) & 0xFFFCFFFCu;   // 9 significant bits
-            add_f16x2_f32x2(lr, lr1, h[e]);
-            s0 = w0;
-            s1 = w1;
+        if (idle) {
+          if (lane == 0) {
+            mbar_signal_remote(sempty + 8u * buf);
+            mbar_arrive(bar(kBarMEmpty + m));
           }
+          named_bar_or(4, 256, false);
+          if (J >= C::kPBufs) W.wait(bar(kBarPEmpty + J % C::kPBufs), (J / C::kPBufs - 1) & 1);
+          __syncwarp();
+          if (lane == 0) mbar_signal_remote(pfull + 8u * (J % C::kPBufs));
+          continue;
+        }
+        tc_fence_after();
+        // The row's view of its 32 keys.
+        {
+          const int up = pos - e0;                       // keys 0 .. up
+          uint32_t v = up >= 31 ? ~0u : up < 0 ? 0u : (2u << up) - 1u;
+          const int dn = lo - e0;                        // keys dn ..
+          const uint32_t win = dn <= 0 ? ~0u : dn > 31 ? 0u : ~0u << dn;
+          const int sk = p.sinks - e0;                   // keys .. sk - 1
+          const uint32_t snk = sk <= 0 ? 0u : sk > 31 ? ~0u : (1u << sk) - 1u;
+          see &= v & (win | snk);
+        }
+        float s[32];
+        {
+          uint32_t w0[16], w1[16];
+          const uint32_t col = tmem + lane_base + kColS + 64 * buf + 32 * wg;
+          tmem_ld16(col, w0);
+          tmem_ld16(col + 16, w1);
+          tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 3; ++x) {
-            pk[8 * x + k / 4] = __byte_perm(h[0], h[1], 0x7531);     // the four upper bytes
-            if (x < 2) {
-              h[0] = sub_f16x2(h[0], h[0] & 0xFF00FF00u);
-              h[1] = sub_f16x2(h[1], h[1] & 0xFF00FF00u);
+          for (int k = 0; k < 16; ++k) {
+            s[k] = __uint_as_float(w0[k]);
+            s[16 + k] = __uint_as_float(w1[k]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_signal_remote(sempty + 8u * buf);
+        // Scores in log2 units are s * cl: where nothing is masked and the 32
+        // keys share their scale they stay as the MMA left them (the factor is
+        // positive and keeps their order).
+        float cl = scale;
+        // E4M3: the weights are 2^(t - m), t = s + log2(key's scale); `shift` is
+        // that log2 and `back` the reciprocal for the 32 keys' common scale.
+        float shift = 0.f, back = 1.f;
+        bool several = false;
+        const float* ks = reinterpret_cast<const float*>(sm + C::kOffScale) + kBN * m + 32 * seg;
+        if (kFp8) {
+          const float4 own = reinterpret_cast<const float4*>(sm + C::kOffSeg)[4 * m + seg];
+          cl *= own.x;
+          shift = own.y;
+          back = own.z;
+          several = !(own.x > 0.f);
+          if (__builtin_expect(several, 0)) {
+            cl = 1.f;
+            back = 0.f;                                  // (their sums are taken below)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[k] = s[k] * (ks[k] * scale) + __log2f(ks[k]);
+          }
+        }
+        if (__builtin_expect(!__all_sync(0xffffffffu, see == ~0u && cl > 0.f), 0)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1u ? s[k] * cl : -INFINITY;
+          cl = 1.f;
+        }
+        float hm = fmaxf(s[0], s[1]);
+#pragma unroll
+        for (int k = 2; k < 32; k += 2) hm = max3(hm, s[k], s[k + 1]);
+        hm = fmaf(hm, cl, shift);
+        // The row's reference is the largest of its four maxima (bf16 rows: rounded
+        // to bf16, any value near the maximum serves): all four threads take the
+        // same one.
+        Red* rb = red + 256 * buf;
+        if constexpr (kFp8)
+          rb[64 * seg + row] = hm;
+        else
+          rb[64 * seg + row] = __float2bfloat16(hm);
+        float alpha = 1.f;
+        if (named_bar_or(4, 256, hm > m_run + 8.f)) {    // also true for the first finite max
+          float bm = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) bm = fmaxf(bm, static_cast<float>(rb[64 * k + row]));
+          if (bm > m_run + 7.f) {
+            alpha = ex2_approx(m_run - bm);              // 0 when m_run = -inf
+            m_run = bm;
+          }
+        }
+        // bf16: 16 pairs of weights.  E4M3: three terms of four weights a word.
+        uint32_t pk[kFp8 ? 24 : 16];
+        float ls = 0.f, ls1 = 0.f, lr = 0.f, lr1 = 0.f;
+        const float mm = (m_run == -INFINITY ? 0.f : m_run) - shift;  // (no score: weights are 0)
+        if constexpr (kFp8) {
+          // 2^(t - m + 7) <= 2^15: within E5M2's range, its grid 2^-23 of a weight
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            uint32_t h[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& s0 = s[k + 2 * e];
+              float& s1 = s[k + 2 * e + 1];
+              fma2_bcast(s0, s1, cl, 7.f - mm);
+              const float w0 = ex2_approx(s0), w1 = ex2_approx(s1);
+              add2(ls, ls1, w0, w1);
+              h[e] = (pack_f16(w0, w1) + 0x00020002u) & 0xFFFCFFFCu;  // 9 significant bits
+              add_f16x2_f32x2(lr, lr1, h[e]);
+              s0 = w0;
+              s1 = w1;
+            }
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+              pk[8 * x + k / 4] = __byte_perm(h[0], h[1], 0x7531);   // the four upper bytes
+              if (x < 2) {
+                h[0] = sub_f16x2(h[0], h[0] & 0xFF00FF00u);
+                h[1] = sub_f16x2(h[1], h[1] & 0xFF00FF00u);
+              }
+            }
+          }
+          back *= 0x1p-7f;
+          ls = (ls + ls1) * back;
+          lr = (lr + lr1) * back;
+          if (__builtin_expect(several, 0)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              ls += ks[k] > 0.f ? __fdividef(s[k] * 0x1p-7f, ks[k]) : 0.f;
+            // (a zero scale: key and value are zero, its weight is 2^(0 - m))
+#pragma unroll 1
+            for (int k = 0; k < 32; ++k)
+              if (ks[k] == 0.f && (see >> k & 1u)) ls += ex2_approx(-mm);
+            lr = ls;                                     // (9 bits: 2^-9 of a weight at most)
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            fma2_bcast(s[k], s[k + 1], cl, -mm);
+            const float w0 = ex2_approx(s[k]), w1 = ex2_approx(s[k + 1]);
+            add2(ls, ls1, w0, w1);
+            pk[k / 2] = pack_bf16(w0, w1);
+            add_bf16x2_f32x2(lr, lr1, pk[k / 2]);
+          }
+          ls += ls1;
+          lr += lr1;
+        }
+        l_run = l_run * alpha + ls;
+        lr_run = lr_run * alpha + lr;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));  // the lookups were read
+        if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);  // PV(j - 1)
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 128 * wg; c < 128 * wg + 128; c += 16) {
+            uint32_t w[16];
+            tmem_ld16(tmem + lane_base + kColO + c, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
+            tmem_st16(tmem + lane_base + kColO + c, w);
+          }
+          tmem_wait_st();
+        }
+        const int pb = J % C::kPBufs;
+        if (J >= C::kPBufs)                              // the buffer was read
+          W.wait(bar(kBarPEmpty + pb), (J / C::kPBufs - 1) & 1);
+        // P row: bf16, keys 64 half + 32 wg .. + 31 as chunks 4 wg .. of atom `half`;
+        // E4M3, bytes 32 seg .. + 31 of each term's row.
+        uint8_t* prow = sm + C::kOffP + pb * (C::kPTerms * C::kPTerm) + row * 128;
+        const uint32_t sw = (uint32_t)row & 7u;
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int x = 0; x < 3; ++x)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<uint4*>(prow + x * C::kPTerm +
+                                        (((uint32_t)(2 * seg + c) ^ sw) << 4)) =
+                  make_uint4(pk[8 * x + 4 * c], pk[8 * x + 4 * c + 1], pk[8 * x + 4 * c + 2],
+                             pk[8 * x + 4 * c + 3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(prow + half * kAtom + (((uint32_t)(4 * wg + c) ^ sw) << 4)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_signal_remote(pfull + 8u * pb);
+      }
+
+      // ---- epilogue -------------------------------------------------------------
+      if (nb > 0) {
+        W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);
+        __syncwarp();
+        tc_fence_after();
+      }
+      float* sums = reinterpret_cast<float*>(sm + C::kOffP + kOffSums);
+      int* flag = reinterpret_cast<int*>(sm + C::kOffP + kOffFlag);
+      sums[64 * seg + row] = l_run;
+      sums[256 + 64 * seg + row] = lr_run;
+      if (seg == 0) flag[row] = 0;
+      named_bar_sync(4, 256);
+      float l = 0.f, lr = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l += sums[64 * k + row];
+        lr += sums[256 + 64 * k + row];
+      }
+      const bool empty = l == 0.f;
+      // (a sum that is not finite: NaN, whatever the weights' terms became)
+      const float top = kFp8 ? kscale * 0x1p-7f : kscale;
+      const float inv = empty ? 0.f : l < INFINITY ? __fdividef(top, lr) : NAN;
+      const bool partial = t->slot >= 0;
+      const int64_t g = (int64_t)t->row0 + 64 * (int)r + row;
+      const bool live = g < t->row1;
+      const int64_t prow_g = (int64_t)t->slot * 128 + 64 * (int)r + row;  // row of the partials
+      // O columns [128 wg, + 128) are channels 256 wg + 128 half ..; a thread's
+      // stores fill whole 32-byte sectors, straight from registers.
+      const int ch0 = 256 * wg + 128 * half;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
+      bool odd = false;                                  // an output that is not finite
+#pragma unroll 1
+      for (int c4 = idle ? 128 : 0; c4 < 128; c4 += 32) {  // (32 columns per TMEM wait)
+        uint32_t wide[2][16];
+        __syncwarp();
+        if (nb > 0) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            tmem_ld16(tmem + lane_base + kColO + 128 * wg + c4 + 16 * x, wide[x]);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t (&w)[16] = wide[x];
+          const int c = c4 + 16 * x;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float o = empty ? 0.f : __uint_as_float(w[k]) * inv;
+            odd |= !(fabsf(o) < INFINITY);
+            w[k] = __float_as_uint(o);
+          }
+          if (live && partial && !empty) {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.o_part + prow_g * 512 + ch0 + c);
+            st_global_32(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+            st_global_32(dst + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+          }
+          if (live && !partial) {
+            uint32_t b[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              b[k] = pack_bf16(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+            uint32_t* dst = reinterpret_cast<uint32_t*>(out + g * 512 + ch0 + c);
+            if (a.wide) {
+              st_global_32(dst, b[0], b[1], b[2], b[3], b[4], b[5], b[6], b[7]);
+            } else {
+              reinterpret_cast<uint4*>(dst)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+              reinterpret_cast<uint4*>(dst)[1] = make_uint4(b[4], b[5], b[6], b[7]);
             }
           }
         }
-        back *= 0x1p-7f;
-        ls = (ls + ls1) * back;
-        lr = (lr + lr1) * back;
-        if (__builtin_expect(several, 0)) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) ls += ks[k] > 0.f ? __fdividef(s[k] * 0x1p-7f, ks[k]) : 0.f;
-          // (a zero scale: key and value are zero, its weight is 2^(0 - m))
-#pragma unroll 1
-          for (int k = 0; k < 32; ++k)
-            if (ks[k] == 0.f && (see >> k & 1u)) ls += ex2_approx(-mm);
-          lr = ls;                                       // (9 bits: 2^-9 of a weight at most)
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          fma2_bcast(s[k], s[k + 1], cl, -mm);
-          const float w0 = ex2_approx(s[k]), w1 = ex2_approx(s[k + 1]);
-          add2(ls, ls1, w0, w1);
-          pk[k / 2] = pack_bf16(w0, w1);
-          add_bf16x2_f32x2(lr, lr1, pk[k / 2]);
-        }
-        ls += ls1;
-        lr += lr1;
       }
-      l_run = l_run * alpha + ls;
-      lr_run = lr_run * alpha + lr;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));   // the lookups were read
-      if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);  // PV(j - 1)
-        __syncwarp();
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 128 * wg; c < 128 * wg + 128; c += 16) {
-          uint32_t w[16];
-          tmem_ld16(tmem + lane_base + kColO + c, w);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
-          tmem_st16(tmem + lane_base + kColO + c, w);
+      if (live && seg == 0) {
+        const float v = empty ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
+        if (partial)
+          p.lse_part[prow_g] = v;
+        else if (p.lse)
+          p.lse[g] = v;
+      }
+      // A softmax that is not finite (a NaN or infinite visible score) is the
+      // answer; a finite one with an output that is not may owe it to a masked
+      // position: the row is computed again and written over.
+      odd = odd && live && l < INFINITY && lr < INFINITY;
+      if (odd) flag[row] = 1;
+      if (__builtin_expect(named_bar_or(4, 256, odd), 0)) {  // (also orders the stores before)
+        for (int rr = warp - 4; rr < kRows; rr += 8) {
+          if (!flag[rr]) continue;
+          const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
+          const int pr = t->p_last - ((t->row1 - 1) / p.h - (int)gr / p.h);
+          slow_row<kFp8>(p, *t, gr, pr, p.window ? max(pr - (p.window - 1), 0) : 0,
+                         partial ? p.o_part + ((int64_t)t->slot * 128 + 64 * (int)r + rr) * 512
+                                 : nullptr,
+                         out + gr * 512);
         }
-        tmem_wait_st();
+        named_bar_sync(4, 256);                          // the flags were read
       }
-      const int pb = J % C::kPBufs;
-      if (J >= C::kPBufs)                                // the buffer was read
-        W.wait(bar(kBarPEmpty + pb), (J / C::kPBufs - 1) & 1);
-      // P row: bf16, keys 64 half + 32 wg .. + 31 as chunks 4 wg .. of atom `half`;
-      // E4M3, bytes 32 seg .. + 31 of each term's row.
-      uint8_t* prow = sm + C::kOffP + pb * (C::kPTerms * C::kPTerm) + row * 128;
-      const uint32_t sw = (uint32_t)row & 7u;
-      if constexpr (kFp8) {
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<uint4*>(prow + x * C::kPTerm + (((uint32_t)(2 * seg + c) ^ sw) << 4)) =
-                make_uint4(pk[8 * x + 4 * c], pk[8 * x + 4 * c + 1], pk[8 * x + 4 * c + 2],
-                           pk[8 * x + 4 * c + 3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(prow + half * kAtom + (((uint32_t)(4 * wg + c) ^ sw) << 4)) =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-      }
-      fence_proxy_async_smem();
+      // (the next unit's first weights are signalled behind these TMEM loads)
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_signal_remote(pfull + 8u * pb);
-    }
-
-    // ---- epilogue -------------------------------------------------------------
-    if (nb > 0) {
-      W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);
-      __syncwarp();
-      tc_fence_after();
-    }
-    float* sums = reinterpret_cast<float*>(sm + C::kOffP + kOffSums);
-    int* flag = reinterpret_cast<int*>(sm + C::kOffP + kOffFlag);
-    sums[64 * seg + row] = l_run;
-    sums[256 + 64 * seg + row] = lr_run;
-    if (seg == 0) flag[row] = 0;
-    named_bar_sync(4, 256);
-    float l = 0.f, lr = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      l += sums[64 * k + row];
-      lr += sums[256 + 64 * k + row];
-    }
-    const bool empty = l == 0.f;
-    // (a sum that is not finite: NaN, whatever the weights' terms became)
-    const float inv = empty ? 0.f : l < INFINITY ? __fdividef(kFp8 ? kscale * 0x1p-7f : kscale, lr)
-                                                 : NAN;
-    const bool partial = t->slot >= 0;
-    const int64_t g = (int64_t)t->row0 + 64 * (int)r + row;
-    const bool live = g < t->row1;
-    const int64_t prow_g = (int64_t)t->slot * 128 + 64 * (int)r + row;  // row of the partials
-    // O columns [128 wg, + 128) are channels 256 wg + 128 half ..; a thread's
-    // stores fill whole 32-byte sectors, straight from registers.
-    const int ch0 = 256 * wg + 128 * half;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-    bool odd = false;                                    // an output that is not finite
-#pragma unroll 1
-    for (int c4 = idle ? 128 : 0; c4 < 128; c4 += 32) {  // (32 columns per TMEM wait)
-      uint32_t wide[2][16];
-      __syncwarp();
-      if (nb > 0) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          tmem_ld16(tmem + lane_base + kColO + 128 * wg + c4 + 16 * x, wide[x]);
-        tmem_wait_ld();
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t (&w)[16] = wide[x];
-        const int c = c4 + 16 * x;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float o = empty ? 0.f : __uint_as_float(w[k]) * inv;
-          odd |= !(fabsf(o) < INFINITY);
-          w[k] = __float_as_uint(o);
-        }
-        if (live && partial && !empty) {
-          uint32_t* dst = reinterpret_cast<uint32_t*>(p.o_part + prow_g * 512 + ch0 + c);
-          st_global_32(dst, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-          st_global_32(dst + 8, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
-        }
-        if (live && !partial) {
-          uint32_t b[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            b[k] = pack_bf16(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
-          uint32_t* dst = reinterpret_cast<uint32_t*>(out + g * 512 + ch0 + c);
-          if (a.wide) {
-            st_global_32(dst, b[0], b[1], b[2], b[3], b[4], b[5], b[6], b[7]);
-          } else {
-            reinterpret_cast<uint4*>(dst)[0] = make_uint4(b[0], b[1], b[2], b[3]);
-            reinterpret_cast<uint4*>(dst)[1] = make_uint4(b[4], b[5], b[6], b[7]);
-          }
-        }
-      }
-    }
-    if (live && seg == 0) {
-      const float v = empty ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
-      if (partial)
-        p.lse_part[prow_g] = v;
-      else if (p.lse)
-        p.lse[g] = v;
-    }
-    // A softmax that is not finite (a NaN or infinite visible score) is the
-    // answer; a finite one with an output that is not may owe it to a masked
-    // position: the row is computed again and written over.
-    odd = odd && live && l < INFINITY && lr < INFINITY;
-    if (odd) flag[row] = 1;
-    if (__builtin_expect(named_bar_or(4, 256, odd), 0)) {                     // (also orders the stores before)
-      for (int rr = warp - 4; rr < kRows; rr += 8) {
-        if (!flag[rr]) continue;
-        const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
-        const int pr = t->p_last - ((t->row1 - 1) / p.h - (int)gr / p.h);
-        slow_row<kFp8>(p, *t, gr, pr, p.window ? max(pr - (p.window - 1), 0) : 0,
-                       partial ? p.o_part + ((int64_t)t->slot * 128 + 64 * (int)r + rr) * 512 : nullptr,
-                       out + gr * 512);
-      }
-      named_bar_sync(4, 256);                            // the flags were read
-    }
-    // (the next unit's first weights are signalled behind these TMEM loads)
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
+      if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
     }
     __syncwarp();
   } else if (kFp8) {
@@ -1723,8 +1745,9 @@ int64_t tile_numbers(int T, int h, int num_reqs) {
 // What is known here are bounds: the tiles are taken as filled (a decode step's
 // requests hold one each), the keys as max_len or the window.  A block takes about
 // 1.6 us on a pair, a unit another 4; ranges cost the merge (4) and write and read
-// the partials, 4 KB a row, at about 9 TB/s (L2).  The smaller sum is taken.
-// Ranges need the list's length, which every cluster counts: up to 1024 tiles.
+// the partials, 4 KB a row, at about 9 TB/s (L2).  Ranges are taken
+// where they save a twentieth.  They need the list's length, which every cluster
+// counts: up to 1024 tiles.
 WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int window, int sinks,
                             int num_sms) {
   WindowPlan pl{};
@@ -1742,7 +1765,7 @@ WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int win
   const double rows = (double)T * h / (double)filled;
   const double ranges = 1.6 * (double)((list + workers - 1) / workers) + 4.0 + 4.0 +
                         (double)(workers + std::min(filled, workers)) * rows * 4096.0 / 9e6;
-  if (workers > 1 && pl.tiles <= 1024 && ranges < one) pl.workers = (int)workers;
+  if (workers > 1 && pl.tiles <= 1024 && ranges < 0.95 * one) pl.workers = (int)workers;
   pl.merge_groups = workers > 16 * filled ? kMergeGroups : 1;
   if (pl.workers > 0)
     pl.workspace_bytes = ((size_t)T * h * sizeof(int) + 255) / 256 * 256 +
@@ -1755,6 +1778,9 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   const bool fp8 = p.kv_format != kBf16;
   const int es = fp8 ? 1 : 2;
   p.num_tiles = tile_numbers(p.b.N, p.h, p.b.num_reqs);
+  p.table_end =
+      (int)std::min<int64_t>((int64_t)p.b.bt_stride * p.b.block_size, 0x7FFFFF00) - 1;
+  p.sinks = std::min(p.sinks, 0x7FFFFF00);             // (more than any position)
   a.atoms = (p.d_qk * es + 127) / 128;
   a.ksteps = p.d_qk * es / 32;
   a.scale_log2 = p.sm_scale * 1.4426950408889634f;

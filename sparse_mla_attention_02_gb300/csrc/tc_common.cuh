@@ -66,11 +66,6 @@ struct Waiter {
     if (*abort) return;
     if (!ptx::mbar_wait_bounded<true>(bar, parity, limit_ns, ctr, ctr0)) fail();
   }
-  // wait() for a phase that is often complete already: the flag is read only
-  // when it is not.
-  __device__ __forceinline__ void wait_ready(uint32_t bar, uint32_t parity) {
-    if (!ptx::mbar_try_wait(bar, parity)) wait(bar, parity);
-  }
   // Teardown: wait for asynchronous work this block started itself (TMA
   // copies into its shared memory, MMAs reading it and writing its TMEM),
   // also after an abort; only the time limit ends it.

@@ -35,13 +35,14 @@ def launch(smla, batch, fmt, q, cache, scale, sm_scale, window, sinks, **kw):
                                 block_stride_rows=batch.stride_rows, **kw)
 
 
-def run(smla, batch, fmt, h, d=576, window=0, sinks=0, seed=1, pow2=True, q_gain=2.0, status=0):
+def run(smla, batch, fmt, h, d=576, window=0, sinks=0, seed=1, pow2=True, q_gain=2.0, status=0,
+        **kw):
     smla.smla_get_device_status(clear=True)
     q, cache, scale = make(batch, fmt, h, d, seed, q_gain, pow2)
     sm = d ** -0.5
     out, lse = Guarded((batch.N, h, 512), torch.bfloat16), Guarded((batch.N, h), torch.float32)
     was = out.t[int(batch.start[-1]):].clone().view(torch.int16)
-    launch(smla, batch, fmt, q, cache, scale, sm, window, sinks, out=out.t, lse=lse.t)
+    launch(smla, batch, fmt, q, cache, scale, sm, window, sinks, out=out.t, lse=lse.t, **kw)
     torch.cuda.synchronize()
     out.check("O")
     lse.check("LSE")
@@ -115,6 +116,109 @@ def test_split_keys(cuda_lib, fmt):
     assert smla.smla_fwd_window_workspace_size(4, b.N, 16, 576, fmt, b.table.shape[1], 64) > 0
     run(smla, b, fmt, 16)
     run(smla, b, fmt, 128, window=3000, sinks=300)
+
+
+def shared_out(smla, b, h, **kw):
+    """Whether the plan cuts the keys of all tiles into ranges."""
+    return smla.smla_fwd_window_workspace_size(len(b.rows), b.N, h, 576, P.BF16, b.table.shape[1],
+                                               b.block, **kw) > 0
+
+
+@pytest.mark.parametrize("fmt", [P.BF16, P.BLOCK])
+def test_ranges_over_many_requests(cuda_lib, fmt):
+    """Ranges that hold several tiles: 80 requests (more than a warp), some of no
+    token, some with more tokens than positions."""
+    rows = [(1, 1 + 97 * r % 1500) for r in range(76)] + [(0, 40), (3, 2), (0, 0), (1, 0)]
+    b = P.Batch(rows, 64, seed=21, pad=3)
+    assert shared_out(cuda_lib, b, 16)
+    run(cuda_lib, b, fmt, 16, pow2=False)
+    b = P.Batch(rows[40:], 16, seed=22)
+    run(cuda_lib, b, fmt, 24, window=200, sinks=33)
+
+
+@pytest.mark.parametrize("fmt", [P.BF16, P.BLOCK])
+def test_ranges_over_tiles_of_a_request(cuda_lib, fmt):
+    b = P.Batch([(46, 3300), (0, 5), (34, 1700)], 64, seed=23)
+    assert shared_out(cuda_lib, b, 128)
+    run(cuda_lib, b, fmt, 128)
+
+
+@pytest.mark.parametrize("fmt", [P.BF16, P.BLOCK])
+def test_fewer_blocks_than_ranges(cuda_lib, fmt):
+    """A wide table lets the plan expect long requests; these are short or empty."""
+    for rows in ([(1, 3), (1, 1), (0, 0), (2, 1)], [(1, 0), (2, 0)], [(1, 129), (1, 300)]):
+        b = P.Batch(rows, 64, seed=24)
+        b.table = torch.cat([b.table, torch.full((len(rows), 200), -1, dtype=torch.int32)], 1)
+        assert shared_out(cuda_lib, b, 16)
+        run(cuda_lib, b, fmt, 16)
+        run(cuda_lib, b, fmt, 16, window=100, sinks=2)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_long_tiles_and_a_wrong_bound(cuda_lib, fmt):
+    """54 key blocks in one piece (the bound says one) and in ranges."""
+    b = P.Batch([(1, 6900), (3, 6500)], 64, seed=25)
+    assert shared_out(cuda_lib, b, 40) and not shared_out(cuda_lib, b, 40, max_seq_len=1)
+    run(cuda_lib, b, fmt, 40, max_seq_len=1)
+    run(cuda_lib, b, fmt, 40)
+    run(cuda_lib, b, fmt, 40, max_seq_len=1, window=5000, sinks=700)
+
+
+def test_a_workspace_used_again(cuda_lib):
+    """Calls of different shapes, one after the other in one workspace: what the
+    last one left does not show."""
+    smla = cuda_lib
+    ws = torch.full((64 << 20,), 0x7F, dtype=torch.uint8, device="cuda")
+    for rows, h, window in (([(1, 5000), (1, 90)], 128, 0), ([(2, 700), (1, 3000), (0, 3)], 16, 0),
+                            ([(1, 40)], 1, 0), ([(1, 5000), (1, 90)], 128, 900)):
+        b = P.Batch(rows, 64, seed=26, pad=2)
+        q, cache, scale = make(b, P.BLOCK, h, 576, 5)
+        want = launch(smla, b, P.BLOCK, q, cache, scale, 0.04, window, 1)
+        got = launch(smla, b, P.BLOCK, q, cache, scale, 0.04, window, 1, workspace=ws)
+        torch.cuda.synchronize()
+        n = int(b.start[-1])
+        assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:n], want[1][:n])
+
+
+@pytest.mark.parametrize("window", [0, 80])
+def test_lengths_that_no_table_holds(cuda_lib, window):
+    """Not followed past the table, however long: the call ends and says so."""
+    smla = cuda_lib
+    smla.smla_get_device_status(clear=True)
+    b = P.Batch([(1, 100), (2, 300), (1, 70)], 64, seed=27)
+    for fmt in (P.BF16, P.BLOCK):
+        q, cache, scale = make(b, fmt, 16, 576, 5)
+        ref = P.attend(q, P.dequant(cache, fmt, scale, b), b, 0.04, window, 2)
+        b.lens[1] = 2 ** 31 - 1
+        out, lse = launch(smla, b, fmt, q, cache, scale, 0.04, window, 2)
+        torch.cuda.synchronize()
+        b.lens[1] = 300
+        assert smla.smla_get_device_status(clear=True) == 5
+        for n in (0, 3):                               # the other requests' tokens
+            one = tuple(x[n:n + 1] for x in ref)
+            alone = P.Batch([(1, 1)], 64)
+            P.check_attention(out[n:n + 1], lse[n:n + 1], one, q[n:n + 1], fmt, 0.04, alone)
+
+
+@pytest.mark.parametrize("h", [16, 40])
+def test_same_as_the_sparse_forward(cuda_lib, h):
+    """The visible positions' rows listed for smla_fwd: two answers, each within
+    its bound of the formula's."""
+    smla = cuda_lib
+    b = P.Batch([(1, 700), (1, 333), (2, 90)], 64, seed=28)
+    q, cache, scale = make(b, P.BF16, h, 576, 6)
+    sm, window, sinks = 576 ** -0.5, 400, 3
+    out, lse = launch(smla, b, P.BF16, q, cache, scale, sm, window, sinks)
+    idx = torch.full((b.N, 512), -1, dtype=torch.int32)
+    for n, r, p in b.tokens():
+        seen = [b.slot(r, e) for e in range(p + 1) if e > p - window or e < sinks]
+        idx[n, :len(seen)] = torch.tensor(seen, dtype=torch.int32)
+    other, lse2 = smla.smla_fwd(q.cuda(), cache.cuda(), P.BF16, None, idx.cuda(), None,
+                                sm)
+    torch.cuda.synchronize()
+    ref = P.attend(q, P.dequant(cache, P.BF16, scale, b), b, sm, window, sinks)
+    P.check_attention(out, lse, ref, q, P.BF16, sm, b)
+    P.check_attention(other, lse2, ref, q, P.BF16, sm, b)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
