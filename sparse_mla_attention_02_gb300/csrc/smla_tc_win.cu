@@ -184,6 +184,14 @@ struct Unit {
   __device__ __forceinline__ int block(int i) const {   // i-th block's index
     return i < sink_blocks ? i : win_block + (i - sink_blocks);
   }
+  // The j-th block in the order of work.  bf16: from the last, so that the slow
+  // copies of the block that a request ends in come while nothing else does (a
+  // prompt of 4096 tokens: 1.30 -> 1.23 ms, 64 decode tokens: 53 -> 50 us).  E4M3:
+  // from the first (from the last, 32 decode tokens took 116 us, not 114).
+  template <bool kFp8>
+  __device__ __forceinline__ int work(int j) const {
+    return block(kFp8 ? b0 + j : b0 + nb - 1 - j);
+  }
 };
 static_assert(sizeof(Unit) == 48, "three 16-byte words");
 
@@ -634,7 +642,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   auto entry = [&](const Unit& u, int j) {
     Entry e{0, -1, 0u};
     if (j >= u.nb) return e;
-    const int pos = u.block(u.b0 + j) * kBN + 4 * lane;
+    const int pos = u.template work<kFp8>(j) * kBN + 4 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       e.seen |= (pos + i <= u.p_last && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
@@ -919,7 +927,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           // Rows behind the last token may never have been written, and a weight of
           // 0 times NaN is NaN: they are read as zeros.  (The other rows of a block
           // were written; one that is not finite costs the tile slow_row.)
-          const int up = u.live - 2 - (u.block(u.b0 + j) * kBN + 4 * lane);
+          const int up = u.live - 2 - (u.template work<kFp8>(j) * kBN + 4 * lane);
           if (up < 0) id.x = -1;
           if (up < 1) id.y = -1;
           if (up < 2) id.z = -1;
@@ -1068,7 +1076,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           e1 = e2;
           e2 = entry(u, j + 3);
         } else {
-          const Rows4 x = lookup4(p, u, u.block(u.b0 + j) * kBN + 4 * lane, bad);
+          const Rows4 x = lookup4(p, u, u.template work<kFp8>(j) * kBN + 4 * lane, bad);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             id[k] = x.id[k];
@@ -1190,12 +1198,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       float m_run = -INFINITY;  // running max (log2 units), the same in a row's four threads
       float l_run = 0.f;       // this thread's sum of exp2(s - m_run)
       float lr_run = 0.f;      // the same sum of the bf16-rounded weights
-      int blk = nb > 0 ? t->block(t->b0) : 0;
-      const int jump = t->sink_blocks - t->b0;           // the block behind the sinks'
+      int blk = nb > 0 ? t->template work<kFp8>(0) : 0;
+      // where the order of work leaves the sinks' blocks, or comes to them
+      const int jump = kFp8 ? t->sink_blocks - t->b0 : t->b0 + nb - t->sink_blocks;
       for (int j = 0; j < nb; ++j, ++J, mr.next()) {
         const int buf = J & 1, m = mr.m;
         const int e0 = blk * kBN + 32 * seg;             // this thread's first key
-        blk = j + 1 == jump ? t->win_block : blk + 1;
+        if (j + 1 == jump)
+          blk = kFp8 ? t->win_block : t->sink_blocks - 1;
+        else
+          blk += kFp8 ? 1 : -1;
         W.wait(bar(kBarMFull + m), mr.ph);
         uint32_t see = words[4 * m + seg];
         W.wait(bar(kBarSFull + buf), (J >> 1) & 1);
