@@ -278,20 +278,19 @@ def smla_cache_write_e4m3_group(kv_c, k_pe, slot_mapping, kv_cache, scales,
     return kv_cache, scales
 
 
-def _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, device):
-    """Check a ragged batch's descriptors; return the C arguments."""
-    import torch
-    i32 = torch.int32
+def _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, index, i32):
+    """Check a ragged batch's descriptors (on CUDA device ``index``); return the
+    C arguments."""
     if not (query_start.dtype is i32 and seq_lens.dtype is i32 and block_table.dtype is i32 and
             query_start.is_contiguous() and seq_lens.is_contiguous() and
             block_table.is_contiguous()):
         raise ValueError("query_start, seq_lens and block_table must be contiguous int32 tensors")
-    if not (query_start.device == device and seq_lens.device == device and
-            block_table.device == device):
+    if not query_start.get_device() == seq_lens.get_device() == block_table.get_device() == index:
         raise ValueError("query_start, seq_lens and block_table must be on the inputs' device")
-    if block_table.dim() != 2:
+    shape = block_table.shape
+    if len(shape) != 2:
         raise ValueError("block_table must be [num_reqs, stride]")
-    R, width = block_table.shape
+    R, width = shape
     if query_start.shape != (R + 1,) or seq_lens.shape != (R,):
         raise ValueError("query_start must be [num_reqs + 1] and seq_lens [num_reqs]")
     if block_size < 1 or (block_stride_rows != 0 and block_stride_rows < block_size):
@@ -302,24 +301,26 @@ def _batch_args(query_start, seq_lens, block_table, block_size, block_stride_row
 
 
 def _device_stream(t, what, stream):
-    """The raw stream of a call on tensor ``t``.  The library works on the
-    current device: tensors of another are refused."""
+    """The CUDA device and the raw stream of a call on tensor ``t``.  The library
+    works on the current device: tensors of another are refused."""
     import torch
-    index = t.get_device()
-    if index < 0 or index != torch.cuda.current_device():
+    index = t.get_device()                    # (-1: a host tensor)
+    if index < 0 or index != torch._C._cuda_getDevice():
         raise ValueError(what + " must be on the current CUDA device")
-    # (torch.cuda.current_stream() builds a Stream object, 3 us a call)
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    # (torch.cuda.current_stream() builds a Stream object, 3 us a call; a tensor's
+    # index costs half of its device)
+    return index, (torch._C._cuda_getCurrentRawStream(index) if stream is None
+                   else stream.cuda_stream)
 
 
-def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, device):
+def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, index):
     """Check a paged cache and its scales; return (slots, k_scale's address)."""
     import torch
     if not 0 <= kv_dtype <= SMLA_KV_FP8_E4M3_BLOCK:
         raise ValueError("kv_dtype must be an SMLA_KV_* value")
     row = DS_MLA_ROW_BYTES if kv_dtype == SMLA_KV_FP8_DS_MLA else d_qk
     if not (kv_cache.dtype is (torch.bfloat16 if kv_dtype == SMLA_KV_BF16 else torch.uint8) and
-            kv_cache.is_contiguous() and kv_cache.device == device):
+            kv_cache.is_contiguous() and kv_cache.get_device() == index):
         raise ValueError("kv_cache must be a contiguous tensor on the inputs' device, bfloat16 "
                          "for a bf16 cache and uint8 for the E4M3 formats")
     S = kv_cache.numel() // row
@@ -333,7 +334,8 @@ def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, de
             -(-S // rows_per_scale) if kv_dtype == SMLA_KV_FP8_E4M3_BLOCK else
             4 * S if kv_dtype == SMLA_KV_FP8_E4M3_GROUP4_KPE else S * ((d_qk + 127) // 128))
     if not (k_scale is not None and k_scale.dtype is torch.float32 and
-            k_scale.is_contiguous() and k_scale.device == device and k_scale.numel() >= need):
+            k_scale.is_contiguous() and k_scale.get_device() == index and
+            k_scale.numel() >= need):
         raise ValueError("k_scale must be a contiguous fp32 tensor on the inputs' device with a "
                          "value for every scale of the format")
     return S, k_scale.data_ptr()
@@ -355,29 +357,30 @@ def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, b
     import torch
     lib = _lib or load()
     bf16 = torch.bfloat16
-    raw_stream = _device_stream(kv_c, "kv_c", stream)
-    dev = kv_c.device
-    if not (kv_c.dtype is bf16 and kv_c.dim() == 2 and kv_c.shape[1] == 512 and
-            kv_c.stride(1) == 1):
+    index, raw_stream = _device_stream(kv_c, "kv_c", stream)
+    shape = kv_c.shape
+    if not (kv_c.dtype is bf16 and len(shape) == 2 and shape[1] == 512 and kv_c.stride(1) == 1):
         raise ValueError("kv_c must be a bf16 tensor [N, 512] with contiguous rows")
-    N = kv_c.shape[0]
+    N = shape[0]
     one = N < 2                               # a single token's stride says nothing
     pe = cs = None
     pe_stride = cs_rows = 0
     d_qk = 512
     if k_pe is not None:
         if not (k_pe.dtype is bf16 and k_pe.shape == (N, 64) and k_pe.stride(1) == 1 and
-                k_pe.device == dev):
+                k_pe.get_device() == index):
             raise ValueError("k_pe must be a bf16 tensor [N, 64] with contiguous rows")
         if not (cos_sin is not None and cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and
-                cos_sin.shape[1] == 64 and cos_sin.is_contiguous() and cos_sin.device == dev):
+                cos_sin.shape[1] == 64 and cos_sin.is_contiguous() and
+                cos_sin.get_device() == index):
             raise ValueError("cos_sin must be a contiguous fp32 tensor [positions, 64]")
         d_qk = 576
         pe, pe_stride = k_pe.data_ptr(), 64 if one else k_pe.stride(0)
         cs, cs_rows = cos_sin.data_ptr(), cos_sin.shape[0]
-    batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, dev)
+    batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, index,
+                        torch.int32)
     S, scale = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
-                           block_stride_rows or block_size, dev)
+                           block_stride_rows or block_size, index)
     q_args = (None, 0, 0, None, 0, 0, 0)
     if q_pe is not None:
         if q_out is None:
@@ -385,7 +388,7 @@ def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, b
         h = q_pe.shape[1] if q_pe.dim() == 3 else 0
         strides = []
         for x in (q_pe, q_out):
-            if not (x.dtype is bf16 and x.shape == (N, h, 64) and x.device == dev):
+            if not (x.dtype is bf16 and x.shape == (N, h, 64) and x.get_device() == index):
                 raise ValueError("q_pe and q_out must be bf16 tensors [N, h, 64]")
             s0, s1, s2 = x.stride()
             if s2 != 1:
@@ -426,25 +429,25 @@ def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block
     request are not written."""
     import torch
     lib = _lib or load()
-    raw_stream = _device_stream(q, "q", stream)
-    dev = q.device
+    index, raw_stream = _device_stream(q, "q", stream)
     bf16 = torch.bfloat16
     if not (q.dtype is bf16 and q.dim() == 3 and q.is_contiguous()):
         raise ValueError("q must be a contiguous bf16 device tensor [T, h, d_qk]")
     T, h, d_qk = q.shape
-    batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, dev)
+    batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, index,
+                        torch.int32)
     S, scale = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
-                           block_stride_rows or block_size, dev)
+                           block_stride_rows or block_size, index)
     if out is None:
-        out = torch.empty((T, h, 512), dtype=bf16, device=dev)
+        out = torch.empty((T, h, 512), dtype=bf16, device=q.device)
     elif not (out.dtype is bf16 and out.shape == (T, h, 512) and out.is_contiguous() and
-              out.device == dev):
+              out.get_device() == index):
         raise ValueError("out must be contiguous bf16 [T, h, 512]")
     if lse is None:
         if want_lse:
-            lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+            lse = torch.empty((T, h), dtype=torch.float32, device=q.device)
     elif not (lse.dtype is torch.float32 and lse.shape == (T, h) and lse.is_contiguous() and
-              lse.device == dev):
+              lse.get_device() == index):
         raise ValueError("lse must be contiguous fp32 [T, h]")
     limit = max_seq_len or 0
     if workspace is None:
@@ -453,12 +456,14 @@ def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block
                                                     block_size, window, sinks, limit)
         if nbytes:
             if stream is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
             else:
                 with torch.cuda.stream(stream):
-                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
     else:
+        if not (workspace.get_device() == index and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
         nbytes = workspace.numel() * workspace.element_size()
         ws = workspace.data_ptr()
     code = lib.smla_fwd_window(

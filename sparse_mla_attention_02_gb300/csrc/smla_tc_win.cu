@@ -656,8 +656,8 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   };
   Entry e0{0, -1, 0u}, e1 = e0, e2 = e0;
   if (warp == 3) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (p.workers > 0) {
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the merge)
       walk = start_walk(p, (int)(blockIdx.x >> 1));
       next = next_part(p, walk, (int)(blockIdx.x >> 1), r == 0);
     } else {
@@ -1759,7 +1759,7 @@ int64_t tile_numbers(int T, int h, int num_reqs) {
 // 1.6 us on a pair, a unit another 4; ranges cost the merge (4) and write and read
 // the partials, 4 KB a row, at about 9 TB/s (L2).  Ranges are taken
 // where they save a twentieth.  They need the list's length, which every cluster
-// counts: up to 1024 tiles.
+// counts: up to 1024 tiles and requests.
 WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int window, int sinks,
                             int num_sms) {
   WindowPlan pl{};
@@ -1777,7 +1777,8 @@ WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int win
   const double rows = (double)T * h / (double)filled;
   const double ranges = 1.6 * (double)((list + workers - 1) / workers) + 4.0 + 4.0 +
                         (double)(workers + std::min(filled, workers)) * rows * 4096.0 / 9e6;
-  if (workers > 1 && pl.tiles <= 1024 && ranges < 0.95 * one) pl.workers = (int)workers;
+  if (workers > 1 && std::max<int64_t>(pl.tiles, num_reqs) <= 1024 && ranges < 0.95 * one)
+    pl.workers = (int)workers;
   pl.merge_groups = workers > 16 * filled ? kMergeGroups : 1;
   if (pl.workers > 0)
     pl.workspace_bytes = ((size_t)T * h * sizeof(int) + 255) / 256 * 256 +

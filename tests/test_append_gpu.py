@@ -202,3 +202,26 @@ def test_group_rows_equal_the_slot_mapped_write(cuda_lib):
     slots = torch.tensor([b.slot(r, p) for _, r, p in b.tokens()], dtype=torch.int32).cuda()
     smla.smla_cache_write_e4m3_group(kv, None, slots, two, s2)
     assert torch.equal(one, two) and torch.equal(s1, s2)
+
+
+def test_binding_refusals(cuda_lib):
+    """Tensors of another device, type or layout never reach a launch."""
+    smla = cuda_lib
+    b = P.Batch([(2, 70), (3, 20)], 64, seed=15)
+    kv_c, k_pe, q_pe, cache, scale = make(b, P.BLOCK, 576, 4, 5)
+    start, lens, tab = b.dev()
+    good = dict(kv_c=on_gpu(kv_c), k_pe=on_gpu(k_pe), cos_sin=table(80).cuda(), query_start=start,
+                seq_lens=lens, block_table=tab, block_size=64, kv_cache=cache.cuda(),
+                kv_dtype=P.BLOCK, k_scale=scale.cuda(), q_pe=on_gpu(q_pe))
+    smla.smla_cache_append(**good)
+    for bad in (dict(kv_c=kv_c), dict(kv_c=good["kv_c"].half()), dict(kv_c=good["kv_c"][:, :500]),
+                dict(k_pe=k_pe), dict(k_pe=good["k_pe"][:2]), dict(cos_sin=None),
+                dict(cos_sin=table(80)), dict(cos_sin=good["cos_sin"].double()),
+                dict(cos_sin=good["cos_sin"].t().contiguous()), dict(query_start=b.start),
+                dict(seq_lens=lens.long()), dict(block_table=b.table), dict(block_size=0),
+                dict(block_stride_rows=32), dict(kv_cache=cache), dict(k_scale=scale),
+                dict(k_scale=None), dict(q_pe=q_pe), dict(q_pe=good["q_pe"][:2]),
+                dict(q_out=q_pe), dict(q_out=good["q_pe"].transpose(1, 2)), dict(kv_dtype=-1)):
+        with pytest.raises(ValueError):
+            smla.smla_cache_append(**{**good, **bad})
+    assert smla.smla_get_device_status(clear=True) == 0

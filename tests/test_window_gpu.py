@@ -411,6 +411,30 @@ def test_append_then_attend(cuda_lib):
             P.check_attention(out, lse, ref, gq.cpu(), fmt, d ** -0.5, b)
 
 
+def test_binding_refusals(cuda_lib):
+    """Tensors of another device, type or layout never reach a launch."""
+    smla = cuda_lib
+    b = P.Batch([(1, 700), (2, 90)], 64, seed=14)
+    q, cache, scale = make(b, P.BLOCK, 16, 576, 4)
+    start, lens, tab = b.dev()
+    good = dict(q=q.cuda(), kv_cache=cache.cuda(), kv_dtype=P.BLOCK, k_scale=scale.cuda(),
+                query_start=start, seq_lens=lens, block_table=tab, block_size=64, sm_scale=0.04)
+    smla.smla_fwd_window(**good)
+    wide = torch.zeros((b.N, 16, 600), dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(q=q), dict(q=wide[:, :, :576]), dict(q=good["q"].float()),
+                dict(kv_cache=cache), dict(kv_cache=good["kv_cache"].view(torch.int8)),
+                dict(k_scale=None), dict(k_scale=scale), dict(k_scale=good["k_scale"][:1]),
+                dict(query_start=b.start), dict(seq_lens=b.lens), dict(block_table=b.table),
+                dict(query_start=start.long()), dict(seq_lens=lens[:1]), dict(block_table=tab[0]),
+                dict(block_table=tab.t()), dict(num_slots=b.num_slots + 1),
+                dict(out=torch.zeros((b.N, 16, 512), dtype=torch.bfloat16)),
+                dict(lse=torch.zeros((b.N, 16))), dict(lse=torch.zeros((b.N, 8), device="cuda")),
+                dict(workspace=torch.zeros(1 << 26, dtype=torch.uint8)), dict(kv_dtype=6)):
+        with pytest.raises(ValueError):
+            smla.smla_fwd_window(**{**good, **bad})
+    assert smla.smla_get_device_status(clear=True) == 0
+
+
 def test_a_wait_that_runs_out(cuda_lib):
     """A stalled launch reports the timeout, and the next one is right."""
     smla = cuda_lib
