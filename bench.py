@@ -87,7 +87,7 @@ KERNEL_SOURCES = {
     "tc_heads": ("smla_tc.cu", "tc_common.cuh", "tc_ptx.cuh", "smla_internal.h"),
     "tc_keys": ("smla_tc_keys.cu", "tc_common.cuh", "tc_ptx.cuh", "smla_internal.h"),
     "tc_keys_fp8": ("smla_tc_fp8.cu", "tc_common.cuh", "tc_ptx.cuh", "smla_internal.h"),
-    "cache_write": ("smla_cache.cu", "smla_internal.h"),
+    "cache_write": ("smla_cache.cu", "e4m3_quant.cuh", "smla_internal.h"),
 }
 
 

@@ -9,7 +9,7 @@
 // to [0, N], table columns and rows are checked before they are used.
 #pragma once
 
-#include "smla_internal.h"
+#include "smla_paged.h"
 
 namespace smla {
 

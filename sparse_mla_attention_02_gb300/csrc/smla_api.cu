@@ -12,6 +12,7 @@
 
 #include "../../include/smla.h"
 #include "smla_internal.h"
+#include "smla_paged.h"
 
 namespace {
 

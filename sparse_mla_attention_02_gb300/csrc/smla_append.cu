@@ -28,7 +28,7 @@
 
 #include "e4m3_quant.cuh"
 #include "paged_batch.cuh"
-#include "smla_internal.h"
+#include "smla_paged.h"
 
 namespace smla {
 namespace {

@@ -90,9 +90,9 @@
 
 #include "e4m3_quant.cuh"
 #include "paged_batch.cuh"
-#include "smla_internal.h"
+#include "smla_paged.h"
 #include "tc_common.cuh"
-#include "tc_ptx.cuh"
+#include "tc_pair.cuh"
 
 namespace smla {
 namespace {

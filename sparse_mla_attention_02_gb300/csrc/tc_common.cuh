@@ -139,30 +139,6 @@ __device__ __forceinline__ float add_bf16x2_f32(float acc, uint32_t pk) {
   return acc;
 }
 
-// The same into two sums, one per half.
-__device__ __forceinline__ void add_bf16x2_f32x2(float& a, float& b, uint32_t pk) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
-      : "+f"(a), "+f"(b) : "r"(pk));
-}
-
-// Packed f16 pairs: conversion, difference, and the two values added to fp32 sums.
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void add_f16x2_f32x2(float& a, float& b, uint32_t pk) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "add.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
-      : "+f"(a), "+f"(b) : "r"(pk));
-}
-
 // The slot ids at top-k positions [k0, k0 + n) of one index row into
 // slots[0, n) (n a multiple of 4), -1 where masked: at or past k1, negative,
 // or >= num_slots (the last makes the return value true).  The nthr threads

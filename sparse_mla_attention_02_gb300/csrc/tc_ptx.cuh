@@ -44,12 +44,6 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
                : "memory");
 }
 
-// The same with the default ordering of an arrival (release within the CTA):
-// for a signal about data that stays in the arriving CTA.
-__device__ __forceinline__ void mbar_signal_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -117,11 +111,6 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
-}
-
-// Write a word of a cluster's shared memory (address from mapa).
-__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // TMA gather: four rows (y0..y3) of a 2-D tensor map, one box of columns
@@ -226,69 +215,11 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
-// Cluster launch control: ask to take over the work of a cluster of this grid
-// that has not started.  The 16-byte answer is written to the same offset in
-// every CTA of the cluster and counted on the same mbarrier of each.
-__device__ __forceinline__ void cluster_take_over(uint32_t answer, uint32_t bar) {
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes."
-      "multicast::cluster::all.b128 [%0], [%1];" ::"r"(answer),
-      "r"(bar)
-      : "memory");
-}
-// Whether the answer hands over a cluster, and its first CTA's index (x).
-__device__ __forceinline__ bool cluster_taken(uint32_t answer, int& first) {
-  uint32_t ok, x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-      "ld.shared.b128 h, [%2];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-      : "=r"(ok), "=r"(x)
-      : "r"(answer)
-      : "memory");
-  first = (int)x;
-  return ok != 0;
-}
-
-// 32 bytes to global memory (32-byte aligned): one whole sector.
-__device__ __forceinline__ void st_global_32(void* dst, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d, uint32_t e, uint32_t f, uint32_t g,
-                                             uint32_t h) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a),
-               "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
-               : "memory");
-}
-
 // 2^x on the SFU (approximate; flushes subnormal results to zero).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// The largest of three (NaN operands are passed over).
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// (a0, a1) * (b, b) + (c, c), each rounded on its own.
-__device__ __forceinline__ void fma2_bcast(float& a0, float& a1, float b, float c) {
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
-      "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b), "f"(c));
-}
-
-// (a0, a1) += (b0, b1)
-__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1));
 }
 
 // -------------------------------------------------------------- tcgen05 --
@@ -414,100 +345,6 @@ __device__ __forceinline__ void tmem_wait_ld() {
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// ------------------------------------------- tcgen05 over a pair of CTAs --
-// cta_group::2: one MMA over the two SMs of a cluster of two, issued by the
-// even-ranked CTA.  Each CTA supplies its half of A's rows and of B's rows
-// (N) at the same shared-memory offsets and holds its own rows of D.  With
-// M = 128 a CTA's 64 rows fill all 128 TMEM lanes: lane i < 64 holds row i,
-// columns [0, N / 2), lane 64 + i the same row, columns [N / 2, N).
-
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   dst_smem),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr),
-               "r"(ncols)
-               : "memory");
-}
-// D (+)= A * B^T over the pair, bf16 operands from shared memory.
-__device__ __forceinline__ void mma_pair_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// The same with 8-bit operands (32 values of K per instruction).
-__device__ __forceinline__ void mma_pair_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                              uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor for .kind::f8f6f4 with E4M3 A/B (K-major) and fp32 D.
-__host__ __device__ constexpr uint32_t idesc_pair_e4m3(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-// The same with E5M2 A (K-major) and E4M3 B (MN-major).
-__host__ __device__ constexpr uint32_t idesc_pair_e5m2_e4m3(int M, int N) {
-  return idesc_pair_e4m3(M, N) | (1u << 7) | (1u << 16);
-}
-// Arrive on the same mbarrier of the CTAs in `mask` (default: both) when all
-// prior MMAs end.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask = 3) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
-}
-// TMA loads into this CTA's shared memory whose bytes are counted on an
-// mbarrier of either CTA of the pair (`bar`: a cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y,
-                                                 uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int x, int y, int z,
-                                                 uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tma_prefetch_map(const void* tmap) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
-}
-// Bring a box into L2.
-__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap),
-               "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const void* tmap, int x, int y0,
-                                                 int y1, int y2, int y3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::"
-      "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
-      : "memory");
 }
 
 }  // namespace ptx
