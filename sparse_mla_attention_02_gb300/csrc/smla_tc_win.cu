@@ -79,6 +79,15 @@
 // threads per row (TMEM lane half x column half), 32 keys each; with E4M3 rows
 // warps 13..15 split Q.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
+//
+// Bound and measured.  A block is 2,176 cycles of MMAs (E4M3, five passes at twice
+// the rate: 2,688) and takes about 3,000: bf16 loads run at 12.5 TB/s from L2, K
+// and V apart, through rings one block deep, all that shared memory holds.  A unit
+// costs about 5 us more (lookups, first copies, epilogue).  A prompt of 4096 tokens
+// with 128 heads through a window of 2048: bf16 1.23 ms = 1.43 PFLOP/s; 2048 tokens
+// with 64 heads behind 6000: E4M3 1.28 ms = 1.42 PFLOP/s; 64 decode tokens with 128
+// heads through the window: bf16 46 us = 3.7 TB/s; 32 of 8 to 16 thousand keys: E4M3
+// 110 us = 0.95 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
