@@ -435,17 +435,46 @@ def test_binding_refusals(cuda_lib):
     assert smla.smla_get_device_status(clear=True) == 0
 
 
-def test_a_wait_that_runs_out(cuda_lib):
-    """A stalled launch reports the timeout, and the next one is right."""
+def test_back_to_back_calls(cuda_lib):
+    """Calls that share their buffers and one workspace on a stream, read between
+    them without a wait of the host: the merge of one is done before the next."""
     smla = cuda_lib
-    b = P.Batch([(1, 300), (20, 90)], 64, seed=13)
+    b = P.Batch([(1, 4000), (2, 2500)], 64, seed=16)
+    assert shared_out(smla, b, 32)
+    start, lens, tab = b.dev()
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.empty((b.N, 32, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((b.N, 32), device="cuda")
+    qs, want, got = [], [], []
+    for seed in (1, 2):
+        q, cache, _ = make(b, P.BF16, 32, 576, seed)
+        qs.append((q.cuda(), cache.cuda()))
+        want.append(smla.smla_fwd_window(*qs[-1], P.BF16, None, start, lens, tab, 64, 0.04))
+        torch.cuda.synchronize()
+    for k in range(12):
+        smla.smla_fwd_window(*qs[k % 2], P.BF16, None, start, lens, tab, 64, 0.04, out=out, lse=lse,
+                             workspace=ws)
+        got.append((out.clone(), lse.clone()))
+    torch.cuda.synchronize()
+    for k, (o, l) in enumerate(got):
+        assert torch.equal(o, want[k % 2][0]) and torch.equal(l, want[k % 2][1])
+
+
+def test_a_wait_that_runs_out(cuda_lib):
+    """A stalled launch reports the timeout, and the next one is right: a tile in
+    one piece, and in ranges."""
+    smla = cuda_lib
+    whole = P.Batch([(1, 300), (20, 90)], 64, seed=13)
+    parts = P.Batch([(1, 6000), (1, 90)], 64, seed=13)
+    assert not shared_out(smla, whole, 16) and shared_out(smla, parts, 16)
     smla.smla_get_device_status(clear=True)
-    for fmt in (P.BF16, P.BLOCK):
-        q, cache, scale = make(b, fmt, 16, 576, 4)
-        smla.smla_test_set_stall(True, 2000)
-        try:
-            launch(smla, b, fmt, q, cache, scale, 0.04, 0, 0)
-            assert smla.smla_get_device_status(clear=True) == 4
-        finally:
-            smla.smla_test_set_stall(False)
-        run(smla, b, fmt, 16)
+    for b in (whole, parts):
+        for fmt in (P.BF16, P.BLOCK):
+            q, cache, scale = make(b, fmt, 16, 576, 4)
+            smla.smla_test_set_stall(True, 2000)
+            try:
+                launch(smla, b, fmt, q, cache, scale, 0.04, 0, 0)
+                assert smla.smla_get_device_status(clear=True) == 4
+            finally:
+                smla.smla_test_set_stall(False)
+            run(smla, b, fmt, 16)
