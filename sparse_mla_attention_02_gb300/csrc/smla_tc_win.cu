@@ -84,10 +84,10 @@
 // the rate: 2,688) and takes about 3,000: bf16 loads run at 12.5 TB/s from L2, K
 // and V apart, through rings one block deep, all that shared memory holds.  A unit
 // costs about 5 us more (lookups, first copies, epilogue).  A prompt of 4096 tokens
-// with 128 heads through a window of 2048: bf16 1.23 ms = 1.43 PFLOP/s; 2048 tokens
-// with 64 heads behind 6000: E4M3 1.28 ms = 1.42 PFLOP/s; 64 decode tokens with 128
+// with 128 heads through a window of 2048: bf16 1.19 ms = 1.47 PFLOP/s; 2048 tokens
+// with 64 heads behind 6000: E4M3 1.25 ms = 1.45 PFLOP/s; 64 decode tokens with 128
 // heads through the window: bf16 46 us = 3.7 TB/s; 32 of 8 to 16 thousand keys: E4M3
-// 110 us = 0.95 PFLOP/s.
+// 108 us = 0.97 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -1441,16 +1441,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const int ch0 = 256 * wg + 128 * half;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
       bool odd = false;                                  // an output that is not finite
-#pragma unroll 1
-      for (int c4 = idle ? 128 : 0; c4 < 128; c4 += 32) {  // (32 columns per TMEM wait)
-        uint32_t wide[2][16];
+      auto fetch = [&](int c, uint32_t (&w)[2][16]) {
         __syncwarp();
-        if (nb > 0) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            tmem_ld16(tmem + lane_base + kColO + 128 * wg + c4 + 16 * x, wide[x]);
-          tmem_wait_ld();
-        }
+        tmem_ld16(tmem + lane_base + kColO + 128 * wg + c, w[0]);
+        tmem_ld16(tmem + lane_base + kColO + 128 * wg + c + 16, w[1]);
+      };
+      auto put = [&](int c4, uint32_t (&wide)[2][16]) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           uint32_t (&w)[16] = wide[x];
@@ -1479,6 +1475,22 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
               reinterpret_cast<uint4*>(dst)[1] = make_uint4(b[4], b[5], b[6], b[7]);
             }
           }
+        }
+      };
+      if (!idle) {
+        // (32 columns are on their way from TMEM while 32 are stored: a prompt's time
+        // is 2.6 % less)
+        uint32_t wa[2][16], wb[2][16];
+        fetch(0, wa);
+        tmem_wait_ld();
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          fetch(c + 32, wb);
+          put(c, wa);
+          tmem_wait_ld();
+          if (c == 0) fetch(64, wa);
+          put(c + 32, wb);
+          tmem_wait_ld();
         }
       }
       if (live && seg == 0) {
@@ -1521,6 +1533,19 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     Unit u;
     for (int i = 0, q = 0; take_unit(i, u); ++i) {
       if (u.nb <= 0) continue;
+      // (a row's loads are on their way while the row before is split, the first
+      // row's before the tile's shared memory is free: 100 decode tokens 117 -> 113 us)
+      uint4 ahead[9];
+      auto load_row = [&](int rr) {
+        const int64_t gr = (int64_t)u.row0 + 64 * (int)r + rr;
+        const bool have = rr < kRows && gr < u.row1;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) + (have ? gr : u.row0) * p.d_qk) + j8;
+#pragma unroll
+        for (int c = 0; c < 9; ++c)
+          ahead[c] = have && c < nch ? __ldg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      load_row(g0);
       if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
       __syncwarp();
       float* qscale = reinterpret_cast<float*>(sm + C::kOffQScale) + kRows * (q & 1);
@@ -1528,13 +1553,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       for (int rr = g0; rr < kRows; rr += 12) {
         const int64_t gr = (int64_t)u.row0 + 64 * (int)r + rr;
         if (gr - (rr & 31) >= u.row1) break;           // (rows of an idle softmax warp)
-        const bool have = gr < u.row1;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) + (have ? gr : u.row0) * p.d_qk) + j8;
         uint4 raw[9];
 #pragma unroll
-        for (int c = 0; c < 9; ++c)
-          raw[c] = have && c < nch ? __ldg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < 9; ++c) raw[c] = ahead[c];
+        load_row(rr + 12);
         float amax = 0.f;
 #pragma unroll
         for (int c = 0; c < 9; ++c) {
