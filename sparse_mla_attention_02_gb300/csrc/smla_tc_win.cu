@@ -86,8 +86,8 @@
 // costs about 5 us more (lookups, first copies, epilogue).  A prompt of 4096 tokens
 // with 128 heads through a window of 2048: bf16 1.19 ms = 1.47 PFLOP/s; 2048 tokens
 // with 64 heads behind 6000: E4M3 1.25 ms = 1.45 PFLOP/s; 64 decode tokens with 128
-// heads through the window: bf16 46 us = 3.7 TB/s; 32 of 8 to 16 thousand keys: E4M3
-// 108 us = 0.97 PFLOP/s.
+// heads through the window: bf16 45 us = 3.75 TB/s; 32 of 8 to 16 thousand keys: E4M3
+// 105 us = 1.0 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -589,6 +589,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 
   // Setup, spread over the warps: barriers, TMEM, the abort flag and the tensor
   // maps; the lookups' warp meanwhile finds the first unit and its table entries.
+  // The launch may come under the end of the kernel before (launch_early): nothing
+  // that it could have written is read before griddepcontrol.wait, which the two
+  // warps that read first execute, and the others pass the barrier behind them.
   if (tid == 32) {
     for (int i = 0; i < kKGroups; ++i) {
       mbar_init(bar(kBarKFull + i), 1);
@@ -623,6 +626,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     fence_mbar_init_cluster();
   }
   if (tid == 64) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     *W.shared(0) = 0;
     *W.shared(1) = *reinterpret_cast<volatile int*>(p.abort_ctr);
   }
@@ -665,6 +669,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   };
   Entry e0{0, -1, 0u}, e1 = e0, e2 = e0;
   if (warp == 3) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.workers > 0) {
       asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the merge)
       walk = start_walk(p, (int)(blockIdx.x >> 1));
@@ -1643,13 +1648,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 // ---- merge of the partials -------------------------------------------------
 //   LSE = ln sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s
 // One CTA per row, four channels a thread, and where a tile may have more than 16
-// parts four groups of threads that share them; the ranges first .. last hold the
+// parts eight groups of threads that share them; the ranges first .. last hold the
 // row's tile (one: it is written already), the last as its first part and the
 // others as their last.  A part without a visible key has LSE_s = -inf and its
 // O_s is not read.  Rows of no request are left alone.  Launched under the end of
-// the kernel before (its launch took 3 us of a short call); it waits for it here.
+// the kernel before (launch_early); it waits for it here.
 constexpr int kMaxParts = 128;
-constexpr int kMergeGroups = 4;
+constexpr int kMergeGroups = 8;
 __global__ void __launch_bounds__(128 * kMergeGroups)
 smla_window_merge_kernel(const WinParams p) {
   __shared__ float weight[kMaxParts];
@@ -1658,10 +1663,9 @@ smla_window_merge_kernel(const WinParams p) {
   const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, groups = blockDim.x >> 7;
   const int64_t row = blockIdx.x;
   const int tok = (int)(row / p.h);
-  const bool owned = tok >= batch_start(p.b, 0) && tok < batch_start(p.b, p.b.num_reqs);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!owned) return;
   const int part = p.parts[row];
+  if (tok < batch_start(p.b, 0) || tok >= batch_start(p.b, p.b.num_reqs)) return;
   const int first = part >> 19, last = (part >> 7) & 0xFFF, off = part & 127;
   // (starts that do not ascend leave rows without a tile, and this word as it was)
   if (part < 0 || first >= last || last >= p.workers) return;
@@ -1760,6 +1764,25 @@ cudaError_t encode_columns(CUtensorMap* map, bool fp8, const void* base, int d, 
              : cudaErrorInvalidValue;
 }
 
+// Launch a kernel that waits for the one before it on the stream by itself
+// (griddepcontrol.wait), so that its launch and setup pass under that one's end:
+// 1 to 2 us of a call, 3 of the merge.
+template <class Params>
+cudaError_t launch_early(void (*kernel)(Params), unsigned ctas, int threads, uint32_t smem,
+                         cudaStream_t stream, const std::remove_const_t<Params>& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 template <bool kFp8>
 cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   using C = Cfg<kFp8>;
@@ -1774,8 +1797,7 @@ cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  smla_window_kernel<kFp8><<<ctas, C::kThreads, C::kSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(smla_window_kernel<kFp8>, ctas, C::kThreads, C::kSmem, stream, a);
 }
 
 int64_t tile_numbers(int T, int h, int num_reqs) {
@@ -1853,16 +1875,8 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   a.p = p;
   e = fp8 ? launch<true>(a, (unsigned)ctas, stream) : launch<false>(a, (unsigned)ctas, stream);
   if (e != cudaSuccess || p.workers == 0) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(p.b.N * p.h));
-  cfg.blockDim = dim3(128 * p.merge_groups);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, smla_window_merge_kernel, p);
+  return launch_early(smla_window_merge_kernel, (unsigned)(p.b.N * p.h), 128 * p.merge_groups, 0,
+                      stream, p);
 }
 
 }  // namespace smla
