@@ -947,7 +947,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           if (up < 2) id.z = -1;
           if (up < 3) id.w = -1;
           const bool boxed = whole_box(id);
-          if (!kFp8 && a.box == 64 && __all_sync(0xffffffffu, boxed)) {  // two whole boxes
+          // Two whole boxes, from one lane (bf16: a prompt 1.31 -> 1.28 ms; E4M3 rows,
+          // whose V comes in half as many bytes, lose by it: 1.26 -> 1.30 ms).
+          if (!kFp8 && a.box == 64 && __all_sync(0xffffffffu, boxed)) {
             const int far = __shfl_sync(0xffffffffu, id.x, 16);
             bool on = true;
             if (elect_one()) {
@@ -960,10 +962,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
                 if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
                 const int ch = 256 * (v >> 1) + 128 * (int)r, row = v & 1 ? far : id.x;
                 const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
-                if (kFp8)
-                  tma_load_2d_pair(slot, &a.box_map, ch, row, vfull0 + 8u * v);
-                else
-                  tma_load_3d_pair(slot, &a.v_map, 0, row, ch / 64, vfull0 + 8u * v);
+                tma_load_3d_pair(slot, &a.v_map, 0, row, ch / 64, vfull0 + 8u * v);
                 ++issued;
               }
             }
