@@ -1009,8 +1009,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     }
   } else if (warp == 3) {
     // ---- units, and lookups: each block's rows, validity bits and scales ------
-    // This cluster's own unit comes first, then those it takes over.  Both CTAs
-    // decode the same answers and read the same batch, so they agree.
+    // This cluster's own tile comes first, then those it takes over; or the parts of
+    // its range.  Both CTAs decode the same answers and read the same batch, so they
+    // agree.
     // Lane l looks up positions 4 l .. 4 l + 3.  Where these share a cache block
     // (quad), the table entry of block j + 2 and the scale of block j + 1 are
     // on their way while block j is written down.
