@@ -48,8 +48,9 @@
 // than bf16 keeps); what falls below E5M2's grid is less than 2^-23 of a weight of
 // 1.  The key's scale belongs to its weight: with t = s + log2(scale) the running
 // maximum is taken over t, the weights are 2^(t - m) = scale 2^(s - m), and the
-// sums that divide add weight / scale.  So blocks of any scales share one range,
-// and nothing is converted on V's way to the tensor core.
+// sum that divides adds weight / scale, in fp32 where the weights are too small for
+// the product.  So blocks of any scales share one range, and nothing is converted on
+// V's way to the tensor core.
 //
 // Masked positions.  A cache block of which a row of the tile sees some position
 // is loaded whole: three columns of 64 rows arrive in 700 cycles as one copy, in
@@ -1310,14 +1311,39 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           for (int k = 0; k < 4; ++k) bm = fmaxf(bm, static_cast<float>(rb[64 * k + row]));
           if (bm > m_run + 7.f) {
             alpha = ex2_approx(m_run - bm);              // 0 when m_run = -inf
+            if (kFp8) {                                  // (the sums' own range is wider)
+              const float half = ex2_approx(0.5f * (m_run - bm));
+              l_run = l_run * half * half;
+              lr_run = lr_run * half * half;
+            }
             m_run = bm;
           }
         }
         // bf16: 16 pairs of weights.  E4M3: three terms of four weights a word.
         uint32_t pk[kFp8 ? 24 : 16];
         float ls = 0.f, ls1 = 0.f, lr = 0.f, lr1 = 0.f;
-        const float mm = (m_run == -INFINITY ? 0.f : m_run) - shift;  // (no score: weights are 0)
+        const float ref = m_run == -INFINITY ? 0.f : m_run;           // (no score: weights are 0)
+        const float mm = ref - shift;
         if constexpr (kFp8) {
+          // The divisor, sum of weight / scale: where the 32 keys share their scale the
+          // weights as the product has them, so that a key that carries the row keeps
+          // its V.  The product has nothing of weights that lie far below the row's
+          // reference (f16 ends at 2^-31 of it), but 1 / scale may make them most of
+          // the softmax: from 2^-15 on their fp32 sum divides, from 2^-90 on (where
+          // fp32 begins to end) the sum of 2^(s - m), without the scale.
+          const bool low = hm < ref - 15.f;
+          float bare = 0.f;
+          if (__builtin_expect(several, 0)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float e = ex2_approx(s[k] - __log2f(ks[k]) - ref);
+              bare += s[k] == -INFINITY ? 0.f : e;       // (masked, whatever its scale)
+            }
+          } else if (__builtin_expect(
+                         __any_sync(0xffffffffu, hm < ref - 90.f && hm > -INFINITY), 0)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) bare += ex2_approx(fmaf(s[k], cl, -ref));
+          }
           // 2^(t - m + 7) <= 2^15: within E5M2's range, its grid 2^-23 of a weight
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
@@ -1344,18 +1370,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             }
           }
           back *= 0x1p-7f;
-          ls = (ls + ls1) * back;
-          lr = (lr + lr1) * back;
-          if (__builtin_expect(several, 0)) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              ls += ks[k] > 0.f ? __fdividef(s[k] * 0x1p-7f, ks[k]) : 0.f;
-            // (a zero scale: key and value are zero, its weight is 2^(0 - m))
-#pragma unroll 1
-            for (int k = 0; k < 32; ++k)
-              if (ks[k] == 0.f && (see >> k & 1u)) ls += ex2_approx(-mm);
-            lr = ls;                                     // (9 bits: 2^-9 of a weight at most)
-          }
+          ls = several || hm < ref - 90.f ? bare : (ls + ls1) * back;
+          lr = several || low ? ls : (lr + lr1) * back;  // (9 bits: 2^-9 of a weight at most)
+          l_run += ls;
+          lr_run += lr;
         } else {
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
@@ -1365,11 +1383,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             pk[k / 2] = pack_bf16(w0, w1);
             add_bf16x2_f32x2(lr, lr1, pk[k / 2]);
           }
-          ls += ls1;
-          lr += lr1;
+          l_run = l_run * alpha + (ls + ls1);
+          lr_run = lr_run * alpha + (lr + lr1);
         }
-        l_run = l_run * alpha + ls;
-        lr_run = lr_run * alpha + lr;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarMEmpty + m));  // the lookups were read
         if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {

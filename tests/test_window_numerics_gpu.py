@@ -1,0 +1,108 @@
+"""smla_fwd_window where its arithmetic has to hold over a wide range: block scales
+that differ by many powers of two."""
+import math
+
+import pytest
+import torch
+
+from tests import _paged as P
+from tests.test_window_gpu import launch, make, shared_out
+
+pytestmark = pytest.mark.gpu
+
+
+def compare(smla, batch, fmt, q, cache, scale, sm, window=0, sinks=0, slack=0.0, **kw):
+    """Against the fp64 formula, within P.check_attention's bounds (``slack``: added
+    to O's)."""
+    smla.smla_get_device_status(clear=True)
+    out, lse = launch(smla, batch, fmt, q, cache, scale, sm, window, sinks, **kw)
+    torch.cuda.synchronize()
+    assert smla.smla_get_device_status(clear=True) == 0
+    rows = P.dequant(cache, fmt, scale, batch)
+    if fmt == P.BLOCK:
+        batch.row_scale = batch.row_scale.clamp(min=2.0 ** -64)
+    O, L, A, D, K, G = P.attend(q, rows, batch, sm, window, sinks)
+    P.check_attention(out, lse, (O, L, A + slack, D, K, G), q, fmt, sm, batch, pow2=False)
+    return out, lse
+
+
+# (rows, bound on the lengths: 1 takes every tile in one piece, None cuts the keys of
+# all tiles into ranges)
+WHOLE = ([(1, 900), (30, 400), (1, 130)], 1)
+RANGES = ([(1, 5000), (2, 700), (1, 130)], None)
+
+
+def mixed_scales(b, seed, low, share):
+    """Scales 2^-6 with a share of 2^low ones among them; codes of normal values."""
+    g = torch.Generator().manual_seed(seed)
+    n = -(-b.num_slots // (b.stride_rows or b.block))
+    return torch.where(torch.rand(n, generator=g) < share, 2.0 ** low, 2.0 ** -6).float()
+
+
+@pytest.mark.parametrize("rows,limit", [WHOLE, RANGES], ids=["whole", "ranges"])
+@pytest.mark.parametrize("block", [7, 16, 32, 64, 128])
+@pytest.mark.parametrize("low", [-24, -30, -40, -64])
+def test_block_scales_far_apart(cuda_lib, rows, limit, block, low):
+    """Rows whose scores are near each other: the blocks of a tiny scale hold their
+    share of the softmax, although their values are next to nothing."""
+    for share, h in ((0.5, 16), (0.93, 128)):
+        b = P.Batch(rows, block, seed=31)
+        q, cache, _ = make(b, P.BLOCK, h, 576, 5, q_gain=0.2)
+        scale = mixed_scales(b, 7, low, share)
+        assert limit or shared_out(cuda_lib, b, h)
+        compare(cuda_lib, b, P.BLOCK, q, cache, scale, 576 ** -0.5, max_seq_len=limit)
+    compare(cuda_lib, b, P.BLOCK, q, cache, scale, 576 ** -0.5, 200, 5, max_seq_len=limit)
+
+
+@pytest.mark.parametrize("rows,limit", [WHOLE, RANGES], ids=["whole", "ranges"])
+@pytest.mark.parametrize("high", [40, 90, 120])
+@pytest.mark.parametrize("block", [16, 64])
+def test_block_scales_of_any_size(cuda_lib, rows, limit, high, block):
+    """Scales 2^high and 2^-64 in one row, to the ends of what the append writes.  Keys of
+    a large scale have only channel 0 (2^-6), to which the queries are blind, the others
+    have all but it: every score is 0 (2^-50 at most), so LSE = ln n and O's channel 0 is
+    a count, to bf16's rounding, 2^-9 of a 9-bit weight and the exponentials' 2^-16; the
+    other channels hold 448 * 2^-64 at most.  LSE: the reference is `high` log2 units, so
+    its sum with log2 l is off by 2^-17 at most, and ln 2 of that."""
+    b = P.Batch(rows, block, seed=32)
+    q, cache, scale = make(b, P.BLOCK, 16, 576, 6)
+    g = torch.Generator().manual_seed(9)
+    top = torch.rand(scale.shape, generator=g) < 0.3
+    codes = cache.view(b.pool, block, 576)
+    codes[top, :, 1:] = 0
+    codes[top, :, 0] = 0x08                            # 2^-6
+    codes[~top, :, 0] = 0
+    q[:, :, 0] = 0
+    scale = torch.where(top, 2.0 ** high, 2.0 ** -64).float()
+    out, lse = launch(cuda_lib, b, P.BLOCK, q, cache, scale, 576 ** -0.5, 0, 0,
+                      max_seq_len=limit)
+    out, lse = out.double().cpu(), lse.double().cpu()
+    assert bool(top[b.table[0].long()].any())
+    for n, r, pos in b.tokens():
+        large = sum(bool(top[b.table[r, e // block]]) for e in range(pos + 1))
+        assert bool(((lse[n] - math.log(pos + 1)).abs() <= 2.0 ** -16).all())
+        want = large / (pos + 1) * 2.0 ** (high - 6)
+        assert bool(((out[n, :, 0] - want).abs() <= (2.0 ** -8 + 2.0 ** -8) * want).all())
+        assert bool((out[n, :, 1:].abs() <= 450 * 2.0 ** -64).all())
+
+
+@pytest.mark.parametrize("rows,limit", [WHOLE, RANGES], ids=["whole", "ranges"])
+@pytest.mark.parametrize("fill", [0.0, 2.0 ** -40])
+def test_appended_rows_of_zeros_beside_normal_ones(cuda_lib, rows, limit, fill):
+    """The append gives a block of zero rows (dummy tokens) the scale 2^-64."""
+    smla = cuda_lib
+    h, block = 16, 64
+    b = P.Batch(rows, block, seed=33)
+    g = torch.Generator().manual_seed(2)
+    full = P.Batch([(L, L) for _, L in rows], block, seed=33)
+    assert torch.equal(full.table, b.table)
+    x = torch.randn((full.N, 512), generator=g)
+    at = torch.tensor([p for _, _, p in full.tokens()])
+    x[(at // block) % 3 == 1] = fill
+    cache = torch.zeros((b.num_slots, 512), dtype=torch.uint8, device="cuda")
+    scale = torch.ones(b.pool, device="cuda")
+    smla.smla_cache_append(x.bfloat16().cuda(), None, None, *full.dev(), block, cache, P.BLOCK,
+                           scale)
+    assert float(scale.min()) <= 2.0 ** -48
+    q = (torch.randn((b.N, h, 512), generator=g) * 0.3).bfloat16()
+    compare(smla, b, P.BLOCK, q, cache.cpu(), scale.cpu(), 512 ** -0.5, max_seq_len=limit)
