@@ -222,7 +222,7 @@ struct Cfg {
   static constexpr uint32_t kOffK = kOffQ + kQTerms * kMaxAtoms * kAtom;
   static constexpr uint32_t kOffV = kOffK + kMaxAtoms * kAtom;
   static constexpr uint32_t kOffP = kOffV + kVUnits * kVUnit;
-  // row maxima [2][4][64]: bf16 (the room that is left), or fp32
+  // row maxima, fp32 [4][64]: one buffer for bf16 rows (the room that is left), else two
   static constexpr uint32_t kOffRed = kOffP + kPBufs * kPTerms * kPTerm;
   static constexpr uint32_t kOffBar = kOffRed + (kFp8 ? 2048 : 1024);
   static constexpr uint32_t kOffMask = kOffBar + 8 * (((kFp8 ? kNumBars : kBarQScale) + 1) & ~1);
@@ -1180,8 +1180,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const int row = tl & 63, half = tl >> 6;           // tile row, key half
     const int seg = 2 * half + wg;                     // its 32 keys of the block
     const uint32_t lane_base = ((uint32_t)(warp & 3) * 32u) << 16;
-    using Red = std::conditional_t<kFp8, float, __nv_bfloat16>;
-    Red* red = reinterpret_cast<Red*>(sm + C::kOffRed);
+    float* red = reinterpret_cast<float*>(sm + C::kOffRed);
     const uint32_t* words = reinterpret_cast<const uint32_t*>(sm + C::kOffMask);
     const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
     // One scale per tensor multiplies every score and the output.
@@ -1232,7 +1231,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             mbar_signal_remote(sempty + 8u * buf);
             mbar_arrive(bar(kBarMEmpty + m));
           }
-          named_bar_or(4, 256, false);
+          if (named_bar_or(4, 256, false) && !kFp8) named_bar_sync(4, 256);
           if (J >= C::kPBufs) W.wait(bar(kBarPEmpty + J % C::kPBufs), (J / C::kPBufs - 1) & 1);
           __syncwarp();
           if (lane == 0) mbar_signal_remote(pfull + 8u * (J % C::kPBufs));
@@ -1296,19 +1295,17 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
         for (int k = 2; k < 32; k += 2) hm = max3(hm, s[k], s[k + 1]);
         hm = fmaf(hm, cl, shift);
-        // The row's reference is the largest of its four maxima (bf16 rows: rounded
-        // to bf16, any value near the maximum serves): all four threads take the
-        // same one.
-        Red* rb = red + 256 * buf;
-        if constexpr (kFp8)
-          rb[64 * seg + row] = hm;
-        else
-          rb[64 * seg + row] = __float2bfloat16(hm);
+        // The row's reference is the largest of its four maxima: all four threads
+        // take the same one.  They are read only where some row needs a new one, so
+        // a single buffer is free again behind a second barrier there; two spare it.
+        float* rb = red + (kFp8 ? 256 * buf : 0);
+        rb[64 * seg + row] = hm;
         float alpha = 1.f;
         if (named_bar_or(4, 256, hm > m_run + 8.f)) {    // also true for the first finite max
           float bm = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) bm = fmaxf(bm, static_cast<float>(rb[64 * k + row]));
+          for (int k = 0; k < 4; ++k) bm = fmaxf(bm, rb[64 * k + row]);
+          if (!kFp8) named_bar_sync(4, 256);             // (the maxima were read)
           if (bm > m_run + 7.f) {
             alpha = ex2_approx(m_run - bm);              // 0 when m_run = -inf
             if (kFp8) {                                  // (the sums' own range is wider)

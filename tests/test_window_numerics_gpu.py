@@ -1,5 +1,5 @@
 """smla_fwd_window where its arithmetic has to hold over a wide range: block scales
-that differ by many powers of two."""
+that differ by many powers of two, and scores of any size."""
 import math
 
 import pytest
@@ -106,3 +106,68 @@ def test_appended_rows_of_zeros_beside_normal_ones(cuda_lib, rows, limit, fill):
     assert float(scale.min()) <= 2.0 ** -48
     q = (torch.randn((b.N, h, 512), generator=g) * 0.3).bfloat16()
     compare(smla, b, P.BLOCK, q, cache.cpu(), scale.cpu(), 512 ** -0.5, max_seq_len=limit)
+
+
+@pytest.mark.parametrize("rows,limit", [WHOLE, RANGES], ids=["whole", "ranges"])
+@pytest.mark.parametrize("fmt", [P.BF16, P.E4M3, P.BLOCK])
+def test_large_scores(cuda_lib, rows, limit, fmt):
+    """Scores up to 1.3e5 of either sign.  Queries have one channel, which no value has,
+    and it takes two values over the keys: a row's scores are S, or S less a thousandth
+    and more.  Products of one bf16 (or E4M3) pair are exact in fp32; S, as a product of
+    three fp32 factors, is off by 2^-22 |S|, the same for all keys of equal value.  So O
+    is the mean of the keys of the larger score (the others' weights underflow, or S is
+    below 100 and their error is 2^-22 * 100)."""
+    sm, h = 1 / 24, 32
+    b = P.Batch(rows, 64, seed=36)
+    q, cache, scale = make(b, fmt, h, 576, 10)
+    g = torch.Generator().manual_seed(3)
+    q.zero_()
+    mag = torch.exp2(torch.rand((b.N, h), generator=g) * 14 - 1)
+    q[:, :, 570] = (mag * torch.where(torch.rand((b.N, h), generator=g) < 0.5, -1.0, 1.0)).bfloat16()
+    q[:, 0, 570], q[:, 1, 570] = 8000.0, -8000.0
+    pick = torch.rand(b.num_slots, generator=g) < 0.4
+    if fmt == P.BF16:
+        cache[:, 570] = torch.where(pick, 384.0, 192.0).bfloat16()
+    else:
+        scale = torch.ones_like(scale)
+        cache[:, 570] = torch.where(pick, 0x7C, 0x74).to(torch.uint8)      # 384 and 192
+    out, lse = launch(cuda_lib, b, fmt, q, cache, scale, sm, 0, 0, max_seq_len=limit)
+    O, L, A, _, _, G = P.attend(q, P.dequant(cache, fmt, scale, b), b, sm, 0, 0)
+    assert float(L.max()) > 1e5 and float(L.min()) < -5e4
+    out, lse = out.double().cpu(), lse.double().cpu()
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    assert bool(((lse - L).abs() <= 2.0 ** -21 * L.abs() + 2.0 ** -16).all())
+    tol = 2.0 ** -8 * O.abs() + (2.0 ** -7 + 2.0 ** -9) * A + 2.0 ** -23 * G
+    assert bool(((out - O).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("size", [3e4, 1e5])
+def test_scores_around_a_large_value(cuda_lib, sign, size):
+    """Normal scores moved by a large common value through one channel."""
+    for rows, limit in (WHOLE, RANGES):
+        b = P.Batch(rows, 64, seed=37)
+        q, cache, _ = make(b, P.BF16, 16, 576, 11)
+        cache[:, 570] = 384.0
+        q[:, :, 570] = sign * size * 24 / 384
+        compare(cuda_lib, b, P.BF16, q, cache, None, 1 / 24, max_seq_len=limit)
+
+
+def test_equal_scores_of_every_size(cuda_lib):
+    """All scores of a row equal: O is the mean of V and LSE = S + ln n, for S over
+    bf16's steps between 2^13 and 2^17 (log2 units)."""
+    n, h = 129, 128
+    b = P.Batch([(1, n)] * 40, 64, seed=38)
+    q, cache, _ = make(b, P.BF16, h, 576, 12)
+    q.zero_()
+    cache[:, 575] = 256.0
+    exact = torch.linspace(2.0 ** 13, 2.0 ** 17, b.N * h).view(b.N, h) * math.log(2) * 24 / 256
+    q[:, :, 575] = exact.bfloat16()
+    out, lse = launch(cuda_lib, b, P.BF16, q, cache, None, 1 / 24, 0, 0)
+    S = q[:, :, 575].double() * 256 / 24
+    assert bool(((lse.double().cpu() - S - math.log(n)).abs() <= 2.0 ** -21 * S).all())
+    V = cache.double()
+    for t in range(b.N):
+        rows = V[[b.slot(t, e) for e in range(n)], :512]
+        tol = 2.0 ** -8 * rows.mean(0).abs() + (2.0 ** -7 + 2.0 ** -9) * rows.abs().mean(0)
+        assert bool(((out[t].double().cpu() - rows.mean(0)).abs() <= tol).all())
