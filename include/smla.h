@@ -78,7 +78,11 @@ extern "C" {
  *    per cache block of tokens (MLA has one latent head, so a block has one
  *    scale): value = e4m3 * k_scale[block], block = an entry of the block
  *    table.  Written by smla_cache_append, read by smla_fwd_window; the entry
- *    points that take slot ids do not serve it (SMLA_ERR_UNSUPPORTED). */
+ *    points that take slot ids do not serve it (SMLA_ERR_UNSUPPORTED).
+ *    Scales lie between 0 and 2^120, the largest that the append writes, and
+ *    may differ by any factor within one row; smla_fwd_window takes one below
+ *    2^-64 (0 too) as 2^-64, and rows that see a block whose scale is
+ *    negative or not finite are NaN. */
 typedef enum {
   SMLA_KV_BF16 = 0,
   SMLA_KV_FP8_E4M3 = 1,

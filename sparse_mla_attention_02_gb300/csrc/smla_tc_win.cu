@@ -483,9 +483,16 @@ struct MetaRing {
   }
 };
 
+// A cache block's scale.  The weights need its logarithm: below 2^-64, the least that
+// the append writes, it counts as that (zero too: values of at most 2^-55, scores
+// next to 0), and a negative one is NaN.
+__device__ __forceinline__ float block_scale(const WinParams& p, int blk) {
+  const float x = __ldg(p.k_scale + blk);
+  return x < 0x1p-64f ? (x < 0.f ? NAN : 0x1p-64f) : x;
+}
 // A key's scale (E4M3 caches).
 __device__ __forceinline__ float key_scale(const WinParams& p, int blk) {
-  return p.kv_format == kE4m3Block ? __ldg(p.k_scale + blk) : __ldg(p.k_scale);
+  return p.kv_format == kE4m3Block ? block_scale(p, blk) : __ldg(p.k_scale);
 }
 
 // One row again, from its visible positions in the unit's blocks alone, by one
@@ -1037,7 +1044,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         f.id[i] = in ? (int)row + i : -1;
         f.seen |= in ? e.seen & 1u << i : 0u;
       }
-      if (keyed && f.id[0] >= 0) f.sc = __ldg(p.k_scale + e.blk);
+      if (keyed && f.id[0] >= 0) f.sc = block_scale(p, e.blk);
       return f;
     };
     int i = 0;                                         // units described
@@ -1096,13 +1103,14 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           for (int k = 0; k < 4; ++k) {
             id[k] = x.id[k];
             seen |= (id[k] >= 0 ? 1u : 0u) << k;
-            if (keyed && id[k] >= 0) sc[k] = key_scale(p, x.blk[k]);
+            if (keyed && id[k] >= 0) sc[k] = block_scale(p, x.blk[k]);
           }
         }
         float own = 1.f;                               // the segment's scale, 0: several
         if (keyed) {
           // (a segment: the 32 keys of eight lanes; keys that no row sees agree
-          // with any scale)
+          // with any scale; one that is not finite is left to the path that masks
+          // every key by itself)
           float top = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -1113,7 +1121,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (id[k] < 0) sc[k] = top > 0.f ? top : 1.f;
-            same &= sc[k] == top;
+            same &= sc[k] == top && top < INFINITY;
           }
           const uint32_t votes = __ballot_sync(0xffffffffu, same) >> (lane & 24);
           own = (votes & 0xFFu) == 0xFFu ? top : 0.f;

@@ -1,5 +1,5 @@
 """smla_fwd_window where its arithmetic has to hold over a wide range: block scales
-that differ by many powers of two, and scores of any size."""
+that differ by many powers of two, scales of zero, and scores of any size."""
 import math
 
 import pytest
@@ -106,6 +106,54 @@ def test_appended_rows_of_zeros_beside_normal_ones(cuda_lib, rows, limit, fill):
     assert float(scale.min()) <= 2.0 ** -48
     q = (torch.randn((b.N, h, 512), generator=g) * 0.3).bfloat16()
     compare(smla, b, P.BLOCK, q, cache.cpu(), scale.cpu(), 512 ** -0.5, max_seq_len=limit)
+
+
+@pytest.mark.parametrize("rows,limit", [WHOLE, RANGES], ids=["whole", "ranges"])
+@pytest.mark.parametrize("block", [16, 64])
+def test_scales_of_zero(cuda_lib, rows, limit, block):
+    """A zero scale makes keys and values zero: score 0, weight 1 of the softmax.  First,
+    among, last and alone; the other scores far below them and far above.  (A scale
+    below 2^-64 counts as 2^-64: values of at most 448 * 2^-64.)"""
+    tiny = 448 * 2.0 ** -64 * 2 ** 7
+    for where in ("first", "last", "mixed", "all"):
+        for shift in (0.0, -60.0, 60.0):
+            b = P.Batch(rows, block, seed=34)
+            q, cache, scale = make(b, P.BLOCK, 16, 576, 8, q_gain=0.2)
+            for r, (_, L) in enumerate(rows):
+                pages = -(-L // block)
+                for k in range(pages):
+                    zero = {"first": k < pages // 2, "last": k >= pages // 2, "mixed": k % 3 == 1,
+                            "all": True}[where]
+                    if zero:
+                        scale[b.table[r, k]] = 0.0
+            # every other key's score moves by `shift` nats (through one channel of its own)
+            cache[:, 575] = 0x7E                       # 448, by 2^-6: 7
+            q[:, :, 575] = shift * 24 / 7
+            scale[(scale > 0)] = 2.0 ** -6
+            compare(cuda_lib, b, P.BLOCK, q, cache, scale, 576 ** -0.5, slack=tiny,
+                    max_seq_len=limit)
+
+
+def test_scales_that_are_no_numbers(cuda_lib):
+    """A scale that is negative or not finite makes the rows that see its block NaN, and
+    no other's."""
+    for bad in (float("nan"), float("inf"), -1.0):
+        for block in (16, 64):
+            b = P.Batch([(100, 300), (1, 500)], block, seed=35)
+            q, cache, scale = make(b, P.BLOCK, 16, 576, 9)
+            cache[(cache & 0x7F) == 0] = 1             # (no infinity times zero)
+            ref = P.attend(q, P.dequant(cache, P.BLOCK, scale, b), b, 576 ** -0.5, 0, 0)
+            page = 256 // block                        # positions from 256 on
+            changed = scale.clone()
+            changed[b.table[0, page]] = bad
+            out, lse = launch(cuda_lib, b, P.BLOCK, q, cache, changed, 576 ** -0.5, 0, 0)
+            O = out.float().cpu()
+            sees = torch.tensor([r == 0 and p >= page * block for _, r, p in b.tokens()])
+            assert bool(torch.isnan(O[sees]).all())
+            clean = (~sees).nonzero().flatten()
+            assert bool(torch.isfinite(O[clean]).all())
+            tol = 2.0 ** -8 * ref[0].abs() + (2.0 ** -7 + 2.0 ** -9) * ref[2] + 2.0 ** -23 * ref[5]
+            assert bool(((O - ref[0]).abs() <= tol)[clean].all())
 
 
 @pytest.mark.parametrize("rows,limit", [WHOLE, RANGES], ids=["whole", "ranges"])
