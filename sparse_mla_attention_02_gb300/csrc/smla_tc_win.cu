@@ -873,6 +873,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         const bool boxed = whole_box(id);
         const uint32_t ktile = sb + C::kOffK;
         if (a.box == 64 && __all_sync(0xffffffffu, boxed)) {  // the 64 rows as one box
+          const int row = __shfl_sync(0xffffffffu, id.x, 0);  // (any lane may be elected)
           if (elect_one()) {
 #pragma unroll 1
             for (int g = 0; g < groups; ++g) {
@@ -887,9 +888,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
                 mbar_arrive_expect_tx(bar(kBarKFull + g),
                                       2u * (half ? 1u : (uint32_t)C::kAtomsPerGroup) * kAtom);
               if (half)
-                tma_load_2d_pair(dst, &a.box_map, cols * c0, id.x, kfull0 + 8u * g);
+                tma_load_2d_pair(dst, &a.box_map, cols * c0, row, kfull0 + 8u * g);
               else
-                tma_load_3d_pair(dst, &a.k_map, 0, id.x, c0, kfull0 + 8u * g);
+                tma_load_3d_pair(dst, &a.k_map, 0, row, c0, kfull0 + 8u * g);
               ++issued;
             }
           }
@@ -958,6 +959,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           // Two whole boxes, from one lane (bf16: a prompt 1.31 -> 1.28 ms; E4M3 rows,
           // whose V comes in half as many bytes, lose by it: 1.26 -> 1.30 ms).
           if (!kFp8 && a.box == 64 && __all_sync(0xffffffffu, boxed)) {
+            const int near = __shfl_sync(0xffffffffu, id.x, 0);  // (any lane may be elected)
             const int far = __shfl_sync(0xffffffffu, id.x, 16);
             bool on = true;
             if (elect_one()) {
@@ -968,7 +970,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
                   break;
                 }
                 if (r == 0) mbar_arrive_expect_tx(bar(kBarVFull + v), 2u * C::kVUnit);
-                const int ch = 256 * (v >> 1) + 128 * (int)r, row = v & 1 ? far : id.x;
+                const int ch = 256 * (v >> 1) + 128 * (int)r, row = v & 1 ? far : near;
                 const uint32_t slot = sb + C::kOffV + v * C::kVUnit;
                 tma_load_3d_pair(slot, &a.v_map, 0, row, ch / 64, vfull0 + 8u * v);
                 ++issued;
