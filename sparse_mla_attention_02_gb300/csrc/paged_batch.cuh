@@ -13,8 +13,23 @@
 
 namespace smla {
 
+// Descriptors and scales: coherent loads, kept behind a griddepcontrol.wait that
+// stands before them.  A kernel launched under the end of the one that writes them
+// (the windowed attention) must not read them through the read-only path, which
+// takes them for constant during its whole life.
+__device__ __forceinline__ int ld_batch(const int32_t* at) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(at));
+  return v;
+}
+__device__ __forceinline__ float ld_batch(const float* at) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at));
+  return v;
+}
+
 __device__ __forceinline__ int batch_start(const PagedBatch& b, int r) {
-  return min(max(__ldg(b.query_start + r), 0), b.N);
+  return min(max(ld_batch(b.query_start + r), 0), b.N);
 }
 
 // Row of block `blk` (an entry of the table) plus `off`, or -1 when the block
@@ -36,7 +51,7 @@ __device__ __forceinline__ int batch_block(const PagedBatch& b, int r, int64_t p
     bad = true;
     return -1;
   }
-  return __ldg(b.block_table + (int64_t)r * b.bt_stride + page);
+  return ld_batch(b.block_table + (int64_t)r * b.bt_stride + page);
 }
 
 // The request of packed token n, or -1 behind the last request; the eight

@@ -122,7 +122,7 @@ __device__ __forceinline__ void rotate8(const uint4 raw, const Turn& t, bool int
 // (a position past the table sets the status).
 __device__ __forceinline__ int token_position(const AppendParams& a, int n, int r, bool& bad) {
   if (r < 0) return -1;
-  const int pos = __ldg(a.b.seq_lens + r) - batch_start(a.b, r + 1) + n;
+  const int pos = ld_batch(a.b.seq_lens + r) - batch_start(a.b, r + 1) + n;
   if (pos >= 0 && a.cos_sin && pos >= a.cos_sin_rows) {
     bad = true;
     return -1;
@@ -295,7 +295,7 @@ __device__ __forceinline__ void write_block(const AppendParams& a, int64_t unit,
   const int r = warp_last_request(b.num_reqs, unit,
                                   [&](int m) { return first_block_unit(b, m); });
   const int t0 = batch_start(b, r), t1 = batch_start(b, r + 1);
-  const int len = __ldg(b.seq_lens + r);
+  const int len = ld_batch(b.seq_lens + r);
   const int p0 = len - (t1 - t0);                    // position of token t0
   const int64_t page = (int64_t)max(p0, 0) / b.block_size + (unit - first_block_unit(b, r));
   const int64_t low = page * b.block_size;           // the block's first position

@@ -304,7 +304,7 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
 __device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
   const int64_t tile = p.num_tiles - 1 - u;
   const int r = warp_last_request(p.b.num_reqs, tile, [&](int m) { return first_tile(p, m); });
-  return tile_unit(p, r, batch_start(p.b, r), batch_start(p.b, r + 1), __ldg(p.b.seq_lens + r),
+  return tile_unit(p, r, batch_start(p.b, r), batch_start(p.b, r + 1), ld_batch(p.b.seq_lens + r),
                    tile - first_tile(p, r));
 }
 
@@ -350,7 +350,7 @@ __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
       if (pass == 0 || p.b.num_reqs > 32) {
         const int r = min(first + lane, p.b.num_reqs - 1);
         const int c0 = batch_start(p.b, r), c1 = batch_start(p.b, r + 1);
-        const int len = __ldg(p.b.seq_lens + r);
+        const int len = ld_batch(p.b.seq_lens + r);
         const int tiles = first + lane < p.b.num_reqs ? request_tiles(p, c0, c1) : 0;
         // One tile: its lane counts it.  More: the warp counts the request together.
         n = tiles == 1 ? kTileCost + max(tile_unit(p, r, c0, c1, len, 0).nb, 1) : 0;
@@ -395,7 +395,7 @@ __device__ __forceinline__ Unit next_part(const WinParams& p, Walk& k, int w, bo
 #pragma unroll 1
   while (k.pos < k.end && k.r < p.b.num_reqs) {
     const int c0 = batch_start(p.b, k.r), c1 = batch_start(p.b, k.r + 1);
-    const int len = __ldg(p.b.seq_lens + k.r);
+    const int len = ld_batch(p.b.seq_lens + k.r);
     const int tiles = request_tiles(p, c0, c1);
     // The request's tile that holds the place: number t, its blocks from t0 on.
     int t = 0;
@@ -487,12 +487,21 @@ struct MetaRing {
 // the append writes, it counts as that (zero too: values of at most 2^-55, scores
 // next to 0), and a negative one is NaN.
 __device__ __forceinline__ float block_scale(const WinParams& p, int blk) {
-  const float x = __ldg(p.k_scale + blk);
+  const float x = ld_batch(p.k_scale + blk);
   return x < 0x1p-64f ? (x < 0.f ? NAN : 0x1p-64f) : x;
 }
 // A key's scale (E4M3 caches).
 __device__ __forceinline__ float key_scale(const WinParams& p, int blk) {
-  return p.kv_format == kE4m3Block ? block_scale(p, blk) : __ldg(p.k_scale);
+  return p.kv_format == kE4m3Block ? block_scale(p, blk) : ld_batch(p.k_scale);
+}
+
+// 16 bytes of q, in order behind what was waited for (ld_batch).
+__device__ __forceinline__ uint4 ld_q16(const uint4* at) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(at));
+  return v;
 }
 
 // One row again, from its visible positions in the unit's blocks alone, by one
@@ -509,7 +518,7 @@ __device__ __forceinline__ void slow_row(const WinParams& p, const Unit& t, int6
                                                          g * p.d_qk) + lane;
 #pragma unroll
   for (int i = 0; i < 9; ++i) {
-    const uint32_t w = i < n2 ? __ldg(qr + 32 * i) : 0u;
+    const uint32_t w = i < n2 ? qr[32 * i] : 0u;
     q[i][0] = __uint_as_float(w << 16);
     q[i][1] = __uint_as_float(w & 0xFFFF0000u);
   }
@@ -532,17 +541,15 @@ __device__ __forceinline__ void slow_row(const WinParams& p, const Unit& t, int6
         k[i][0] = k[i][1] = 0.f;
         if (i < n2) {
           if (kFp8) {
-            const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(
-                                         static_cast<const uint8_t*>(p.kv) +
-                                         (int64_t)row * p.d_qk) + lane + 32 * i);
+            const uint16_t w = reinterpret_cast<const uint16_t*>(
+                static_cast<const uint8_t*>(p.kv) + (int64_t)row * p.d_qk)[lane + 32 * i];
             float x, y;
             e4m3x4_to_f32(w, k[i][0], k[i][1], x, y);
             k[i][0] *= sc;
             k[i][1] *= sc;
           } else {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(
-                                         static_cast<const uint16_t*>(p.kv) +
-                                         (int64_t)row * p.d_qk) + lane + 32 * i);
+            const uint32_t w = reinterpret_cast<const uint32_t*>(
+                static_cast<const uint16_t*>(p.kv) + (int64_t)row * p.d_qk)[lane + 32 * i];
             k[i][0] = __uint_as_float(w << 16);
             k[i][1] = __uint_as_float(w & 0xFFFF0000u);
           }
@@ -1194,7 +1201,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const uint32_t* words = reinterpret_cast<const uint32_t*>(sm + C::kOffMask);
     const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
     // One scale per tensor multiplies every score and the output.
-    const float kscale = p.kv_format == kE4m3 ? __ldg(p.k_scale) : 1.f;
+    const float kscale = p.kv_format == kE4m3 ? ld_batch(p.k_scale) : 1.f;
     MetaRing mr;
     int J = 0, q = 0;                                  // blocks, units with blocks
     for (int i = 0;; ++i) {
@@ -1571,7 +1578,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             static_cast<const uint16_t*>(p.q) + (have ? gr : u.row0) * p.d_qk) + j8;
 #pragma unroll
         for (int c = 0; c < 9; ++c)
-          ahead[c] = have && c < nch ? __ldg(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+          ahead[c] = have && c < nch ? ld_q16(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
       };
       load_row(g0);
       if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
