@@ -59,7 +59,7 @@
 // token, which may never have been written, and blocks that are not allocated are
 // read as zeros.  Any other masked position was written; should it hold an infinity
 // or NaN, a row whose output is not finite although its softmax is is computed
-// again from its visible positions alone (slow_row).
+// again from its visible positions alone (slow_rows).
 //
 // Scheduling.  A unit is a tile with some of its key blocks.  Many tiles: a unit
 // is a tile; the grid has one cluster per tile, and a running cluster takes over
@@ -147,7 +147,8 @@ enum {
 // line: the roles' loops then stay small, and they have to share one
 // instruction cache (waits in line cost this kernel 1.2x).
 struct PairWaiter {
-  uint32_t flags;                          // shared address: abort flag, abort counter at the start
+  uint32_t flags;                          // shared address: abort flag, abort counter at
+                                           // the start, beat
   const WinParams* p;
   __device__ __forceinline__ volatile int* shared(int i) const {
     return static_cast<volatile int*>(__cvta_shared_to_generic(flags)) + i;
@@ -163,14 +164,21 @@ struct PairWaiter {
   __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const;
 };
 
+// A wait that runs out gives up, unless a CTA of the pair has been computing rows
+// again meanwhile (slow_rows), which may take longer than any limit and says so by
+// its beat.
 static __device__ __noinline__ void pair_wait_slow(uint32_t bar, uint32_t parity, uint32_t flags,
                                                    const WinParams* p, bool drain) {
   const PairWaiter w{flags, p};
   Waiter slow{w.shared(0), p->status, p->abort_ctr, *w.shared(1), p->wait_limit_ns};
-  if (drain)
-    slow.drain(bar, parity);
-  else
-    slow.wait(bar, parity);
+  if (!drain && *slow.abort) return;
+  const volatile int* stop = drain ? nullptr : slow.ctr;
+  int beat;
+  do {
+    beat = *w.shared(2);
+    if (mbar_wait_bounded<false>(bar, parity, slow.limit_ns, stop, slow.ctr0)) return;
+  } while (*w.shared(2) != beat && !(stop && *stop != slow.ctr0));
+  slow.fail();
 }
 __device__ __forceinline__ bool PairWaiter::wait(uint32_t bar, uint32_t parity) const {
   if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
@@ -234,7 +242,7 @@ struct Cfg {
   static constexpr uint32_t kOffAbort = kOffTmem + 4;
   // E4M3: the keys' scales, each 32 keys' common scale (0: several), its log2
   // and its reciprocal, the Q rows' scales (two units')
-  static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 8 + 15) & ~15u : kOffAbort + 8;
+  static constexpr uint32_t kOffScale = kFp8 ? (kOffAbort + 12 + 15) & ~15u : kOffAbort + 12;
   static constexpr uint32_t kOffSeg = kOffScale + (kFp8 ? kMeta * kBN * 4 : 0); // float4 [kMeta][4]
   static constexpr uint32_t kOffQScale = kOffSeg + (kFp8 ? kMeta * 64 : 0);
   static constexpr uint32_t kSmem = kOffQScale + (kFp8 ? 2 * kRows * 4 : 0);
@@ -243,6 +251,9 @@ struct Cfg {
 // The epilogue's areas in P: row sums and flags.
 constexpr uint32_t kOffSums = 4096;        // float [2][4][64]
 constexpr uint32_t kOffFlag = 4096 + 2048; // int [64]
+// slow_rows': maxima and sums of eight warps, four rows of O
+constexpr uint32_t kOffWarpSums = 0;       // float2 [8]
+constexpr uint32_t kOffRows = 8192;        // float [4][512]
 
 struct WinArgs {
   CUtensorMap row_map;   // the cache, boxes of one row x 128 bytes (gather4)
@@ -504,88 +515,181 @@ __device__ __forceinline__ uint4 ld_q16(const uint4* at) {
   return v;
 }
 
-// One row again, from its visible positions in the unit's blocks alone, by one
-// warp.  O is written to `out_f32` or
-// `out_bf16` (512 channels).  Lane l holds channels 2 l + 64 i, + 1.
+// The unit's marked rows again, each from its visible positions in the unit's blocks
+// alone, by the eight softmax warps together: each warp takes 16 keys of every block,
+// two at a time, and the eight partial rows are merged in P's place.  A lane holds
+// twice eight neighbouring channels of a row's 512, and two of its rope.  131,072 keys
+// take 8 ms a row; meanwhile the pair's other warps wait (pair_wait_slow), for which a
+// beat goes to both CTAs.
 template <bool kFp8>
-__device__ __forceinline__ void slow_row(const WinParams& p, const Unit& t, int64_t g, int pos,
-                                             int lo, float* out_f32,
-                                             __nv_bfloat16* out_bf16) {
-  const int lane = threadIdx.x & 31;
-  const int n2 = p.d_qk / 64;
-  float q[9][2], acc[8][2];
-  const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.q) +
-                                                         g * p.d_qk) + lane;
+static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t, uint8_t* sp,
+                                              const PairWaiter w, uint32_t rank) {
+  constexpr int kKeys = 2;
+  const int lane = threadIdx.x & 31, sw = (threadIdx.x >> 5) - 4;
+  const bool rope = p.d_qk > 512;
+  // the lane's channels: ch .. + 7, ch + far .. + 7 (in one 16-byte load, or two)
+  constexpr int kFar = kFp8 ? 8 : 256;
+  const int ch = kFp8 ? 16 * lane : 8 * lane;
+  const int* flag = reinterpret_cast<const int*>(sp + kOffFlag);
+  float2* ml = reinterpret_cast<float2*>(sp + kOffWarpSums);
+  float* part = reinterpret_cast<float*>(sp + kOffRows) + 512 * (sw & 3) + ch;
+  const uint32_t beat = w.flags + 8, far_beat = mapa(beat, rank ^ 1u);
+#pragma unroll 1
+  for (int rr = 0; rr < kRows; ++rr) {
+    if (!flag[rr]) continue;
+    const int64_t g = (int64_t)t.row0 + 64 * (int)rank + rr;
+    const int pos = t.p_last - ((t.row1 - 1) / p.h - (int)g / p.h);
+    const int lo = p.window ? max(pos - (p.window - 1), 0) : 0;
+    const uint16_t* qr = static_cast<const uint16_t*>(p.q) + g * p.d_qk;
+    const uint4 q0 = *reinterpret_cast<const uint4*>(qr + ch);
+    const uint4 q1 = *reinterpret_cast<const uint4*>(qr + ch + kFar);
+    const uint32_t q[9] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w,
+                           rope ? reinterpret_cast<const uint32_t*>(qr + 512)[lane] : 0u};
+    float acc[8][2];
 #pragma unroll
-  for (int i = 0; i < 9; ++i) {
-    const uint32_t w = i < n2 ? qr[32 * i] : 0u;
-    q[i][0] = __uint_as_float(w << 16);
-    q[i][1] = __uint_as_float(w & 0xFFFF0000u);
-  }
+    for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    bool bad = false;                                  // (the lookups have said so)
+#pragma unroll 1
+    for (int b = t.b0; b < t.b0 + t.nb; ++b) {
+      const int e = t.block(b) * kBN + 16 * sw + (lane & 15);
+      if (lane == 0) {
+        const int now = (int)globaltimer_ns();
+        *w.shared(2) = now;
+        st_cluster_s32(far_beat, now);
+      }
+      if (__any_sync(0xffffffffu, w.aborted())) break;
+      int row = -1;
+      float scale = 1.f;
+      if (e <= pos && (e >= lo || e < p.sinks)) {
+        const int page = e / p.b.block_size;
+        const int blk = batch_block(p.b, t.r, page, bad);
+        row = batch_row(p.b, blk, e - page * p.b.block_size, bad);
+        if (kFp8 && row >= 0) scale = key_scale(p, blk);
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu;
+#pragma unroll 1
+      while (todo) {
+        uint32_t k[kKeys][kFp8 ? 5 : 9];               // (a row's last word: its rope)
+        float s[kKeys], sc[kKeys];
+        bool have[kKeys];
+        int src = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i][0] = acc[i][1] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  for (int b = t.b0; b < t.b0 + t.nb; ++b) {
-    const int e0 = t.block(b) * kBN;
-    for (int e = e0; e < e0 + kBN && e <= pos; ++e) {
-      if (!(e >= lo || e < p.sinks)) continue;
-      const int page = e / p.b.block_size;
-      const int blk = batch_block(p.b, t.r, page, bad);
-      const int row = batch_row(p.b, blk, e - page * p.b.block_size, bad);
-      if (row < 0) continue;
-      float k[9][2], s = 0.f;
-      const float sc = kFp8 ? key_scale(p, blk) : 1.f;
-#pragma unroll
-      for (int i = 0; i < 9; ++i) {
-        k[i][0] = k[i][1] = 0.f;
-        if (i < n2) {
+        for (int c = 0; c < kKeys; ++c) {              // (past the last: that key once more)
+          have[c] = todo != 0;
+          if (todo) src = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int64_t at = (int64_t)__shfl_sync(0xffffffffu, row, src) * p.d_qk;
+          sc[c] = __shfl_sync(0xffffffffu, scale, src);
           if (kFp8) {
-            const uint16_t w = reinterpret_cast<const uint16_t*>(
-                static_cast<const uint8_t*>(p.kv) + (int64_t)row * p.d_qk)[lane + 32 * i];
-            float x, y;
-            e4m3x4_to_f32(w, k[i][0], k[i][1], x, y);
-            k[i][0] *= sc;
-            k[i][1] *= sc;
+            const uint8_t* kr = static_cast<const uint8_t*>(p.kv) + at;
+            const uint4 x = *reinterpret_cast<const uint4*>(kr + ch);
+            k[c][0] = x.x; k[c][1] = x.y; k[c][2] = x.z; k[c][3] = x.w;
+            k[c][4] = rope ? reinterpret_cast<const uint16_t*>(kr + 512)[lane] : 0u;
           } else {
-            const uint32_t w = reinterpret_cast<const uint32_t*>(
-                static_cast<const uint16_t*>(p.kv) + (int64_t)row * p.d_qk)[lane + 32 * i];
-            k[i][0] = __uint_as_float(w << 16);
-            k[i][1] = __uint_as_float(w & 0xFFFF0000u);
+            const uint16_t* kr = static_cast<const uint16_t*>(p.kv) + at;
+            const uint4 x = *reinterpret_cast<const uint4*>(kr + ch);
+            const uint4 y = *reinterpret_cast<const uint4*>(kr + ch + kFar);
+            k[c][0] = x.x; k[c][1] = x.y; k[c][2] = x.z; k[c][3] = x.w;
+            k[c][kFp8 ? 0 : 4] = y.x; k[c][kFp8 ? 0 : 5] = y.y;
+            k[c][kFp8 ? 0 : 6] = y.z; k[c][kFp8 ? 0 : 7] = y.w;
+            k[c][kFp8 ? 0 : 8] =
+                rope ? reinterpret_cast<const uint32_t*>(kr + 512)[lane] : 0u;
           }
-          s = fmaf(q[i][0], k[i][0], fmaf(q[i][1], k[i][1], s));
         }
-      }
+        // The i-th pair of the lane's channels (8: the rope's).
+        auto key = [&](int c, int i, float& x, float& y) {
+          if (kFp8) {
+            float z, u;
+            e4m3x4_to_f32(i == 8 ? k[c][4] : k[c][i / 2] >> (16 * (i & 1)), x, y, z, u);
+          } else {
+            x = __uint_as_float(k[c][kFp8 ? 0 : i] << 16);
+            y = __uint_as_float(k[c][kFp8 ? 0 : i] & 0xFFFF0000u);
+          }
+        };
+        float top = m;
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= p.sm_scale;
-      if (s > m) {
-        const float a = expf(m - s);
-        l *= a;
+        for (int c = 0; c < kKeys; ++c) {
+          float s1 = 0.f;
+          s[c] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc[i][0] *= a;
-          acc[i][1] *= a;
+          for (int i = 0; i < 9; ++i) {
+            float x, y;
+            key(c, i, x, y);
+            s[c] = fmaf(__uint_as_float(q[i] << 16), x, s[c]);
+            s1 = fmaf(__uint_as_float(q[i] & 0xFFFF0000u), y, s1);
+          }
+          s[c] += s1;
         }
-        m = s;
-      }
-      const float w = s == -INFINITY ? 0.f : expf(s - m);
-      l += w;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[i][0] = fmaf(w, k[i][0], acc[i][0]);
-        acc[i][1] = fmaf(w, k[i][1], acc[i][1]);
+        for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] += __shfl_xor_sync(0xffffffffu, s[c], o);
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) {
+          s[c] = have[c] ? s[c] * sc[c] * p.sm_scale : -INFINITY;
+          top = fmaxf(top, s[c]);
+        }
+        if (top > m) {
+          const float a = expf(m - top);
+          l *= a;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[i][0] *= a;
+            acc[i][1] *= a;
+          }
+          m = top;
+        }
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) {
+          if (!have[c]) continue;
+          const float e2 = s[c] == -INFINITY ? 0.f : expf(s[c] - m);
+          l += e2;
+          const float wt = e2 * sc[c];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x, y;
+            key(c, i, x, y);
+            acc[i][0] = fmaf(wt, x, acc[i][0]);
+            acc[i][1] = fmaf(wt, y, acc[i][1]);
+          }
+        }
       }
     }
-  }
+    // The eight warps' rows: the upper four's, then with the lower four's, then in one.
+    if (lane == 0) ml[sw] = make_float2(m, l);
+    named_bar_sync(4, 256);
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = acc[i][0] / l, y = acc[i][1] / l;
-    const int c = 2 * lane + 64 * i;
-    if (out_f32)
-      *reinterpret_cast<float2*>(out_f32 + c) = make_float2(x, y);
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, ml[i].x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += ml[i].x == -INFINITY ? 0.f : ml[i].y * expf(ml[i].x - top);
+    // (a warp without a key: its sums are 0, or NaN where 0 met an infinity)
+    const float f = (m == -INFINITY ? 1.f : expf(m - top)) / sum;
+    auto at = [&](int i) { return reinterpret_cast<float2*>(part + (i & 4 ? kFar - 8 : 0) + 2 * i); };
+    if (sw >= 4)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *at(i) = make_float2(acc[i][0] * f, acc[i][1] * f);
+    named_bar_sync(4, 256);
+    if (sw < 4)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 o = *at(i);
+        *at(i) = make_float2(fmaf(acc[i][0], f, o.x), fmaf(acc[i][1], f, o.y));
+      }
+    named_bar_sync(4, 256);
+    const int c = threadIdx.x - 128;                   // two channels a thread
+    const float2* o = reinterpret_cast<const float2*>(sp + kOffRows) + c;
+    const float x = (o[0].x + o[256].x) + (o[512].x + o[768].x);
+    const float y = (o[0].y + o[256].y) + (o[512].y + o[768].y);
+    if (t.slot >= 0)
+      reinterpret_cast<float2*>(p.o_part +
+                                ((int64_t)t.slot * 128 + 64 * (int)rank + rr) * 512)[c] =
+          make_float2(x, y);
     else
-      *reinterpret_cast<uint32_t*>(out_bf16 + c) = pack_bf16(x, y);
+      reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + g * 512)[c] =
+          pack_bf16(x, y);
+    named_bar_sync(4, 256);                            // (the next row's sums take their place)
   }
 }
 
@@ -643,6 +747,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   if (tid == 64) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     *W.shared(0) = 0;
+    *W.shared(2) = 0;
     *W.shared(1) = *reinterpret_cast<volatile int*>(p.abort_ctr);
   }
   if (tid == 128) {
@@ -956,7 +1061,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
           // Rows behind the last token may never have been written, and a weight of
           // 0 times NaN is NaN: they are read as zeros.  (The other rows of a block
-          // were written; one that is not finite costs the tile slow_row.)
+          // were written; one that is not finite costs the tile slow_rows.)
           const int up = u.live - 2 - (u.template work<kFp8>(j) * kBN + 4 * lane);
           if (up < 0) id.x = -1;
           if (up < 1) id.y = -1;
@@ -1541,16 +1646,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       odd = odd && live && l < INFINITY && lr < INFINITY;
       if (odd) flag[row] = 1;
       if (__builtin_expect(named_bar_or(4, 256, odd), 0)) {  // (also orders the stores before)
-        for (int rr = warp - 4; rr < kRows; rr += 8) {
-          if (!flag[rr]) continue;
-          const int64_t gr = (int64_t)t->row0 + 64 * (int)r + rr;
-          const int pr = t->p_last - ((t->row1 - 1) / p.h - (int)gr / p.h);
-          slow_row<kFp8>(p, *t, gr, pr, p.window ? max(pr - (p.window - 1), 0) : 0,
-                         partial ? p.o_part + ((int64_t)t->slot * 128 + 64 * (int)r + rr) * 512
-                                 : nullptr,
-                         out + gr * 512);
-        }
-        named_bar_sync(4, 256);                          // the flags were read
+        slow_rows<kFp8>(p, *t, sm + C::kOffP, W, r);
       }
       // (the next unit's first weights are signalled behind these TMEM loads)
       tc_fence_before();
