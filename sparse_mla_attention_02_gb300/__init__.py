@@ -117,6 +117,23 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on ``stream`` (None: the current one) writes and the
+    current stream may read.  It comes from ``stream``'s memory: the current stream's
+    may have held a tensor that work still queued there reads.  Once let go it is
+    used again only when both streams are done with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _check(code, what):
     if code != SMLA_OK:
         raise SmlaError(code, what)
@@ -170,7 +187,7 @@ def _in_args(q, kv_cache, kv_dtype, k_scale, indices, valid_len, sm_scale,
 
 
 def _fwd_args(q, kv_cache, kv_dtype, k_scale, indices, valid_len, sm_scale,
-              out, lse, num_slots):
+              out, lse, num_slots, stream):
     import torch
     _require(q.is_cuda and q.dtype == torch.bfloat16 and q.is_contiguous() and q.dim() == 3,
              "q must be a contiguous bf16 device tensor [T, h, d_qk]")
@@ -180,7 +197,7 @@ def _fwd_args(q, kv_cache, kv_dtype, k_scale, indices, valid_len, sm_scale,
     topk = indices.shape[1]
     d_v = 512
     if out is None:
-        out = torch.empty((T, h, d_v), dtype=torch.bfloat16, device=q.device)
+        out = _empty((T, h, d_v), torch.bfloat16, q.device, stream)
     _require(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (T, h, d_v),
              "out must be contiguous bf16 [T, h, 512]")
     if lse is not None:
@@ -202,9 +219,9 @@ def smla_fwd(q, kv_cache, kv_dtype, k_scale, indices, valid_len, sm_scale,
     import torch
     lib = load()
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(q.shape[:2], torch.float32, q.device, stream)
     args, out, lse = _fwd_args(q, kv_cache, kv_dtype, k_scale, indices,
-                               valid_len, sm_scale, out, lse, num_slots)
+                               valid_len, sm_scale, out, lse, num_slots, stream)
     _check(lib.smla_fwd(*args, _stream(stream)), "smla_fwd")
     return out, lse
 
@@ -232,11 +249,11 @@ def smla_fwd_split_q(q_nope, q_pe, kv_cache, kv_dtype, k_scale, indices, valid_l
     S = _kv_slots(kv_cache, kv_dtype, k_scale, d_qk, num_slots)
     _idx_checks(indices, valid_len, T)
     if out is None:
-        out = torch.empty((T, h, 512), dtype=torch.bfloat16, device=q_nope.device)
+        out = _empty((T, h, 512), torch.bfloat16, q_nope.device, stream)
     _require(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (T, h, 512),
              "out must be contiguous bf16 [T, h, 512]")
     if lse is None and want_lse:
-        lse = torch.empty((T, h), dtype=torch.float32, device=q_nope.device)
+        lse = _empty((T, h), torch.float32, q_nope.device, stream)
     if lse is not None:
         _require(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (T, h),
                  "lse must be contiguous fp32 [T, h]")
@@ -439,13 +456,13 @@ def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block
     S, scale = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
                            block_stride_rows or block_size, index)
     if out is None:
-        out = torch.empty((T, h, 512), dtype=bf16, device=q.device)
+        out = _empty((T, h, 512), bf16, q.device, stream)
     elif not (out.dtype is bf16 and out.shape == (T, h, 512) and out.is_contiguous() and
               out.get_device() == index):
         raise ValueError("out must be contiguous bf16 [T, h, 512]")
     if lse is None:
         if want_lse:
-            lse = torch.empty((T, h), dtype=torch.float32, device=q.device)
+            lse = _empty((T, h), torch.float32, q.device, stream)
     elif not (lse.dtype is torch.float32 and lse.shape == (T, h) and lse.is_contiguous() and
               lse.get_device() == index):
         raise ValueError("lse must be contiguous fp32 [T, h]")
@@ -455,11 +472,7 @@ def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block
         nbytes = lib.smla_fwd_window_workspace_size(batch[3], T, h, d_qk, 512, kv_dtype, batch[4],
                                                     block_size, window, sinks, limit)
         if nbytes:
-            if stream is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-            else:
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _empty((nbytes,), torch.uint8, q.device, stream)
             ws = workspace.data_ptr()
     else:
         if not (workspace.get_device() == index and workspace.is_contiguous()):
@@ -483,9 +496,9 @@ def smla_fwd_partial(q, kv_cache, kv_dtype, k_scale, indices, valid_len,
     lib = load()
     T, h, _ = q.shape
     if out is None:
-        out = torch.empty((T, h, 512), dtype=torch.float32, device=q.device)
+        out = _empty((T, h, 512), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, h), dtype=torch.float32, device=q.device)
+        lse = _empty((T, h), torch.float32, q.device, stream)
     _require(out.dtype == torch.float32 and out.is_contiguous() and out.shape == (T, h, 512),
              "out must be contiguous fp32 [T, h, 512]")
     _require(lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (T, h),
@@ -511,9 +524,9 @@ def smla_fwd_paged(q, kv_cache, kv_dtype, k_scale, token_indices, req_id,
     import torch
     lib = load()
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(q.shape[:2], torch.float32, q.device, stream)
     args, out, lse = _fwd_args(q, kv_cache, kv_dtype, k_scale, token_indices,
-                               valid_len, sm_scale, out, lse, num_slots)
+                               valid_len, sm_scale, out, lse, num_slots, stream)
     for x in (req_id, block_table):
         _require(x.is_cuda and x.dtype == torch.int32 and x.is_contiguous(),
                  "req_id and block_table must be contiguous int32 device tensors")
@@ -566,9 +579,9 @@ def smla_fwd_ws(q, kv_cache, kv_dtype, k_scale, indices, valid_len, sm_scale,
     import torch
     lib = load()
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(q.shape[:2], torch.float32, q.device, stream)
     args, out, lse = _fwd_args(q, kv_cache, kv_dtype, k_scale, indices,
-                               valid_len, sm_scale, out, lse, num_slots)
+                               valid_len, sm_scale, out, lse, num_slots, stream)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.smla_fwd_ws(*args, _p(workspace), nbytes, _stream(stream)),
            "smla_fwd_ws")
@@ -618,8 +631,7 @@ def smla_fwd_host(q, kv_cache, kv_dtype, k_scale, indices, valid_len, sm_scale,
     nbytes = smla_fwd_host_workspace_size(T, h, d_qk, topk, kv_dtype, d_v,
                                           chunk_tokens)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8,
-                                device=kv_cache.device)
+        workspace = _empty((max(nbytes, 1),), torch.uint8, kv_cache.device, stream)
     _check(lib.smla_fwd_host(_p(q), _p(kv_cache), kv_dtype, _p(k_scale),
                              _p(indices), _p(valid_len), T, h, d_qk, d_v, topk,
                              S, float(sm_scale), _p(out), _p(lse),
@@ -639,9 +651,9 @@ def smla_combine(o_parts, lse_parts, out=None, lse=None, stream=None):
     _require(lse_parts.dtype == torch.float32 and lse_parts.is_contiguous() and
              lse_parts.shape == (P, rows), "lse_parts must be contiguous fp32 [P, rows]")
     if out is None:
-        out = torch.empty((rows, d_v), dtype=torch.bfloat16, device=o_parts.device)
+        out = _empty((rows, d_v), torch.bfloat16, o_parts.device, stream)
     if lse is None:
-        lse = torch.empty((rows,), dtype=torch.float32, device=o_parts.device)
+        lse = _empty((rows,), torch.float32, o_parts.device, stream)
     _check(lib.smla_combine(_p(o_parts), _p(lse_parts), P, rows, d_v, _p(out),
                             _p(lse), _stream(stream)), "smla_combine")
     return out, lse
