@@ -34,9 +34,9 @@
  *    bf16 rounding of O alone takes up to 2^-8 |O| there) and
  *    |dLSE| <= 1e-3.  The softmax weights reach the PV product rounded to
  *    bf16 (bf16 caches, O divided by the sum of the rounded weights) or as
- *    three E4M3 terms that keep them to their f16 rounding (E4M3 caches), so
- *    a row that one key carries keeps that key's V row to within the output's
- *    own rounding.
+ *    three E4M3 terms that keep them to their f16 rounding (E4M3 caches;
+ *    smla_fwd_window has its own form, described there), so a row that one key
+ *    carries keeps that key's V row to within the output's own rounding.
  */
 #ifndef SMLA_H_
 #define SMLA_H_
@@ -336,6 +336,15 @@ SMLA_API smla_status smla_cache_append(
  *               smla_fwd_window_workspace_size(...) bytes; NULL allowed when
  *               that is 0.  One workspace must not be shared by calls, or by
  *               captured graphs, that may overlap on the GPU.
+ * Accuracy: the contract at the top of this file, with bf16 caches as there.
+ * With E4M3 caches a weight w_e = softmax(s)_e * scale_e reaches the PV product
+ * to 9 significant bits (2^-9 of it), rounded to a grid of 2^-27 of the row's
+ * largest w (or a finer one): O is off by at most
+ *   2^-8 |O| + 2^-8 sum w_e |V_e| / scale_e + 2^-28 max(w) sum |V_e| / scale_e
+ * beside the scores' own rounding (fp32 accumulation; Q as two E4M3 terms, off by
+ * 2^-17.8 of its row's largest value).  Keys 11 nats below the top one keep their
+ * 9 bits, keys 16 nats below may be off by 3 %, keys 20 nats below vanish from O
+ * (LSE counts them all).
  * Rows of tokens behind query_start[num_reqs] are left alone.  A position past
  * the block table or a row past the cache is not seen and sets the
  * SMLA_ERR_BAD_INDEX device status.  Asynchronous on `stream`, no allocation.

@@ -45,8 +45,9 @@
 // PV: a weight is the sum of three E5M2 terms.  E5M2 is the upper byte of f16 and
 // holds 3 significant bits, so a weight rounded to 9 of f16's 11 bits is exactly
 // its upper byte + that of the rest + that of what then remains (one bit more
-// than bf16 keeps); what falls below E5M2's grid is less than 2^-23 of a weight of
-// 1.  The key's scale belongs to its weight: with t = s + log2(scale) the running
+// than bf16 keeps); the third is rounded to E5M2's grid, 2^-27 of the row's reference
+// weight (so that keys 11 nats below the top still have their 9 bits, keys 16 nats
+// below are off by 3 %).  The key's scale belongs to its weight: with t = s + log2(scale) the running
 // maximum is taken over t, the weights are 2^(t - m) = scale 2^(s - m), and the
 // sum that divides adds weight / scale, in fp32 where the weights are too small for
 // the product.  So blocks of any scales share one range, and nothing is converted on
@@ -221,6 +222,11 @@ struct Cfg {
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
   static constexpr int kMaxAtoms = kFp8 ? 5 : 9;        // 128-byte columns of a row
+  // O is rescaled where a row's maximum grows by more than 2^kRaise; E4M3 rows' weights
+  // are multiplied by 2^kUp, into E5M2's range.
+  static constexpr float kRaise = kFp8 ? 4.f : 8.f;
+  static constexpr float kUp = kFp8 ? 15.f - kRaise : 0.f;
+  static constexpr float kBack = kFp8 ? 0x1p-11f : 1.f;          // 2^-kUp
   static constexpr int kPBufs = kFp8 ? 2 : 1;
   static constexpr int kQTerms = kFp8 ? 2 : 1;
   static constexpr int kPTerms = kFp8 ? 3 : 1;
@@ -1423,12 +1429,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         float* rb = red + (kFp8 ? 256 * buf : 0);
         rb[64 * seg + row] = hm;
         float alpha = 1.f;
-        if (named_bar_or(4, 256, hm > m_run + 8.f)) {    // also true for the first finite max
+        if (named_bar_or(4, 256, hm > m_run + C::kRaise)) {    // also true for the first finite max
           float bm = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) bm = fmaxf(bm, rb[64 * k + row]);
           if (!kFp8) named_bar_sync(4, 256);             // (the maxima were read)
-          if (bm > m_run + 7.f) {
+          if (bm > m_run + (C::kRaise - 1.f)) {
             alpha = ex2_approx(m_run - bm);              // 0 when m_run = -inf
             if (kFp8) {                                  // (the sums' own range is wider)
               const float half = ex2_approx(0.5f * (m_run - bm));
@@ -1447,7 +1453,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           // The divisor, sum of weight / scale: where the 32 keys share their scale the
           // weights as the product has them, so that a key that carries the row keeps
           // its V.  The product has nothing of weights that lie far below the row's
-          // reference (f16 ends at 2^-31 of it), but 1 / scale may make them most of
+          // reference (f16 ends at 2^-33 of it), but 1 / scale may make them most of
           // the softmax: from 2^-15 on their fp32 sum divides, from 2^-90 on (where
           // fp32 begins to end) the sum of 2^(s - m), without the scale.
           const bool low = hm < ref - 15.f;
@@ -1463,7 +1469,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) bare += ex2_approx(fmaf(s[k], cl, -ref));
           }
-          // 2^(t - m + 7) <= 2^15: within E5M2's range, its grid 2^-23 of a weight
+          // 2^(t - m + kUp) <= 2^15: within E5M2's range, its grid 2^-27 of a weight of 1
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             uint32_t h[2];
@@ -1471,7 +1477,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             for (int e = 0; e < 2; ++e) {
               float& s0 = s[k + 2 * e];
               float& s1 = s[k + 2 * e + 1];
-              fma2_bcast(s0, s1, cl, 7.f - mm);
+              fma2_bcast(s0, s1, cl, C::kUp - mm);
               const float w0 = ex2_approx(s0), w1 = ex2_approx(s1);
               add2(ls, ls1, w0, w1);
               h[e] = (pack_f16(w0, w1) + 0x00020002u) & 0xFFFCFFFCu;  // 9 significant bits
@@ -1481,6 +1487,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             }
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
+              if (x == 2) {                              // what is left, to the nearest
+                h[0] += 0x00800080u;
+                h[1] += 0x00800080u;
+              }
               pk[8 * x + k / 4] = __byte_perm(h[0], h[1], 0x7531);   // the four upper bytes
               if (x < 2) {
                 h[0] = sub_f16x2(h[0], h[0] & 0xFF00FF00u);
@@ -1488,7 +1498,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
               }
             }
           }
-          back *= 0x1p-7f;
+          back *= C::kBack;
           ls = several || hm < ref - 90.f ? bare : (ls + ls1) * back;
           lr = several || low ? ls : (lr + lr1) * back;  // (9 bits: 2^-9 of a weight at most)
           l_run += ls;
@@ -1570,7 +1580,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       const bool empty = l == 0.f;
       // (a sum that is not finite: NaN, whatever the weights' terms became)
-      const float top = kFp8 ? kscale * 0x1p-7f : kscale;
+      const float top = kFp8 ? kscale * C::kBack : kscale;
       const float inv = empty ? 0.f : l < INFINITY ? __fdividef(top, lr) : NAN;
       const bool partial = t->slot >= 0;
       const int64_t g = (int64_t)t->row0 + 64 * (int)r + row;

@@ -219,3 +219,32 @@ def test_equal_scores_of_every_size(cuda_lib):
         rows = V[[b.slot(t, e) for e in range(n)], :512]
         tol = 2.0 ** -8 * rows.mean(0).abs() + (2.0 ** -7 + 2.0 ** -9) * rows.abs().mean(0)
         assert bool(((out[t].double().cpu() - rows.mean(0)).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("fmt", [P.E4M3, P.BLOCK])
+@pytest.mark.parametrize("nats", [2.0, 11.0, 13.0, 14.5, 16.0, 17.5])
+@pytest.mark.parametrize("first", [True, False])
+def test_many_small_weights_behind_a_large_one(cuda_lib, fmt, nats, first):
+    """E4M3 rows: 16,384 keys of equal score `nats` below that of one key, whose value is
+    zero.  Their weights are 2^-b, b = nats / ln 2, of the row's reference, held to 9
+    bits (2^-9 of each) on a grid of 2^-27 (half of it: 2^(b - 28) of each); the large
+    one's is exact; 2^-8 for O's rounding, 2^-12 for exponentials and sums."""
+    n = 16385
+    b = P.Batch([(1, n), (1, 40)], 64, seed=39)
+    q, cache, scale = make(b, fmt, 16, 576, 13)
+    scale = torch.full_like(scale, 2.0 ** -6)
+    cache &= 0x7F                                      # (values of one sign)
+    cache[:, 575] = 0
+    large = b.slot(0, 0 if first else n - 1)
+    cache[large, :512] = 0
+    cache[large, 575] = 0x7E                           # 448 * 2^-6 = 7
+    q.zero_()
+    q[:, :, 575] = nats * 24 / 7
+    exact = float(q[0, 0, 575]) * 7 / 24               # (q's rounding)
+    out, lse = launch(cuda_lib, b, fmt, q, cache, scale, 1 / 24, 0, 0, max_seq_len=1)
+    rows = P.dequant(cache, fmt, scale, b)
+    total = sum(rows[b.slot(0, e), :512] for e in range(n))
+    want = total / (n - 1 + math.exp(exact))
+    rel = 2.0 ** -8 + 2.0 ** -9 + 2.0 ** (exact / math.log(2) - 28) + 2.0 ** -12
+    assert bool(((out[0].double().cpu() - want).abs() <= rel * want).all())
+    assert abs(float(lse[0, 0]) - math.log(n - 1 + math.exp(exact))) <= 2.0 ** -16
