@@ -32,6 +32,11 @@ __device__ __forceinline__ int batch_start(const PagedBatch& b, int r) {
   return min(max(ld_batch(b.query_start + r), 0), b.N);
 }
 
+// Length of request r (a negative one is 0, so that no position wraps round).
+__device__ __forceinline__ int batch_len(const PagedBatch& b, int r) {
+  return max(ld_batch(b.seq_lens + r), 0);
+}
+
 // Row of block `blk` (an entry of the table) plus `off`, or -1 when the block
 // is not allocated (blk < 0) or the row lies past the cache (sets *bad).
 __device__ __forceinline__ int batch_row(const PagedBatch& b, int blk, int off, bool& bad) {

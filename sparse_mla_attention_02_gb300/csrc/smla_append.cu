@@ -122,7 +122,7 @@ __device__ __forceinline__ void rotate8(const uint4 raw, const Turn& t, bool int
 // (a position past the table sets the status).
 __device__ __forceinline__ int token_position(const AppendParams& a, int n, int r, bool& bad) {
   if (r < 0) return -1;
-  const int pos = ld_batch(a.b.seq_lens + r) - batch_start(a.b, r + 1) + n;
+  const int pos = batch_len(a.b, r) - batch_start(a.b, r + 1) + n;
   if (pos >= 0 && a.cos_sin && pos >= a.cos_sin_rows) {
     bad = true;
     return -1;
@@ -295,21 +295,22 @@ __device__ __forceinline__ void write_block(const AppendParams& a, int64_t unit,
   const int r = warp_last_request(b.num_reqs, unit,
                                   [&](int m) { return first_block_unit(b, m); });
   const int t0 = batch_start(b, r), t1 = batch_start(b, r + 1);
-  const int len = ld_batch(b.seq_lens + r);
+  const int len = batch_len(b, r);
   const int p0 = len - (t1 - t0);                    // position of token t0
   const int64_t page = (int64_t)max(p0, 0) / b.block_size + (unit - first_block_unit(b, r));
   const int64_t low = page * b.block_size;           // the block's first position
   // positions [pa, pb) of the block are written; [low, p0) hold older rows
-  const int pa = (int)max(low, (int64_t)max(p0, 0));
+  const int64_t from = max(low, (int64_t)max(p0, 0));
   int pb = (int)min(low + b.block_size, (int64_t)len);
-  if (t1 <= t0 || pa >= pb) return;                  // (the same for every thread)
+  if (t1 <= t0 || from >= pb) return;                // (the same for every thread)
+  const int pa = (int)from;
   bool bad = false;
   if (kRope && pb > a.cos_sin_rows) {                // positions without a rope row
     bad = true;
     pb = (int)min((int64_t)pb, a.cos_sin_rows);
   }
   const int blk = batch_block(b, r, page, bad);
-  // (all of the block's rows lie in the cache, or none is written)
+  // (rows past the cache are not written)
   const int row0 = batch_row(b, blk, 0, bad);
   if (row0 >= 0 && row0 + (pb - 1 - low) >= b.num_slots) {
     bad = true;
@@ -319,6 +320,8 @@ __device__ __forceinline__ void write_block(const AppendParams& a, int64_t unit,
   if (row0 < 0 || pa >= pb) return;
   const int64_t base = row0 - low;                   // cache row of position p: base + p
 
+  // (i: rows from pa on; pa + i ends below pb, so it holds every position)
+  const int rows = pb - pa;
   auto load_row = [&](int p, uint4 (&raw)[9]) {
     const int64_t n = t0 + (p - p0);
 #pragma unroll
@@ -347,7 +350,8 @@ __device__ __forceinline__ void write_block(const AppendParams& a, int64_t unit,
       amax = fold(y, amax);
     }
   };
-  for (int p = pa + grp; p < pb; p += kGroups) {
+  for (int i = grp; i < rows; i += kGroups) {
+    const int p = pa + i;
     uint4 raw[9];
     float y[8];
     load_row(p, raw);
@@ -384,7 +388,8 @@ __device__ __forceinline__ void write_block(const AppendParams& a, int64_t unit,
       *reinterpret_cast<uint2*>(row + 512 + 8 * j) = codes8_of(y);
     }
   };
-  for (int p = pa + grp; p < pb; p += kGroups) {
+  for (int i = grp; i < rows; i += kGroups) {
+    const int p = pa + i;
     uint4 raw[9];
     float y[8];
     load_row(p, raw);

@@ -300,7 +300,7 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
   t.b0 = t.nb = t.sink_blocks = t.win_block = 0;
   t.p_last = t.lo = -1;
   t.sinks = 0;
-  t.live = 1 + min(max(len, 0), 0x7FFFFFFE);
+  t.live = 1 + min(len, 0x7FFFFFFE);
   if (!used) return t;
   const int tok0 = t.row0 / p.h, tok1 = (t.row1 - 1) / p.h;
   t.p_last = len - (c1 - tok1);
@@ -321,7 +321,7 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
 __device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
   const int64_t tile = p.num_tiles - 1 - u;
   const int r = warp_last_request(p.b.num_reqs, tile, [&](int m) { return first_tile(p, m); });
-  return tile_unit(p, r, batch_start(p.b, r), batch_start(p.b, r + 1), ld_batch(p.b.seq_lens + r),
+  return tile_unit(p, r, batch_start(p.b, r), batch_start(p.b, r + 1), batch_len(p.b, r),
                    tile - first_tile(p, r));
 }
 
@@ -367,7 +367,7 @@ __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
       if (pass == 0 || p.b.num_reqs > 32) {
         const int r = min(first + lane, p.b.num_reqs - 1);
         const int c0 = batch_start(p.b, r), c1 = batch_start(p.b, r + 1);
-        const int len = ld_batch(p.b.seq_lens + r);
+        const int len = batch_len(p.b, r);
         const int tiles = first + lane < p.b.num_reqs ? request_tiles(p, c0, c1) : 0;
         // One tile: its lane counts it.  More: the warp counts the request together.
         n = tiles == 1 ? kTileCost + max(tile_unit(p, r, c0, c1, len, 0).nb, 1) : 0;
@@ -412,7 +412,7 @@ __device__ __forceinline__ Unit next_part(const WinParams& p, Walk& k, int w, bo
 #pragma unroll 1
   while (k.pos < k.end && k.r < p.b.num_reqs) {
     const int c0 = batch_start(p.b, k.r), c1 = batch_start(p.b, k.r + 1);
-    const int len = ld_batch(p.b.seq_lens + k.r);
+    const int len = batch_len(p.b, k.r);
     const int tiles = request_tiles(p, c0, c1);
     // The request's tile that holds the place: number t, its blocks from t0 on.
     int t = 0;
