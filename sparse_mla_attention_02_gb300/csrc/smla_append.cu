@@ -396,8 +396,8 @@ __device__ __forceinline__ void write_block(const AppendParams& a, int64_t unit,
     if (kRope) rotate8(raw[8], load_turn(a, p), a.interleaved, y);
     store_row(raw, p, y);
   }
-  if (kept && old > 0.f && scale > old) {            // older rows follow the scale
-    const float ratio = old / scale;
+  if (kept && scale > old) {                         // older rows follow the scale
+    const float ratio = old / scale;                 // (from a zero one: they stay zero)
     uint2* codes = reinterpret_cast<uint2*>(cache + (base + low) * kD);
     const int64_t n8 = (int64_t)(p0 - low) * (kD / 8);
     for (int64_t i = threadIdx.x; i < n8; i += kThreads) {

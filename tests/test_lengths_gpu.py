@@ -16,6 +16,7 @@ LOW, HIGH = -2 ** 31, 2 ** 31 - 1
 def test_append_of_a_negative_length(cuda_lib, fmt, length):
     """Its tokens are at negative positions: skipped, and no error."""
     smla = cuda_lib
+    torch.manual_seed(1)
     smla.smla_get_device_status(clear=True)
     S, row = 128, P.DS_MLA_ROW if fmt == P.DS_MLA else 576
     cache = torch.full((S, row), 3, device="cuda",
@@ -46,6 +47,7 @@ def test_append_of_a_negative_length(cuda_lib, fmt, length):
 @pytest.mark.parametrize("limit", [None, 1])
 def test_attention_of_a_negative_length(cuda_lib, fmt, length, limit):
     smla = cuda_lib
+    torch.manual_seed(1)
     smla.smla_get_device_status(clear=True)
     b = P.Batch([(3, 500), (2, 700), (1, 300)], 64, seed=51)
     q, cache, scale = make(b, fmt, 16, 576, 4)
@@ -68,6 +70,7 @@ def test_append_at_the_last_position(cuda_lib, columns):
     """The last positions that an int holds, in a table that reaches them (its entries
     are all block 0 but the last two of the positions')."""
     smla = cuda_lib
+    torch.manual_seed(1)
     smla.smla_get_device_status(clear=True)
     block, n = 64, 70
     tab = torch.zeros((1, columns), dtype=torch.int32, device="cuda")
