@@ -269,8 +269,9 @@ SMLA_API smla_status smla_cache_write_e4m3_group(const void* kv_c, const void* k
  *  q_pe, q_out   device bf16, token n and head p at
  *                q_pe + n * q_pe_token_stride + p * q_pe_head_stride, 64
  *                channels, h heads (1..128); q_out may be q_pe (rotation in
- *                place), otherwise the two must not overlap.  NULL = no
- *                queries to rotate.
+ *                place, with the same strides), otherwise the two must not
+ *                overlap; rows of q_out lie apart (one stride steps over all
+ *                rows of the other).  NULL = no queries to rotate.
  *  query_start   device int32 [num_reqs + 1], non-decreasing
  *  seq_lens      device int32 [num_reqs]
  *  block_table   device int32 [num_reqs, block_table_stride]; a negative entry
@@ -289,8 +290,9 @@ SMLA_API smla_status smla_cache_write_e4m3_group(const void* kv_c, const void* k
  * SMLA_ERR_BAD_INDEX device status.  Asynchronous on `stream`, no allocation.
  * Errors: SMLA_ERR_INVALID_ARG (N < 0; num_reqs, block_table_stride,
  * block_size or num_slots < 1; 0 < block_stride_rows < block_size; NULL or
- * misaligned pointers, bad strides; k_pe or cos_sin given for d_qk = 512 or
- * missing for 576; q_pe without q_out or with d_qk = 512),
+ * misaligned pointers, bad strides, q_out rows that overlap; k_pe or cos_sin
+ * given for d_qk = 512 or missing for 576; q_pe without q_out or with d_qk =
+ * 512),
  * SMLA_ERR_UNSUPPORTED (d_qk not 512 or 576, h > 128, a format that d_qk does
  * not have), SMLA_ERR_CUDA.  N = 0 is OK.
  */

@@ -132,6 +132,12 @@ smla::WindowPlan window_plan(int num_reqs, int T, int h, int block_table_stride,
 // A row stride (in bf16 elements) that keeps 16-byte loads aligned.
 bool row_strides(int64_t stride, int64_t least) { return stride >= least && stride % 8 == 0; }
 
+// Whether the 64-channel rows of [N, h] with these strides lie apart: one stride steps
+// over all rows of the other.
+bool rows_apart(int64_t tok, int64_t head, int N, int h) {
+  return N < 2 || h < 2 || (tok - 64) / head >= h - 1 || (head - 64) / tok >= N - 1;
+}
+
 // Request-local index translation (smla_fwd_paged); table == nullptr for
 // global slot ids.
 struct Paged {
@@ -429,6 +435,11 @@ smla_status smla_cache_append(const void* kv_c, int64_t kv_c_stride, const void*
         !row_strides(q_pe_token_stride, 64) || !row_strides(q_out_token_stride, 64))
       return SMLA_ERR_INVALID_ARG;
     if (h > 128) return SMLA_ERR_UNSUPPORTED;
+    // (in place means row by row; rows written twice would depend on the order)
+    if (!rows_apart(q_out_token_stride, q_out_head_stride, N, h) ||
+        (q_pe == q_out && ((N > 1 && q_pe_token_stride != q_out_token_stride) ||
+                           (h > 1 && q_pe_head_stride != q_out_head_stride))))
+      return SMLA_ERR_INVALID_ARG;
   }
   DeviceInfo* dev = nullptr;
   {
