@@ -340,6 +340,9 @@ def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, in
             kv_cache.is_contiguous() and kv_cache.get_device() == index):
         raise ValueError("kv_cache must be a contiguous tensor on the inputs' device, bfloat16 "
                          "for a bf16 cache and uint8 for the E4M3 formats")
+    if row < 1 or (kv_cache.dim() > 1 and kv_cache.shape[-1] != row):
+        raise ValueError("kv_cache must have the rows of the format, as its last dimension or "
+                         "one behind the other")
     S = kv_cache.numel() // row
     if num_slots is not None:
         if num_slots > S:
@@ -394,6 +397,10 @@ def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, b
         d_qk = 576
         pe, pe_stride = k_pe.data_ptr(), 64 if one else k_pe.stride(0)
         cs, cs_rows = cos_sin.data_ptr(), cos_sin.shape[0]
+    elif cos_sin is not None or q_pe is not None:
+        raise ValueError("cos_sin and q_pe go with k_pe")
+    if q_out is not None and q_pe is None:
+        raise ValueError("q_out goes with q_pe")
     batch = _batch_args(query_start, seq_lens, block_table, block_size, block_stride_rows, index,
                         torch.int32)
     S, scale = _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots,
