@@ -45,13 +45,13 @@
 // PV: a weight is the sum of three E5M2 terms.  E5M2 is the upper byte of f16 and
 // holds 3 significant bits, so a weight rounded to 9 of f16's 11 bits is exactly
 // its upper byte + that of the rest + that of what then remains (one bit more
-// than bf16 keeps); the third is rounded to E5M2's grid, 2^-27 of the row's reference
-// weight (so that keys 11 nats below the top still have their 9 bits, keys 16 nats
-// below are off by 3 %).  The key's scale belongs to its weight: with t = s + log2(scale) the running
-// maximum is taken over t, the weights are 2^(t - m) = scale 2^(s - m), and the
-// sum that divides adds weight / scale, in fp32 where the weights are too small for
-// the product.  So blocks of any scales share one range, and nothing is converted on
-// V's way to the tensor core.
+// than bf16 keeps); the third is rounded to E5M2's grid, 2^-27 of the row's
+// reference weight (keys 11 nats below the top still have their 9 bits, keys 16
+// nats below are off by 3 %).  The key's scale belongs to its weight: with
+// t = s + log2(scale) the running maximum is taken over t, the weights are
+// 2^(t - m) = scale 2^(s - m), and the sum that divides adds weight / scale, in
+// fp32 where the weights are too small for the product.  So blocks of any scales
+// share one range, and nothing is converted on V's way to the tensor core.
 //
 // Masked positions.  A cache block of which a row of the tile sees some position
 // is loaded whole: three columns of 64 rows arrive in 700 cycles as one copy, in
@@ -222,11 +222,11 @@ struct Cfg {
   static constexpr int kElem = kFp8 ? 1 : 2;
   static constexpr int kAtomsPerGroup = kFp8 ? 2 : 3;
   static constexpr int kMaxAtoms = kFp8 ? 5 : 9;        // 128-byte columns of a row
-  // O is rescaled where a row's maximum grows by more than 2^kRaise; E4M3 rows' weights
-  // are multiplied by 2^kUp, into E5M2's range.
+  // O is rescaled where a row's maximum grows by more than 2^kRaise.  E4M3 rows' weights
+  // are multiplied by 1 / kBack, so that they end at 2^15, within E5M2's range: 2^4 and
+  // not 2^8 leaves them four more bits below (32 decode tokens: 102.9 -> 104.5 us).
   static constexpr float kRaise = kFp8 ? 4.f : 8.f;
-  static constexpr float kUp = kFp8 ? 15.f - kRaise : 0.f;
-  static constexpr float kBack = kFp8 ? 0x1p-11f : 1.f;          // 2^-kUp
+  static constexpr float kBack = kFp8 ? 0x1p-11f : 1.f;
   static constexpr int kPBufs = kFp8 ? 2 : 1;
   static constexpr int kQTerms = kFp8 ? 2 : 1;
   static constexpr int kPTerms = kFp8 ? 3 : 1;
@@ -672,7 +672,9 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
     for (int i = 0; i < 8; ++i) sum += ml[i].x == -INFINITY ? 0.f : ml[i].y * expf(ml[i].x - top);
     // (a warp without a key: its sums are 0, or NaN where 0 met an infinity)
     const float f = (m == -INFINITY ? 1.f : expf(m - top)) / sum;
-    auto at = [&](int i) { return reinterpret_cast<float2*>(part + (i & 4 ? kFar - 8 : 0) + 2 * i); };
+    auto at = [&](int i) {
+      return reinterpret_cast<float2*>(part + (i & 4 ? kFar - 8 : 0) + 2 * i);
+    };
     if (sw >= 4)
 #pragma unroll
       for (int i = 0; i < 8; ++i) *at(i) = make_float2(acc[i][0] * f, acc[i][1] * f);
@@ -1429,7 +1431,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         float* rb = red + (kFp8 ? 256 * buf : 0);
         rb[64 * seg + row] = hm;
         float alpha = 1.f;
-        if (named_bar_or(4, 256, hm > m_run + C::kRaise)) {    // also true for the first finite max
+        if (named_bar_or(4, 256, hm > m_run + C::kRaise)) {  // (true for the first finite max)
           float bm = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) bm = fmaxf(bm, rb[64 * k + row]);
@@ -1469,7 +1471,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) bare += ex2_approx(fmaf(s[k], cl, -ref));
           }
-          // 2^(t - m + kUp) <= 2^15: within E5M2's range, its grid 2^-27 of a weight of 1
+          // at most 2^15: within E5M2's range, whose grid is 2^-27 of a weight of 1
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
             uint32_t h[2];
@@ -1477,7 +1479,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             for (int e = 0; e < 2; ++e) {
               float& s0 = s[k + 2 * e];
               float& s1 = s[k + 2 * e + 1];
-              fma2_bcast(s0, s1, cl, C::kUp - mm);
+              fma2_bcast(s0, s1, cl, 15.f - C::kRaise - mm);
               const float w0 = ex2_approx(s0), w1 = ex2_approx(s1);
               add2(ls, ls1, w0, w1);
               h[e] = (pack_f16(w0, w1) + 0x00020002u) & 0xFFFCFFFCu;  // 9 significant bits
@@ -1580,7 +1582,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       const bool empty = l == 0.f;
       // (a sum that is not finite: NaN, whatever the weights' terms became)
-      const float top = kFp8 ? kscale * C::kBack : kscale;
+      const float top = kscale * C::kBack;
       const float inv = empty ? 0.f : l < INFINITY ? __fdividef(top, lr) : NAN;
       const bool partial = t->slot >= 0;
       const int64_t g = (int64_t)t->row0 + 64 * (int)r + row;
