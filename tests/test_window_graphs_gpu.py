@@ -157,3 +157,22 @@ def test_softmax_scales_of_zero_and_below(cuda_lib, fmt, sm):
                                             sm, window=900, sinks=3, max_seq_len=limit)
         ref = P.attend(q, P.dequant(cache, fmt, scale, b), b, sm, 900, 3)
         P.check_attention(out, lse, ref, q, fmt, sm, b)
+
+
+@pytest.mark.parametrize("fmt", [P.BF16, P.BLOCK])
+@pytest.mark.parametrize("h", [3, 128])
+def test_thousands_of_requests(cuda_lib, fmt, h):
+    """A wide decode batch, a third of its requests without a token."""
+    smla = cuda_lib
+    smla.smla_get_device_status(clear=True)
+    rows = [((1, 1 + 7 * r % 90), (0, 30), (2, 5 + r % 60))[r % 3] for r in range(4000 if h < 9
+                                                                                  else 1500)]
+    b = P.Batch(rows, 16, seed=100, pad=7)
+    q, cache, scale = make(b, fmt, h, 576, 4)
+    out, lse = smla.smla_fwd_window(q.cuda(), cache.cuda(), fmt,
+                                    None if scale is None else scale.cuda(), *b.dev(), 16, 0.04,
+                                    window=50, sinks=2)
+    torch.cuda.synchronize()
+    ref = P.attend(q, P.dequant(cache, fmt, scale, b), b, 0.04, 50, 2)
+    P.check_attention(out, lse, ref, q, fmt, 0.04, b)
+    assert smla.smla_get_device_status(clear=True) == 0
