@@ -12,18 +12,20 @@
 // Bound: HBM for a prefill, where the queries' rope part (256 bytes per token
 // and head, in and out) is most of the traffic; latency for a decode step
 // (the chain start -> length -> table entry and table row -> row).  Measured in a
-// captured graph: 8192 tokens with 128 heads into bf16 rows 47.9 us = 6.0 TB/s, 11
-// thousand ragged ones with 16 heads into E4M3 blocks 15.8 us = 5.6 TB/s; decode
-// steps of 64 and 128 requests 2.8 us (bf16) and 3.9 us (E4M3 blocks, whose older
-// rows may follow a growing scale).
+// captured graph, on two sets of inputs in turn: 8192 tokens with 128 heads into bf16
+// rows 48.2 us = 6.0 TB/s, 11 thousand ragged ones with 16 heads into E4M3 blocks
+// 18.2 us = 4.9 TB/s (15.8 on one set, most of which stays in L2); 8192 with 16 heads
+// into every format 9.5 to 10.6 us for 7.4 to 8.1 of bytes; decode steps of 64 and 128
+// requests 2.8 us (bf16) and 3.9 us (E4M3 blocks, whose older rows may follow a
+// growing scale).
 //
 // Work split.  Eight lanes hold one 64-channel vector (16 bytes a lane), four
 // vectors a warp, as in smla_cache.cu.  One launch holds two kinds of CTAs:
 // the first write cache rows, the others rotate queries, kHeads heads of one
 // token per eight lanes so that the position lookup and the cos/sin row are
-// read once for them and kHeads loads are in flight (2 heads: 61.6 us, 8: 48.9).
+// read once for them and kHeads loads are in flight (2 heads: 61.6 us, 8: 48.9, 4: 47.7).
 // Loads in flight are threads here, so every instance keeps to 64 registers, four
-// CTAs an SM (three, of 80 registers: 52.1 us; five spill, and decode takes 3.2).
+// CTAs an SM (three, of 80 registers: 52.1 us; five spill more, and decode takes 3.2).
 #include <cuda_bf16.h>
 
 #include "e4m3_quant.cuh"

@@ -83,13 +83,14 @@
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
 //
 // Bound and measured.  A block is 2,176 cycles of MMAs (E4M3, five passes at twice
-// the rate: 2,688) and takes about 3,000: bf16 loads run at 12.5 TB/s from L2, K
+// the rate: 2,688) and takes about 3,000: bf16 loads run at 12 TB/s from L2, K
 // and V apart, through rings one block deep, all that shared memory holds.  A unit
-// costs about 5 us more (lookups, first copies, epilogue).  A prompt of 4096 tokens
-// with 128 heads through a window of 2048: bf16 1.19 ms = 1.47 PFLOP/s; 2048 tokens
-// with 64 heads behind 6000: E4M3 1.25 ms = 1.45 PFLOP/s; 64 decode tokens with 128
-// heads through the window: bf16 45 us = 3.75 TB/s; 32 of 8 to 16 thousand keys: E4M3
-// 105 us = 1.0 PFLOP/s.
+// costs about 5 us more (lookups, first copies, epilogue).  In a captured graph: a
+// prompt of 4096 tokens with 128 heads through a window of 2048, bf16, 1.19 to 1.25 ms
+// in short bursts, 1.31 ms = 1.34 PFLOP/s where the power limit holds the clocks
+// down; 2048 tokens with 64 heads behind 6000, E4M3, 1.28 to 1.35 and 1.40 ms = 1.29
+// PFLOP/s; 64 decode tokens with 128 heads through the window, bf16, 45 us = 3.8
+// TB/s; 32 of 8 to 16 thousand keys, E4M3, 107 to 110 us = 0.97 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
