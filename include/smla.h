@@ -307,6 +307,132 @@ SMLA_API smla_status smla_cache_append(
     float kpe_scale, cudaStream_t stream);
 
 /*
+ * The block operators on a paged cache.  A table row, block_table[r], lists the
+ * cache blocks of request r in the order of its positions (negative: none);
+ * refcount[b] is the number of table entries that hold block b, 0 for a free block.
+ * Rows may share blocks.  These two arrays are all the state there is: a free block
+ * is one whose count is 0, and the lowest is taken first, so a call's result does
+ * not depend on the order of its threads.
+ *  kv_caches      host array of num_layers device pointers: the caches of layers
+ *                 that share the table (of one format and size, 16-byte aligned),
+ *                 read during the call
+ *  k_scales       host array of num_layers device pointers for the formats whose
+ *                 scales belong to rows or blocks (SMLA_KV_FP8_E4M3_GROUP128,
+ *                 SMLA_KV_FP8_E4M3_GROUP4_KPE, SMLA_KV_FP8_E4M3_BLOCK): the scales
+ *                 move with their blocks; else ignored, may be NULL
+ *  kv_dtype, d_qk, num_slots, block_size, block_stride_rows
+ *                 as for smla_cache_append; block b has the cache rows
+ *                 [b * block_stride_rows, + block_size)
+ *  block_table, refcount, seq_lens and their _out
+ *                 device int32 [num_rows, block_table_stride], [num_blocks],
+ *                 [num_rows]; the result goes to the _out array, which is the array
+ *                 itself (in place) or lies apart from it (then it is written
+ *                 whole: a step in flight may still read the old one)
+ *  num_blocks     counted blocks, all of them within num_slots
+ * Entries at or above num_blocks are no blocks; where one is met, as where a row
+ * or block number is past its end, SMLA_ERR_BAD_INDEX is set in the device status.
+ * Asynchronous on `stream`, no allocation.  Errors: SMLA_ERR_INVALID_ARG (a size
+ * < 1, n < 0, num_slots < block_size, 0 < block_stride_rows < block_size, more
+ * blocks than num_slots holds, NULL or misaligned pointers, among kv_caches and
+ * k_scales too), SMLA_ERR_UNSUPPORTED (d_qk not 512 or 576, a format that d_qk does
+ * not have, num_slots >= 2^31, num_rows > 2^24, n * (block_table_stride + 1) >=
+ * 2^31), SMLA_ERR_WORKSPACE, SMLA_ERR_CUDA.  n = 0 is OK.
+ *
+ * smla_cache_copy — copy the rows, and the scales, of blocks src[i] to blocks
+ * dst[i], 0 <= i < n, in every layer.
+ *  src, dst       device int32 [n]; a pair with a negative number, or with src =
+ *                 dst, is passed over.  No block is the destination of two pairs,
+ *                 or destination and source (its rows would depend on the order).
+ */
+SMLA_API smla_status smla_cache_copy(void* const* kv_caches, float* const* k_scales,
+                                     int num_layers, int kv_dtype, int d_qk, int64_t num_slots,
+                                     int block_size, int block_stride_rows, const int32_t* src,
+                                     const int32_t* dst, int n, cudaStream_t stream);
+
+/*
+ * smla_cache_fork — make table rows the continuations of others, and give them
+ * blocks of their own for the tokens that come next: samples of one prompt, a step
+ * of beam search, new requests, the next step of running ones.  For every i the
+ * row children[i] becomes a copy of row parents[i] as it was before the call, with
+ * its length, len = seq_lens[parents[i]]: it shares the blocks of the positions
+ * [0, len) and lets go of what it held.  A negative parent makes an empty row.  Then
+ * the row gets room for room[i] more tokens:
+ *  - Where room[i] > 0 and len ends inside a block that others hold too, the row
+ *    takes a free block in its place and the rows [0, len % block_size) of it are
+ *    copied in every layer, with their scales.  Of children that would all write
+ *    into one block, and are its only holders, the first one keeps it.
+ *  - Free blocks are taken for the positions from the next block's on, up to len +
+ *    room[i] - 1.
+ * Blocks are taken pair by pair, a pair's copy first, then its columns in order.
+ * Where there are not enough, the last ones stay -1.  Entries behind the room are
+ * -1, blocks that the row held there are let go.
+ *  parents        device int32 [n], rows of the table, or NULL: the children
+ *                 themselves (rows that go on)
+ *  children       device int32 [n]; a negative one is passed over, and of pairs with
+ *                 the same child only the last counts
+ *  room           device int32 [n] or NULL (0 for every pair: sharing alone)
+ *  missing        device int32 [1] or NULL: how many blocks could not be had
+ *  workspace      device, caller-owned, 256-byte aligned, at least
+ *                 smla_cache_fork_workspace_size(...) bytes.  One workspace must not
+ *                 be shared by calls, or by captured graphs, that may overlap on the
+ *                 GPU.
+ * A position past the table's end gets no block and sets SMLA_ERR_BAD_INDEX.
+ * smla_cache_append wants lengths after the append: seq_lens_out[child] + its new
+ * tokens.
+ */
+SMLA_API smla_status smla_cache_fork(
+    const int32_t* parents, const int32_t* children, const int32_t* room, int n,
+    const int32_t* seq_lens, int32_t* seq_lens_out, const int32_t* block_table,
+    int32_t* block_table_out, int num_rows, int block_table_stride, const int32_t* refcount,
+    int32_t* refcount_out, int num_blocks, void* const* kv_caches, float* const* k_scales,
+    int num_layers, int kv_dtype, int d_qk, int64_t num_slots, int block_size,
+    int block_stride_rows, int32_t* missing, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream);
+
+/* Bytes of device workspace smla_cache_fork needs (0 for arguments it rejects). */
+SMLA_API size_t smla_cache_fork_workspace_size(int n, int block_table_stride, int num_blocks);
+
+/*
+ * smla_cache_free — give back the blocks of rows[i] that lie in the positions
+ * [begin[i], end[i]) with all of their own: a request that is done (NULL for both), a
+ * drafted tail that was not accepted (begin), what a sliding window has left behind
+ * (begin = its first tokens that stay, end = the window's first position).  The
+ * entries become -1 (smla_fwd_window, smla_fwd_scored and smla_fwd_paged see no
+ * position there), the blocks' counts fall by one.
+ *  rows           device int32 [n]; a negative one is passed over, and of equal ones
+ *                 only the last counts
+ *  begin, end     device int32 [n], positions, or NULL: from the first, to the
+ *                 table's end
+ */
+SMLA_API smla_status smla_cache_free(const int32_t* rows, const int32_t* begin,
+                                     const int32_t* end, int n, const int32_t* block_table,
+                                     int32_t* block_table_out, int num_rows,
+                                     int block_table_stride, const int32_t* refcount,
+                                     int32_t* refcount_out, int num_blocks, int block_size,
+                                     cudaStream_t stream);
+
+/*
+ * smla_cache_compact — move the live blocks (count > 0) to the start of the pool, so
+ * that what lies behind can be given away.  With L live blocks, the k-th highest of
+ * those numbered L or more moves to the k-th lowest free number below L, in every
+ * layer, with its scales and its count; the table's entries follow.
+ *  block_map      device int32 [num_blocks], written: the new number of each live
+ *                 block, -1 for the free ones (for holders outside the table)
+ *  num_live       device int32 [1] or NULL: L
+ *  workspace      as for smla_cache_fork, smla_cache_compact_workspace_size(...) bytes
+ * Table entries that name a free block become -1.
+ */
+SMLA_API smla_status smla_cache_compact(
+    const int32_t* block_table, int32_t* block_table_out, int num_rows, int block_table_stride,
+    const int32_t* refcount, int32_t* refcount_out, int num_blocks, void* const* kv_caches,
+    float* const* k_scales, int num_layers, int kv_dtype, int d_qk, int64_t num_slots,
+    int block_size, int block_stride_rows, int32_t* block_map, int32_t* num_live,
+    void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace smla_cache_compact needs (0 for num_blocks < 1). */
+SMLA_API size_t smla_cache_compact_workspace_size(int num_blocks);
+
+/*
  * smla_fwd_window — causal attention of a ragged batch over its paged cache,
  * whole or through a sliding window with first tokens that stay visible (what
  * a serving stack runs beside the sparse forward: contexts shorter than

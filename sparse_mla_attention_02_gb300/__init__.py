@@ -67,6 +67,20 @@ def load():
         lib.smla_cache_append.argtypes = [P, I64, P, I64, P, I64, I, P, I64, I64, P, I64, I64,
                                           I, P, P, P, I, I, I, I, I, I, I, I64, P, P, F, P]
         lib.smla_cache_append.restype = I
+        pool = [P, P, I, I, I, I64, I, I]
+        lib.smla_cache_copy.argtypes = pool + [P, P, I, P]
+        lib.smla_cache_copy.restype = I
+        lib.smla_cache_fork.argtypes = [P, P, P, I, P, P, P, P, I, I, P, P, I] + pool + [
+            P, P, SZ, P]
+        lib.smla_cache_fork.restype = I
+        lib.smla_cache_fork_workspace_size.argtypes = [I, I, I]
+        lib.smla_cache_fork_workspace_size.restype = SZ
+        lib.smla_cache_free.argtypes = [P, P, P, I, P, P, I, I, P, P, I, I, P]
+        lib.smla_cache_free.restype = I
+        lib.smla_cache_compact.argtypes = [P, P, I, I, P, P, I] + pool + [P, P, P, SZ, P]
+        lib.smla_cache_compact.restype = I
+        lib.smla_cache_compact_workspace_size.argtypes = [I]
+        lib.smla_cache_compact_workspace_size.restype = SZ
         lib.smla_fwd_window.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I64,
                                         F, P, P, P, SZ, P]
         lib.smla_fwd_window.restype = I
@@ -330,7 +344,8 @@ def _device_stream(t, what, stream):
                    else stream.cuda_stream)
 
 
-def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, index):
+def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, index,
+                need_scale=True):
     """Check a paged cache and its scales; return (slots, k_scale's address)."""
     import torch
     if not 0 <= kv_dtype <= SMLA_KV_FP8_E4M3_BLOCK:
@@ -348,7 +363,7 @@ def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, in
         if num_slots > S:
             raise ValueError("num_slots is larger than kv_cache")
         S = int(num_slots)
-    if kv_dtype == SMLA_KV_BF16 or kv_dtype == SMLA_KV_FP8_DS_MLA:
+    if kv_dtype == SMLA_KV_BF16 or kv_dtype == SMLA_KV_FP8_DS_MLA or not need_scale:
         return S, None
     need = (1 if kv_dtype == SMLA_KV_FP8_E4M3 else
             -(-S // rows_per_scale) if kv_dtype == SMLA_KV_FP8_E4M3_BLOCK else
@@ -425,6 +440,188 @@ def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, b
     if code:
         raise SmlaError(code, "smla_cache_append")
     return kv_cache, q_out
+
+
+def _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots, index):
+    """Check the caches of the layers that share a block table; return the C
+    arguments (kv_caches, k_scales, layers, format, d_qk, slots, block, stride)."""
+    import torch
+    if isinstance(kv_caches, torch.Tensor):
+        one = kv_caches.dim() != 3                # [layers, slots, row]: a layer each
+        kv_caches = [kv_caches] if one else list(kv_caches)
+        if isinstance(k_scales, torch.Tensor):
+            k_scales = [k_scales] if one else list(k_scales)
+    if block_size < 1 or (block_stride_rows != 0 and block_stride_rows < block_size):
+        raise ValueError("block_size must be positive and block_stride_rows 0 or at least "
+                         "block_size")
+    L = len(kv_caches)
+    if L < 1 or kv_caches[0].dim() < 2:
+        raise ValueError("kv_caches must be a tensor [layers, slots, row], or a cache with rows "
+                         "as its last dimension for every layer")
+    shape = kv_caches[0].shape
+    d_qk = 576 if kv_dtype == SMLA_KV_FP8_DS_MLA else shape[-1]
+    scaled = kv_dtype in (SMLA_KV_FP8_E4M3_GROUP128, SMLA_KV_FP8_E4M3_GROUP4_KPE,
+                          SMLA_KV_FP8_E4M3_BLOCK)
+    if scaled and (k_scales is None or len(k_scales) != L):
+        raise ValueError("k_scales must hold the scales of every layer's cache")
+    S = 0
+    for l, c in enumerate(kv_caches):
+        if c.shape != shape:
+            raise ValueError("the layers' caches must have one shape")
+        S, _ = _cache_rows(c, kv_dtype, k_scales[l] if scaled else None, d_qk, num_slots,
+                           block_stride_rows or block_size, index, need_scale=scaled)
+    ptrs = (ctypes.c_void_p * L)(*[c.data_ptr() for c in kv_caches])
+    scales = (ctypes.c_void_p * L)(*[s.data_ptr() for s in k_scales]) if scaled else None
+    return ptrs, scales, L, kv_dtype, d_qk, S, block_size, block_stride_rows
+
+
+def _int32(t, what, shape, index):
+    """The address of a contiguous int32 tensor of this shape (None: NULL)."""
+    import torch
+    if t is None:
+        return None
+    if not (t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and
+            t.get_device() == index):
+        raise ValueError(f"{what} must be a contiguous int32 tensor {list(shape)} on the inputs' "
+                         "device")
+    return t.data_ptr()
+
+
+def _table_args(block_table, out_block_table, refcount, out_refcount, index):
+    """The C arguments (table, table out, rows, width, counts, counts out, blocks)."""
+    if block_table.dim() != 2 or refcount.dim() != 1:
+        raise ValueError("block_table must be [rows, stride] and refcount [blocks]")
+    R, width = block_table.shape
+    NB = refcount.shape[0]
+    out_block_table = block_table if out_block_table is None else out_block_table
+    out_refcount = refcount if out_refcount is None else out_refcount
+    return (_int32(block_table, "block_table", (R, width), index),
+            _int32(out_block_table, "out_block_table", (R, width), index), R, width,
+            _int32(refcount, "refcount", (NB,), index),
+            _int32(out_refcount, "out_refcount", (NB,), index), NB)
+
+
+def _workspace(workspace, nbytes, like, index, stream):
+    """(a caller's workspace or a new one, its address, its bytes)."""
+    import torch
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = _empty((nbytes,), torch.uint8, like.device, stream)
+    elif not (workspace.get_device() == index and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def smla_cache_copy(kv_caches, kv_dtype, k_scales, src, dst, block_size, block_stride_rows=0,
+                    num_slots=None, stream=None):
+    """``smla_cache_copy``: copy the blocks src[i] to dst[i] (int32 [n]) in every
+    layer's cache.
+
+    kv_caches: a tensor [layers, slots, row], one cache [slots, row], or a list of
+    caches; k_scales likewise for the formats whose scales belong to rows or blocks,
+    else None."""
+    lib = _lib or load()
+    index, raw_stream = _device_stream(src, "src", stream)
+    pool = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots,
+                      index)
+    n = src.numel()
+    code = lib.smla_cache_copy(*pool, _int32(src, "src", (n,), index),
+                               _int32(dst, "dst", (n,), index), n, raw_stream)
+    if code:
+        raise SmlaError(code, "smla_cache_copy")
+
+
+def smla_cache_fork_workspace_size(n, block_table_stride, num_blocks) -> int:
+    return int(load().smla_cache_fork_workspace_size(n, block_table_stride, num_blocks))
+
+
+def smla_cache_fork(parents, children, room, seq_lens, block_table, refcount, block_size,
+                    kv_caches, kv_dtype, k_scales=None, out_seq_lens=None, out_block_table=None,
+                    out_refcount=None, missing=None, block_stride_rows=0, num_slots=None,
+                    workspace=None, stream=None):
+    """``smla_cache_fork``: rows ``children`` of the block table become copies of rows
+    ``parents`` (None: of themselves; negative: empty) that share their blocks, with
+    blocks of their own for ``room`` more tokens (None: no room).
+
+    children, parents, room int32 [n]; seq_lens int32 [R], block_table int32
+    [R,stride], refcount int32 [blocks]; the results go to the ``out_`` tensors
+    (None: in place); kv_caches and k_scales as for ``smla_cache_copy``.
+    Returns ``missing`` int32 [1]: how many blocks could not be had."""
+    import torch
+    lib = _lib or load()
+    index, raw_stream = _device_stream(children, "children", stream)
+    pool = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots,
+                      index)
+    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
+    n, R = children.numel(), tables[2]
+    pairs = (_int32(parents, "parents", (n,), index), _int32(children, "children", (n,), index),
+             _int32(room, "room", (n,), index), n)
+    lens = (_int32(seq_lens, "seq_lens", (R,), index),
+            _int32(seq_lens if out_seq_lens is None else out_seq_lens, "out_seq_lens", (R,),
+                   index))
+    if missing is None:
+        missing = _empty((1,), torch.int32, children.device, stream)
+    workspace, ws, nbytes = _workspace(
+        workspace, lib.smla_cache_fork_workspace_size(n, tables[3], tables[6]), children, index,
+        stream)
+    code = lib.smla_cache_fork(*pairs, *lens, *tables, *pool,
+                               _int32(missing, "missing", (1,), index), ws, nbytes, raw_stream)
+    if code:
+        raise SmlaError(code, "smla_cache_fork")
+    return missing
+
+
+def smla_cache_free(rows, begin, end, block_table, refcount, block_size, out_block_table=None,
+                    out_refcount=None, stream=None):
+    """``smla_cache_free``: give back the blocks of the table's ``rows`` (int32 [n])
+    that lie in the positions [begin, end) (int32 [n], or None: from the first, to
+    the last).  The results go to the ``out_`` tensors (None: in place).
+    Returns (block_table, refcount) as they are after it."""
+    lib = _lib or load()
+    index, raw_stream = _device_stream(rows, "rows", stream)
+    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
+    n = rows.numel()
+    code = lib.smla_cache_free(_int32(rows, "rows", (n,), index),
+                               _int32(begin, "begin", (n,), index),
+                               _int32(end, "end", (n,), index), n, *tables, block_size,
+                               raw_stream)
+    if code:
+        raise SmlaError(code, "smla_cache_free")
+    return (block_table if out_block_table is None else out_block_table,
+            refcount if out_refcount is None else out_refcount)
+
+
+def smla_cache_compact_workspace_size(num_blocks) -> int:
+    return int(load().smla_cache_compact_workspace_size(num_blocks))
+
+
+def smla_cache_compact(block_table, refcount, block_size, kv_caches, kv_dtype, k_scales=None,
+                       out_block_table=None, out_refcount=None, block_map=None, num_live=None,
+                       block_stride_rows=0, num_slots=None, workspace=None, stream=None):
+    """``smla_cache_compact``: move the live blocks to the start of the pool.
+
+    Arguments as for ``smla_cache_fork``.  Returns (block_map int32 [blocks]: the new
+    number of each live block, -1 for free ones; num_live int32 [1])."""
+    import torch
+    lib = _lib or load()
+    index, raw_stream = _device_stream(block_table, "block_table", stream)
+    pool = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots,
+                      index)
+    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
+    if block_map is None:
+        block_map = _empty((tables[6],), torch.int32, block_table.device, stream)
+    if num_live is None:
+        num_live = _empty((1,), torch.int32, block_table.device, stream)
+    workspace, ws, nbytes = _workspace(
+        workspace, lib.smla_cache_compact_workspace_size(tables[6]), block_table, index, stream)
+    code = lib.smla_cache_compact(*tables, *pool,
+                                  _int32(block_map, "block_map", (tables[6],), index),
+                                  _int32(num_live, "num_live", (1,), index), ws, nbytes,
+                                  raw_stream)
+    if code:
+        raise SmlaError(code, "smla_cache_compact")
+    return block_map, num_live
 
 
 def smla_fwd_window_workspace_size(num_reqs, T, h, d_qk, kv_dtype, block_table_stride,

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/smla.h"
+#include "smla_blocks.h"
 #include "smla_internal.h"
 #include "smla_paged.h"
 
@@ -127,6 +128,61 @@ smla::WindowPlan window_plan(int num_reqs, int T, int h, int block_table_stride,
   int64_t len = (int64_t)block_table_stride * block_size;
   if (max_seq_len > 0 && max_seq_len < len) len = max_seq_len;
   return smla::make_window_plan(T, h, num_reqs, len, window, sinks, num_sms);
+}
+
+// The caches of the block operators, and the blocks that they hold.
+smla_status make_pool(void* const* kv_caches, float* const* k_scales, int num_layers,
+                      int kv_dtype, int d_qk, int64_t num_slots, int block_size,
+                      int block_stride_rows, smla::Pool* pool, int64_t* blocks) {
+  if (num_layers < 1 || block_size < 1 || num_slots < block_size ||
+      (block_stride_rows != 0 && block_stride_rows < block_size))
+    return SMLA_ERR_INVALID_ARG;
+  if ((d_qk != 512 && d_qk != 576) || num_slots > 0x7FFFFFFFLL || kv_dtype < SMLA_KV_BF16 ||
+      kv_dtype > SMLA_KV_FP8_E4M3_BLOCK ||
+      ((kv_dtype == SMLA_KV_FP8_DS_MLA || kv_dtype == SMLA_KV_FP8_E4M3_GROUP4_KPE) &&
+       d_qk != 576))
+    return SMLA_ERR_UNSUPPORTED;
+  const int groups = kv_dtype == SMLA_KV_FP8_E4M3_GROUP128     ? (d_qk + 127) / 128
+                     : kv_dtype == SMLA_KV_FP8_E4M3_GROUP4_KPE ? 4
+                     : kv_dtype == SMLA_KV_FP8_E4M3_BLOCK      ? -1
+                                                               : 0;
+  if (!kv_caches || (groups && !k_scales)) return SMLA_ERR_INVALID_ARG;
+  for (int l = 0; l < num_layers; ++l)
+    if (!kv_caches[l] || !aligned(kv_caches[l], 16) ||
+        (groups && (!k_scales[l] || !aligned(k_scales[l], 4))))
+      return SMLA_ERR_INVALID_ARG;
+  const int step = block_stride_rows ? block_stride_rows : block_size;
+  *pool = smla::Pool{kv_caches, groups ? k_scales : nullptr, num_layers,
+                     kv_dtype == SMLA_KV_BF16         ? 2 * d_qk
+                     : kv_dtype == SMLA_KV_FP8_DS_MLA ? smla::kDsMlaRowBytes
+                                                      : d_qk,
+                     groups, block_size, step};
+  *blocks = (num_slots - block_size) / step + 1;
+  return SMLA_OK;
+}
+
+// The block tables that the block operators change.
+smla_status make_tables(const int32_t* block_table, int32_t* block_table_out, int num_rows,
+                        int block_table_stride, const int32_t* refcount, int32_t* refcount_out,
+                        int num_blocks, int block_size, smla::Tables* t) {
+  if (num_rows < 1 || block_table_stride < 1 || num_blocks < 1 || block_size < 1)
+    return SMLA_ERR_INVALID_ARG;
+  if (num_rows > (1 << 24)) return SMLA_ERR_UNSUPPORTED;
+  for (const void* x : {(const void*)block_table, (const void*)block_table_out,
+                        (const void*)refcount, (const void*)refcount_out})
+    if (!x || !aligned(x, 4)) return SMLA_ERR_INVALID_ARG;
+  *t = smla::Tables{block_table, block_table_out, nullptr, nullptr, refcount, refcount_out,
+                    num_rows, block_table_stride, num_blocks, block_size, nullptr};
+  return SMLA_OK;
+}
+
+// The current device's status word.
+smla_status device_status_word(int** status) {
+  std::lock_guard<std::mutex> lk(g_mutex);
+  DeviceInfo* dev = nullptr;
+  const smla_status st = device_info(&dev);
+  if (st == SMLA_OK) *status = dev->status;
+  return st;
 }
 
 // A row stride (in bf16 elements) that keeps 16-byte loads aligned.
@@ -468,6 +524,121 @@ smla_status smla_cache_append(const void* kv_c, int64_t kv_c_stride, const void*
   a.status = dev->status;
   return smla::launch_append(a, kv_dtype, rope, stream) == cudaSuccess ? SMLA_OK
                                                                        : SMLA_ERR_CUDA;
+}
+
+smla_status smla_cache_copy(void* const* kv_caches, float* const* k_scales, int num_layers,
+                            int kv_dtype, int d_qk, int64_t num_slots, int block_size,
+                            int block_stride_rows, const int32_t* src, const int32_t* dst, int n,
+                            cudaStream_t stream) {
+  smla::Pool pool{};
+  int64_t blocks = 0;
+  smla_status st = make_pool(kv_caches, k_scales, num_layers, kv_dtype, d_qk, num_slots,
+                             block_size, block_stride_rows, &pool, &blocks);
+  if (st != SMLA_OK) return st;
+  if (n < 0) return SMLA_ERR_INVALID_ARG;
+  if (n == 0) return SMLA_OK;
+  if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return SMLA_ERR_INVALID_ARG;
+  int* status = nullptr;
+  if ((st = device_status_word(&status)) != SMLA_OK) return st;
+  return smla::launch_block_copy(pool, src, dst, n, (int)blocks, status, stream) == cudaSuccess
+             ? SMLA_OK
+             : SMLA_ERR_CUDA;
+}
+
+size_t smla_cache_fork_workspace_size(int n, int block_table_stride, int num_blocks) {
+  if (n < 1 || block_table_stride < 1 || num_blocks < 1 ||
+      (int64_t)n * ((int64_t)block_table_stride + 1) > 0x7FFFFFFFLL)
+    return 0;
+  return smla::fork_workspace_bytes(n, block_table_stride, num_blocks);
+}
+
+smla_status smla_cache_fork(const int32_t* parents, const int32_t* children, const int32_t* room,
+                            int n, const int32_t* seq_lens, int32_t* seq_lens_out,
+                            const int32_t* block_table, int32_t* block_table_out, int num_rows,
+                            int block_table_stride, const int32_t* refcount,
+                            int32_t* refcount_out, int num_blocks, void* const* kv_caches,
+                            float* const* k_scales, int num_layers, int kv_dtype, int d_qk,
+                            int64_t num_slots, int block_size, int block_stride_rows,
+                            int32_t* missing, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  smla::Pool pool{};
+  int64_t blocks = 0;
+  smla_status st = make_pool(kv_caches, k_scales, num_layers, kv_dtype, d_qk, num_slots,
+                             block_size, block_stride_rows, &pool, &blocks);
+  if (st != SMLA_OK) return st;
+  smla::Tables t{};
+  st = make_tables(block_table, block_table_out, num_rows, block_table_stride, refcount,
+                   refcount_out, num_blocks, block_size, &t);
+  if (st != SMLA_OK) return st;
+  if (n < 0 || num_blocks > blocks || !seq_lens || !seq_lens_out || !aligned(seq_lens, 4) ||
+      !aligned(seq_lens_out, 4) || (missing && !aligned(missing, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  if ((int64_t)n * ((int64_t)block_table_stride + 1) > 0x7FFFFFFFLL) return SMLA_ERR_UNSUPPORTED;
+  if (n > 0) {
+    if (!children || !aligned(children, 4) || (parents && !aligned(parents, 4)) ||
+        (room && !aligned(room, 4)))
+      return SMLA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < smla::fork_workspace_bytes(n, block_table_stride,
+                                                                   num_blocks))
+      return SMLA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
+  }
+  if ((st = device_status_word(&t.status)) != SMLA_OK) return st;
+  t.lens = seq_lens;
+  t.lens_out = seq_lens_out;
+  return smla::launch_fork(pool, t, parents, children, room, n, missing, workspace, stream) ==
+                 cudaSuccess
+             ? SMLA_OK
+             : SMLA_ERR_CUDA;
+}
+
+smla_status smla_cache_free(const int32_t* rows, const int32_t* begin, const int32_t* end, int n,
+                            const int32_t* block_table, int32_t* block_table_out, int num_rows,
+                            int block_table_stride, const int32_t* refcount,
+                            int32_t* refcount_out, int num_blocks, int block_size,
+                            cudaStream_t stream) {
+  smla::Tables t{};
+  smla_status st = make_tables(block_table, block_table_out, num_rows, block_table_stride,
+                               refcount, refcount_out, num_blocks, block_size, &t);
+  if (st != SMLA_OK) return st;
+  if (n < 0 || (n > 0 && (!rows || !aligned(rows, 4))) || (begin && !aligned(begin, 4)) ||
+      (end && !aligned(end, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  if ((st = device_status_word(&t.status)) != SMLA_OK) return st;
+  return smla::launch_block_free(t, rows, begin, end, n, stream) == cudaSuccess ? SMLA_OK
+                                                                                : SMLA_ERR_CUDA;
+}
+
+size_t smla_cache_compact_workspace_size(int num_blocks) {
+  return num_blocks < 1 ? 0 : smla::compact_workspace_bytes(num_blocks);
+}
+
+smla_status smla_cache_compact(const int32_t* block_table, int32_t* block_table_out, int num_rows,
+                               int block_table_stride, const int32_t* refcount,
+                               int32_t* refcount_out, int num_blocks, void* const* kv_caches,
+                               float* const* k_scales, int num_layers, int kv_dtype, int d_qk,
+                               int64_t num_slots, int block_size, int block_stride_rows,
+                               int32_t* block_map, int32_t* num_live, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+  smla::Pool pool{};
+  int64_t blocks = 0;
+  smla_status st = make_pool(kv_caches, k_scales, num_layers, kv_dtype, d_qk, num_slots,
+                             block_size, block_stride_rows, &pool, &blocks);
+  if (st != SMLA_OK) return st;
+  smla::Tables t{};
+  st = make_tables(block_table, block_table_out, num_rows, block_table_stride, refcount,
+                   refcount_out, num_blocks, block_size, &t);
+  if (st != SMLA_OK) return st;
+  if (num_blocks > blocks || !block_map || !aligned(block_map, 4) ||
+      (num_live && !aligned(num_live, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < smla::compact_workspace_bytes(num_blocks))
+    return SMLA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
+  if ((st = device_status_word(&t.status)) != SMLA_OK) return st;
+  return smla::launch_compact(pool, t, block_map, num_live, workspace, stream) == cudaSuccess
+             ? SMLA_OK
+             : SMLA_ERR_CUDA;
 }
 
 smla_status smla_fwd_window(const void* q, const void* kv_cache, int kv_dtype,

@@ -98,9 +98,9 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "e4m3_quant.cuh"
+#include "launch.cuh"
 #include "paged_batch.cuh"
 #include "smla_paged.h"
 #include "tc_common.cuh"
@@ -1901,25 +1901,6 @@ cudaError_t encode_columns(CUtensorMap* map, bool fp8, const void* base, int d, 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
-}
-
-// Launch a kernel that waits for the one before it on the stream by itself
-// (griddepcontrol.wait), so that its launch and setup pass under that one's end:
-// 1 to 2 us of a call, 3 of the merge.
-template <class Params>
-cudaError_t launch_early(void (*kernel)(Params), unsigned ctas, int threads, uint32_t smem,
-                         cudaStream_t stream, const std::remove_const_t<Params>& p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <bool kFp8>
