@@ -344,6 +344,13 @@ def _device_stream(t, what, stream):
                    else stream.cuda_stream)
 
 
+def _scale_count(kv_dtype, S, d_qk, rows_per_scale):
+    """Scales of a cache of S rows in an E4M3 format that has them beside the rows."""
+    return (1 if kv_dtype == SMLA_KV_FP8_E4M3 else
+            -(-S // rows_per_scale) if kv_dtype == SMLA_KV_FP8_E4M3_BLOCK else
+            4 * S if kv_dtype == SMLA_KV_FP8_E4M3_GROUP4_KPE else S * ((d_qk + 127) // 128))
+
+
 def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, index,
                 need_scale=True):
     """Check a paged cache and its scales; return (slots, k_scale's address)."""
@@ -365,9 +372,7 @@ def _cache_rows(kv_cache, kv_dtype, k_scale, d_qk, num_slots, rows_per_scale, in
         S = int(num_slots)
     if kv_dtype == SMLA_KV_BF16 or kv_dtype == SMLA_KV_FP8_DS_MLA or not need_scale:
         return S, None
-    need = (1 if kv_dtype == SMLA_KV_FP8_E4M3 else
-            -(-S // rows_per_scale) if kv_dtype == SMLA_KV_FP8_E4M3_BLOCK else
-            4 * S if kv_dtype == SMLA_KV_FP8_E4M3_GROUP4_KPE else S * ((d_qk + 127) // 128))
+    need = _scale_count(kv_dtype, S, d_qk, rows_per_scale)
     if not (k_scale is not None and k_scale.dtype is torch.float32 and
             k_scale.is_contiguous() and k_scale.get_device() == index and
             k_scale.numel() >= need):
@@ -446,33 +451,59 @@ def _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num
     """Check the caches of the layers that share a block table; return the C
     arguments (kv_caches, k_scales, layers, format, d_qk, slots, block, stride)."""
     import torch
-    if isinstance(kv_caches, torch.Tensor):
-        one = kv_caches.dim() != 3                # [layers, slots, row]: a layer each
-        kv_caches = [kv_caches] if one else list(kv_caches)
-        if isinstance(k_scales, torch.Tensor):
-            k_scales = [k_scales] if one else list(k_scales)
     if block_size < 1 or (block_stride_rows != 0 and block_stride_rows < block_size):
         raise ValueError("block_size must be positive and block_stride_rows 0 or at least "
                          "block_size")
-    L = len(kv_caches)
-    if L < 1 or kv_caches[0].dim() < 2:
-        raise ValueError("kv_caches must be a tensor [layers, slots, row], or a cache with rows "
-                         "as its last dimension for every layer")
-    shape = kv_caches[0].shape
-    d_qk = 576 if kv_dtype == SMLA_KV_FP8_DS_MLA else shape[-1]
     scaled = kv_dtype in (SMLA_KV_FP8_E4M3_GROUP128, SMLA_KV_FP8_E4M3_GROUP4_KPE,
                           SMLA_KV_FP8_E4M3_BLOCK)
-    if scaled and (k_scales is None or len(k_scales) != L):
-        raise ValueError("k_scales must hold the scales of every layer's cache")
-    S = 0
-    for l, c in enumerate(kv_caches):
-        if c.shape != shape:
-            raise ValueError("the layers' caches must have one shape")
-        S, _ = _cache_rows(c, kv_dtype, k_scales[l] if scaled else None, d_qk, num_slots,
-                           block_stride_rows or block_size, index, need_scale=scaled)
-    ptrs = (ctypes.c_void_p * L)(*[c.data_ptr() for c in kv_caches])
-    scales = (ctypes.c_void_p * L)(*[s.data_ptr() for s in k_scales]) if scaled else None
-    return ptrs, scales, L, kv_dtype, d_qk, S, block_size, block_stride_rows
+    rows_per_scale = block_stride_rows or block_size
+    scale_ptrs = None
+    if isinstance(kv_caches, torch.Tensor):
+        if kv_caches.dim() == 3:                  # [layers, slots, row]
+            L, S = kv_caches.shape[:2]
+        else:
+            L, S = 1, kv_caches.shape[0] if kv_caches.dim() == 2 else 0
+        if L < 1 or S < 1:
+            raise ValueError("kv_caches must be [layers, slots, row] or [slots, row]")
+        row = kv_caches.shape[-1]
+        d_qk = 576 if kv_dtype == SMLA_KV_FP8_DS_MLA else row
+        # (as one tall cache; the layers' scales are looked at below)
+        _cache_rows(kv_caches, kv_dtype, None, d_qk, None, rows_per_scale, index, need_scale=False)
+        step = S * row * kv_caches.element_size()
+        base = kv_caches.data_ptr()
+        ptrs = (ctypes.c_void_p * L)(*range(base, base + L * step, step))
+        if num_slots is not None:
+            if num_slots > S:
+                raise ValueError("num_slots is larger than a layer's cache")
+            S = int(num_slots)
+        if scaled:
+            one = isinstance(k_scales, torch.Tensor) and k_scales.dtype is torch.float32 and \
+                k_scales.is_contiguous() and k_scales.get_device() == index
+            n = k_scales.numel() // L if one else 0
+            if not one or k_scales.numel() != n * L or (L > 1 and k_scales.shape[0] != L) or \
+                    n < _scale_count(kv_dtype, S, d_qk, rows_per_scale):
+                raise ValueError("k_scales must be a contiguous fp32 tensor on the inputs' device "
+                                 "with the scales of every layer")
+            base = k_scales.data_ptr()
+            scale_ptrs = (ctypes.c_void_p * L)(*range(base, base + 4 * L * n, 4 * n))
+    else:
+        L = len(kv_caches)
+        if L < 1 or kv_caches[0].dim() < 2:
+            raise ValueError("kv_caches must hold a cache, rows as its last dimension, for every "
+                             "layer")
+        shape = kv_caches[0].shape
+        d_qk = 576 if kv_dtype == SMLA_KV_FP8_DS_MLA else shape[-1]
+        if scaled and (k_scales is None or len(k_scales) != L):
+            raise ValueError("k_scales must hold the scales of every layer's cache")
+        for l, c in enumerate(kv_caches):
+            if c.shape != shape:
+                raise ValueError("the layers' caches must have one shape")
+            S, _ = _cache_rows(c, kv_dtype, k_scales[l] if scaled else None, d_qk, num_slots,
+                               rows_per_scale, index, need_scale=scaled)
+        ptrs = (ctypes.c_void_p * L)(*[c.data_ptr() for c in kv_caches])
+        if scaled:
+            scale_ptrs = (ctypes.c_void_p * L)(*[s.data_ptr() for s in k_scales])
+    return ptrs, scale_ptrs, L, kv_dtype, d_qk, S, block_size, block_stride_rows
 
 
 def _int32(t, what, shape, index):
@@ -507,7 +538,8 @@ def _workspace(workspace, nbytes, like, index, stream):
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = _empty((nbytes,), torch.uint8, like.device, stream)
+        workspace = like.new_empty((nbytes + 3) // 4) if stream is None else \
+            _empty((nbytes,), torch.uint8, like.device, stream)
     elif not (workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -561,7 +593,8 @@ def smla_cache_fork(parents, children, room, seq_lens, block_table, refcount, bl
             _int32(seq_lens if out_seq_lens is None else out_seq_lens, "out_seq_lens", (R,),
                    index))
     if missing is None:
-        missing = _empty((1,), torch.int32, children.device, stream)
+        missing = children.new_empty(1) if stream is None else \
+            _empty((1,), torch.int32, children.device, stream)
     workspace, ws, nbytes = _workspace(
         workspace, lib.smla_cache_fork_workspace_size(n, tables[3], tables[6]), children, index,
         stream)
@@ -610,9 +643,11 @@ def smla_cache_compact(block_table, refcount, block_size, kv_caches, kv_dtype, k
                       index)
     tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
     if block_map is None:
-        block_map = _empty((tables[6],), torch.int32, block_table.device, stream)
+        block_map = refcount.new_empty(tables[6]) if stream is None else \
+            _empty((tables[6],), torch.int32, refcount.device, stream)
     if num_live is None:
-        num_live = _empty((1,), torch.int32, block_table.device, stream)
+        num_live = refcount.new_empty(1) if stream is None else \
+            _empty((1,), torch.int32, refcount.device, stream)
     workspace, ws, nbytes = _workspace(
         workspace, lib.smla_cache_compact_workspace_size(tables[6]), block_table, index, stream)
     code = lib.smla_cache_compact(*tables, *pool,

@@ -190,47 +190,68 @@ __device__ __forceinline__ int2 warp_base(const int32_t* counts, int warp) {
 
 constexpr int kRowThreads = 256;
 
-// Tables and counts to their new place.
-struct CarryParams {
+// Tables and counts to their new place (n = 0: in place already).
+struct Carry {
   const int32_t* from[3];
   int32_t* to[3];
   int64_t n[3];
 };
-__global__ void __launch_bounds__(kRowThreads) smla_tables_carry_kernel(const CarryParams p) {
-  wait_before();
-  allow_next();
-  const int64_t id = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  const int64_t threads = (int64_t)gridDim.x * kRowThreads;
+__device__ __forceinline__ void carry(const Carry& p, int64_t id, int64_t threads) {
 #pragma unroll
   for (int k = 0; k < 3; ++k)
 #pragma unroll 4
     for (int64_t i = id; i < p.n[k]; i += threads) p.to[k][i] = p.from[k][i];
 }
+__global__ void __launch_bounds__(kRowThreads) smla_tables_carry_kernel(const Carry p) {
+  wait_before();
+  allow_next();
+  carry(p, (int64_t)blockIdx.x * kRowThreads + threadIdx.x, (int64_t)gridDim.x * kRowThreads);
+}
 
-cudaError_t launch_carry(const Tables& t, cudaStream_t stream) {
-  CarryParams p{};
-  int64_t most = 0;
+Carry make_carry(const Tables& t) {
+  Carry p{};
   auto add = [&](int k, const int32_t* from, int32_t* to, int64_t n) {
-    if (!from || from == to) return;
     p.from[k] = from;
     p.to[k] = to;
-    p.n[k] = n;
-    most = n > most ? n : most;
+    p.n[k] = from && from != to ? n : 0;
   };
   add(0, t.table, t.table_out, (int64_t)t.rows * t.width);
   add(1, t.lens, t.lens_out, t.rows);
   add(2, t.ref, t.ref_out, t.blocks);
-  if (most == 0) return cudaSuccess;
-  const int64_t ctas = (most + 4 * kRowThreads - 1) / (4 * kRowThreads);
+  return p;
+}
+int64_t most_of(const Carry& p) {
+  int64_t most = p.n[0] > p.n[1] ? p.n[0] : p.n[1];
+  return p.n[2] > most ? p.n[2] : most;
+}
+cudaError_t launch_carry(const Carry& p, cudaStream_t stream) {
+  const int64_t ctas = (most_of(p) + 4 * kRowThreads - 1) / (4 * kRowThreads);
+  if (ctas == 0) return cudaSuccess;
   return launch_early(smla_tables_carry_kernel, (unsigned)(ctas < 152 * 8 ? ctas : 152 * 8),
                       kRowThreads, 0, stream, p);
 }
 
-// Whether a later element of rows[0, n) names `row` too (the CTA asks together).
+// Tables and pairs of a fork this small are handled by one cluster in one launch, larger
+// ones by a launch for each step that needs the one before it complete.
+constexpr int64_t kSmallWords = 1 << 17;
+
+// A row is worked on by a CTA, or (kWarp) by each warp of a cluster.
+template <bool kWarp>
+struct Team {
+  static constexpr int kSize = kWarp ? 32 : kRowThreads;
+  static __device__ __forceinline__ int rank() { return threadIdx.x & (kSize - 1); }
+  static __device__ __forceinline__ bool any(bool x) {
+    return kWarp ? __any_sync(0xffffffffu, x) : __syncthreads_or(x);
+  }
+};
+
+// Whether a later element of rows[0, n) names `row` too (the team asks together).
+template <bool kWarp>
 __device__ __forceinline__ bool named_later(const int32_t* rows, int i, int n, int row) {
   bool again = false;
-  for (int j = i + 1 + (int)threadIdx.x; j < n; j += kRowThreads) again |= rows[j] == row;
-  return __syncthreads_or(again);
+#pragma unroll 4
+  for (int j = i + 1 + Team<kWarp>::rank(); j < n; j += Team<kWarp>::kSize) again |= rows[j] == row;
+  return Team<kWarp>::any(again);
 }
 
 // ----------------------------------------------------------------- fork --
@@ -287,18 +308,18 @@ struct ForkParams {
   const int32_t* room;         // nullptr: none
   int32_t* missing;
   int n;
+  Carry c;
 };
 
 // Pair i: the child's new row, and the counts of what it lets go and takes.
-__global__ void __launch_bounds__(kRowThreads) smla_fork_share_kernel(const ForkParams p) {
-  wait_before();
-  allow_next();
+template <bool kWarp>
+__device__ __forceinline__ void share_pair(const ForkParams& p, int i) {
   const Tables& t = p.t;
-  const int i = blockIdx.x, tid = threadIdx.x;
+  const int tid = Team<kWarp>::rank();
   const int child = p.children[i];
   int parent = p.parents ? p.parents[i] : child;
   bool bad = child >= t.rows || parent >= t.rows;
-  const bool skip = child < 0 || child >= t.rows || named_later(p.children, i, p.n, child);
+  const bool skip = child < 0 || child >= t.rows || named_later<kWarp>(p.children, i, p.n, child);
   if (skip) {
     if (tid == 0) {
       p.s.open[i] = -1;
@@ -319,7 +340,8 @@ __global__ void __launch_bounds__(kRowThreads) smla_fork_share_kernel(const Fork
   const int32_t* old_row = t.table + (int64_t)child * t.width;
   const int32_t* new_row = t.table + (int64_t)max(parent, 0) * t.width;
   int32_t* stage = p.s.stage + (int64_t)i * t.width;
-  for (int c = tid; c < t.width; c += kRowThreads) {
+#pragma unroll 2
+  for (int c = tid; c < t.width; c += Team<kWarp>::kSize) {
     const int was = old_row[c];
     int now = c < have ? new_row[c] : -1;
     if (now >= t.blocks) {
@@ -347,38 +369,71 @@ __global__ void __launch_bounds__(kRowThreads) smla_fork_share_kernel(const Fork
   if (bad) bad_index(t.status);
 }
 
+__global__ void __launch_bounds__(kRowThreads) smla_fork_share_kernel(const ForkParams p) {
+  wait_before();
+  allow_next();
+  share_pair<false>(p, (int)blockIdx.x);
+}
+
+// Inclusive sum over a CTA's threads in two words of one; the total to `all`.
+__device__ __forceinline__ long long cta_scan(long long x, long long* sums, long long& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long w = sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  all = __shfl_sync(0xffffffffu, w, 31);
+  const long long below = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  __syncthreads();                                     // (the sums' room is used again)
+  return warp > 0 ? x + below : x;
+}
+
 // One cluster: which rows get a copy of their last block, and the free blocks.
+// kSmall: the carrying and sharing too.  What other CTAs of the cluster wrote is read
+// past L1.
+template <bool kSmall>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads, 1)
 smla_fork_take_kernel(const ForkParams p) {
+  static_assert(kScanThreads == 1024, "cta_scan: as many warps as lanes");
   wait_before();
   allow_next();
   const Tables& t = p.t;
   const ForkSpace& s = p.s;
   const int tid = threadIdx.x, lane = tid & 31;
   const int id = (int)blockIdx.x * kScanThreads + tid, warp = id >> 5;
-  __shared__ long long sums[kScanThreads / 32];
+  __shared__ long long sums[32];
+  if constexpr (kSmall) {
+    carry(p.c, id, kCluster * kScanThreads);
+    cluster_sync();
+    for (int i = warp; i < p.n; i += kScanWarps) share_pair<true>(p, i);
+    cluster_sync();
+  }
   // A block that is written by some of its holders: of the writers all but the first
   // copy it; where somebody else holds it too, the first as well.
-  for (int i = id; i < p.n; i += kCluster * kScanThreads) {
-    const int open = s.open[i];
+  for (int i = warp; i < p.n; i += kScanWarps) {
+    const int open = __ldcg(s.open + i);
     int own = 0;
     if (open >= 0) {
       int writers = 0, before = 0;
-      const int4* all = reinterpret_cast<const int4*>(s.open);
 #pragma unroll 4
-      for (int j = 0; j < (p.n + 3) / 4; ++j) {
-        const int4 x = all[j];
-        const int y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool same = 4 * j + k < p.n && y[k] == open;
-          writers += same ? 1 : 0;
-          before += same && 4 * j + k < i ? 1 : 0;
-        }
+      for (int j = lane; j < p.n; j += 32) {
+        const bool same = __ldcg(s.open + j) == open;
+        writers += same ? 1 : 0;
+        before += same && j < i ? 1 : 0;
       }
-      own = before > 0 || __ldcg(t.ref_out + open) > writers ? 1 : 0;
+      writers = warp_sum(writers);
+      own = __any_sync(0xffffffffu, before > 0) || __ldcg(t.ref_out + open) > writers ? 1 : 0;
     }
-    s.own[i] = own;
+    if (lane == 0) s.own[i] = own;
   }
   const Range range = warp_range(t.blocks, warp);
   const int mine = count_range(t.ref_out, range, [](int r) { return r == 0; });
@@ -386,38 +441,27 @@ smla_fork_take_kernel(const ForkParams p) {
   cluster_sync();
   // Each pair's place in the list of the blocks taken, and its move's number.
   if (blockIdx.x == 0) {
-    long long carry = 0;                               // moves << 32 | blocks
+    long long carried = 0;                             // moves << 32 | blocks
     for (int i0 = 0; i0 < p.n; i0 += kScanThreads) {
       const int i = i0 + tid;
       const int own = i < p.n ? __ldcg(s.own + i) : 0;
       const long long x =
-          i < p.n ? ((long long)own << 32) + own + s.fresh[i] : 0ll;
-      long long upto = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+          i < p.n ? ((long long)own << 32) + own + __ldcg(s.fresh + i) : 0ll;
+      long long all;
+      const long long at = carried + cta_scan(x, sums, all) - x;
+      carried += all;
+      if (i >= p.n) continue;
+      const int place = (int)(at & 0xffffffffll), m = (int)(at >> 32);
+      s.first[i] = place;
+      if (own) {
+        s.src[m] = __ldcg(s.open + i);
+        s.place[m] = place;
+        s.rows[m] = __ldcg(s.len + i) % t.block_size;
       }
-      if (lane == 31) sums[tid >> 5] = upto;
-      __syncthreads();
-      long long base = carry;
-      for (int w = 0; w < (tid >> 5); ++w) base += sums[w];
-      for (int w = 0; w < kScanThreads / 32; ++w) carry += sums[w];
-      const long long at = base + upto - x;
-      if (i < p.n) {
-        s.first[i] = (int)(at & 0xffffffffll);
-        if (own) {
-          const int m = (int)(at >> 32);
-          s.src[m] = s.open[i];
-          s.place[m] = (int)(at & 0xffffffffll);
-          s.rows[m] = s.len[i] % t.block_size;
-        }
-      }
-      __syncthreads();                                 // (the sums' room is used again)
     }
     if (tid == 0) {
-      s.head[0] = (int)(carry & 0xffffffffll);
-      s.head[1] = (int)(carry >> 32);
+      s.head[0] = (int)(carried & 0xffffffffll);
+      s.head[1] = (int)(carried >> 32);
     }
   }
   cluster_sync();
@@ -437,7 +481,7 @@ smla_fork_take_kernel(const ForkParams p) {
   }
   // (a block that is copied keeps a holder: its count was above the copies made)
   for (int i = id; i < p.n; i += kCluster * kScanThreads)
-    if (__ldcg(s.own + i)) atomicSub(t.ref_out + s.open[i], 1);
+    if (__ldcg(s.own + i)) atomicSub(t.ref_out + __ldcg(s.open + i), 1);
   if (id == 0) {
     s.head[2] = base.y;
     if (p.missing) *p.missing = max(wanted - base.y, 0);
@@ -493,18 +537,19 @@ __global__ void __launch_bounds__(kRowThreads) smla_block_free_kernel(const Free
   wait_before();
   allow_next();
   const Tables& t = p.t;
-  const int i = blockIdx.x, row = p.rows[i];
+  const int i = blockIdx.x, row = p.rows[i], tid = threadIdx.x;
   if (row < 0) return;
   if (row >= t.rows) {
-    if (threadIdx.x == 0) bad_index(t.status);
+    if (tid == 0) bad_index(t.status);
     return;
   }
-  if (named_later(p.rows, i, p.n, row)) return;
+  if (named_later<false>(p.rows, i, p.n, row)) return;
   const int64_t B = t.block_size;
   const int64_t lo = p.begin ? (max(p.begin[i], 0) + B - 1) / B : 0;
   const int64_t hi = p.end ? min(max(p.end[i], 0) / B, (int64_t)t.width) : t.width;
   int32_t* at = t.table_out + (int64_t)row * t.width;
-  for (int c = (int)min(lo, (int64_t)t.width) + (int)threadIdx.x; c < hi; c += kRowThreads) {
+#pragma unroll 4
+  for (int c = (int)min(lo, (int64_t)t.width) + tid; c < hi; c += kRowThreads) {
     const int b = at[c];
     if (b < 0) continue;
     at[c] = -1;
@@ -514,7 +559,6 @@ __global__ void __launch_bounds__(kRowThreads) smla_block_free_kernel(const Free
       bad_index(t.status);
   }
 }
-
 // -------------------------------------------------------------- compact --
 
 struct CompactSpace {
@@ -647,19 +691,25 @@ size_t fork_workspace_bytes(int n, int width, int blocks) {
 cudaError_t launch_fork(const Pool& pool, const Tables& t, const int32_t* parents,
                         const int32_t* children, const int32_t* room, int n, int32_t* missing,
                         void* workspace, cudaStream_t stream) {
+  const Carry carried = make_carry(t);
   if (n == 0) {
-    const cudaError_t e = launch_carry(t, stream);
+    const cudaError_t e = launch_carry(carried, stream);
     return e == cudaSuccess && missing ? cudaMemsetAsync(missing, 0, 4, stream) : e;
   }
   int64_t words = 0;
   ForkWrite w{};
   w.f = ForkParams{t, fork_space(workspace, n, t.width, t.blocks, &words), parents, children,
-                   room, missing, n};
-  cudaError_t e = launch_carry(t, stream);
-  if (e == cudaSuccess)
-    e = launch_early(smla_fork_share_kernel, (unsigned)n, kRowThreads, 0, stream, w.f);
-  if (e == cudaSuccess)
-    e = launch_early(smla_fork_take_kernel, kCluster, kScanThreads, 0, stream, w.f);
+                   room, missing, n, carried};
+  cudaError_t e = cudaSuccess;
+  if (most_of(carried) + (int64_t)n * t.width <= kSmallWords) {
+    e = launch_early(smla_fork_take_kernel<true>, kCluster, kScanThreads, 0, stream, w.f);
+  } else {
+    e = launch_carry(carried, stream);
+    if (e == cudaSuccess)
+      e = launch_early(smla_fork_share_kernel, (unsigned)n, kRowThreads, 0, stream, w.f);
+    if (e == cudaSuccess)
+      e = launch_early(smla_fork_take_kernel<false>, kCluster, kScanThreads, 0, stream, w.f);
+  }
   for (int first = 0; first < pool.layers && e == cudaSuccess; first += kPoolLayers) {
     w.c = copy_params(pool, first);
     w.c.src = w.f.s.src;
@@ -681,7 +731,7 @@ cudaError_t launch_fork(const Pool& pool, const Tables& t, const int32_t* parent
 
 cudaError_t launch_block_free(const Tables& t, const int32_t* rows, const int32_t* begin,
                               const int32_t* end, int n, cudaStream_t stream) {
-  cudaError_t e = launch_carry(t, stream);
+  cudaError_t e = launch_carry(make_carry(t), stream);
   if (e == cudaSuccess && n > 0)
     e = launch_early(smla_block_free_kernel, (unsigned)n, kRowThreads, 0, stream,
                      FreeParams{t, rows, begin, end, n});
