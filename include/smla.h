@@ -502,6 +502,41 @@ SMLA_API size_t smla_fwd_window_workspace_size(int num_reqs, int T, int h, int d
                                                int max_seq_len);
 
 /*
+ * smla_fwd_scored — smla_fwd_window with scores that are capped by a tanh and
+ * lowered with the distance, and with a span of positions for every token (packed
+ * documents, prefixes whose tokens see each other).  The token t of position p sees
+ * the positions
+ *   e <= last_pos[t]  with  (e >= first_pos[t] and (window == 0 or e > p - window))
+ *                           or  e < sinks
+ * that the request has (e < seq_lens[r]) and whose block is allocated.  For these
+ *   x_e = sm_scale <q, K_e>
+ *   y_e = softcap tanh(x_e / softcap)   (softcap = 0: x_e)
+ *   s_e = y_e - slopes[head] |p - e|    (slopes NULL: y_e)
+ * and O and LSE follow from s_e as there.
+ *  softcap      0 = none, or between 1e-30 and 1e30
+ *  slopes       device fp32 [h] or NULL
+ *  first_pos    device int32 [T] or NULL (0): the token's first position, e.g. that
+ *               of its document.  Within a request it must not fall from one token
+ *               to the next (or keys that a token sees are left out).
+ *  last_pos     device int32 [T] or NULL (p, the token's own): its last position, e.g.
+ *               max(p, the prefix's last).  Must not fall within a request either.
+ * Every other argument, the workspace (smla_fwd_window_workspace_size), the results
+ * and the errors are those of smla_fwd_window (SMLA_ERR_INVALID_ARG for any other
+ * softcap, too).  first_pos and last_pos of tokens behind
+ * query_start[num_reqs] are not read.  The capped score is within 2^-20 of the larger
+ * of |softcap| / 8 and |x_e|, the bias within 2^-22 of itself.  With softcap = 0 and the
+ * three pointers NULL the call is smla_fwd_window.
+ */
+SMLA_API smla_status smla_fwd_scored(
+    const void* q, const void* kv_cache, int kv_dtype, const float* k_scale,
+    const int32_t* query_start, const int32_t* seq_lens, const int32_t* block_table,
+    int num_reqs, int block_table_stride, int block_size, int block_stride_rows, int window,
+    int sinks, int max_seq_len, int T, int h, int d_qk, int d_v, int64_t num_slots,
+    float sm_scale, float softcap, const float* slopes, const int32_t* first_pos,
+    const int32_t* last_pos, void* out, float* lse, void* workspace, size_t workspace_bytes,
+    cudaStream_t stream);
+
+/*
  * smla_fwd_partial — smla_fwd that writes the normalised output in fp32 and
  * its LSE, for a later LSE-weighted merge of partial results over disjoint
  * key sets (the DCP path of the vLLM API docs' flashmla_sparse page: each

@@ -84,6 +84,9 @@ def load():
         lib.smla_fwd_window.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I64,
                                         F, P, P, P, SZ, P]
         lib.smla_fwd_window.restype = I
+        lib.smla_fwd_scored.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, I64,
+                                        F, F, P, P, P, P, P, P, SZ, P]
+        lib.smla_fwd_scored.restype = I
         lib.smla_fwd_window_workspace_size.argtypes = [I] * 11
         lib.smla_fwd_window_workspace_size.restype = SZ
         lib.smla_fwd_partial.argtypes = fwd_args + [P]
@@ -667,25 +670,13 @@ def smla_fwd_window_workspace_size(num_reqs, T, h, d_qk, kv_dtype, block_table_s
         max_seq_len or 0))
 
 
-def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table,
-                    block_size, sm_scale, window=0, sinks=0, max_seq_len=None,
-                    block_stride_rows=0, out=None, lse=None, want_lse=True, num_slots=None,
-                    workspace=None, stream=None):
-    """``smla_fwd_window``: causal attention of a ragged batch over its paged
-    cache, through a sliding window (0: none) with ``sinks`` first positions
-    that stay visible.
-
-    q bf16 [T,h,d_qk]; kv_cache bf16 or uint8 [S,d_qk] (SMLA_KV_BF16,
-    SMLA_KV_FP8_E4M3 or SMLA_KV_FP8_E4M3_BLOCK); query_start int32 [R+1],
-    seq_lens int32 [R], block_table int32 [R,stride] as for
-    ``smla_cache_append``; max_seq_len: a bound on seq_lens that sizes the
-    split plan; workspace: a uint8 device tensor of at least
-    smla_fwd_window_workspace_size bytes, or None to allocate one.
-    Returns (out bf16 [T,h,512], lse f32 [T,h] or None); rows behind the last
-    request are not written."""
+def _window_args(lib, q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table,
+                 block_size, window, sinks, max_seq_len, block_stride_rows, out, lse, want_lse,
+                 num_slots, workspace, index, stream):
+    """Check the arguments of the windowed attention; return its C arguments up to
+    num_slots, (out, lse, workspace) as addresses with the workspace's bytes, and the
+    tensors behind them."""
     import torch
-    lib = _lib or load()
-    index, raw_stream = _device_stream(q, "q", stream)
     bf16 = torch.bfloat16
     if not (q.dtype is bf16 and q.dim() == 3 and q.is_contiguous()):
         raise ValueError("q must be a contiguous bf16 device tensor [T, h, d_qk]")
@@ -718,12 +709,69 @@ def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block
             raise ValueError("workspace must be a contiguous tensor on the inputs' device")
         nbytes = workspace.numel() * workspace.element_size()
         ws = workspace.data_ptr()
-    code = lib.smla_fwd_window(
-        q.data_ptr(), kv_cache.data_ptr(), kv_dtype, scale, *batch, window, sinks, limit, T, h,
-        d_qk, 512, S, sm_scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
-        nbytes, raw_stream)
+    args = (q.data_ptr(), kv_cache.data_ptr(), kv_dtype, scale, *batch, window, sinks, limit, T, h,
+            d_qk, 512, S)
+    return (args, (out.data_ptr(), None if lse is None else lse.data_ptr(), ws, nbytes), out, lse,
+            workspace)
+
+
+def smla_fwd_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table,
+                    block_size, sm_scale, window=0, sinks=0, max_seq_len=None,
+                    block_stride_rows=0, out=None, lse=None, want_lse=True, num_slots=None,
+                    workspace=None, stream=None):
+    """``smla_fwd_window``: causal attention of a ragged batch over its paged
+    cache, through a sliding window (0: none) with ``sinks`` first positions
+    that stay visible.
+
+    q bf16 [T,h,d_qk]; kv_cache bf16 or uint8 [S,d_qk] (SMLA_KV_BF16,
+    SMLA_KV_FP8_E4M3 or SMLA_KV_FP8_E4M3_BLOCK); query_start int32 [R+1],
+    seq_lens int32 [R], block_table int32 [R,stride] as for
+    ``smla_cache_append``; max_seq_len: a bound on seq_lens that sizes the
+    split plan; workspace: a uint8 device tensor of at least
+    smla_fwd_window_workspace_size bytes, or None to allocate one.
+    Returns (out bf16 [T,h,512], lse f32 [T,h] or None); rows behind the last
+    request are not written."""
+    lib = _lib or load()
+    index, raw_stream = _device_stream(q, "q", stream)
+    args, ends, out, lse, _ws = _window_args(
+        lib, q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table, block_size,
+        window, sinks, max_seq_len, block_stride_rows, out, lse, want_lse, num_slots, workspace,
+        index, stream)
+    code = lib.smla_fwd_window(*args, sm_scale, *ends, raw_stream)
     if code:
         raise SmlaError(code, "smla_fwd_window")
+    return out, lse
+
+
+def smla_fwd_scored(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table,
+                    block_size, sm_scale, softcap=0.0, slopes=None, first_pos=None, last_pos=None,
+                    window=0, sinks=0, max_seq_len=None, block_stride_rows=0, out=None, lse=None,
+                    want_lse=True, num_slots=None, workspace=None, stream=None):
+    """``smla_fwd_scored``: ``smla_fwd_window`` with scores that become
+    softcap * tanh(score / softcap) (0: as they are), less slopes[head] times the
+    distance (fp32 [h] or None), and with a span [first_pos, last_pos] of positions for
+    every token (int32 [T] each, ascending within a request; None: from 0, to its own).
+
+    Every other argument and the results are those of ``smla_fwd_window``."""
+    import torch
+    lib = _lib or load()
+    index, raw_stream = _device_stream(q, "q", stream)
+    args, ends, out, lse, _ws = _window_args(
+        lib, q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table, block_size,
+        window, sinks, max_seq_len, block_stride_rows, out, lse, want_lse, num_slots, workspace,
+        index, stream)
+    slope = None
+    if slopes is not None:
+        if not (slopes.dtype is torch.float32 and slopes.shape == (q.shape[1],) and
+                slopes.is_contiguous() and slopes.get_device() == index):
+            raise ValueError("slopes must be a contiguous fp32 tensor [h] on the inputs' device")
+        slope = slopes.data_ptr()
+    T = (q.shape[0],)
+    code = lib.smla_fwd_scored(*args, sm_scale, softcap, slope,
+                               _int32(first_pos, "first_pos", T, index),
+                               _int32(last_pos, "last_pos", T, index), *ends, raw_stream)
+    if code:
+        raise SmlaError(code, "smla_fwd_scored")
     return out, lse
 
 

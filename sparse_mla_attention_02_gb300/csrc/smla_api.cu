@@ -322,6 +322,75 @@ smla_status run_fwd(const void* q, const void* kv, int kv_dtype,
   return SMLA_OK;
 }
 
+// What smla_fwd_scored does to the scores and the positions that a token sees.
+struct Scoring {
+  float softcap = 0.f;
+  const float* slopes = nullptr;
+  const int32_t* first_pos = nullptr;
+  const int32_t* last_pos = nullptr;
+};
+
+smla_status run_window(const void* q, const void* kv_cache, int kv_dtype,
+                       const float* k_scale, const int32_t* query_start,
+                       const int32_t* seq_lens, const int32_t* block_table, int num_reqs,
+                       int block_table_stride, int block_size, int block_stride_rows,
+                       int window, int sinks, int max_seq_len, int T, int h, int d_qk,
+                       int d_v, int64_t num_slots, float sm_scale, const Scoring& scoring,
+                       void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream) {
+  smla_status st = check_window_shape(T, h, d_qk, d_v, kv_dtype, window, sinks);
+  if (st != SMLA_OK) return st;
+  smla::PagedBatch b{};
+  st = make_batch(query_start, seq_lens, block_table, num_reqs, block_table_stride, block_size,
+                  block_stride_rows, T, num_slots, &b);
+  if (st != SMLA_OK || T == 0) return st;
+  if (!q || !kv_cache || !out || (kv_dtype != SMLA_KV_BF16 && !k_scale))
+    return SMLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) ||
+      (k_scale && !aligned(k_scale, 4)) || (lse && !aligned(lse, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  smla::WinParams p{};
+  {
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if ((st = device_info(&dev)) != SMLA_OK) return st;
+    p.inject_stall = dev->stall;
+    p.wait_limit_ns = dev->wait_limit_ns ? dev->wait_limit_ns : smla::kWaitLimitNs;
+  }
+  const smla::WindowPlan plan =
+      window_plan(num_reqs, T, h, block_table_stride, block_size, window, sinks, max_seq_len,
+                  dev->num_sms);
+  if (plan.workspace_bytes > 0) {
+    if (!workspace || workspace_bytes < plan.workspace_bytes) return SMLA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
+    p.parts = static_cast<int*>(workspace);
+    p.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                   ((size_t)T * h * sizeof(int) + 255) / 256 * 256);
+    p.lse_part = p.o_part + (size_t)plan.workers * 2 * 128 * 512;
+  }
+  p.b = b;
+  p.q = q;
+  p.kv = kv_cache;
+  p.k_scale = k_scale;
+  p.out = out;
+  p.lse = lse;
+  p.status = dev->status;
+  p.abort_ctr = dev->abort_ctr;
+  p.kv_format = kv_dtype;
+  p.h = h;
+  p.d_qk = d_qk;
+  p.window = window;
+  p.sinks = sinks;
+  p.workers = plan.workers;
+  p.merge_groups = plan.merge_groups;
+  p.sm_scale = sm_scale;
+  p.softcap = scoring.softcap;
+  p.slopes = scoring.slopes;
+  p.first_pos = scoring.first_pos;
+  p.last_pos = scoring.last_pos;
+  return smla::launch_window(p, stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
 }  // namespace
 
 namespace smla {
@@ -648,53 +717,29 @@ smla_status smla_fwd_window(const void* q, const void* kv_cache, int kv_dtype,
                             int window, int sinks, int max_seq_len, int T, int h, int d_qk,
                             int d_v, int64_t num_slots, float sm_scale, void* out, float* lse,
                             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  smla_status st = check_window_shape(T, h, d_qk, d_v, kv_dtype, window, sinks);
-  if (st != SMLA_OK) return st;
-  smla::PagedBatch b{};
-  st = make_batch(query_start, seq_lens, block_table, num_reqs, block_table_stride, block_size,
-                  block_stride_rows, T, num_slots, &b);
-  if (st != SMLA_OK || T == 0) return st;
-  if (!q || !kv_cache || !out || (kv_dtype != SMLA_KV_BF16 && !k_scale))
+  return run_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table, num_reqs,
+                    block_table_stride, block_size, block_stride_rows, window, sinks, max_seq_len,
+                    T, h, d_qk, d_v, num_slots, sm_scale, Scoring(), out, lse, workspace,
+                    workspace_bytes, stream);
+}
+
+smla_status smla_fwd_scored(const void* q, const void* kv_cache, int kv_dtype,
+                            const float* k_scale, const int32_t* query_start,
+                            const int32_t* seq_lens, const int32_t* block_table, int num_reqs,
+                            int block_table_stride, int block_size, int block_stride_rows,
+                            int window, int sinks, int max_seq_len, int T, int h, int d_qk,
+                            int d_v, int64_t num_slots, float sm_scale, float softcap,
+                            const float* slopes, const int32_t* first_pos,
+                            const int32_t* last_pos, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+  if (!(softcap == 0.f || (softcap >= 1e-30f && softcap <= 1e30f)) || !aligned(slopes, 4) ||
+      !aligned(first_pos, 4) || !aligned(last_pos, 4))
     return SMLA_ERR_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) ||
-      (k_scale && !aligned(k_scale, 4)) || (lse && !aligned(lse, 4)))
-    return SMLA_ERR_INVALID_ARG;
-  DeviceInfo* dev = nullptr;
-  smla::WinParams p{};
-  {
-    std::lock_guard<std::mutex> lk(g_mutex);
-    if ((st = device_info(&dev)) != SMLA_OK) return st;
-    p.inject_stall = dev->stall;
-    p.wait_limit_ns = dev->wait_limit_ns ? dev->wait_limit_ns : smla::kWaitLimitNs;
-  }
-  const smla::WindowPlan plan =
-      window_plan(num_reqs, T, h, block_table_stride, block_size, window, sinks, max_seq_len,
-                  dev->num_sms);
-  if (plan.workspace_bytes > 0) {
-    if (!workspace || workspace_bytes < plan.workspace_bytes) return SMLA_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return SMLA_ERR_INVALID_ARG;
-    p.parts = static_cast<int*>(workspace);
-    p.o_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        ((size_t)T * h * sizeof(int) + 255) / 256 * 256);
-    p.lse_part = p.o_part + (size_t)plan.workers * 2 * 128 * 512;
-  }
-  p.b = b;
-  p.q = q;
-  p.kv = kv_cache;
-  p.k_scale = k_scale;
-  p.out = out;
-  p.lse = lse;
-  p.status = dev->status;
-  p.abort_ctr = dev->abort_ctr;
-  p.kv_format = kv_dtype;
-  p.h = h;
-  p.d_qk = d_qk;
-  p.window = window;
-  p.sinks = sinks;
-  p.workers = plan.workers;
-  p.merge_groups = plan.merge_groups;
-  p.sm_scale = sm_scale;
-  return smla::launch_window(p, stream) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  return run_window(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block_table, num_reqs,
+                    block_table_stride, block_size, block_stride_rows, window, sinks, max_seq_len,
+                    T, h, d_qk, d_v, num_slots, sm_scale,
+                    Scoring{softcap, slopes, first_pos, last_pos}, out, lse, workspace,
+                    workspace_bytes, stream);
 }
 
 size_t smla_fwd_window_workspace_size(int num_reqs, int T, int h, int d_qk, int d_v,

@@ -39,7 +39,8 @@ struct AppendParams {
   int64_t row_ctas;            // CTAs that write cache rows (set by launch_append)
 };
 
-// A windowed attention (smla_tc_win.cu).
+// A windowed attention (smla_tc_win.cu); with scores that are capped, lowered with the
+// distance or seen through a span per token where one of the last four is set.
 struct WinParams {
   PagedBatch b;
   const void* q;               // bf16 [N, h, d_qk]
@@ -63,6 +64,10 @@ struct WinParams {
   int64_t num_tiles;           // set by launch_window
   int table_end;               // the last position a block table can hold (launch_window)
   float sm_scale;
+  float softcap;               // c tanh(s / c); 0: none
+  const float* slopes;         // [h] or nullptr
+  const int32_t* first_pos;    // [N] the first and the last position that a token sees,
+  const int32_t* last_pos;     // or nullptr: 0, its own
 };
 
 struct WindowPlan {

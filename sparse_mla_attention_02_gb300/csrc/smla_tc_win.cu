@@ -98,6 +98,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstddef>
 
 #include "e4m3_quant.cuh"
 #include "launch.cuh"
@@ -201,6 +202,10 @@ struct Unit {
   int b0, nb;
   int slot;                                // of its partial; -1: the tile's only part
   int live;                                // 1 + the request's length; 0: no more units
+  int hi;                                  // scored: the last position that some row sees
+                                           // (the lookups' warp alone has it)
+  template <bool kScored>
+  __device__ __forceinline__ int last_seen() const { return kScored ? hi : p_last; }
   __device__ __forceinline__ int block(int i) const {   // i-th block's index
     return i < sink_blocks ? i : win_block + (i - sink_blocks);
   }
@@ -213,7 +218,7 @@ struct Unit {
     return block(kFp8 ? b0 + j : b0 + nb - 1 - j);
   }
 };
-static_assert(sizeof(Unit) == 48, "three 16-byte words");
+static_assert(offsetof(Unit, hi) == 48, "three 16-byte words are handed on");
 
 constexpr int kWarpPv = 12;                // issues PV
 
@@ -289,6 +294,9 @@ __device__ __forceinline__ int64_t first_tile(const WinParams& p, int r) {
 
 // The k-th tile of request r, whose tokens are [c0, c1) and whose length is len,
 // with all of its key blocks; row1 = row0 where there is no such tile.
+// Scored: a request's first_pos and last_pos ascend, so the tile's first token has the
+// first position that it sees, and its last token the last.
+template <bool kScored>
 __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int c1, int len,
                                           int64_t k) {
   Unit t;
@@ -299,7 +307,7 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
   t.row0 = used ? (int)r0 : 0;
   t.row1 = used ? (int)r1 : 0;
   t.b0 = t.nb = t.sink_blocks = t.win_block = 0;
-  t.p_last = t.lo = -1;
+  t.p_last = t.lo = t.hi = -1;
   t.sinks = 0;
   t.live = 1 + min(len, 0x7FFFFFFE);
   if (!used) return t;
@@ -308,10 +316,15 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
   if (t.p_last < 0) return t;
   const int p_first = max(len - (c1 - tok0), 0);
   t.lo = p.window ? max(p_first - (p.window - 1), 0) : 0;
+  if (kScored) {
+    if (p.first_pos) t.lo = max(t.lo, ld_batch(p.first_pos + (c1 - (len - p_first))));
+    t.hi = p.last_pos ? min(ld_batch(p.last_pos + tok1), len - 1) : t.p_last;
+    if (t.hi < 0) return t;
+  }
   t.sinks = min(p.sinks, t.lo);
   t.win_block = t.lo / kBN;
   // (blocks past the table hold nothing, whatever a length says)
-  const int end = min(t.p_last, p.table_end) / kBN + 1;
+  const int end = min(t.last_seen<kScored>(), p.table_end) / kBN + 1;
   t.sink_blocks = min(min((t.sinks + kBN - 1) / kBN, t.win_block), end);
   t.nb = t.sink_blocks + max(end - t.win_block, 0);
   return t;
@@ -319,11 +332,12 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
 
 // Unit number u where a unit is a tile: the tiles from the last, as a prompt's
 // later tokens see more keys.
+template <bool kScored>
 __device__ __forceinline__ Unit find_unit(const WinParams& p, int64_t u) {
   const int64_t tile = p.num_tiles - 1 - u;
   const int r = warp_last_request(p.b.num_reqs, tile, [&](int m) { return first_tile(p, m); });
-  return tile_unit(p, r, batch_start(p.b, r), batch_start(p.b, r + 1), batch_len(p.b, r),
-                   tile - first_tile(p, r));
+  return tile_unit<kScored>(p, r, batch_start(p.b, r), batch_start(p.b, r + 1),
+                            batch_len(p.b, r), tile - first_tile(p, r));
 }
 
 // A cluster's range of the list of all tiles' blocks (a tile without one counts
@@ -356,6 +370,7 @@ __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
   return divide_wide(x, y);
 }
 // The w-th range.  First the list's length, then the range's place.
+template <bool kScored>
 __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
   const int lane = threadIdx.x & 31;
   Walk k{0, 0, 0, 0, 0, 0};
@@ -371,7 +386,7 @@ __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
         const int len = batch_len(p.b, r);
         const int tiles = first + lane < p.b.num_reqs ? request_tiles(p, c0, c1) : 0;
         // One tile: its lane counts it.  More: the warp counts the request together.
-        n = tiles == 1 ? kTileCost + max(tile_unit(p, r, c0, c1, len, 0).nb, 1) : 0;
+        n = tiles == 1 ? kTileCost + max(tile_unit<kScored>(p, r, c0, c1, len, 0).nb, 1) : 0;
         for (uint32_t many = __ballot_sync(0xffffffffu, tiles > 1); many; many &= many - 1) {
           const int src = __ffs(many) - 1;
           const int s0 = __shfl_sync(0xffffffffu, c0, src), s1 = __shfl_sync(0xffffffffu, c1, src);
@@ -380,7 +395,7 @@ __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
           int64_t sum = 0;
 #pragma unroll 1
           for (int t = lane; t < st; t += 32)
-            sum += kTileCost + max(tile_unit(p, 0, s0, s1, sl, t).nb, 1);
+            sum += kTileCost + max(tile_unit<kScored>(p, 0, s0, s1, sl, t).nb, 1);
           sum = __shfl_sync(0xffffffffu, warp_scan(sum), 31);
           if (lane == src) n = sum;
         }
@@ -407,6 +422,7 @@ __device__ __forceinline__ Walk start_walk(const WinParams& p, int w) {
 }
 // The next part of a tile in the range; its row1 = row0 behind the last.  `note`:
 // this CTA writes down which ranges hold the tile, for the merge.
+template <bool kScored>
 __device__ __forceinline__ Unit next_part(const WinParams& p, Walk& k, int w, bool note) {
   const int lane = threadIdx.x & 31;
   Unit u{};
@@ -421,7 +437,9 @@ __device__ __forceinline__ Unit next_part(const WinParams& p, Walk& k, int w, bo
 #pragma unroll 1
     for (; tiles > 1 && t < tiles; t += 32) {
       const int64_t n =
-          t + lane < tiles ? kTileCost + max(tile_unit(p, k.r, c0, c1, len, t + lane).nb, 1) : 0;
+          t + lane < tiles
+              ? kTileCost + max(tile_unit<kScored>(p, k.r, c0, c1, len, t + lane).nb, 1)
+              : 0;
       const int64_t upto = warp_scan(n), all = __shfl_sync(0xffffffffu, upto, 31);
       if (k.pos < t0 + all) {
         const int src = __ffs(__ballot_sync(0xffffffffu, k.pos < t0 + upto)) - 1;
@@ -432,7 +450,7 @@ __device__ __forceinline__ Unit next_part(const WinParams& p, Walk& k, int w, bo
       t0 += all;
     }
     if (t < tiles) {
-      u = tile_unit(p, k.r, c0, c1, len, t);
+      u = tile_unit<kScored>(p, k.r, c0, c1, len, t);
       const int blocks = max(u.nb, 1);
       t0 += kTileCost;                                 // its first block
       if (k.pos < t0 + blocks) {
@@ -467,6 +485,7 @@ struct Rows4 {
   int id[4];
   int blk[4];
 };
+template <bool kScored>
 static __device__ __noinline__ Rows4 lookup4(const WinParams& p, const Unit& t, int pos,
                                              bool& bad) {
   Rows4 o;
@@ -474,7 +493,7 @@ static __device__ __noinline__ Rows4 lookup4(const WinParams& p, const Unit& t, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = pos + i;
-    const bool seen = e <= t.p_last && (e >= t.lo || e < t.sinks);
+    const bool seen = e <= t.last_seen<kScored>() && (e >= t.lo || e < t.sinks);
     o.id[i] = -1;
     o.blk[i] = -1;
     if (seen) {
@@ -522,13 +541,58 @@ __device__ __forceinline__ uint4 ld_q16(const uint4* at) {
   return v;
 }
 
+// A row of a scored call: its token's position, the span it sees, its head's slope.
+struct RowView {
+  int pos, lo, hi;
+  float slope;
+};
+__device__ __forceinline__ RowView row_view(const WinParams& p, int64_t g, int p_last, int last_tok,
+                                            int len) {
+  const int tok = (int)(g / p.h);
+  RowView v{p_last - (last_tok - tok), 0, -1, 0.f};
+  if (p.window) v.lo = max(v.pos - (p.window - 1), 0);
+  if (p.first_pos) v.lo = max(v.lo, ld_batch(p.first_pos + tok));
+  if (v.pos >= 0) v.hi = p.last_pos ? max(min(ld_batch(p.last_pos + tok), len - 1), -1) : v.pos;
+  if (p.slopes) v.slope = ld_batch(p.slopes + (int)(g - (int64_t)tok * p.h));
+  return v;
+}
+
+// Scores x in log2 units capped: cap tanh(x / cap).  With u = 2^(2 log2(e) x / cap),
+// tanh = 1 - 2 / (1 + u): two steps of the special function unit and an error of at
+// most 2^-21 of the cap, which is as much of x as the score's own rounding only where
+// x is no small part of the cap.  Where all of a warp's scores are below an eighth of
+// it, the odd series of tanh to y^9 (off by less than 2^-30 of x there) takes its place.
+__device__ __forceinline__ void cap_scores(float (&x)[32], float cap) {
+  const float inv = __fdividef(1.f, cap);
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) top = max3(top, fabsf(x[k]), fabsf(x[k + 1]));
+  if (__all_sync(0xffffffffu, top * inv < 0.125f)) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float y = x[k] * inv, z = y * y;
+      float w = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
+      w = fmaf(z, w, 2.f / 15.f);
+      w = fmaf(z, w, -1.f / 3.f);
+      x[k] = fmaf(x[k] * z, w, x[k]);
+    }
+    return;
+  }
+  const float f = 2.f * 1.4426950408889634f * inv;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float u = ex2_approx(x[k] * f);
+    x[k] = fmaf(-2.f * cap, rcp_approx(1.f + u), cap);
+  }
+}
+
 // The unit's marked rows again, each from its visible positions in the unit's blocks
 // alone, by the eight softmax warps together: each warp takes 16 keys of every block,
 // two at a time, and the eight partial rows are merged in P's place.  A lane holds
 // twice eight neighbouring channels of a row's 512, and two of its rope.  131,072 keys
 // take 8 ms a row; meanwhile the pair's other warps wait (pair_wait_slow), for which a
 // beat goes to both CTAs.
-template <bool kFp8>
+template <bool kFp8, bool kScored>
 static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t, uint8_t* sp,
                                               const PairWaiter w, uint32_t rank) {
   constexpr int kKeys = 2;
@@ -546,7 +610,8 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
     if (!flag[rr]) continue;
     const int64_t g = (int64_t)t.row0 + 64 * (int)rank + rr;
     const int pos = t.p_last - ((t.row1 - 1) / p.h - (int)g / p.h);
-    const int lo = p.window ? max(pos - (p.window - 1), 0) : 0;
+    RowView v{pos, p.window ? max(pos - (p.window - 1), 0) : 0, pos, 0.f};
+    if (kScored) v = row_view(p, g, t.p_last, (t.row1 - 1) / p.h, t.live - 1);
     const uint16_t* qr = static_cast<const uint16_t*>(p.q) + g * p.d_qk;
     const uint4 q0 = *reinterpret_cast<const uint4*>(qr + ch);
     const uint4 q1 = *reinterpret_cast<const uint4*>(qr + ch + kFar);
@@ -568,7 +633,7 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
       if (__any_sync(0xffffffffu, w.aborted())) break;
       int row = -1;
       float scale = 1.f;
-      if (e <= pos && (e >= lo || e < p.sinks)) {
+      if (e <= v.hi && (e >= v.lo || e < p.sinks)) {
         const int page = e / p.b.block_size;
         const int blk = batch_block(p.b, t.r, page, bad);
         row = batch_row(p.b, blk, e - page * p.b.block_size, bad);
@@ -578,7 +643,7 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
 #pragma unroll 1
       while (todo) {
         uint32_t k[kKeys][kFp8 ? 5 : 9];               // (a row's last word: its rope)
-        float s[kKeys], sc[kKeys];
+        float s[kKeys], sc[kKeys], far[kKeys];
         bool have[kKeys];
         int src = 0;
 #pragma unroll
@@ -588,6 +653,7 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
           todo &= todo - 1;
           const int64_t at = (int64_t)__shfl_sync(0xffffffffu, row, src) * p.d_qk;
           sc[c] = __shfl_sync(0xffffffffu, scale, src);
+          far[c] = (float)abs(v.pos - (e - (lane & 15) + src));
           if (kFp8) {
             const uint8_t* kr = static_cast<const uint8_t*>(p.kv) + at;
             const uint4 x = *reinterpret_cast<const uint4*>(kr + ch);
@@ -634,7 +700,12 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
           for (int c = 0; c < kKeys; ++c) s[c] += __shfl_xor_sync(0xffffffffu, s[c], o);
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) {
-          s[c] = have[c] ? s[c] * sc[c] * p.sm_scale : -INFINITY;
+          s[c] = s[c] * sc[c] * p.sm_scale;
+          if (kScored) {
+            if (p.softcap > 0.f) s[c] = p.softcap * tanhf(s[c] / p.softcap);
+            if (p.slopes) s[c] -= v.slope * far[c];
+          }
+          if (!have[c]) s[c] = -INFINITY;
           top = fmaxf(top, s[c]);
         }
         if (top > m) {
@@ -702,7 +773,9 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
   }
 }
 
-template <bool kFp8>
+// kScored: scores are capped, lowered with the distance, or seen through a span per
+// token.  (Both in one kernel would cost the plain call.)
+template <bool kFp8, bool kScored>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
 smla_window_kernel(const __grid_constant__ WinArgs a) {
   using C = Cfg<kFp8>;
@@ -787,7 +860,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const int pos = u.template work<kFp8>(j) * kBN + 4 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      e.seen |= (pos + i <= u.p_last && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
+      e.seen |= (pos + i <= u.template last_seen<kScored>() && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
     // (a copy brings its rows whole where a row of the tile sees one of them)
     if (__ballot_sync(0xffffffffu, e.seen != 0) & mine) {
       const int page = a.shift >= 0 ? pos >> a.shift : pos / p.b.block_size;
@@ -801,10 +874,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (p.workers > 0) {
       asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the merge)
-      walk = start_walk(p, (int)(blockIdx.x >> 1));
-      next = next_part(p, walk, (int)(blockIdx.x >> 1), r == 0);
+      walk = start_walk<kScored>(p, (int)(blockIdx.x >> 1));
+      next = next_part<kScored>(p, walk, (int)(blockIdx.x >> 1), r == 0);
     } else {
-      next = find_unit(p, (int64_t)(blockIdx.x >> 1));
+      next = find_unit<kScored>(p, (int64_t)(blockIdx.x >> 1));
     }
     if (a.quad) {
       e0 = entry(next, 0);
@@ -1202,7 +1275,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         __syncwarp();
       }
       const Unit u = next;
-      bad |= u.row1 > u.row0 && u.p_last > p.table_end;
+      bad |= u.row1 > u.row0 && u.template last_seen<kScored>() > p.table_end;
       if (u.row1 > u.row0) publish(u);
       Found f = found(e0);
       for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
@@ -1221,7 +1294,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           e1 = e2;
           e2 = entry(u, j + 3);
         } else {
-          const Rows4 x = lookup4(p, u, u.template work<kFp8>(j) * kBN + 4 * lane, bad);
+          const Rows4 x = lookup4<kScored>(p, u, u.template work<kFp8>(j) * kBN + 4 * lane, bad);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             id[k] = x.id[k];
@@ -1276,7 +1349,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       }
       if (stopped()) break;
       if (p.workers > 0) {
-        next = next_part(p, walk, (int)(blockIdx.x >> 1), r == 0);
+        next = next_part<kScored>(p, walk, (int)(blockIdx.x >> 1), r == 0);
         if (next.row1 <= next.row0) break;
       } else {
         W.wait(cfull, (n >> 1) & 1);
@@ -1288,7 +1361,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         __syncwarp();
         if (lane == 0) mbar_signal_remote(bar0(kBarCEmpty + (n & 1)));
         if (!taken) break;
-        next = find_unit(p, (int64_t)(first >> 1));
+        next = find_unit<kScored>(p, (int64_t)(first >> 1));
         ++n;
       }
       if (a.quad) {
@@ -1322,11 +1395,23 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const Unit* t = peek_unit(i);
       // (all eight warps leave together: they share the named barriers below)
       if (named_bar_or(4, 256, !t->live || W.aborted())) break;
-      int pos = -1, lo = 0;                            // the row's token sees [lo, pos], sinks
+      int hi = -1, lo = 0;                             // the row's token sees [lo, hi], sinks
+      int pos = 0;                                     // scored: its position, its head's slope
+      float slope = 0.f;                               // in log2 units
       {
         const int g = t->row0 + 64 * (int)r + row;
-        if (g < t->row1) pos = t->p_last - ((t->row1 - 1) / p.h - g / p.h);
-        if (p.window) lo = max(pos - (p.window - 1), 0);
+        if constexpr (kScored) {
+          if (g < t->row1) {
+            const RowView v = row_view(p, g, t->p_last, (t->row1 - 1) / p.h, t->live - 1);
+            hi = v.hi;
+            lo = v.lo;
+            pos = v.pos;
+            slope = v.slope * 1.4426950408889634f;
+          }
+        } else {
+          if (g < t->row1) hi = t->p_last - ((t->row1 - 1) / p.h - g / p.h);
+          if (p.window) lo = max(hi - (p.window - 1), 0);
+        }
       }
       const int nb = t->nb;
       // A warp whose 32 rows lie behind the tile's last only keeps step: nothing reads
@@ -1371,7 +1456,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         tc_fence_after();
         // The row's view of its 32 keys.
         {
-          const int up = pos - e0;                       // keys 0 .. up
+          const int up = hi - e0;                        // keys 0 .. up
           uint32_t v = up >= 31 ? ~0u : up < 0 ? 0u : (2u << up) - 1u;
           const int dn = lo - e0;                        // keys dn ..
           const uint32_t win = dn <= 0 ? ~0u : dn > 31 ? 0u : ~0u << dn;
@@ -1414,8 +1499,25 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             cl = 1.f;
             back = 0.f;                                  // (their sums are taken below)
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = s[k] * (ks[k] * scale) + __log2f(ks[k]);
+            for (int k = 0; k < 32; ++k) {
+              s[k] = s[k] * (ks[k] * scale);
+              if (!kScored) s[k] += __log2f(ks[k]);
+            }
           }
+        }
+        if constexpr (kScored) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[k] *= cl;
+          cl = 1.f;
+          if (p.softcap > 0.f) cap_scores(s, p.softcap * 1.4426950408889634f);
+          if (p.slopes) {
+            const float d0 = (float)(e0 - pos);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[k] = fmaf(-slope, fabsf(d0 + (float)k), s[k]);
+          }
+          if (kFp8 && __builtin_expect(several, 0))
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[k] += __log2f(ks[k]);
         }
         if (__builtin_expect(!__all_sync(0xffffffffu, see == ~0u && cl > 0.f), 0)) {
 #pragma unroll
@@ -1659,7 +1761,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       odd = odd && live && l < INFINITY && lr < INFINITY;
       if (odd) flag[row] = 1;
       if (__builtin_expect(named_bar_or(4, 256, odd), 0)) {  // (also orders the stores before)
-        slow_rows<kFp8>(p, *t, sm + C::kOffP, W, r);
+        slow_rows<kFp8, kScored>(p, *t, sm + C::kOffP, W, r);
       }
       // (the next unit's first weights are signalled behind these TMEM loads)
       tc_fence_before();
@@ -1903,7 +2005,7 @@ cudaError_t encode_columns(CUtensorMap* map, bool fp8, const void* base, int d, 
              : cudaErrorInvalidValue;
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kScored>
 cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   using C = Cfg<kFp8>;
   // (once per device: the attribute call costs as much as a launch)
@@ -1912,12 +2014,12 @@ cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-    e = cudaFuncSetAttribute(smla_window_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)C::kSmem);
+    e = cudaFuncSetAttribute(smla_window_kernel<kFp8, kScored>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  return launch_early(smla_window_kernel<kFp8>, ctas, C::kThreads, C::kSmem, stream, a);
+  return launch_early(smla_window_kernel<kFp8, kScored>, ctas, C::kThreads, C::kSmem, stream, a);
 }
 
 int64_t tile_numbers(int T, int h, int num_reqs) {
@@ -1993,7 +2095,12 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   if (ctas > 0x7FFFFFFFll || (int64_t)p.b.N * p.h > 0x7FFFFFFFll)
     return cudaErrorInvalidConfiguration;
   a.p = p;
-  e = fp8 ? launch<true>(a, (unsigned)ctas, stream) : launch<false>(a, (unsigned)ctas, stream);
+  if (p.softcap > 0.f || p.slopes || p.first_pos || p.last_pos)
+    e = fp8 ? launch<true, true>(a, (unsigned)ctas, stream)
+            : launch<false, true>(a, (unsigned)ctas, stream);
+  else
+    e = fp8 ? launch<true, false>(a, (unsigned)ctas, stream)
+            : launch<false, false>(a, (unsigned)ctas, stream);
   if (e != cudaSuccess || p.workers == 0) return e;
   return launch_early(smla_window_merge_kernel, (unsigned)(p.b.N * p.h), 128 * p.merge_groups, 0,
                       stream, p);

@@ -54,6 +54,11 @@ __device__ __forceinline__ void st_global_32(void* dst, uint32_t a, uint32_t b, 
 }
 
 // The largest of three (NaN operands are passed over).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
