@@ -9,6 +9,7 @@ or ``__graft_entry__.build()``), every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -25,6 +26,8 @@ SMLA_KV_FP8_DS_MLA = 3            # 656-byte rows: 512 E4M3 | 4 fp32 scales | 64
 SMLA_KV_FP8_E4M3_GROUP4_KPE = 4   # E4M3 [S, 576], k_scale [S, 4], one kpe scale
 SMLA_KV_FP8_E4M3_BLOCK = 5        # E4M3 [S, d_qk], one fp32 scale per cache block
 DS_MLA_ROW_BYTES = 656
+# formats with scales that belong to a row or a block
+_BLOCK_SCALED = (SMLA_KV_FP8_E4M3_GROUP128, SMLA_KV_FP8_E4M3_GROUP4_KPE, SMLA_KV_FP8_E4M3_BLOCK)
 
 SMLA_OK = 0
 STATUS_NAMES = {0: "SMLA_OK", 1: "SMLA_ERR_INVALID_ARG",
@@ -452,44 +455,16 @@ def smla_cache_append(kv_c, k_pe, cos_sin, query_start, seq_lens, block_table, b
 
 def _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots, index):
     """Check the caches of the layers that share a block table; return the C
-    arguments (kv_caches, k_scales, layers, format, d_qk, slots, block, stride)."""
+    arguments (kv_caches, k_scales, layers, format, d_qk, slots, block, stride), and
+    what has to live until the call."""
     import torch
     if block_size < 1 or (block_stride_rows != 0 and block_stride_rows < block_size):
         raise ValueError("block_size must be positive and block_stride_rows 0 or at least "
                          "block_size")
-    scaled = kv_dtype in (SMLA_KV_FP8_E4M3_GROUP128, SMLA_KV_FP8_E4M3_GROUP4_KPE,
-                          SMLA_KV_FP8_E4M3_BLOCK)
+    scaled = kv_dtype in _BLOCK_SCALED
     rows_per_scale = block_stride_rows or block_size
-    scale_ptrs = None
-    if isinstance(kv_caches, torch.Tensor):
-        if kv_caches.dim() == 3:                  # [layers, slots, row]
-            L, S = kv_caches.shape[:2]
-        else:
-            L, S = 1, kv_caches.shape[0] if kv_caches.dim() == 2 else 0
-        if L < 1 or S < 1:
-            raise ValueError("kv_caches must be [layers, slots, row] or [slots, row]")
-        row = kv_caches.shape[-1]
-        d_qk = 576 if kv_dtype == SMLA_KV_FP8_DS_MLA else row
-        # (as one tall cache; the layers' scales are looked at below)
-        _cache_rows(kv_caches, kv_dtype, None, d_qk, None, rows_per_scale, index, need_scale=False)
-        step = S * row * kv_caches.element_size()
-        base = kv_caches.data_ptr()
-        ptrs = (ctypes.c_void_p * L)(*range(base, base + L * step, step))
-        if num_slots is not None:
-            if num_slots > S:
-                raise ValueError("num_slots is larger than a layer's cache")
-            S = int(num_slots)
-        if scaled:
-            one = isinstance(k_scales, torch.Tensor) and k_scales.dtype is torch.float32 and \
-                k_scales.is_contiguous() and k_scales.get_device() == index
-            n = k_scales.numel() // L if one else 0
-            if not one or k_scales.numel() != n * L or (L > 1 and k_scales.shape[0] != L) or \
-                    n < _scale_count(kv_dtype, S, d_qk, rows_per_scale):
-                raise ValueError("k_scales must be a contiguous fp32 tensor on the inputs' device "
-                                 "with the scales of every layer")
-            base = k_scales.data_ptr()
-            scale_ptrs = (ctypes.c_void_p * L)(*range(base, base + 4 * L * n, 4 * n))
-    else:
+    scales = None
+    if isinstance(kv_caches, (list, tuple)):
         L = len(kv_caches)
         if L < 1 or kv_caches[0].dim() < 2:
             raise ValueError("kv_caches must hold a cache, rows as its last dimension, for every "
@@ -503,10 +478,38 @@ def _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num
                 raise ValueError("the layers' caches must have one shape")
             S, _ = _cache_rows(c, kv_dtype, k_scales[l] if scaled else None, d_qk, num_slots,
                                rows_per_scale, index, need_scale=scaled)
-        ptrs = (ctypes.c_void_p * L)(*[c.data_ptr() for c in kv_caches])
+        caches = array.array("Q", [c.data_ptr() for c in kv_caches])
         if scaled:
-            scale_ptrs = (ctypes.c_void_p * L)(*[s.data_ptr() for s in k_scales])
-    return ptrs, scale_ptrs, L, kv_dtype, d_qk, S, block_size, block_stride_rows
+            scales = array.array("Q", [x.data_ptr() for x in k_scales])
+    else:
+        shape = kv_caches.shape
+        dims = len(shape)                         # [layers, slots, row] or [slots, row]
+        if dims != 3 and dims != 2:
+            raise ValueError("kv_caches must be [layers, slots, row] or [slots, row]")
+        L, S, row = shape if dims == 3 else (1, *shape)
+        if L < 1 or S < 1:
+            raise ValueError("kv_caches must hold a cache for every layer")
+        d_qk = 576 if kv_dtype == SMLA_KV_FP8_DS_MLA else row
+        # (as one tall cache; the layers' scales are looked at below)
+        _cache_rows(kv_caches, kv_dtype, None, d_qk, None, rows_per_scale, index, need_scale=False)
+        step = S * row * (2 if kv_dtype == SMLA_KV_BF16 else 1)
+        base = kv_caches.data_ptr()
+        caches = array.array("Q", range(base, base + L * step, step))
+        if num_slots is not None:
+            if num_slots > S:
+                raise ValueError("num_slots is larger than a layer's cache")
+            S = int(num_slots)
+        if scaled:
+            if not (k_scales is not None and not isinstance(k_scales, (list, tuple)) and
+                    k_scales.dtype is torch.float32 and k_scales.is_contiguous() and
+                    k_scales.get_device() == index and (L == 1 or k_scales.shape[0] == L) and
+                    k_scales.numel() >= L * _scale_count(kv_dtype, S, d_qk, rows_per_scale)):
+                raise ValueError("k_scales must be a contiguous fp32 tensor on the inputs' device "
+                                 "with the scales of every layer")
+            base, step = k_scales.data_ptr(), 4 * (k_scales.numel() // L)
+            scales = array.array("Q", range(base, base + L * step, step))
+    return (caches.buffer_info()[0], scales.buffer_info()[0] if scaled else None, L, kv_dtype,
+            d_qk, S, block_size, block_stride_rows), (caches, scales)
 
 
 def _int32(t, what, shape, index):
@@ -523,29 +526,36 @@ def _int32(t, what, shape, index):
 
 def _table_args(block_table, out_block_table, refcount, out_refcount, index):
     """The C arguments (table, table out, rows, width, counts, counts out, blocks)."""
-    if block_table.dim() != 2 or refcount.dim() != 1:
+    shape, blocks = block_table.shape, refcount.shape
+    if len(shape) != 2 or len(blocks) != 1:
         raise ValueError("block_table must be [rows, stride] and refcount [blocks]")
-    R, width = block_table.shape
-    NB = refcount.shape[0]
-    out_block_table = block_table if out_block_table is None else out_block_table
-    out_refcount = refcount if out_refcount is None else out_refcount
-    return (_int32(block_table, "block_table", (R, width), index),
-            _int32(out_block_table, "out_block_table", (R, width), index), R, width,
-            _int32(refcount, "refcount", (NB,), index),
-            _int32(out_refcount, "out_refcount", (NB,), index), NB)
+    table = _int32(block_table, "block_table", shape, index)
+    ref = _int32(refcount, "refcount", blocks, index)
+    return (table, table if out_block_table is None else
+            _int32(out_block_table, "out_block_table", shape, index), shape[0], shape[1], ref,
+            ref if out_refcount is None else
+            _int32(out_refcount, "out_refcount", blocks, index), blocks[0])
 
 
-def _workspace(workspace, nbytes, like, index, stream):
-    """(a caller's workspace or a new one, its address, its bytes)."""
+def _own_memory(words, nbytes, workspace, like, index, stream):
+    """One new int32 tensor for `words` words of results and, where the caller gave
+    none, a workspace of `nbytes` bytes; (that tensor or None, the workspace's address,
+    its bytes)."""
     import torch
-    if workspace is None:
-        if nbytes == 0:
-            return None, None, 0
-        workspace = like.new_empty((nbytes + 3) // 4) if stream is None else \
-            _empty((nbytes,), torch.uint8, like.device, stream)
-    elif not (workspace.get_device() == index and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ws_bytes = nbytes
+    if workspace is not None:
+        if not (workspace.get_device() == index and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+        nbytes = 0
+    words = (words + 63) // 64 * 64               # (a workspace behind them is aligned)
+    n = words + (nbytes + 3) // 4
+    if n == 0:
+        return None, workspace.data_ptr() if workspace is not None else None, ws_bytes
+    memory = like.new_empty(n) if stream is None else \
+        _empty((n,), torch.int32, like.device, stream)
+    return memory, (memory.data_ptr() + 4 * words if workspace is None else
+                    workspace.data_ptr()), ws_bytes
 
 
 def smla_cache_copy(kv_caches, kv_dtype, k_scales, src, dst, block_size, block_stride_rows=0,
@@ -558,9 +568,9 @@ def smla_cache_copy(kv_caches, kv_dtype, k_scales, src, dst, block_size, block_s
     else None."""
     lib = _lib or load()
     index, raw_stream = _device_stream(src, "src", stream)
-    pool = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots,
-                      index)
-    n = src.numel()
+    pool, _alive = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows,
+                              num_slots, index)
+    n = src.shape[0]
     code = lib.smla_cache_copy(*pool, _int32(src, "src", (n,), index),
                                _int32(dst, "dst", (n,), index), n, raw_stream)
     if code:
@@ -582,27 +592,27 @@ def smla_cache_fork(parents, children, room, seq_lens, block_table, refcount, bl
     children, parents, room int32 [n]; seq_lens int32 [R], block_table int32
     [R,stride], refcount int32 [blocks]; the results go to the ``out_`` tensors
     (None: in place); kv_caches and k_scales as for ``smla_cache_copy``.
-    Returns ``missing`` int32 [1]: how many blocks could not be had."""
-    import torch
+    Returns ``missing`` int32 [1]: how many blocks could not be had (a new one shares
+    its memory with the call's workspace, where that is new too)."""
     lib = _lib or load()
     index, raw_stream = _device_stream(children, "children", stream)
-    pool = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots,
-                      index)
+    pool, _alive = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows,
+                              num_slots, index)
     tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
-    n, R = children.numel(), tables[2]
+    n, R = children.shape[0], tables[2]
     pairs = (_int32(parents, "parents", (n,), index), _int32(children, "children", (n,), index),
              _int32(room, "room", (n,), index), n)
-    lens = (_int32(seq_lens, "seq_lens", (R,), index),
-            _int32(seq_lens if out_seq_lens is None else out_seq_lens, "out_seq_lens", (R,),
-                   index))
-    if missing is None:
-        missing = children.new_empty(1) if stream is None else \
-            _empty((1,), torch.int32, children.device, stream)
-    workspace, ws, nbytes = _workspace(
-        workspace, lib.smla_cache_fork_workspace_size(n, tables[3], tables[6]), children, index,
+    lens = _int32(seq_lens, "seq_lens", (R,), index)
+    memory, ws, nbytes = _own_memory(
+        1 if missing is None else 0,
+        lib.smla_cache_fork_workspace_size(n, tables[3], tables[6]), workspace, children, index,
         stream)
-    code = lib.smla_cache_fork(*pairs, *lens, *tables, *pool,
-                               _int32(missing, "missing", (1,), index), ws, nbytes, raw_stream)
+    if missing is None:
+        missing = memory[:1]
+    code = lib.smla_cache_fork(
+        *pairs, lens, lens if out_seq_lens is None else
+        _int32(out_seq_lens, "out_seq_lens", (R,), index), *tables, *pool,
+        _int32(missing, "missing", (1,), index), ws, nbytes, raw_stream)
     if code:
         raise SmlaError(code, "smla_cache_fork")
     return missing
@@ -617,7 +627,7 @@ def smla_cache_free(rows, begin, end, block_table, refcount, block_size, out_blo
     lib = _lib or load()
     index, raw_stream = _device_stream(rows, "rows", stream)
     tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
-    n = rows.numel()
+    n = rows.shape[0]
     code = lib.smla_cache_free(_int32(rows, "rows", (n,), index),
                                _int32(begin, "begin", (n,), index),
                                _int32(end, "end", (n,), index), n, *tables, block_size,
@@ -638,23 +648,24 @@ def smla_cache_compact(block_table, refcount, block_size, kv_caches, kv_dtype, k
     """``smla_cache_compact``: move the live blocks to the start of the pool.
 
     Arguments as for ``smla_cache_fork``.  Returns (block_map int32 [blocks]: the new
-    number of each live block, -1 for free ones; num_live int32 [1])."""
-    import torch
+    number of each live block, -1 for free ones; num_live int32 [1]), new ones sharing
+    their memory with a new workspace."""
     lib = _lib or load()
     index, raw_stream = _device_stream(block_table, "block_table", stream)
-    pool = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num_slots,
-                      index)
+    pool, _alive = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows,
+                              num_slots, index)
     tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
-    if block_map is None:
-        block_map = refcount.new_empty(tables[6]) if stream is None else \
-            _empty((tables[6],), torch.int32, refcount.device, stream)
-    if num_live is None:
-        num_live = refcount.new_empty(1) if stream is None else \
-            _empty((1,), torch.int32, refcount.device, stream)
-    workspace, ws, nbytes = _workspace(
-        workspace, lib.smla_cache_compact_workspace_size(tables[6]), block_table, index, stream)
+    blocks = tables[6]
+    own_map, own_live = block_map is None, num_live is None
+    words = (blocks if own_map else 0) + (1 if own_live else 0)
+    memory, ws, nbytes = _own_memory(words, lib.smla_cache_compact_workspace_size(blocks),
+                                     workspace, refcount, index, stream)
+    if own_map:
+        block_map = memory[:blocks]
+    if own_live:
+        num_live = memory[words - 1:words]
     code = lib.smla_cache_compact(*tables, *pool,
-                                  _int32(block_map, "block_map", (tables[6],), index),
+                                  _int32(block_map, "block_map", (blocks,), index),
                                   _int32(num_live, "num_live", (1,), index), ws, nbytes,
                                   raw_stream)
     if code:

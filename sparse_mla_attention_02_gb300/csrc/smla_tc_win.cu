@@ -212,10 +212,14 @@ struct Unit {
   // The j-th block in the order of work.  bf16: from the last, so that the slow
   // copies of the block that a request ends in come while nothing else does (a
   // prompt of 4096 tokens: 1.30 -> 1.23 ms, 64 decode tokens: 53 -> 50 us).  E4M3:
-  // from the first (from the last, 32 decode tokens took 116 us, not 114).
-  template <bool kFp8>
+  // from the first (from the last, 32 decode tokens took 116 us, not 114), but with a
+  // distance bias from the last too: the near keys' scores are the largest then, and from
+  // the far end the running maximum would grow, and O be rescaled, block after block (a
+  // mixed batch: 430 -> 408 us; the scored kernel has this order for every score, as a
+  // choice at run time costs more than it gives).
+  template <bool kForward>
   __device__ __forceinline__ int work(int j) const {
-    return block(kFp8 ? b0 + j : b0 + nb - 1 - j);
+    return block(kForward ? b0 + j : b0 + nb - 1 - j);
   }
 };
 static_assert(offsetof(Unit, hi) == 48, "three 16-byte words are handed on");
@@ -281,6 +285,7 @@ struct WinArgs {
   int atoms;             // 128-byte columns of a row
   int ksteps;            // 32-byte MMA steps of a row
   float scale_log2;      // sm_scale * log2(e)
+  float two_over_cap;    // 2 / softcap
 };
 
 // The tiles of a request are numbered from first_tile on.  h = 128: a tile is
@@ -557,32 +562,68 @@ __device__ __forceinline__ RowView row_view(const WinParams& p, int64_t g, int p
   return v;
 }
 
-// Scores x in log2 units capped: cap tanh(x / cap).  With u = 2^(2 log2(e) x / cap),
-// tanh = 1 - 2 / (1 + u): two steps of the special function unit and an error of at
-// most 2^-21 of the cap, which is as much of x as the score's own rounding only where
-// x is no small part of the cap.  Where all of a warp's scores are below an eighth of
-// it, the odd series of tanh to y^9 (off by less than 2^-30 of x there) takes its place.
-__device__ __forceinline__ void cap_scores(float (&x)[32], float cap) {
-  const float inv = __fdividef(1.f, cap);
-  float top = 0.f;
+// Caps up to here take the exponential form below, whose error is in proportion to the
+// cap; larger ones, which hardly bend a score, that of far_scores.
+constexpr float kCapNear = 256.f;
+
+// Scores s * cl (log2 units) capped, cap tanh(s cl / cap), and lowered by the distance.
+// With u = 2^(two_over_cap s cl) = exp(2 y), tanh(y) = 1 - 2 / (1 + u): two steps of the
+// special function unit, the sums and products packed, the bias on the way.  Error of
+// tanh: rcp 2^-23 and the sum 2^-24 of a quotient of at most 1, ex2 2^-21.5 times at most
+// a quarter, all twice: less than 2^-20.
+// The bias of key k, side * (d0 + k) with side = -+slope, is added up in steps of two
+// from every eighth key's own product: off by at most 2^-22 of itself.
+template <bool kCap, bool kBias>
+__device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap, float two_over_cap,
+                                            float side, float d0) {
+  const float f = cl * two_over_cap, base = kCap ? cap : 0.f;
+  float c0 = base, c1 = base;
 #pragma unroll
-  for (int k = 0; k < 32; k += 2) top = max3(top, fabsf(x[k]), fabsf(x[k + 1]));
-  if (__all_sync(0xffffffffu, top * inv < 0.125f)) {
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float y = x[k] * inv, z = y * y;
-      float w = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
-      w = fmaf(z, w, 2.f / 15.f);
-      w = fmaf(z, w, -1.f / 3.f);
-      x[k] = fmaf(x[k] * z, w, x[k]);
+  for (int k = 0; k < 32; k += 2) {
+    if (kBias) {
+      if (k % 8 == 0) {
+        c0 = fmaf(side, d0 + (float)k, base);
+        c1 = c0 + side;
+      } else {
+        add2(c0, c1, 2.f * side, 2.f * side);
+      }
     }
-    return;
+    if (kCap) {
+      float u0 = s[k], u1 = s[k + 1];
+      fma2_bcast(u0, u1, f, 0.f);
+      u0 = ex2_approx(u0);
+      u1 = ex2_approx(u1);
+      add2(u0, u1, 1.f, 1.f);
+      s[k] = rcp_approx(u0);
+      s[k + 1] = rcp_approx(u1);
+    }
+    fma2(s[k], s[k + 1], kCap ? -2.f * cap : cl, c0, c1);
   }
-  const float f = 2.f * 1.4426950408889634f * inv;
-#pragma unroll
+}
+
+// The scores of a large cap: where all of a warp's lie below an eighth of it the odd
+// series of tanh to y^9 (off by less than 2^-30 of x there), else the form above, off by
+// 2^-20 of a cap that some score has an eighth of.  Rare, and out of line: the roles
+// share one instruction cache.
+static __device__ __noinline__ void far_scores(float* x, float cl, float cap, float two_over_cap,
+                                               float side, float d0) {
+  float top = 0.f;
+#pragma unroll 8
   for (int k = 0; k < 32; ++k) {
-    const float u = ex2_approx(x[k] * f);
-    x[k] = fmaf(-2.f * cap, rcp_approx(1.f + u), cap);
+    x[k] *= cl;
+    top = fmaxf(top, fabsf(x[k]));
+  }
+  const float inv = __fdividef(1.f, cap);
+  const bool series = __all_sync(0xffffffffu, top * inv < 0.125f);
+#pragma unroll 8
+  for (int k = 0; k < 32; ++k) {
+    const float y = x[k] * inv, z = y * y;
+    float w = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
+    w = fmaf(z, w, 2.f / 15.f);
+    w = fmaf(z, w, -1.f / 3.f);
+    const float near = fmaf(x[k] * z, w, x[k]);
+    const float u = ex2_approx(x[k] * two_over_cap);
+    x[k] = fmaf(side, d0 + (float)k, series ? near : fmaf(-2.f * cap, rcp_approx(1.f + u), cap));
   }
 }
 
@@ -779,6 +820,7 @@ template <bool kFp8, bool kScored>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
 smla_window_kernel(const __grid_constant__ WinArgs a) {
   using C = Cfg<kFp8>;
+  constexpr bool kForward = kFp8 && !kScored;          // Unit::work
   extern __shared__ __align__(1024) uint8_t sm[];
   const WinParams& p = a.p;
   const uint32_t sb = smem_u32(sm);
@@ -857,7 +899,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   auto entry = [&](const Unit& u, int j) {
     Entry e{0, -1, 0u};
     if (j >= u.nb) return e;
-    const int pos = u.template work<kFp8>(j) * kBN + 4 * lane;
+    const int pos = u.template work<kForward>(j) * kBN + 4 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       e.seen |= (pos + i <= u.template last_seen<kScored>() && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
@@ -1144,7 +1186,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           // Rows behind the last token may never have been written, and a weight of
           // 0 times NaN is NaN: they are read as zeros.  (The other rows of a block
           // were written; one that is not finite costs the tile slow_rows.)
-          const int up = u.live - 2 - (u.template work<kFp8>(j) * kBN + 4 * lane);
+          const int up = u.live - 2 - (u.template work<kForward>(j) * kBN + 4 * lane);
           if (up < 0) id.x = -1;
           if (up < 1) id.y = -1;
           if (up < 2) id.z = -1;
@@ -1294,7 +1336,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           e1 = e2;
           e2 = entry(u, j + 3);
         } else {
-          const Rows4 x = lookup4<kScored>(p, u, u.template work<kFp8>(j) * kBN + 4 * lane, bad);
+          const Rows4 x = lookup4<kScored>(p, u, u.template work<kForward>(j) * kBN + 4 * lane, bad);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             id[k] = x.id[k];
@@ -1389,6 +1431,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const uint32_t sempty = bar0(kBarSEmpty), pfull = bar0(kBarPFull);
     // One scale per tensor multiplies every score and the output.
     const float kscale = p.kv_format == kE4m3 ? ld_batch(p.k_scale) : 1.f;
+    const float cap2 = p.softcap * 1.4426950408889634f;      // (scored) in log2 units
     MetaRing mr;
     int J = 0, q = 0;                                  // blocks, units with blocks
     for (int i = 0;; ++i) {
@@ -1428,16 +1471,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       float m_run = -INFINITY;  // running max (log2 units), the same in a row's four threads
       float l_run = 0.f;       // this thread's sum of exp2(s - m_run)
       float lr_run = 0.f;      // the same sum of the bf16-rounded weights
-      int blk = nb > 0 ? t->template work<kFp8>(0) : 0;
+      int blk = nb > 0 ? t->template work<kForward>(0) : 0;
       // where the order of work leaves the sinks' blocks, or comes to them
-      const int jump = kFp8 ? t->sink_blocks - t->b0 : t->b0 + nb - t->sink_blocks;
+      const int jump = kForward ? t->sink_blocks - t->b0 : t->b0 + nb - t->sink_blocks;
       for (int j = 0; j < nb; ++j, ++J, mr.next()) {
         const int buf = J & 1, m = mr.m;
         const int e0 = blk * kBN + 32 * seg;             // this thread's first key
         if (j + 1 == jump)
-          blk = kFp8 ? t->win_block : t->sink_blocks - 1;
+          blk = kForward ? t->win_block : t->sink_blocks - 1;
         else
-          blk += kFp8 ? 1 : -1;
+          blk += kForward ? 1 : -1;
         W.wait(bar(kBarMFull + m), mr.ph);
         uint32_t see = words[4 * m + seg];
         W.wait(bar(kBarSFull + buf), (J >> 1) & 1);
@@ -1506,14 +1549,30 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           }
         }
         if constexpr (kScored) {
+          const float side = e0 >= pos ? -slope : slope, d0 = (float)(e0 - pos);
+          if (__builtin_expect(p.softcap > kCapNear, 0)) {
+            float x[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) s[k] *= cl;
-          cl = 1.f;
-          if (p.softcap > 0.f) cap_scores(s, p.softcap * 1.4426950408889634f);
-          if (p.slopes) {
-            const float d0 = (float)(e0 - pos);
+            for (int k = 0; k < 32; ++k) x[k] = s[k];
+            far_scores(x, cl, cap2, a.two_over_cap, side, d0);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = fmaf(-slope, fabsf(d0 + (float)k), s[k]);
+            for (int k = 0; k < 32; ++k) s[k] = x[k];
+          } else if (p.softcap > 0.f) {
+            if (p.slopes)
+              near_scores<true, true>(s, cl, cap2, a.two_over_cap, side, d0);
+            else
+              near_scores<true, false>(s, cl, cap2, a.two_over_cap, 0.f, 0.f);
+          } else if (p.slopes) {
+            near_scores<false, true>(s, cl, 0.f, 0.f, side, d0);
+          }
+          if (p.softcap > 0.f || p.slopes) cl = 1.f;
+          // Where the row's own position lies inside of the segment, and its later keys
+          // may be seen, their bias was added with the wrong sign.
+          if (p.last_pos && p.slopes &&
+              __builtin_expect(__any_sync(0xffffffffu, e0 < pos && e0 + 31 > pos), 0)) {
+#pragma unroll
+            for (int k = 1; k < 32; ++k)
+              if (e0 < pos) s[k] = fmaf(-2.f * slope, fmaxf(d0 + (float)k, 0.f), s[k]);
           }
           if (kFp8 && __builtin_expect(several, 0))
 #pragma unroll
@@ -2072,6 +2131,7 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   a.atoms = (p.d_qk * es + 127) / 128;
   a.ksteps = p.d_qk * es / 32;
   a.scale_log2 = p.sm_scale * 1.4426950408889634f;
+  a.two_over_cap = p.softcap > 0.f ? 2.f / p.softcap : 0.f;
   // Boxes: the largest power of two that divides the block (and 64); blocks of
   // other sizes than multiples of 4 take gather4 alone.
   a.box = p.b.block_size & -p.b.block_size;

@@ -53,12 +53,14 @@ __device__ __forceinline__ void st_global_32(void* dst, uint32_t a, uint32_t b, 
                : "memory");
 }
 
-// The largest of three (NaN operands are passed over).
+// 1 / x on the SFU (approximate; 0 for infinity).
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// The largest of three (NaN operands are passed over).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -71,6 +73,14 @@ __device__ __forceinline__ void fma2_bcast(float& a0, float& a1, float b, float 
       "mov.b64 z, {%3, %3};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "+f"(a0), "+f"(a1)
       : "f"(b), "f"(c));
+}
+
+// (a0, a1) * (b, b) + (c0, c1), each rounded on its own.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b, float c0, float c1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
+      "mov.b64 z, {%3, %4};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b), "f"(c0), "f"(c1));
 }
 
 // (a0, a1) += (b0, b1)
