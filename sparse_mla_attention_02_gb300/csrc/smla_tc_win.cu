@@ -568,25 +568,24 @@ constexpr float kCapNear = 256.f;
 
 // Scores s * cl (log2 units) capped, cap tanh(s cl / cap), and lowered by the distance.
 // With u = 2^(two_over_cap s cl) = exp(2 y), tanh(y) = 1 - 2 / (1 + u): two steps of the
-// special function unit, the sums and products packed, the bias on the way.  Error of
-// tanh: rcp 2^-23 and the sum 2^-24 of a quotient of at most 1, ex2 2^-21.5 times at most
-// a quarter, all twice: less than 2^-20.
+// special function unit, the sums and products packed, the bias on the way (a form of its
+// own for a cap without a bias made a longer kernel: 439 -> 450 us).  Error of tanh: rcp
+// 2^-23 and the sum 2^-24 of a quotient of at most 1, ex2 2^-21.5 times at most a quarter,
+// all twice: less than 2^-20.
 // The bias of key k, side * (d0 + k) with side = -+slope, is added up in steps of two
 // from every eighth key's own product: off by at most 2^-22 of itself.
-template <bool kCap, bool kBias>
+template <bool kCap>
 __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap, float two_over_cap,
                                             float side, float d0) {
   const float f = cl * two_over_cap, base = kCap ? cap : 0.f;
   float c0 = base, c1 = base;
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
-    if (kBias) {
-      if (k % 8 == 0) {
-        c0 = fmaf(side, d0 + (float)k, base);
-        c1 = c0 + side;
-      } else {
-        add2(c0, c1, 2.f * side, 2.f * side);
-      }
+    if (k % 8 == 0) {
+      c0 = fmaf(side, d0 + (float)k, base);
+      c1 = c0 + side;
+    } else {
+      add2(c0, c1, 2.f * side, 2.f * side);
     }
     if (kCap) {
       float u0 = s[k], u1 = s[k + 1];
@@ -1558,12 +1557,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) s[k] = x[k];
           } else if (p.softcap > 0.f) {
-            if (p.slopes)
-              near_scores<true, true>(s, cl, cap2, a.two_over_cap, side, d0);
-            else
-              near_scores<true, false>(s, cl, cap2, a.two_over_cap, 0.f, 0.f);
+            near_scores<true>(s, cl, cap2, a.two_over_cap, side, d0);
           } else if (p.slopes) {
-            near_scores<false, true>(s, cl, 0.f, 0.f, side, d0);
+            near_scores<false>(s, cl, 0.f, 0.f, side, d0);
           }
           if (p.softcap > 0.f || p.slopes) cl = 1.f;
           // Where the row's own position lies inside of the segment, and its later keys
