@@ -1354,10 +1354,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
             if (id[k] >= 0) top = fmaxf(top, sc[k]);
 #pragma unroll
           for (int o = 1; o <= 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (top == 0.f) top = 1.f;                   // (no key: all scores are masked)
           bool same = true;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (id[k] < 0) sc[k] = top > 0.f ? top : 1.f;
+            if (id[k] < 0) sc[k] = top;
             same &= sc[k] == top && top < INFINITY;
           }
           const uint32_t votes = __ballot_sync(0xffffffffu, same) >> (lane & 24);
