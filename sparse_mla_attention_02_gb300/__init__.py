@@ -608,7 +608,7 @@ def smla_cache_fork(parents, children, room, seq_lens, block_table, refcount, bl
         lib.smla_cache_fork_workspace_size(n, tables[3], tables[6]), workspace, children, index,
         stream)
     if missing is None:
-        missing = memory[:1]
+        missing = memory.narrow(0, 0, 1)
     code = lib.smla_cache_fork(
         *pairs, lens, lens if out_seq_lens is None else
         _int32(out_seq_lens, "out_seq_lens", (R,), index), *tables, *pool,
@@ -661,9 +661,9 @@ def smla_cache_compact(block_table, refcount, block_size, kv_caches, kv_dtype, k
     memory, ws, nbytes = _own_memory(words, lib.smla_cache_compact_workspace_size(blocks),
                                      workspace, refcount, index, stream)
     if own_map:
-        block_map = memory[:blocks]
+        block_map = memory.narrow(0, 0, blocks)
     if own_live:
-        num_live = memory[words - 1:words]
+        num_live = memory.narrow(0, words - 1, 1)
     code = lib.smla_cache_compact(*tables, *pool,
                                   _int32(block_map, "block_map", (blocks,), index),
                                   _int32(num_live, "num_live", (1,), index), ws, nbytes,
