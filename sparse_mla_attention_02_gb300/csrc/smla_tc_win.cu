@@ -198,7 +198,7 @@ __device__ __forceinline__ void PairWaiter::drain(uint32_t bar, uint32_t parity)
 // [b0, b0 + nb) of the tile's list (block()).
 struct Unit {
   int row0, row1, p_last, r;
-  int lo, sinks, sink_blocks, win_block;
+  int lo, sinks, sink_blocks, win_pos;
   int b0, nb;
   int slot;                                // of its partial; -1: the tile's only part
   int live;                                // 1 + the request's length; 0: no more units
@@ -206,10 +206,10 @@ struct Unit {
                                            // (the lookups' warp alone has it)
   template <bool kScored>
   __device__ __forceinline__ int last_seen() const { return kScored ? hi : p_last; }
-  __device__ __forceinline__ int block(int i) const {   // i-th block's index
-    return i < sink_blocks ? i : win_block + (i - sink_blocks);
+  __device__ __forceinline__ int block(int i) const {   // i-th block's first position
+    return i < sink_blocks ? i * kBN : win_pos + (i - sink_blocks) * kBN;
   }
-  // The j-th block in the order of work.  bf16: from the last, so that the slow
+  // The j-th block's first position in the order of work.  bf16: from the last, so that the slow
   // copies of the block that a request ends in come while nothing else does (a
   // prompt of 4096 tokens: 1.30 -> 1.23 ms, 64 decode tokens: 53 -> 50 us).  E4M3:
   // from the first (from the last, 32 decode tokens took 116 us, not 114), but with a
@@ -311,7 +311,7 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
   const bool used = k >= 0 && r1 > r0;
   t.row0 = used ? (int)r0 : 0;
   t.row1 = used ? (int)r1 : 0;
-  t.b0 = t.nb = t.sink_blocks = t.win_block = 0;
+  t.b0 = t.nb = t.sink_blocks = t.win_pos = 0;
   t.p_last = t.lo = t.hi = -1;
   t.sinks = 0;
   t.live = 1 + min(len, 0x7FFFFFFE);
@@ -327,11 +327,14 @@ __device__ __forceinline__ Unit tile_unit(const WinParams& p, int r, int c0, int
     if (t.hi < 0) return t;
   }
   t.sinks = min(p.sinks, t.lo);
-  t.win_block = t.lo / kBN;
   // (blocks past the table hold nothing, whatever a length says)
-  const int end = min(t.last_seen<kScored>(), p.table_end) / kBN + 1;
-  t.sink_blocks = min(min((t.sinks + kBN - 1) / kBN, t.win_block), end);
-  t.nb = t.sink_blocks + max(end - t.win_block, 0);
+  const int last = min(t.last_seen<kScored>(), p.table_end);
+  t.sink_blocks = min(min((t.sinks + kBN - 1) / kBN, t.lo / kBN), last / kBN + 1);
+  // The other blocks begin where the first seen position's 128 do, scored its 64 where no
+  // sinks lie in between (documents of 1500 tokens: 868 -> 850 us).
+  t.win_pos = t.lo / kBN * kBN;
+  if (kScored && t.sinks <= t.win_pos) t.win_pos = t.lo / 64 * 64;
+  t.nb = t.sink_blocks + (last >= t.win_pos ? (last - t.win_pos) / kBN + 1 : 0);
   return t;
 }
 
@@ -664,7 +667,7 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
     bool bad = false;                                  // (the lookups have said so)
 #pragma unroll 1
     for (int b = t.b0; b < t.b0 + t.nb; ++b) {
-      const int e = t.block(b) * kBN + 16 * sw + (lane & 15);
+      const int e = t.block(b) + 16 * sw + (lane & 15);
       if (lane == 0) {
         const int now = (int)globaltimer_ns();
         *w.shared(2) = now;
@@ -898,7 +901,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   auto entry = [&](const Unit& u, int j) {
     Entry e{0, -1, 0u};
     if (j >= u.nb) return e;
-    const int pos = u.template work<kForward>(j) * kBN + 4 * lane;
+    const int pos = u.template work<kForward>(j) + 4 * lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       e.seen |= (pos + i <= u.template last_seen<kScored>() && (pos + i >= u.lo || pos + i < u.sinks) ? 1u : 0u) << i;
@@ -946,7 +949,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     const int4* src = reinterpret_cast<const int4*>(sm + C::kOffUnit + 48 * (i & 1));
     const int4 x = src[0], y = src[1], z = src[2];
     u.row0 = x.x; u.row1 = x.y; u.p_last = x.z; u.r = x.w;
-    u.lo = y.x; u.sinks = y.y; u.sink_blocks = y.z; u.win_block = y.w;
+    u.lo = y.x; u.sinks = y.y; u.sink_blocks = y.z; u.win_pos = y.w;
     u.b0 = z.x; u.nb = z.y; u.slot = z.z; u.live = z.w;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTEmpty + (i & 1)));
@@ -1185,7 +1188,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           // Rows behind the last token may never have been written, and a weight of
           // 0 times NaN is NaN: they are read as zeros.  (The other rows of a block
           // were written; one that is not finite costs the tile slow_rows.)
-          const int up = u.live - 2 - (u.template work<kForward>(j) * kBN + 4 * lane);
+          const int up = u.live - 2 - (u.template work<kForward>(j) + 4 * lane);
           if (up < 0) id.x = -1;
           if (up < 1) id.y = -1;
           if (up < 2) id.z = -1;
@@ -1291,7 +1294,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       int4* dst = reinterpret_cast<int4*>(sm + C::kOffUnit + 48 * (i & 1));
       if (lane == 0) {
         dst[0] = make_int4(x.row0, x.row1, x.p_last, x.r);
-        dst[1] = make_int4(x.lo, x.sinks, x.sink_blocks, x.win_block);
+        dst[1] = make_int4(x.lo, x.sinks, x.sink_blocks, x.win_pos);
         dst[2] = make_int4(x.b0, x.nb, x.slot, x.live);
         mbar_arrive(bar(kBarTFull + (i & 1)));
       }
@@ -1335,7 +1338,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           e1 = e2;
           e2 = entry(u, j + 3);
         } else {
-          const Rows4 x = lookup4<kScored>(p, u, u.template work<kForward>(j) * kBN + 4 * lane, bad);
+          const Rows4 x = lookup4<kScored>(p, u, u.template work<kForward>(j) + 4 * lane, bad);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             id[k] = x.id[k];
@@ -1476,11 +1479,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const int jump = kForward ? t->sink_blocks - t->b0 : t->b0 + nb - t->sink_blocks;
       for (int j = 0; j < nb; ++j, ++J, mr.next()) {
         const int buf = J & 1, m = mr.m;
-        const int e0 = blk * kBN + 32 * seg;             // this thread's first key
+        const int e0 = blk + 32 * seg;                   // this thread's first key
         if (j + 1 == jump)
-          blk = kForward ? t->win_block : t->sink_blocks - 1;
+          blk = kForward ? t->win_pos : (t->sink_blocks - 1) * kBN;
         else
-          blk += kForward ? 1 : -1;
+          blk += kForward ? kBN : -kBN;
         W.wait(bar(kBarMFull + m), mr.ph);
         uint32_t see = words[4 * m + seg];
         W.wait(bar(kBarSFull + buf), (J >> 1) & 1);
