@@ -572,12 +572,14 @@ constexpr float kCapNear = 256.f;
 // Scores s * cl (log2 units) capped, cap tanh(s cl / cap), and lowered by the distance.
 // With u = 2^(two_over_cap s cl) = exp(2 y), tanh(y) = 1 - 2 / (1 + u): two steps of the
 // special function unit, the sums and products packed, the bias on the way (a form of its
-// own for a cap without a bias made a longer kernel: 439 -> 450 us).  Error of tanh: rcp
-// 2^-23 and the sum 2^-24 of a quotient of at most 1, ex2 2^-21.5 times at most a quarter,
-// all twice: less than 2^-20.
+// own for a cap without a bias made a longer kernel: 439 -> 450 us).  kPairs: one
+// reciprocal for two keys, 1 / a = b / (a b), u up to 2^60, where tanh is 1 (bf16 rows,
+// documents 851 -> 841 us; E4M3 rows, whose softmax has more to issue, 425 -> 435 us).
+// Error of tanh: the reciprocal 2^-22 in pairs and the sum 2^-24 of a quotient of at most
+// 1, ex2 2^-21.5 times at most a quarter, all twice: less than 2^-20.
 // The bias of key k, side * (d0 + k) with side = -+slope, is added up in steps of two
 // from every eighth key's own product: off by at most 2^-22 of itself.
-template <bool kCap>
+template <bool kCap, bool kPairs>
 __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap, float two_over_cap,
                                             float side, float d0) {
   const float f = cl * two_over_cap, base = kCap ? cap : 0.f;
@@ -593,11 +595,21 @@ __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap,
     if (kCap) {
       float u0 = s[k], u1 = s[k + 1];
       fma2_bcast(u0, u1, f, 0.f);
-      u0 = ex2_approx(u0);
-      u1 = ex2_approx(u1);
-      add2(u0, u1, 1.f, 1.f);
-      s[k] = rcp_approx(u0);
-      s[k + 1] = rcp_approx(u1);
+      if (kPairs) {
+        u0 = ex2_approx(min_nan(u0, 60.f));
+        u1 = ex2_approx(min_nan(u1, 60.f));
+        add2(u0, u1, 1.f, 1.f);
+        const float r = rcp_approx(u0 * u1);
+        s[k] = u1;
+        s[k + 1] = u0;
+        fma2_bcast(s[k], s[k + 1], r, 0.f);
+      } else {
+        u0 = ex2_approx(u0);
+        u1 = ex2_approx(u1);
+        add2(u0, u1, 1.f, 1.f);
+        s[k] = rcp_approx(u0);
+        s[k + 1] = rcp_approx(u1);
+      }
     }
     fma2(s[k], s[k + 1], kCap ? -2.f * cap : cl, c0, c1);
   }
@@ -1561,9 +1573,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) s[k] = x[k];
           } else if (p.softcap > 0.f) {
-            near_scores<true>(s, cl, cap2, a.two_over_cap, side, d0);
+            near_scores<true, !kFp8>(s, cl, cap2, a.two_over_cap, side, d0);
           } else if (p.slopes) {
-            near_scores<false>(s, cl, 0.f, 0.f, side, d0);
+            near_scores<false, false>(s, cl, 0.f, 0.f, side, d0);
           }
           if (p.softcap > 0.f || p.slopes) cl = 1.f;
           // Where the row's own position lies inside of the segment, and its later keys

@@ -60,6 +60,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// The smaller of two; NaN where one of them is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float c;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
 // The largest of three (NaN operands are passed over).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
