@@ -277,7 +277,7 @@ struct ForkSpace {
   int32_t* open;       // [n] the block that pair i will write into, -1: none
   int32_t* len;        // [n] the child's length, -1: the pair is passed over
   int32_t* fresh;      // [n] columns to fill behind the length
-  int32_t* own;        // [n] 1: gets its own copy of `open`
+  int32_t* own;        // [n] 1: gets its own copy of `open`; and twice `fresh`
   int32_t* first;      // [n] its first place in `list`
   int32_t* src;        // [moves]
   int32_t* place;      // [moves] the destination's place in `list`
@@ -325,68 +325,94 @@ struct ForkParams {
   Carry c;
 };
 
-// Pair i: the child's new row, and the counts of what it lets go and takes.
-template <bool kWarp>
-__device__ __forceinline__ void share_pair(const ForkParams& p, int i) {
+// A pair as the later steps need it (ForkSpace).
+struct Pair {
+  int open, len, fresh;
+};
+
+// Pair i: the child's new row, and the counts of what it lets go and takes.  The loads of
+// a step that do not need one another's answers are on their way together; `ready` is
+// called before the first count changes.
+template <bool kWarp, class Ready>
+__device__ __forceinline__ Pair share_pair(const ForkParams& p, int i, Ready ready) {
+  using Q = Team<kWarp>;
+  constexpr int kAhead = 2;                            // columns of a thread read at once
   const Tables& t = p.t;
-  const int tid = Team<kWarp>::rank();
+  const int tid = Q::rank();
   const int child = p.children[i];
   int parent = p.parents ? p.parents[i] : child;
+  const uint32_t room = p.room ? (uint32_t)max(p.room[i], 0) : 0u;
   bool bad = child >= t.rows || parent >= t.rows;
-  const bool skip = child < 0 || child >= t.rows || named_later<kWarp>(p.children, i, p.n, child);
-  if (skip) {
-    if (tid == 0) {
-      p.s.open[i] = -1;
-      p.s.len[i] = -1;
-      p.s.fresh[i] = 0;
-      if (bad) bad_index(t.status);
-    }
-    return;
-  }
   if (parent >= t.rows) parent = -1;
-  const int B = t.block_size;
-  int64_t len = parent < 0 ? 0 : max(t.lens[parent], 0);
-  if (len > (int64_t)t.width * B) {
-    len = (int64_t)t.width * B;
-    bad = true;
-  }
-  const int have = (int)((len + B - 1) / B);
-  const int32_t* old_row = t.table + (int64_t)child * t.width;
+  const bool in = child >= 0 && child < t.rows;
+  const int32_t* old_row = t.table + (int64_t)(in ? child : 0) * t.width;
   const int32_t* new_row = t.table + (int64_t)max(parent, 0) * t.width;
-  int32_t* stage = p.s.stage + (int64_t)i * t.width;
-#pragma unroll 2
-  for (int c = tid; c < t.width; c += Team<kWarp>::kSize) {
-    const int was = old_row[c];
-    int now = c < have ? new_row[c] : -1;
-    if (now >= t.blocks) {
-      now = -1;
+  uint32_t len = parent < 0 ? 0u : (uint32_t)max(t.lens[parent], 0);
+  int was[kAhead], now[kAhead];
+  auto read = [&](int c0) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int c = c0 + k * Q::kSize;
+      was[k] = c < t.width ? old_row[c] : -1;
+      now[k] = c < t.width ? new_row[c] : -1;
+    }
+  };
+  read(tid);
+  const bool again = named_later<kWarp>(p.children, i, p.n, child);
+  Pair q{-1, -1, 0};
+  if (in && !again) {
+    const uint32_t B = (uint32_t)t.block_size;
+    if (len > (uint64_t)t.width * B) {
+      len = (uint32_t)((uint64_t)t.width * B);
       bad = true;
     }
-    stage[c] = now;
-    if (was == now) continue;
-    if (was >= 0 && was < t.blocks) atomicSub(t.ref_out + was, 1);
-    if (now >= 0) atomicAdd(t.ref_out + now, 1);
+    const uint32_t part = len % B;                     // positions in the last block, 0: full
+    const int have = (int)(len / B) + (part ? 1 : 0);
+    const uint32_t slack = part ? B - part : 0u;
+    int64_t end = have;
+    if (room > slack) end += (room - slack + (B - 1)) / B;
+    if (end > t.width) bad = true;
+    q.len = (int)len;
+    q.fresh = (int)min(end, (int64_t)t.width) - have;
+    if (room > 0 && part) {
+      q.open = new_row[have - 1];
+      if (q.open >= t.blocks) q.open = -1;
+    }
+    int32_t* stage = p.s.stage + (int64_t)i * t.width;
+    ready();
+    for (int c0 = tid; c0 < t.width; c0 += kAhead * Q::kSize) {
+      if (c0 != tid) read(c0);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int c = c0 + k * Q::kSize;
+        if (c >= t.width) break;
+        int b = c < have ? now[k] : -1;
+        if (b >= t.blocks) {
+          b = -1;
+          bad = true;
+        }
+        stage[c] = b;
+        if (was[k] == b) continue;
+        if (was[k] >= 0 && was[k] < t.blocks) atomicSub(t.ref_out + was[k], 1);
+        if (b >= 0) atomicAdd(t.ref_out + b, 1);
+      }
+    }
+  } else {
+    ready();
   }
   if (tid == 0) {
-    const int64_t room = p.room ? max(p.room[i], 0) : 0;
-    const int64_t end = (len + room + B - 1) / B;
-    if (end > t.width) bad = true;
-    int open = -1;
-    if (room > 0 && len % B != 0) {
-      open = new_row[have - 1];
-      if (open < 0 || open >= t.blocks) open = -1;
-    }
-    p.s.open[i] = open;
-    p.s.len[i] = (int)len;
-    p.s.fresh[i] = (int)min(end, (int64_t)t.width) - have;
+    p.s.open[i] = q.open;
+    p.s.len[i] = q.len;
+    p.s.fresh[i] = q.fresh;
   }
   if (bad) bad_index(t.status);
+  return q;
 }
 
 __global__ void __launch_bounds__(kRowThreads) smla_fork_share_kernel(const ForkParams p) {
   wait_before();
   allow_next();
-  share_pair<false>(p, (int)blockIdx.x);
+  share_pair<false>(p, (int)blockIdx.x, [] {});
 }
 
 // Inclusive sum over a CTA's threads in two words of one; the total to `all`.
@@ -412,8 +438,10 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* sums, long
 }
 
 // One cluster: which rows get a copy of their last block, and the free blocks.
-// kSmall: the carrying and sharing too.  What other CTAs of the cluster wrote is read
-// past L1.
+// kSmall: the carrying and sharing too, a warp per pair, and each warp counts the pairs
+// before its own instead of a scan over all.  What other CTAs of the cluster wrote is
+// read past L1.
+constexpr int kSmallPairs = 1024;
 template <bool kSmall>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads, 1)
 smla_fork_take_kernel(const ForkParams p) {
@@ -425,62 +453,107 @@ smla_fork_take_kernel(const ForkParams p) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int id = (int)blockIdx.x * kScanThreads + tid, warp = id >> 5;
   __shared__ long long sums[32];
+  Pair mine{-1, -1, 0};                                // pair `warp` (kSmall)
   if constexpr (kSmall) {
     carry(p.c, id, kCluster * kScanThreads);
-    cluster_sync();
-    for (int i = warp; i < p.n; i += kScanWarps) share_pair<true>(p, i);
+    // (the counts have to be in place before the first of them changes)
+    bool synced = p.c.n[2] == 0;
+    auto ready = [&] {
+      if (!synced) cluster_sync();
+      synced = true;
+    };
+    if (warp < p.n) mine = share_pair<true>(p, warp, ready);
+    ready();
+    for (int i = warp + kScanWarps; i < p.n; i += kScanWarps) share_pair<true>(p, i, ready);
     cluster_sync();
   }
   // A block that is written by some of its holders: of the writers all but the first
   // copy it; where somebody else holds it too, the first as well.
+  auto pair_at = [&](int i) {
+    if (kSmall && i == warp) return mine;
+    return Pair{__ldcg(s.open + i), __ldcg(s.len + i), __ldcg(s.fresh + i)};
+  };
   for (int i = warp; i < p.n; i += kScanWarps) {
-    const int open = __ldcg(s.open + i);
+    const Pair q = pair_at(i);
     int own = 0;
-    if (open >= 0) {
+    if (q.open >= 0) {
+      const int ref = __ldcg(t.ref_out + q.open);
       int writers = 0, before = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int j = lane; j < p.n; j += 32) {
-        const bool same = __ldcg(s.open + j) == open;
+        const bool same = __ldcg(s.open + j) == q.open;
         writers += same ? 1 : 0;
         before += same && j < i ? 1 : 0;
       }
       writers = warp_sum(writers);
-      own = __any_sync(0xffffffffu, before > 0) || __ldcg(t.ref_out + open) > writers ? 1 : 0;
+      own = __any_sync(0xffffffffu, before > 0) || ref > writers ? 1 : 0;
     }
-    if (lane == 0) s.own[i] = own;
+    if (lane == 0) s.own[i] = own | q.fresh << 1;
   }
   const Range range = warp_range(t.blocks, warp);
-  const int mine = count_range(t.ref_out, range, [](int r) { return r == 0; });
-  if (lane == 0) s.counts[warp] = mine;
+  const int free_here = count_range(t.ref_out, range, [](int r) { return r == 0; });
+  if (lane == 0) s.counts[warp] = free_here;
   cluster_sync();
   // Each pair's place in the list of the blocks taken, and its move's number.
-  if (blockIdx.x == 0) {
-    long long carried = 0;                             // moves << 32 | blocks
-    for (int i0 = 0; i0 < p.n; i0 += kScanThreads) {
-      const int i = i0 + tid;
-      const int own = i < p.n ? __ldcg(s.own + i) : 0;
-      const long long x =
-          i < p.n ? ((long long)own << 32) + own + __ldcg(s.fresh + i) : 0ll;
-      long long all;
-      const long long at = carried + cta_scan(x, sums, all) - x;
-      carried += all;
-      if (i >= p.n) continue;
-      const int place = (int)(at & 0xffffffffll), m = (int)(at >> 32);
-      s.first[i] = place;
-      if (own) {
-        s.src[m] = __ldcg(s.open + i);
-        s.place[m] = place;
-        s.rows[m] = __ldcg(s.len + i) % t.block_size;
+  const int2 base = warp_base(s.counts, warp);
+  auto place = [&](int i, int cost, int at, int m) {
+    s.first[i] = at;
+    if (cost & 1) {
+      const Pair q = pair_at(i);
+      s.src[m] = q.open;
+      s.place[m] = at;
+      s.rows[m] = (int)((uint32_t)q.len % (uint32_t)t.block_size);
+      // (a block that is copied keeps a holder: its count was above the copies made)
+      atomicSub(t.ref_out + q.open, 1);
+    }
+  };
+  int wanted;
+  if (kSmall) {
+    wanted = 0;
+    int moves = 0;
+    for (int i = warp; i < p.n || i == warp; i += kScanWarps) {
+      int blocks = 0, copies = 0, at = 0, m = 0, cost = 0;
+#pragma unroll 8
+      for (int j = lane; j < p.n; j += 32) {
+        const int x = __ldcg(s.own + j), need = (x & 1) + (x >> 1);
+        blocks += need;
+        copies += x & 1;
+        at += j < i ? need : 0;
+        m += j < i ? x & 1 : 0;
+        if (j == i) cost = x;
+      }
+      wanted = warp_sum(blocks);
+      moves = warp_sum(copies);
+      if (i >= p.n) break;
+      at = warp_sum(at);
+      m = warp_sum(m);
+      cost = warp_sum(cost);
+      if (lane == 0) place(i, cost, at, m);
+    }
+    if (id == 0) {
+      s.head[0] = wanted;
+      s.head[1] = moves;
+    }
+  } else {
+    if (blockIdx.x == 0) {
+      long long carried = 0;                           // moves << 32 | blocks
+      for (int i0 = 0; i0 < p.n; i0 += kScanThreads) {
+        const int i = i0 + tid;
+        const int x = i < p.n ? __ldcg(s.own + i) : 0;
+        const long long y = ((long long)(x & 1) << 32) + (x & 1) + (x >> 1);
+        long long all;
+        const long long at = carried + cta_scan(y, sums, all) - y;
+        carried += all;
+        if (i < p.n) place(i, x, (int)(at & 0xffffffffll), (int)(at >> 32));
+      }
+      if (tid == 0) {
+        s.head[0] = (int)(carried & 0xffffffffll);
+        s.head[1] = (int)(carried >> 32);
       }
     }
-    if (tid == 0) {
-      s.head[0] = (int)(carried & 0xffffffffll);
-      s.head[1] = (int)(carried >> 32);
-    }
+    cluster_sync();
+    wanted = __ldcg(s.head);
   }
-  cluster_sync();
-  const int wanted = __ldcg(s.head);
-  const int2 base = warp_base(s.counts, warp);
   int rank = base.x;
   for (int b0 = range.lo; b0 < range.hi && rank < wanted; b0 += 32) {
     const int b = b0 + lane;
@@ -493,9 +566,6 @@ smla_fork_take_kernel(const ForkParams p) {
     }
     rank += __popc(votes);
   }
-  // (a block that is copied keeps a holder: its count was above the copies made)
-  for (int i = id; i < p.n; i += kCluster * kScanThreads)
-    if (__ldcg(s.own + i)) atomicSub(t.ref_out + __ldcg(s.open + i), 1);
   if (id == 0) {
     s.head[2] = base.y;
     if (p.missing) *p.missing = max(wanted - base.y, 0);
@@ -523,8 +593,8 @@ __global__ void __launch_bounds__(kCopyThreads) smla_fork_write_kernel(
   const int i = bid, len = s.len[i];
   if (len < 0) return;
   const int child = p.f.children[i];
-  const int have = (int)(((int64_t)len + t.block_size - 1) / t.block_size);
-  const int own = s.own[i], fresh = s.fresh[i], first = s.first[i];
+  const int have = (int)(((uint32_t)len + (uint32_t)(t.block_size - 1)) / (uint32_t)t.block_size);
+  const int own = s.own[i] & 1, fresh = s.fresh[i], first = s.first[i];
   const int got = s.head[2];
   const int32_t* stage = s.stage + (int64_t)i * t.width;
   int32_t* row = t.table_out + (int64_t)child * t.width;
@@ -715,7 +785,7 @@ cudaError_t launch_fork(const Pool& pool, const Tables& t, const int32_t* parent
   w.f = ForkParams{t, fork_space(workspace, n, t.width, t.blocks, &words), parents, children,
                    room, missing, n, carried};
   cudaError_t e = cudaSuccess;
-  if (most_of(carried) + (int64_t)n * t.width <= kSmallWords) {
+  if (n <= kSmallPairs && most_of(carried) + (int64_t)n * t.width <= kSmallWords) {
     e = launch_early(smla_fork_take_kernel<true>, kCluster, kScanThreads, 0, stream, w.f);
   } else {
     e = launch_carry(carried, stream);
