@@ -512,29 +512,30 @@ def _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows, num
             d_qk, S, block_size, block_stride_rows), (caches, scales)
 
 
-def _int32(t, what, shape, index):
-    """The address of a contiguous int32 tensor of this shape (None: NULL)."""
-    import torch
+def _int32(t, what, n, index, i32):
+    """The address of a contiguous int32 tensor of n elements (None: NULL).  (Its count
+    alone is looked at: a torch.Size costs as much as the rest of a check.)"""
     if t is None:
         return None
-    if not (t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and
-            t.get_device() == index):
-        raise ValueError(f"{what} must be a contiguous int32 tensor {list(shape)} on the inputs' "
-                         "device")
+    if t.dtype is not i32 or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of {n} elements on the "
+                         "inputs' device")
     return t.data_ptr()
 
 
-def _table_args(block_table, out_block_table, refcount, out_refcount, index):
+def _table_args(block_table, out_block_table, refcount, out_refcount, index, i32):
     """The C arguments (table, table out, rows, width, counts, counts out, blocks)."""
-    shape, blocks = block_table.shape, refcount.shape
-    if len(shape) != 2 or len(blocks) != 1:
+    shape = block_table.shape
+    if len(shape) != 2 or refcount.dim() != 1:
         raise ValueError("block_table must be [rows, stride] and refcount [blocks]")
-    table = _int32(block_table, "block_table", shape, index)
-    ref = _int32(refcount, "refcount", blocks, index)
+    R, width = shape
+    entries, blocks = R * width, refcount.numel()
+    table = _int32(block_table, "block_table", entries, index, i32)
+    ref = _int32(refcount, "refcount", blocks, index, i32)
     return (table, table if out_block_table is None else
-            _int32(out_block_table, "out_block_table", shape, index), shape[0], shape[1], ref,
+            _int32(out_block_table, "out_block_table", entries, index, i32), R, width, ref,
             ref if out_refcount is None else
-            _int32(out_refcount, "out_refcount", blocks, index), blocks[0])
+            _int32(out_refcount, "out_refcount", blocks, index, i32), blocks)
 
 
 def _own_memory(words, nbytes, workspace, like, index, stream):
@@ -566,13 +567,14 @@ def smla_cache_copy(kv_caches, kv_dtype, k_scales, src, dst, block_size, block_s
     kv_caches: a tensor [layers, slots, row], one cache [slots, row], or a list of
     caches; k_scales likewise for the formats whose scales belong to rows or blocks,
     else None."""
+    import torch
     lib = _lib or load()
     index, raw_stream = _device_stream(src, "src", stream)
     pool, _alive = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows,
                               num_slots, index)
-    n = src.shape[0]
-    code = lib.smla_cache_copy(*pool, _int32(src, "src", (n,), index),
-                               _int32(dst, "dst", (n,), index), n, raw_stream)
+    n, i32 = src.numel(), torch.int32
+    code = lib.smla_cache_copy(*pool, _int32(src, "src", n, index, i32),
+                               _int32(dst, "dst", n, index, i32), n, raw_stream)
     if code:
         raise SmlaError(code, "smla_cache_copy")
 
@@ -594,15 +596,15 @@ def smla_cache_fork(parents, children, room, seq_lens, block_table, refcount, bl
     (None: in place); kv_caches and k_scales as for ``smla_cache_copy``.
     Returns ``missing`` int32 [1]: how many blocks could not be had (a new one shares
     its memory with the call's workspace, where that is new too)."""
+    import torch
     lib = _lib or load()
     index, raw_stream = _device_stream(children, "children", stream)
     pool, _alive = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows,
                               num_slots, index)
-    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
-    n, R = children.shape[0], tables[2]
-    pairs = (_int32(parents, "parents", (n,), index), _int32(children, "children", (n,), index),
-             _int32(room, "room", (n,), index), n)
-    lens = _int32(seq_lens, "seq_lens", (R,), index)
+    i32 = torch.int32
+    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index, i32)
+    n, R = children.numel(), tables[2]
+    lens = _int32(seq_lens, "seq_lens", R, index, i32)
     memory, ws, nbytes = _own_memory(
         1 if missing is None else 0,
         lib.smla_cache_fork_workspace_size(n, tables[3], tables[6]), workspace, children, index,
@@ -610,9 +612,10 @@ def smla_cache_fork(parents, children, room, seq_lens, block_table, refcount, bl
     if missing is None:
         missing = memory.narrow(0, 0, 1)
     code = lib.smla_cache_fork(
-        *pairs, lens, lens if out_seq_lens is None else
-        _int32(out_seq_lens, "out_seq_lens", (R,), index), *tables, *pool,
-        _int32(missing, "missing", (1,), index), ws, nbytes, raw_stream)
+        _int32(parents, "parents", n, index, i32), _int32(children, "children", n, index, i32),
+        _int32(room, "room", n, index, i32), n, lens, lens if out_seq_lens is None else
+        _int32(out_seq_lens, "out_seq_lens", R, index, i32), *tables, *pool,
+        _int32(missing, "missing", 1, index, i32), ws, nbytes, raw_stream)
     if code:
         raise SmlaError(code, "smla_cache_fork")
     return missing
@@ -624,13 +627,15 @@ def smla_cache_free(rows, begin, end, block_table, refcount, block_size, out_blo
     that lie in the positions [begin, end) (int32 [n], or None: from the first, to
     the last).  The results go to the ``out_`` tensors (None: in place).
     Returns (block_table, refcount) as they are after it."""
+    import torch
     lib = _lib or load()
     index, raw_stream = _device_stream(rows, "rows", stream)
-    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
-    n = rows.shape[0]
-    code = lib.smla_cache_free(_int32(rows, "rows", (n,), index),
-                               _int32(begin, "begin", (n,), index),
-                               _int32(end, "end", (n,), index), n, *tables, block_size,
+    i32 = torch.int32
+    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index, i32)
+    n = rows.numel()
+    code = lib.smla_cache_free(_int32(rows, "rows", n, index, i32),
+                               _int32(begin, "begin", n, index, i32),
+                               _int32(end, "end", n, index, i32), n, *tables, block_size,
                                raw_stream)
     if code:
         raise SmlaError(code, "smla_cache_free")
@@ -650,11 +655,13 @@ def smla_cache_compact(block_table, refcount, block_size, kv_caches, kv_dtype, k
     Arguments as for ``smla_cache_fork``.  Returns (block_map int32 [blocks]: the new
     number of each live block, -1 for free ones; num_live int32 [1]), new ones sharing
     their memory with a new workspace."""
+    import torch
     lib = _lib or load()
     index, raw_stream = _device_stream(block_table, "block_table", stream)
     pool, _alive = _pool_args(kv_caches, kv_dtype, k_scales, block_size, block_stride_rows,
                               num_slots, index)
-    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index)
+    i32 = torch.int32
+    tables = _table_args(block_table, out_block_table, refcount, out_refcount, index, i32)
     blocks = tables[6]
     own_map, own_live = block_map is None, num_live is None
     words = (blocks if own_map else 0) + (1 if own_live else 0)
@@ -665,8 +672,8 @@ def smla_cache_compact(block_table, refcount, block_size, kv_caches, kv_dtype, k
     if own_live:
         num_live = memory.narrow(0, words - 1, 1)
     code = lib.smla_cache_compact(*tables, *pool,
-                                  _int32(block_map, "block_map", (blocks,), index),
-                                  _int32(num_live, "num_live", (1,), index), ws, nbytes,
+                                  _int32(block_map, "block_map", blocks, index, i32),
+                                  _int32(num_live, "num_live", 1, index, i32), ws, nbytes,
                                   raw_stream)
     if code:
         raise SmlaError(code, "smla_cache_compact")
@@ -777,10 +784,10 @@ def smla_fwd_scored(q, kv_cache, kv_dtype, k_scale, query_start, seq_lens, block
                 slopes.is_contiguous() and slopes.get_device() == index):
             raise ValueError("slopes must be a contiguous fp32 tensor [h] on the inputs' device")
         slope = slopes.data_ptr()
-    T = (q.shape[0],)
+    T, i32 = q.shape[0], torch.int32
     code = lib.smla_fwd_scored(*args, sm_scale, softcap, slope,
-                               _int32(first_pos, "first_pos", T, index),
-                               _int32(last_pos, "last_pos", T, index), *ends, raw_stream)
+                               _int32(first_pos, "first_pos", T, index, i32),
+                               _int32(last_pos, "last_pos", T, index, i32), *ends, raw_stream)
     if code:
         raise SmlaError(code, "smla_fwd_scored")
     return out, lse
