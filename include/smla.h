@@ -335,8 +335,9 @@ SMLA_API smla_status smla_cache_append(
  * < 1, n < 0, num_slots < block_size, 0 < block_stride_rows < block_size, more
  * blocks than num_slots holds, NULL or misaligned pointers, among kv_caches and
  * k_scales too), SMLA_ERR_UNSUPPORTED (d_qk not 512 or 576, a format that d_qk does
- * not have, num_slots >= 2^31, num_rows > 2^24, n * (block_table_stride + 1) >=
- * 2^31), SMLA_ERR_WORKSPACE, SMLA_ERR_CUDA.  n = 0 is OK.
+ * not have, num_slots >= 2^31, num_rows > 2^24, more than 65536 rows named by a fork
+ * or a free, a fork's n * (block_table_stride + 1) >= 2^31), SMLA_ERR_WORKSPACE,
+ * SMLA_ERR_CUDA.  n = 0 is OK.
  *
  * smla_cache_copy — copy the rows, and the scales, of blocks src[i] to blocks
  * dst[i], 0 <= i < n, in every layer.

@@ -176,6 +176,9 @@ smla_status make_tables(const int32_t* block_table, int32_t* block_table_out, in
   return SMLA_OK;
 }
 
+// Rows that a fork or a free names: each looks at all the others (a name given twice).
+constexpr int kMaxPairs = 1 << 16;
+
 // The current device's status word.
 smla_status device_status_word(int** status) {
   std::lock_guard<std::mutex> lk(g_mutex);
@@ -615,7 +618,7 @@ smla_status smla_cache_copy(void* const* kv_caches, float* const* k_scales, int 
 }
 
 size_t smla_cache_fork_workspace_size(int n, int block_table_stride, int num_blocks) {
-  if (n < 1 || block_table_stride < 1 || num_blocks < 1 ||
+  if (n < 1 || n > kMaxPairs || block_table_stride < 1 || num_blocks < 1 ||
       (int64_t)n * ((int64_t)block_table_stride + 1) > 0x7FFFFFFFLL)
     return 0;
   return smla::fork_workspace_bytes(n, block_table_stride, num_blocks);
@@ -642,7 +645,8 @@ smla_status smla_cache_fork(const int32_t* parents, const int32_t* children, con
   if (n < 0 || num_blocks > blocks || !seq_lens || !seq_lens_out || !aligned(seq_lens, 4) ||
       !aligned(seq_lens_out, 4) || (missing && !aligned(missing, 4)))
     return SMLA_ERR_INVALID_ARG;
-  if ((int64_t)n * ((int64_t)block_table_stride + 1) > 0x7FFFFFFFLL) return SMLA_ERR_UNSUPPORTED;
+  if (n > kMaxPairs || (int64_t)n * ((int64_t)block_table_stride + 1) > 0x7FFFFFFFLL)
+    return SMLA_ERR_UNSUPPORTED;
   if (n > 0) {
     if (!children || !aligned(children, 4) || (parents && !aligned(parents, 4)) ||
         (room && !aligned(room, 4)))
@@ -673,6 +677,7 @@ smla_status smla_cache_free(const int32_t* rows, const int32_t* begin, const int
   if (n < 0 || (n > 0 && (!rows || !aligned(rows, 4))) || (begin && !aligned(begin, 4)) ||
       (end && !aligned(end, 4)))
     return SMLA_ERR_INVALID_ARG;
+  if (n > kMaxPairs) return SMLA_ERR_UNSUPPORTED;
   if ((st = device_status_word(&t.status)) != SMLA_OK) return st;
   return smla::launch_block_free(t, rows, begin, end, n, stream) == cudaSuccess ? SMLA_OK
                                                                                 : SMLA_ERR_CUDA;

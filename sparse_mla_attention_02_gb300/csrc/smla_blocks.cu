@@ -395,6 +395,7 @@ __device__ __forceinline__ Pair share_pair(const ForkParams& p, int i, Ready rea
           bad = true;
         }
         stage[c] = b;
+        bad |= was[k] >= t.blocks;
         if (was[k] == b) continue;
         if (was[k] >= 0 && was[k] < t.blocks) atomicSub(t.ref_out + was[k], 1);
         if (b >= 0) atomicAdd(t.ref_out + b, 1);

@@ -86,7 +86,7 @@ def test_copy_refusals(lib, kw, code):
     (dict(n=-1), 1), (dict(NB=11), 1), (dict(lens=None), 1), (dict(lens_out=None), 1),
     (dict(lens=A + 2), 1), (dict(missing=A + 2), 1), (dict(children=None), 1),
     (dict(children=A + 2), 1), (dict(parents=A + 2), 1), (dict(room=A + 1), 1),
-    (dict(n=1 << 30), 2), (dict(), 6), (dict(ws=A, ws_n=8), 6),
+    (dict(n=1 << 30), 2), (dict(n=65537), 2), (dict(n=65536, stride=1 << 15), 2), (dict(), 6), (dict(ws=A, ws_n=8), 6),
     (dict(ws=A + 4, ws_n=1 << 20), 1)])
 def test_fork_refusals(lib, kw, code):
     assert fork(lib, **kw) == code
@@ -94,7 +94,7 @@ def test_fork_refusals(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", TABLE_BAD + [
     (dict(block=0), 1), (dict(n=-1), 1), (dict(rows=None), 1), (dict(rows=A + 2), 1),
-    (dict(begin=A + 2), 1), (dict(end=A + 2), 1)])
+    (dict(begin=A + 2), 1), (dict(end=A + 2), 1), (dict(n=65537), 2)])
 def test_free_refusals(lib, kw, code):
     assert free(lib, **kw) == code
 
@@ -109,7 +109,7 @@ def test_compact_refusals(lib, kw, code):
 def test_nothing_to_do_and_sizes(lib):
     assert copy(lib, n=0, src=None, dst=None) == 0
     size = lib.smla_cache_fork_workspace_size
-    assert size(0, 4, 10) == size(3, 0, 10) == size(3, 4, 0) == size(1 << 30, 4, 10) == 0
+    assert size(0, 4, 10) == size(3, 0, 10) == size(3, 4, 0) == size(65537, 4, 10) == 0
     assert size(3, 4, 10) > 3 * 4 * 4 and size(3, 4, 10) % 16 == 0
     assert lib.smla_cache_compact_workspace_size(0) == 0
     assert lib.smla_cache_compact_workspace_size(10) >= 2 * 4 * 5

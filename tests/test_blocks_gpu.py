@@ -388,3 +388,27 @@ def test_binding_refusals(cuda_lib):
         smla.smla_cache_free(one, i32([1, 2]), None, table, ref, 16)
     with pytest.raises(ValueError):
         smla.smla_cache_compact(table, ref, 16, cache, P.BLOCK, scale, block_map=ref[:3])
+
+
+def test_fork_and_free_of_most_rows(cuda_lib):
+    """65536 rows at once (the most that a call names), each its own."""
+    smla = cuda_lib
+    R = 65536
+    table = torch.arange(R, dtype=torch.int32, device="cuda")[:, None].repeat(1, 2)
+    table[:, 1] = -1
+    lens = torch.ones(R, dtype=torch.int32, device="cuda")
+    ref = torch.zeros(2 * R, dtype=torch.int32, device="cuda")
+    ref[:R] = 1
+    cache = torch.zeros((2 * R * 2, 512), dtype=torch.uint8, device="cuda")
+    names = torch.randperm(R, device="cuda").to(torch.int32)
+    parents = names ^ 1                                   # pairs of rows trade places
+    room = torch.full_like(names, 2)
+    missing = smla.smla_cache_fork(parents, names, room, lens, table, ref, 2, cache, P.E4M3)
+    assert int(missing) == 0
+    # a row keeps its parent's only block and gets one free block, in the order of the pairs
+    assert torch.equal(table[names.long(), 0], parents)
+    assert torch.equal(table[names.long(), 1], torch.arange(R, 2 * R, dtype=torch.int32,
+                                                            device="cuda"))
+    assert bool((ref == 1).all())
+    smla.smla_cache_free(names, None, None, table, ref, 2)
+    assert bool((ref == 0).all()) and bool((table == -1).all())
