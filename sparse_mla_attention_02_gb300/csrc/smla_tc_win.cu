@@ -226,6 +226,16 @@ static_assert(offsetof(Unit, hi) == 48, "three 16-byte words are handed on");
 
 constexpr int kWarpPv = 12;                // issues PV
 
+// bf16 rows: cache blocks whose boxes have fewer rows than this are copied row by row by
+// the loaders' threads, the others as boxes by TMA.  A TMA copy of a small box takes 27
+// cycles or more for its 128-byte rows, whoever issues it, and a block of keys is up to
+// 272 of them a CTA; four warps with 16-byte copies bring the same in about half the time.
+// Decode of 64 tokens / documents of 1500 tokens, boxes -> rows: blocks of 1 row 400 ->
+// 185 / 2139 -> 1184 us, of 4 363 -> 171 / 1943 -> 1059, of 16 183 -> 171 / 1087 -> 1060;
+// of 32 156 -> 179 / 974 -> 1134 (boxes), of 64 118 / 844 (boxes).  E4M3 rows have no
+// warps to spare: two of their loaders were slower than the boxes (763 -> 1041 us).
+constexpr int kRowsBox = 32;
+
 template <bool kFp8>
 struct Cfg {
   static constexpr int kThreads = kFp8 ? 512 : 416;
@@ -572,14 +582,14 @@ constexpr float kCapNear = 256.f;
 // Scores s * cl (log2 units) capped, cap tanh(s cl / cap), and lowered by the distance.
 // With u = 2^(two_over_cap s cl) = exp(2 y), tanh(y) = 1 - 2 / (1 + u): two steps of the
 // special function unit, the sums and products packed, the bias on the way (a form of its
-// own for a cap without a bias made a longer kernel: 439 -> 450 us).  kPairs: one
-// reciprocal for two keys, 1 / a = b / (a b), u up to 2^60, where tanh is 1 (bf16 rows,
-// documents 851 -> 841 us; E4M3 rows, whose softmax has more to issue, 425 -> 435 us).
-// Error of tanh: the reciprocal 2^-22 in pairs and the sum 2^-24 of a quotient of at most
-// 1, ex2 2^-21.5 times at most a quarter, all twice: less than 2^-20.
+// own for a cap without a bias made a longer kernel: 439 -> 450 us).  One reciprocal for
+// two keys, 1 / a = b / (a b), saves 1 % on bf16 rows and gives it back where a key that
+// is not seen has to be kept from its neighbour.  Error of tanh: rcp 2^-23 and the sum
+// 2^-24 of a quotient of at most 1, ex2 2^-21.5 times at most a quarter, all twice: less
+// than 2^-20.
 // The bias of key k, side * (d0 + k) with side = -+slope, is added up in steps of two
 // from every eighth key's own product: off by at most 2^-22 of itself.
-template <bool kCap, bool kPairs>
+template <bool kCap>
 __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap, float two_over_cap,
                                             float side, float d0) {
   const float f = cl * two_over_cap, base = kCap ? cap : 0.f;
@@ -595,21 +605,11 @@ __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap,
     if (kCap) {
       float u0 = s[k], u1 = s[k + 1];
       fma2_bcast(u0, u1, f, 0.f);
-      if (kPairs) {
-        u0 = ex2_approx(min_nan(u0, 60.f));
-        u1 = ex2_approx(min_nan(u1, 60.f));
-        add2(u0, u1, 1.f, 1.f);
-        const float r = rcp_approx(u0 * u1);
-        s[k] = u1;
-        s[k + 1] = u0;
-        fma2_bcast(s[k], s[k + 1], r, 0.f);
-      } else {
-        u0 = ex2_approx(u0);
-        u1 = ex2_approx(u1);
-        add2(u0, u1, 1.f, 1.f);
-        s[k] = rcp_approx(u0);
-        s[k + 1] = rcp_approx(u1);
-      }
+      u0 = ex2_approx(u0);
+      u1 = ex2_approx(u1);
+      add2(u0, u1, 1.f, 1.f);
+      s[k] = rcp_approx(u0);
+      s[k + 1] = rcp_approx(u1);
     }
     fma2(s[k], s[k + 1], kCap ? -2.f * cap : cl, c0, c1);
   }
@@ -829,11 +829,16 @@ static __device__ __noinline__ void slow_rows(const WinParams& p, const Unit& t,
 }
 
 // kScored: scores are capped, lowered with the distance, or seen through a span per
-// token.  (Both in one kernel would cost the plain call.)
-template <bool kFp8, bool kScored>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
+// token.  kByRow: the loaders' threads copy the cache's rows themselves, 16 bytes each,
+// for cache blocks of few rows (kRowsBox): 4, four positions share a block; 1, they need
+// not.  (In one kernel either would cost the other calls 2 to 15 %: the roles share one
+// instruction cache.)
+template <bool kFp8, bool kScored, int kByRow>
+__global__ void __cluster_dims__(2, 1, 1)
+__launch_bounds__(kByRow != 0 ? 512 : Cfg<kFp8>::kThreads, 1)
 smla_window_kernel(const __grid_constant__ WinArgs a) {
   using C = Cfg<kFp8>;
+  static_assert(!kFp8 || kByRow == 0, "bf16 rows");
   constexpr bool kForward = kFp8 && !kScored;          // Unit::work
   extern __shared__ __align__(1024) uint8_t sm[];
   const WinParams& p = a.p;
@@ -851,11 +856,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
   // warps that read first execute, and the others pass the barrier behind them.
   if (tid == 32) {
     for (int i = 0; i < kKGroups; ++i) {
-      mbar_init(bar(kBarKFull + i), 1);
+      mbar_init(bar(kBarKFull + i), kByRow != 0 ? 4 : 1);  // (both CTAs' two loaders)
       mbar_init(bar(kBarKEmpty + i), 1);
     }
     for (int i = 0; i < kVUnits; ++i) {
-      mbar_init(bar(kBarVFull + i), 1);
+      mbar_init(bar(kBarVFull + i), kByRow != 0 ? 4 : 1);
       mbar_init(bar(kBarVEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -868,13 +873,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     if (kFp8) mbar_init(bar(kBarQScale), 3);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(bar(kBarMFull + i), 1);
-      mbar_init(bar(kBarMEmpty + i), 10);              // softmax, loaders
+      mbar_init(bar(kBarMEmpty + i), kByRow != 0 ? 12 : 10); // softmax, loaders
     }
     mbar_init(bar(kBarQEmpty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarTFull + i), 1);
       // those, the even CTA's issuers, E4M3: the warps that split Q
-      mbar_init(bar(kBarTEmpty + i), 10 + (r == 0 ? 2 : 0) + (kFp8 ? 3 : 0));
+      mbar_init(bar(kBarTEmpty + i), (kByRow != 0 ? 12 : 10) + (r == 0 ? 2 : 0) + (kFp8 ? 3 : 0));
       mbar_init(bar(kBarCFull + i), 1);
       mbar_init(bar(kBarCEmpty + i), 2);
     }
@@ -925,6 +930,24 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     }
     return e;
   };
+  // kByRow == 1: each position has its own.
+  struct Entry4 {
+    Entry at[4];
+  };
+  auto entry4 = [&](const Unit& u, int j) {
+    Entry4 e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e.at[i] = Entry{0, -1, 0u};
+      if (j >= u.nb) continue;
+      const int pos = u.template work<kForward>(j) + 4 * lane + i;
+      if (pos > u.template last_seen<kScored>() || (pos < u.lo && pos >= u.sinks)) continue;
+      const int page = a.shift >= 0 ? pos >> a.shift : pos / p.b.block_size;
+      e.at[i] = Entry{pos - page * p.b.block_size, batch_block(p.b, u.r, page, bad), 1u};
+    }
+    return e;
+  };
+  Entry4 f0, f1, f2;
   Entry e0{0, -1, 0u}, e1 = e0, e2 = e0;
   if (warp == 3) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -935,7 +958,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     } else {
       next = find_unit<kScored>(p, (int64_t)(blockIdx.x >> 1));
     }
-    if (a.quad) {
+    if constexpr (kByRow == 1) {
+      f0 = entry4(next, 0);
+      f1 = entry4(next, 1);
+      f2 = entry4(next, 2);
+    } else if (kByRow == 4 || a.quad) {
       e0 = entry(next, 0);
       e1 = entry(next, 1);
       e2 = entry(next, 2);
@@ -981,6 +1008,35 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
     if (per == 0) return false;
     if ((absent & mine) == mine) id.x = -64;
     return (there & mine) == mine || (absent & mine) == mine;
+  };
+  // kByRow: lane l copies 16-byte chunk l % 8 of the rows 4 i + l / 8 of a tile (64 rows
+  // of 128 bytes, chunks permuted as TMA would).  A tile's copies are signalled to the MMA
+  // issuer's barrier once they have landed: behind the next tile's, or before the loader
+  // waits for anything.
+  uint32_t waiting = 0;                                // that barrier
+  auto signal_rows = [&] {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_signal_remote(waiting);
+  };
+  auto flush_rows = [&] {
+    if (waiting == 0) return;
+    cp_async_wait_group<0>();
+    signal_rows();
+    waiting = 0;
+  };
+  auto next_rows = [&](uint32_t full) {
+    cp_async_commit();
+    if (waiting != 0) {
+      cp_async_wait_group<1>();
+      signal_rows();
+    }
+    waiting = full;
+  };
+  auto wait_rows = [&](uint32_t b, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
+    flush_rows();
+    W.wait(b, parity);
   };
   // Blocks are counted across units (J): a barrier's n-th phase is block n's.
 
@@ -1090,6 +1146,108 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       __syncwarp();
       W.drain(bar(kBarDrain + 1), 0);
     }
+  } else if (kByRow != 0 && (warp == 1 || warp == 13)) {
+    // ---- K loads row by row: each of two warps has 32 of this CTA's 64 keys --
+    const int half = warp == 13, row = lane >> 3;
+    const uint32_t kfull0 = bar0(kBarKFull);
+    const uint32_t tile = sb + C::kOffK + 4096u * half + 128u * row + (((lane & 7) ^ row) << 4);
+    const uint8_t* kv = static_cast<const uint8_t*>(p.kv) + 16 * (lane & 7);
+    MetaRing mr;
+    Unit u;
+    int q = 0, J = 0;
+    for (int i = 0; take_unit(i, u); ++i) {
+      if (half == 0 && u.nb > 0) {
+        if (q >= 1) W.wait(bar(kBarQEmpty), (q - 1) & 1);
+        if (stopped()) break;
+        if (lane == 0) {
+          if (r == 0) mbar_arrive_expect_tx(bar(kBarQFull), 2u * (uint32_t)a.atoms * kAtom);
+#pragma unroll 1
+          for (int c = 0; c < a.atoms; ++c)
+            tma_load_2d_pair(sb + C::kOffQ + c * kAtom, &a.q_map, 64 * c, u.row0 + 64 * (int)r,
+                             bar0(kBarQFull));
+        }
+        ++q;
+        __syncwarp();
+      }
+      for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
+        wait_rows(bar(kBarMFull + mr.m), mr.ph);
+        const uint8_t* src[8];
+        uint32_t bytes[8];
+        const int* ids =
+            reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * mr.m + 64 * r + 32 * half + row;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int id = ids[4 * k];
+          src[k] = kv + (int64_t)max(id, 0) * (2 * p.d_qk);
+          bytes[k] = id < 0 ? 0u : 16u;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
+#pragma unroll
+        for (int g = 0; g < kKGroups; ++g) {
+          if (J >= 1) wait_rows(bar(kBarKEmpty + g), (J - 1) & 1);
+          if (stopped()) break;
+#pragma unroll
+          for (int c = 3 * g; c < 3 * g + 3; ++c) {
+            if (c == 8 && a.atoms == 8) break;         // (rows of 512 channels)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              cp_async16((k & 1 ? tile ^ 64u : tile) + c * kAtom + 512u * k, src[k] + 128 * c,
+                         bytes[k]);
+          }
+          next_rows(kfull0 + 8u * g);
+        }
+        if (stopped()) break;
+      }
+      flush_rows();
+    }
+    flush_rows();
+    if (r == 0 && lane == 0 && q > 0) W.drain(bar(kBarQFull), (q - 1) & 1);
+    __syncwarp();
+  } else if (kByRow != 0 && (warp == 2 || warp == 14)) {
+    // ---- V loads row by row: this CTA's channels, 32 of each 64 keys ----------
+    const int half = warp == 14, row = lane >> 3;
+    const uint32_t vfull0 = bar0(kBarVFull);
+    const uint32_t tile = sb + C::kOffV + 4096u * half + 128u * row + (((lane & 7) ^ row) << 4);
+    const uint8_t* kv = static_cast<const uint8_t*>(p.kv) + 16 * (lane & 7) + 256 * (int)r;
+    MetaRing mr;
+    Unit u;
+    for (int i = 0, J = 0; take_unit(i, u); ++i) {
+      for (int j = 0; j < u.nb; ++j, ++J, mr.next()) {
+        wait_rows(bar(kBarMFull + mr.m), mr.ph);
+        const uint8_t* src[2][8];
+        uint32_t bytes[2][8];
+        const int* ids = reinterpret_cast<const int*>(sm + C::kOffIds) + kBN * mr.m;
+        // (rows behind the last token as zeros: see the copies by TMA)
+        const int up = u.live - 2 - u.template work<kForward>(j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int e = 64 * h + 32 * half + 4 * k + row, id = e <= up ? ids[e] : -1;
+            src[h][k] = kv + (int64_t)max(id, 0) * (2 * p.d_qk);
+            bytes[h][k] = id < 0 ? 0u : 16u;
+          }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarMEmpty + mr.m));
+#pragma unroll
+        for (int v = 0; v < kVUnits; ++v) {            // v = 2 n + key half
+          if (J >= 1) wait_rows(bar(kBarVEmpty + v), (J - 1) & 1);
+          if (stopped()) break;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              cp_async16((k & 1 ? tile ^ 64u : tile) + v * C::kVUnit + c * kAtom + 512u * k,
+                         src[v & 1][k] + 512 * (v >> 1) + 128 * c, bytes[v & 1][k]);
+          next_rows(vfull0 + 8u * v);
+        }
+        if (stopped()) break;
+      }
+      flush_rows();
+      if (stopped()) break;
+    }
+    flush_rows();
   } else if (warp == 1) {
     // ---- K loads: this CTA's 64 of each block's 128 keys --------------------
     const int groups = (a.atoms + C::kAtomsPerGroup - 1) / C::kAtomsPerGroup;
@@ -1339,7 +1497,20 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         int id[4];
         uint32_t seen = 0;
         float sc[4] = {1.f, 1.f, 1.f, 1.f};
-        if (a.quad) {
+        if constexpr (kByRow == 1) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const Entry& x = f0.at[k];
+            const int64_t row = (int64_t)x.blk * p.b.block_stride_rows + x.off;
+            const bool in = x.blk >= 0 && row < p.b.num_slots;
+            bad |= x.blk >= 0 && !in;
+            id[k] = in ? (int)row : -1;
+            seen |= in ? 1u << k : 0u;
+          }
+          f0 = f1;
+          f1 = f2;
+          f2 = entry4(u, j + 3);
+        } else if (kByRow == 4 || a.quad) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             id[k] = f.id[k];
@@ -1385,6 +1556,12 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll 1
           for (int c = 0; c < p.d_qk * C::kElem / 128; c += C::kAtomsPerGroup)
             tma_prefetch_3d(&a.k_map, 0, id[0], c);
+        if (kByRow != 0 && (lane >> 4) == (int)r)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (id[k] >= 0)
+              prefetch_l2(static_cast<const uint8_t*>(p.kv) + (int64_t)id[k] * (p.d_qk * C::kElem),
+                          (uint32_t)(p.d_qk * C::kElem));
         if (J >= kMeta) W.wait(bar(kBarMEmpty + m), mr.ph ^ 1);
         if (stopped()) break;
         __syncwarp();
@@ -1421,7 +1598,11 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         next = find_unit<kScored>(p, (int64_t)(first >> 1));
         ++n;
       }
-      if (a.quad) {
+      if constexpr (kByRow == 1) {
+        f0 = entry4(next, 0);
+        f1 = entry4(next, 1);
+        f2 = entry4(next, 2);
+      } else if (kByRow == 4 || a.quad) {
         e0 = entry(next, 0);
         e1 = entry(next, 1);
         e2 = entry(next, 2);
@@ -1573,9 +1754,9 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) s[k] = x[k];
           } else if (p.softcap > 0.f) {
-            near_scores<true, !kFp8>(s, cl, cap2, a.two_over_cap, side, d0);
+            near_scores<true>(s, cl, cap2, a.two_over_cap, side, d0);
           } else if (p.slopes) {
-            near_scores<false, false>(s, cl, 0.f, 0.f, side, d0);
+            near_scores<false>(s, cl, 0.f, 0.f, side, d0);
           }
           if (p.softcap > 0.f || p.slopes) cl = 1.f;
           // Where the row's own position lies inside of the segment, and its later keys
@@ -2076,7 +2257,7 @@ cudaError_t encode_columns(CUtensorMap* map, bool fp8, const void* base, int d, 
              : cudaErrorInvalidValue;
 }
 
-template <bool kFp8, bool kScored>
+template <bool kFp8, bool kScored, int kByRow = 0>
 cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   using C = Cfg<kFp8>;
   // (once per device: the attribute call costs as much as a launch)
@@ -2085,12 +2266,13 @@ cudaError_t launch(const WinArgs& a, unsigned ctas, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-    e = cudaFuncSetAttribute(smla_window_kernel<kFp8, kScored>,
+    e = cudaFuncSetAttribute(smla_window_kernel<kFp8, kScored, kByRow>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  return launch_early(smla_window_kernel<kFp8, kScored>, ctas, C::kThreads, C::kSmem, stream, a);
+  return launch_early(smla_window_kernel<kFp8, kScored, kByRow>, ctas,
+                      kByRow != 0 ? 512 : C::kThreads, C::kSmem, stream, a);
 }
 
 int64_t tile_numbers(int T, int h, int num_reqs) {
@@ -2167,12 +2349,16 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   if (ctas > 0x7FFFFFFFll || (int64_t)p.b.N * p.h > 0x7FFFFFFFll)
     return cudaErrorInvalidConfiguration;
   a.p = p;
-  if (p.softcap > 0.f || p.slopes || p.first_pos || p.last_pos)
-    e = fp8 ? launch<true, true>(a, (unsigned)ctas, stream)
-            : launch<false, true>(a, (unsigned)ctas, stream);
-  else
-    e = fp8 ? launch<true, false>(a, (unsigned)ctas, stream)
-            : launch<false, false>(a, (unsigned)ctas, stream);
+  const bool rows = !fp8 && a.box < kRowsBox;
+  const auto run = [&](auto scored) {
+    constexpr bool kScored = decltype(scored)::value;
+    if (fp8) return launch<true, kScored>(a, (unsigned)ctas, stream);
+    if (!rows) return launch<false, kScored>(a, (unsigned)ctas, stream);
+    return a.quad ? launch<false, kScored, 4>(a, (unsigned)ctas, stream)
+                  : launch<false, kScored, 1>(a, (unsigned)ctas, stream);
+  };
+  e = p.softcap > 0.f || p.slopes || p.first_pos || p.last_pos ? run(std::true_type())
+                                                               : run(std::false_type());
   if (e != cudaSuccess || p.workers == 0) return e;
   return launch_early(smla_window_merge_kernel, (unsigned)(p.b.N * p.h), 128 * p.merge_groups, 0,
                       stream, p);

@@ -165,14 +165,15 @@ def test_nothing_set_is_the_windowed_call(cuda_lib, fmt):
     assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:n], want[1][:n])
 
 
+@pytest.mark.parametrize("docs", [[30, 200, 410], [31, 207, 401]])
 @pytest.mark.parametrize("fmt", [P.BF16, P.BLOCK])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_unseen_positions_may_hold_anything(cuda_lib, fmt, bad):
+def test_unseen_positions_may_hold_anything(cuda_lib, fmt, bad, docs):
     """Rows of other documents, of the window's past and of other requests' ends that are
     not finite: the tokens that do not see them are as without them."""
     smla = cuda_lib
-    b = P.Batch([(20, 420), (1, 300), (60, 60)], 64, seed=11)
-    first, last = R.spans(b, docs=[30, 200, 410], prefix=8)
+    b = P.Batch([(20, 420), (1, 301), (61, 61)], 64, seed=11)
+    first, last = R.spans(b, docs=docs, prefix=7)
     q, cache, scale = make(b, fmt, 16, 576, 4)
     seen = torch.zeros(b.num_slots, dtype=torch.bool)
     for n, r, pos in b.tokens():
