@@ -232,8 +232,8 @@ constexpr int kWarpPv = 12;                // issues PV
 // 272 of them a CTA; four warps with 16-byte copies bring the same in about half the time.
 // Decode of 64 tokens / documents of 1500 tokens, boxes -> rows: blocks of 1 row 400 ->
 // 185 / 2139 -> 1184 us, of 4 363 -> 171 / 1943 -> 1059, of 16 183 -> 171 / 1087 -> 1060;
-// of 32 156 -> 179 / 974 -> 1134 (boxes), of 64 118 / 844 (boxes).  E4M3 rows have no
-// warps to spare: two of their loaders were slower than the boxes (763 -> 1041 us).
+// of 32 156 -> 179 / 974 -> 1134 (boxes), of 64 118 / 844 (boxes).  E4M3 rows, whose
+// softmax is what bounds them, lose by it (blocks of 1 row 763 -> 923 us, of 16 591 -> 856).
 constexpr int kRowsBox = 32;
 
 template <bool kFp8>
