@@ -1,7 +1,8 @@
 // smla_tc_win.cu — causal MLA attention over a paged latent cache, whole or
 // through a sliding window with first tokens that stay visible
 // (smla_fwd_window), for bf16 rows and for E4M3 rows with one scale per cache
-// block or per tensor.
+// block or per tensor; and with scores that are capped, lowered with the distance or
+// seen through a span of positions per token (smla_fwd_scored).
 //
 // Mathematics.  The row (token at position p, head) sees the positions
 //   V(p) = { e <= p : window == 0  or  e > p - window  or  e < sinks }
@@ -9,6 +10,14 @@
 // K_e[0:512], LSE = ln sum exp(s_e); no visible position gives (0, -inf).
 // One pass over the keys with a running maximum (raised lazily: O is rescaled
 // only when it grows by more than 2^8) and the running sum in fp32.
+// Scored: y = cap tanh(s / cap), then y - slope[head] |p - e|, and V(p) = { first[t] <= e
+// <= last[t], in the window, or e < sinks }.  A tile's keys run from its first token's
+// first position to its last token's last, in blocks that begin at a multiple of 64; a
+// segment of 32 keys costs a thread two more steps of the special function unit a key for
+// the cap, and half a packed product for the bias (near_scores).  That is hidden behind
+// the MMAs of bf16 rows but for 3 to 6 % (64 capped decode tokens of 4 to 8 thousand keys,
+// 128 heads, 119 us, uncapped 115); E4M3 rows, whose softmax is as long as their MMAs, pay
+// for it (a mixed batch 360 -> 388 us with a bias, 421 with a cap, 425 with both).
 //
 // Tile.  All heads share the key rows, and neighbouring tokens of a request
 // share most of them, so a tile is 128 consecutive rows of the flattened
@@ -79,7 +88,8 @@
 // the other); warps 1 and 2 load K and V; warp 3 takes units and looks up
 // each block's rows (validity, scales, row ids); warps 4..11 are the softmax: four
 // threads per row (TMEM lane half x column half), 32 keys each; with E4M3 rows
-// warps 13..15 split Q.
+// warps 13..15 split Q; cache blocks of few bf16 rows: warps 13 and 14 are a second K and
+// a second V loader.
 // Every wait is bounded, as in the sparse kernels (tc_common.cuh).
 //
 // Bound and measured.  A block is 2,176 cycles of MMAs (E4M3, five passes at twice
