@@ -20,8 +20,8 @@
 //
 // Bound: latency for the tables (the launches of a call follow one another, each
 // under the end of the one before), HBM for the rows of a pool.  Measured in a captured
-// graph, on two sets of inputs in turn: 280 bf16 blocks of 64 rows in 24 layers 123 us =
-// 8.0 TB/s read and written (part of it in L2), one block in 60 layers 2.5 us; eight samples
+// graph, on two sets of inputs in turn: 224 bf16 blocks of 64 rows in 24 layers 123 us =
+// 6.4 TB/s read and written (94 % of a copy's rate), one block in 60 layers 2.5 us; eight samples
 // of a prompt 10.9 us, 256 beams in 32 layers of E4M3 blocks 32.7 us (100 MB, of them 17 us
 // the tables); a finished sixteenth of 64 rows 4 us, 1024 rows' windows 11.3 us; half a
 // pool of 4000 blocks in 6 layers 138 us = 6.1 TB/s.
