@@ -625,29 +625,21 @@ __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap,
   }
 }
 
-// The scores of a large cap: where all of a warp's lie below an eighth of it the odd
-// series of tanh to y^9 (off by less than 2^-30 of x there), else the form above, off by
-// 2^-20 of a cap that some score has an eighth of.  Rare, and out of line: the roles
-// share one instruction cache.
-static __device__ __noinline__ void far_scores(float* x, float cl, float cap, float two_over_cap,
+// The scores of a large cap: below an eighth of it the odd series of tanh to y^9 (off by
+// less than 2^-30 of x there), from there on the form above, off by 2^-20 of the cap, less
+// than 2^-16 of the score.  Rare, and out of line: the roles share one instruction cache.
+static __device__ __noinline__ void far_scores(float* s, float cl, float cap, float two_over_cap,
                                                float side, float d0) {
-  float top = 0.f;
-#pragma unroll 8
-  for (int k = 0; k < 32; ++k) {
-    x[k] *= cl;
-    top = fmaxf(top, fabsf(x[k]));
-  }
   const float inv = __fdividef(1.f, cap);
-  const bool series = __all_sync(0xffffffffu, top * inv < 0.125f);
 #pragma unroll 8
   for (int k = 0; k < 32; ++k) {
-    const float y = x[k] * inv, z = y * y;
+    const float x = s[k] * cl, y = x * inv, z = y * y;
     float w = fmaf(z, 62.f / 2835.f, -17.f / 315.f);
     w = fmaf(z, w, 2.f / 15.f);
     w = fmaf(z, w, -1.f / 3.f);
-    const float near = fmaf(x[k] * z, w, x[k]);
-    const float u = ex2_approx(x[k] * two_over_cap);
-    x[k] = fmaf(side, d0 + (float)k, series ? near : fmaf(-2.f * cap, rcp_approx(1.f + u), cap));
+    const float near = fmaf(x * z, w, x);
+    const float far = fmaf(-2.f * cap, rcp_approx(1.f + ex2_approx(x * two_over_cap)), cap);
+    s[k] = fmaf(side, d0 + (float)k, fabsf(y) < 0.125f ? near : far);
   }
 }
 

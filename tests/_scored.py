@@ -61,10 +61,9 @@ def attend(q, rows, batch, sm_scale, window=0, sinks=0, cap=0.0, slopes=None, fi
         if cap:
             s = cap * torch.tanh(x / cap)
             # tanh = 1 - 2 / (1 + u): 2 (2^-23 + 2^-24 + 2^-21.5 / 4) < 2^-20 of the cap, up
-            # to a cap of 256; above only where a score of the block is an eighth of the cap
-            top = qd[n].abs().amax() * k.abs().sum(1).max() * abs(sm_scale)
-            err = err + 2.0 ** -20 * (cap if cap <= 256 else
-                                      cap if cap <= 8 * float(top) else x.abs())
+            # to a cap of 256; above only for scores of an eighth of the cap, whose tanh is
+            # 0.124 at least: 2^-20 / 0.124 < 2^-16 of the score (others: 2^-22, products)
+            err = err + (2.0 ** -20 * cap if cap <= 256 else 2.0 ** -16 * s.abs())
         if slopes is not None:
             bias = slopes.double()[:, None] * (e - pos).abs().double()
             s = s - bias

@@ -52,7 +52,7 @@ def run(smla, batch, fmt, h, d=576, seed=1, pow2=True, q_gain=2.0, window=0, sin
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("cap,gain", [(30.0, 8.0), (50.0, 2.0), (1.0, 30.0), (1e-3, 4.0),
-                                      (1e6, 4.0), (1e30, 30.0)])
+                                      (300.0, 200.0), (1e4, 3000.0), (1e6, 4.0), (1e30, 30.0)])
 def test_caps(cuda_lib, fmt, cap, gain):
     run(cuda_lib, P.Batch(RAGGED, 64, seed=3, pad=2), fmt, 16, cap=cap, q_gain=gain)
 
@@ -165,10 +165,11 @@ def test_nothing_set_is_the_windowed_call(cuda_lib, fmt):
     assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:n], want[1][:n])
 
 
-@pytest.mark.parametrize("docs", [[30, 200, 410], [31, 207, 401]])
+@pytest.mark.parametrize("docs,cap", [([30, 200, 410], 8.0), ([31, 207, 401], 8.0),
+                                      ([31, 207, 401], 1e6), ([31, 207, 401], 1e30)])
 @pytest.mark.parametrize("fmt", [P.BF16, P.BLOCK])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_unseen_positions_may_hold_anything(cuda_lib, fmt, bad, docs):
+def test_unseen_positions_may_hold_anything(cuda_lib, fmt, bad, docs, cap):
     """Rows of other documents, of the window's past and of other requests' ends that are
     not finite: the tokens that do not see them are as without them."""
     smla = cuda_lib
@@ -179,7 +180,7 @@ def test_unseen_positions_may_hold_anything(cuda_lib, fmt, bad, docs):
     for n, r, pos in b.tokens():
         for e in range(int(first[n]), int(last[n]) + 1):
             seen[b.slot(r, e)] = True
-    kw = dict(cap=8.0, slopes=slopes_of(16), first=first, last=last)
+    kw = dict(cap=cap, slopes=slopes_of(16), first=first, last=last)
     want = call(smla, b, fmt, q, cache, scale, 0.04, **kw)
     dirty = cache.clone()
     if fmt == P.BF16:
@@ -189,7 +190,7 @@ def test_unseen_positions_may_hold_anything(cuda_lib, fmt, bad, docs):
     got = call(smla, b, fmt, q, dirty, scale, 0.04, **kw)
     rows = P.dequant(cache, fmt, scale, b)
     b.fp8 = fmt != P.BF16
-    ref = R.attend(q, rows, b, 0.04, cap=8.0, slopes=kw["slopes"], first=first, last=last)
+    ref = R.attend(q, rows, b, 0.04, cap=cap, slopes=kw["slopes"], first=first, last=last)
     R.check(want[0], want[1], ref, b, fmt)
     R.check(got[0], got[1], ref, b, fmt)
 
