@@ -1880,14 +1880,23 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);  // PV(j - 1)
           __syncwarp();
           tc_fence_after();
+          // (bf16 rows, scored: 32 columns on their way at once, documents 850 -> 841 us; the
+          // others lose by the longer code, 8-bit decode 105 -> 108)
+          constexpr int kSixteens = kScored && !kFp8 ? 2 : 1;
 #pragma unroll 1
-          for (int c = 128 * wg; c < 128 * wg + 128; c += 16) {
-            uint32_t w[16];
-            tmem_ld16(tmem + lane_base + kColO + c, w);
+          for (int c = 128 * wg; c < 128 * wg + 128; c += 16 * kSixteens) {
+            uint32_t w[kSixteens][16];
+#pragma unroll
+            for (int x = 0; x < kSixteens; ++x)
+              tmem_ld16(tmem + lane_base + kColO + c + 16 * x, w[x]);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
-            tmem_st16(tmem + lane_base + kColO + c, w);
+            for (int x = 0; x < kSixteens; ++x) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                w[x][k] = __float_as_uint(__uint_as_float(w[x][k]) * alpha);
+              tmem_st16(tmem + lane_base + kColO + c + 16 * x, w[x]);
+            }
           }
           tmem_wait_st();
         }
