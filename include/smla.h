@@ -335,9 +335,9 @@ SMLA_API smla_status smla_cache_append(
  * < 1, n < 0, num_slots < block_size, 0 < block_stride_rows < block_size, more
  * blocks than num_slots holds, NULL or misaligned pointers, among kv_caches and
  * k_scales too), SMLA_ERR_UNSUPPORTED (d_qk not 512 or 576, a format that d_qk does
- * not have, num_slots >= 2^31, num_rows > 2^24, more than 65536 rows named by a fork
- * or a free, a fork's n * (block_table_stride + 1) >= 2^31), SMLA_ERR_WORKSPACE,
- * SMLA_ERR_CUDA.  n = 0 is OK.
+ * not have, num_slots >= 2^31, num_rows or block_table_stride > 2^24, more than
+ * 65536 rows named by a fork or a free, a fork's n * (block_table_stride + 1) >=
+ * 2^31), SMLA_ERR_WORKSPACE, SMLA_ERR_CUDA.  n = 0 is OK.
  *
  * smla_cache_copy — copy the rows, and the scales, of blocks src[i] to blocks
  * dst[i], 0 <= i < n, in every layer.
@@ -524,11 +524,11 @@ SMLA_API size_t smla_fwd_window_workspace_size(int num_reqs, int T, int h, int d
  *  max_seq_len  as there; where first_pos makes spans much shorter than the requests,
  *               rather a bound on the spans
  *  workspace    as there, smla_fwd_window_workspace_size(...) bytes
- * Every other argument, the results and the errors are those of smla_fwd_window (SMLA_ERR_INVALID_ARG for any other
- * softcap, too).  first_pos and last_pos of tokens behind
- * query_start[num_reqs] are not read.  y_e is within 2^-20 softcap of its value, for a
- * softcap above 256 within 2^-16 |y_e|, the bias within 2^-22 of itself.  With softcap = 0 and the
- * three pointers NULL the call is smla_fwd_window.
+ * Every other argument, the results and the errors are those of smla_fwd_window
+ * (SMLA_ERR_INVALID_ARG for any other softcap, too).  first_pos and last_pos of tokens
+ * behind query_start[num_reqs] are not read.  y_e is within 2^-20 softcap of its value,
+ * for a softcap above 256 within 2^-16 |y_e|, the bias within 2^-22 of itself.  With
+ * softcap = 0 and the three pointers NULL the call is smla_fwd_window.
  */
 SMLA_API smla_status smla_fwd_scored(
     const void* q, const void* kv_cache, int kv_dtype, const float* k_scale,

@@ -167,7 +167,7 @@ smla_status make_tables(const int32_t* block_table, int32_t* block_table_out, in
                         int num_blocks, int block_size, smla::Tables* t) {
   if (num_rows < 1 || block_table_stride < 1 || num_blocks < 1 || block_size < 1)
     return SMLA_ERR_INVALID_ARG;
-  if (num_rows > (1 << 24)) return SMLA_ERR_UNSUPPORTED;
+  if (num_rows > (1 << 24) || block_table_stride > (1 << 24)) return SMLA_ERR_UNSUPPORTED;
   for (const void* x : {(const void*)block_table, (const void*)block_table_out,
                         (const void*)refcount, (const void*)refcount_out})
     if (!x || !aligned(x, 4)) return SMLA_ERR_INVALID_ARG;

@@ -15,8 +15,8 @@
 // first position to its last token's last, in blocks that begin at a multiple of 64; a
 // segment of 32 keys costs a thread two more steps of the special function unit a key for
 // the cap, and half a packed product for the bias (near_scores).  That is hidden behind
-// the MMAs of bf16 rows but for 3 to 6 % (64 capped decode tokens of 4 to 8 thousand keys,
-// 128 heads, 119 us, uncapped 115); E4M3 rows, whose softmax is as long as their MMAs, pay
+// the MMAs of bf16 rows but for 3 to 7 % (64 capped decode tokens of 4 to 8 thousand keys,
+// 128 heads, 118 us, uncapped 115); E4M3 rows, whose softmax is as long as their MMAs, pay
 // for it (a mixed batch 360 -> 388 us with a bias, 421 with a cap, 425 with both).
 //
 // Tile.  All heads share the key rows, and neighbouring tokens of a request

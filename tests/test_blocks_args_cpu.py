@@ -71,6 +71,7 @@ POOL_BAD = [(dict(L=0), 1), (dict(block=0), 1), (dict(S=63), 1), (dict(S=0), 1),
             (dict(fmt=2, scale=None), 1), (dict(fmt=4, scale=[A, None]), 1),
             (dict(fmt=5, scale=[A + 2, A]), 1)]
 TABLE_BAD = [(dict(R=0), 1), (dict(stride=0), 1), (dict(NB=0), 1), (dict(R=(1 << 24) + 1), 2),
+             (dict(stride=(1 << 24) + 1), 2),
              (dict(table=None), 1), (dict(table_out=None), 1), (dict(ref=None), 1),
              (dict(ref_out=None), 1), (dict(table=A + 2), 1), (dict(table_out=A + 1), 1),
              (dict(ref=A + 2), 1), (dict(ref_out=A + 2), 1)]
