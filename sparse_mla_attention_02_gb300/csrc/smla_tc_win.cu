@@ -1788,12 +1788,16 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         float* rb = red + (kFp8 ? 256 * buf : 0);
         rb[64 * seg + row] = hm;
         float alpha = 1.f;
-        if (named_bar_or(4, 256, hm > m_run + C::kRaise)) {  // (true for the first finite max)
+        // (Scored bf16 rows: a row may see one key of its first block, and its maximum then
+        // grow by more than 2^8.  2^32 costs no range, and weights' exponents of up to 32
+        // are rounded to 2^-20.  Documents of 1500 tokens: 816 -> 727 us, with 2^16 775.)
+        constexpr float kRaise = kScored && !kFp8 ? 32.f : C::kRaise;
+        if (named_bar_or(4, 256, hm > m_run + kRaise)) {  // (true for the first finite max)
           float bm = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 4; ++k) bm = fmaxf(bm, rb[64 * k + row]);
           if (!kFp8) named_bar_sync(4, 256);             // (the maxima were read)
-          if (bm > m_run + (C::kRaise - 1.f)) {
+          if (bm > m_run + (kRaise - 1.f)) {
             alpha = ex2_approx(m_run - bm);              // 0 when m_run = -inf
             if (kFp8) {                                  // (the sums' own range is wider)
               const float half = ex2_approx(0.5f * (m_run - bm));
@@ -1880,23 +1884,14 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           W.wait(bar(kBarPEmpty + (J - 1) % C::kPBufs), ((J - 1) / C::kPBufs) & 1);  // PV(j - 1)
           __syncwarp();
           tc_fence_after();
-          // (bf16 rows, scored: 32 columns on their way at once, documents 850 -> 841 us; the
-          // others lose by the longer code, 8-bit decode 105 -> 108)
-          constexpr int kSixteens = kScored && !kFp8 ? 2 : 1;
 #pragma unroll 1
-          for (int c = 128 * wg; c < 128 * wg + 128; c += 16 * kSixteens) {
-            uint32_t w[kSixteens][16];
-#pragma unroll
-            for (int x = 0; x < kSixteens; ++x)
-              tmem_ld16(tmem + lane_base + kColO + c + 16 * x, w[x]);
+          for (int c = 128 * wg; c < 128 * wg + 128; c += 16) {
+            uint32_t w[16];
+            tmem_ld16(tmem + lane_base + kColO + c, w);
             tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < kSixteens; ++x) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                w[x][k] = __float_as_uint(__uint_as_float(w[x][k]) * alpha);
-              tmem_st16(tmem + lane_base + kColO + c + 16 * x, w[x]);
-            }
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
+            tmem_st16(tmem + lane_base + kColO + c, w);
           }
           tmem_wait_st();
         }
@@ -2062,7 +2057,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         }
       }
       if (live && seg == 0) {
-        const float v = empty ? -INFINITY : (m_run + log2f(l)) * 0.69314718055994530942f;
+        int up = 0;                                      // (scored bf16 rows: l may be 2^32)
+        if (kScored && !kFp8 && l >= 256.f && l < INFINITY) up = (__float_as_int(l) >> 23) - 127;
+        const float log2l = log2f(__int_as_float(__float_as_int(l) - (up << 23)));
+        const float v = empty ? -INFINITY : (m_run + (float)up + log2l) * 0.69314718055994530942f;
         if (partial)
           p.lse_part[prow_g] = v;
         else if (p.lse)

@@ -213,6 +213,60 @@ def test_seen_positions_that_are_not_finite(cuda_lib):
             assert bool(torch.isfinite(lse[n]).all()) != (sees and bad != bad)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("toward_start", [True, False])
+@pytest.mark.parametrize("step", [3.0, 9.0, 15.5, 16.5, 40.0, 150.0])
+@pytest.mark.parametrize("cap", [0.0, 1e4])
+def test_scores_that_grow_block_by_block(cuda_lib, fmt, toward_start, step, cap):
+    """Every 128 keys' scores lie 2^step above or below the next ones': the running
+    maximum rises by less and by more than O is rescaled for."""
+    smla = cuda_lib
+    b = P.Batch([(130, 700), (1, 513), (40, 40)], 64, seed=21)
+    h, sm = 16, 0.0625
+    q, cache, scale = make(b, fmt, h, 576, 5)
+    q[:] *= 0.03125 if fmt == P.BF16 else 0.00390625
+    q[:, :, 575] = step                                   # (bf16 has all of the steps)
+    level = lambda e: float(8 * (e // 128) if not toward_start else 8 * (5 - e // 128))
+    codes = torch.tensor([8 * level(128 * i) for i in range(6)]).to(torch.float8_e4m3fn)
+    for r, (_, length) in enumerate(b.rows):
+        for e in range(length):
+            s = b.slot(r, e)
+            if s >= 0:
+                cache[s, 575] = level(e) if fmt == P.BF16 else codes.view(torch.uint8)[e // 128]
+    if scale is not None:
+        scale[:] = 0.125
+    # a score's difference from one 128 keys to the next: step * 8 * sm nats / ln 2
+    sm_scale = sm * 2 * 0.6931471805599453
+    rows = P.dequant(cache, fmt, scale, b)
+    b.fp8 = fmt != P.BF16
+    slopes = slopes_of(h)
+    out, lse = call(smla, b, fmt, q, cache, scale, sm_scale, cap=cap, slopes=slopes)
+    R.check(out, lse, R.attend(q, rows, b, sm_scale, cap=cap, slopes=slopes), b, fmt)
+    # and no cap or bias, but a span: documents that begin inside of a block
+    first, last = R.spans(b, docs=[127, 300], prefix=9)
+    out, lse = call(smla, b, fmt, q, cache, scale, sm_scale, first=first, last=last)
+    R.check(out, lse, R.attend(q, rows, b, sm_scale, first=first, last=last), b, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("h", [16, 40, 64])
+@pytest.mark.parametrize("at", [0, 8, 16, 24])
+def test_output_alignments(cuda_lib, fmt, h, at):
+    """O on any 16-byte boundary, with whole tiles and partial ones."""
+    smla = cuda_lib
+    b = P.Batch([(1200, 1200), (7, 90), (150, 300)] if at < 16 else [(5, 90), (33, 300)], 64,
+                seed=31)
+    q, cache, scale = make(b, fmt, h, 576, 6)
+    slopes = slopes_of(h)
+    kw = dict(cap=20.0, slopes=slopes, max_seq_len=1200)
+    want, _ = call(smla, b, fmt, q, cache, scale, 0.04, **kw)
+    flat = torch.full((b.N * h * 512 + 32,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[at:at + b.N * h * 512].view(b.N, h, 512)
+    call(smla, b, fmt, q, cache, scale, 0.04, out=out, **kw)
+    assert torch.equal(out, want)
+    assert bool((flat[:at] == 7).all()) and bool((flat[at + b.N * h * 512:] == 7).all())
+
+
 def test_captured_and_on_another_stream(cuda_lib):
     smla = cuda_lib
     b = P.Batch([(1, 3000), (5, 700), (1, 64)], 64, seed=13)
