@@ -2199,21 +2199,30 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 
 // ---- merge of the partials -------------------------------------------------
 //   LSE = ln sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s
-// One CTA per row, four channels a thread, and where a tile may have more than 16
-// parts eight groups of threads that share them; the ranges first .. last hold the
-// row's tile (one: it is written already), the last as its first part and the
-// others as their last.  A part without a visible key has LSE_s = -inf and its
-// O_s is not read.  Rows of no request are left alone.  Launched under the end of
-// the kernel before (launch_early); it waits for it here.
+// One CTA per row, four channels a thread.  Where a tile may have more than 16 parts
+// eight groups of threads share them, and four CTAs a row's channels (eight: the same).
+// A thread's partials are on their way while the weights are made.  One token with 16
+// heads on 20 thousand keys, 76 parts: 22.3 -> 18.5 us with both.  The ranges first ..
+// last hold the row's tile (one: it is written already), the last as its first part and
+// the others as their last.  A part without a visible key has LSE_s = -inf and its O_s,
+// which nothing wrote, is not used.  Rows of no request are left alone.  Launched under
+// the end of the kernel before (launch_early); it waits for it here.
 constexpr int kMaxParts = 128;
 constexpr int kMergeGroups = 8;
-__global__ void __launch_bounds__(128 * kMergeGroups)
+template <int kGroups>
+__global__ void __launch_bounds__(kGroups == 1 ? 128 : 256)
 smla_window_merge_kernel(const WinParams p) {
+  constexpr int kWide = kGroups == 1 ? 128 : 32;       // threads over the channels
+  constexpr int kCtas = 128 / kWide;
+  constexpr int kAhead = kGroups == 1 ? 8 : 16;        // parts of a thread on their way
+  static_assert(kGroups == 1 || kGroups * kAhead >= kMaxParts, "one turn");
   __shared__ float weight[kMaxParts];
   __shared__ float red[2][4];
-  __shared__ float4 sums[kMergeGroups][128];
-  const int tid = threadIdx.x & 127, group = threadIdx.x >> 7, groups = blockDim.x >> 7;
-  const int64_t row = blockIdx.x;
+  __shared__ float4 sums[kGroups][kWide];
+  const int tid = threadIdx.x & 127;                   // its part's weight
+  const int lane = threadIdx.x % kWide, group = threadIdx.x / kWide;
+  const int64_t row = blockIdx.x / kCtas;
+  const int c = ((int)(blockIdx.x % kCtas) * kWide + lane) * 4;
   const int tok = (int)(row / p.h);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int part = p.parts[row];
@@ -2225,11 +2234,20 @@ smla_window_merge_kernel(const WinParams p) {
   auto at = [&](int s) {
     return (int64_t)(2 * (first + s) + (first + s < last ? 1 : 0)) * 128 + off;
   };
-  const float ls = tid < n ? p.lse_part[at(tid)] : -INFINITY;   // (every group alike)
+  const float ls = tid < n ? p.lse_part[at(tid)] : -INFINITY;
+  float4 x[kAhead];
+  auto read = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i * kGroups;
+      if (s < n) x[i] = *reinterpret_cast<const float4*>(p.o_part + at(s) * 512 + c);
+    }
+  };
+  read(group);
   float top = ls;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (group == 0 && (tid & 31) == 0) red[0][tid >> 5] = top;
+  if (threadIdx.x < 128 && (tid & 31) == 0) red[0][tid >> 5] = top;
   __syncthreads();
   top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   // (fmaxf passes over a NaN; its weight is NaN and so is the row)
@@ -2237,44 +2255,40 @@ smla_window_merge_kernel(const WinParams p) {
   float z = e;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  if (group == 0 && (tid & 31) == 0) red[1][tid >> 5] = z;
-  if (group == 0) weight[tid] = e;
+  if (threadIdx.x < 128) {
+    if ((tid & 31) == 0) red[1][tid >> 5] = z;
+    weight[tid] = e;
+  }
   __syncthreads();
   z = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int c = tid * 4;
-  for (int s0 = group; s0 < n; s0 += 8 * groups) {     // eight parts on their way at once
-    float4 x[8];
-    float w[8];
+  for (int s0 = group; s0 < n; s0 += kAhead * kGroups) {
+    if (s0 != group) read(s0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = s0 + i * groups;
-      w[i] = s < n ? weight[s] : 0.f;
-      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (w[i] != 0.f) x[i] = *reinterpret_cast<const float4*>(p.o_part + at(s) * 512 + c);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      o.x = fmaf(w[i], x[i].x, o.x);
-      o.y = fmaf(w[i], x[i].y, o.y);
-      o.z = fmaf(w[i], x[i].z, o.z);
-      o.w = fmaf(w[i], x[i].w, o.w);
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i * kGroups;
+      const float w = s < n ? weight[s] : 0.f;
+      if (w == 0.f) continue;
+      o.x = fmaf(w, x[i].x, o.x);
+      o.y = fmaf(w, x[i].y, o.y);
+      o.z = fmaf(w, x[i].z, o.z);
+      o.w = fmaf(w, x[i].w, o.w);
     }
   }
-  if (groups > 1) {
-    sums[group][tid] = o;
+  if (kGroups > 1) {
+    sums[group][lane] = o;
     __syncthreads();
     if (group > 0) return;
-    for (int g = 1; g < groups; ++g) {
-      const float4 x = sums[g][tid];
-      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+    for (int g = 1; g < kGroups; ++g) {
+      const float4 y = sums[g][lane];
+      o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
     }
   }
   const bool none = z == 0.f;
   const float inv = none ? 0.f : 1.f / z;
   uint2 packed = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * 512 + c) = packed;
-  if (tid == 0 && p.lse) p.lse[row] = none ? -INFINITY : top + logf(z);
+  if (c == 0 && p.lse) p.lse[row] = none ? -INFINITY : top + logf(z);
 }
 
 cudaError_t encode_rows(CUtensorMap* map, bool fp8, const void* base, int d, int64_t rows,
@@ -2419,8 +2433,11 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   e = p.softcap > 0.f || p.slopes || p.first_pos || p.last_pos ? run(std::true_type())
                                                                : run(std::false_type());
   if (e != cudaSuccess || p.workers == 0) return e;
-  return launch_early(smla_window_merge_kernel, (unsigned)(p.b.N * p.h), 128 * p.merge_groups, 0,
-                      stream, p);
+  return p.merge_groups > 1
+             ? launch_early(smla_window_merge_kernel<kMergeGroups>, 4u * (unsigned)(p.b.N * p.h),
+                            256, 0, stream, p)
+             : launch_early(smla_window_merge_kernel<1>, (unsigned)(p.b.N * p.h), 128, 0, stream,
+                            p);
 }
 
 }  // namespace smla
