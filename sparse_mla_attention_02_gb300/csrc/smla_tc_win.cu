@@ -15,9 +15,10 @@
 // first position to its last token's last, in blocks that begin at a multiple of 64; a
 // segment of 32 keys costs a thread two more steps of the special function unit a key for
 // the cap, and half a packed product for the bias (near_scores).  That is hidden behind
-// the MMAs of bf16 rows but for 3 to 7 % (64 capped decode tokens of 4 to 8 thousand keys,
-// 128 heads, 118 us, uncapped 115); E4M3 rows, whose softmax is as long as their MMAs, pay
-// for it (a mixed batch 360 -> 388 us with a bias, 421 with a cap, 425 with both).
+// the MMAs of bf16 rows but for 5 % (packed documents of 1500 tokens, 64 heads, 728 us,
+// uncapped 695; 64 capped decode tokens of 4 to 8 thousand keys, 128 heads, 112 us); E4M3
+// rows, whose softmax is as long as their MMAs, pay for it (a mixed batch 361 -> 386 us
+// with a bias, 417 with a cap, 428 with both).
 //
 // Tile.  All heads share the key rows, and neighbouring tokens of a request
 // share most of them, so a tile is 128 consecutive rows of the flattened
