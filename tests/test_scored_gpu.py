@@ -195,6 +195,40 @@ def test_unseen_positions_may_hold_anything(cuda_lib, fmt, bad, docs, cap):
     R.check(got[0], got[1], ref, b, fmt)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("fmt", [P.BF16, P.BLOCK])
+def test_unseen_positions_in_whole_tiles(cuda_lib, fmt, bad):
+    """The same where every tile is one unit: its rows are computed again and written
+    over what the tile stored."""
+    smla = cuda_lib
+    b = P.Batch([(199, 300), (3, 40)], 64, seed=13, pad=2)
+    h = 64
+    first, last = R.spans(b, docs=[131, 207], prefix=7)
+    q, cache, scale = make(b, fmt, h, 576, 9)
+    assert smla.smla_fwd_window_workspace_size(2, b.N, h, 576, fmt, b.table.shape[1], 64) == 0
+    seen = torch.zeros(b.num_slots, dtype=torch.bool)
+    for n, r, pos in b.tokens():
+        for e in range(int(first[n]), int(last[n]) + 1):
+            seen[b.slot(r, e)] = True
+    dirty = cache.clone()
+    dirty[~seen] = bad if fmt == P.BF16 else 0x7F          # E4M3's NaN
+    # (and a position that only the second document's tokens see)
+    dirty[b.slot(0, 135)] = bad if fmt == P.BF16 else 0x7F
+    kw = dict(cap=8.0, slopes=slopes_of(h), first=first, last=last)
+    out, lse = call(smla, b, fmt, q, dirty, scale, 0.04, **kw)
+    rows = P.dequant(cache, fmt, scale, b)
+    b.fp8 = fmt != P.BF16
+    ref = R.attend(q, rows, b, 0.04, cap=8.0, slopes=kw["slopes"], first=first, last=last)
+    sees = torch.zeros(b.N, dtype=torch.bool)
+    for n, r, pos in b.tokens():
+        sees[n] = r == 0 and int(first[n]) <= 135 <= int(last[n])
+    assert bool(sees.any()) and not bool(sees.all())
+    assert not bool(torch.isfinite(out[sees].float()).all(-1).any())
+    out[sees] = ref[0][sees].to(out)                       # (the others are checked)
+    lse[sees] = ref[1][sees].to(lse)
+    R.check(out, lse, ref, b, fmt)
+
+
 def test_seen_positions_that_are_not_finite(cuda_lib):
     """A key with an infinite channel, seen: its score is capped, and O has its V; a NaN
     makes the rows that see it NaN and no others."""
