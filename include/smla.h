@@ -365,14 +365,20 @@ SMLA_API smla_status smla_cache_copy(void* const* kv_caches, float* const* k_sca
  *  - Free blocks are taken for the positions from the next block's on, up to len +
  *    room[i] - 1.
  * Blocks are taken pair by pair, a pair's copy first, then its columns in order.
- * Where there are not enough, the last ones stay -1.  Entries behind the room are
- * -1, blocks that the row held there are let go.
+ * Where there are not enough, the last columns stay -1, and a row that no block was
+ * left to copy its last one into goes on sharing it: the positions [0, len) of every
+ * row stay as they are.  Such a row gets no other block either and must not be
+ * appended to (its tokens would go into a block that others hold); once blocks are
+ * free, a call with its parent itself (parents NULL) makes the copy.  Entries behind
+ * the room are -1, blocks that the row held there are let go.  Where the entry that
+ * len ends in is negative, nothing is copied or counted for it.
  *  parents        device int32 [n], rows of the table, or NULL: the children
  *                 themselves (rows that go on)
  *  children       device int32 [n]; a negative one is passed over, and of pairs with
  *                 the same child only the last counts
  *  room           device int32 [n] or NULL (0 for every pair: sharing alone)
- *  missing        device int32 [1] or NULL: how many blocks could not be had
+ *  missing        device int32 [1] or NULL: how many blocks could not be had, for
+ *                 copies and columns
  *  workspace      device, caller-owned, 256-byte aligned, at least
  *                 smla_cache_fork_workspace_size(...) bytes.  One workspace must not
  *                 be shared by calls, or by captured graphs, that may overlap on the

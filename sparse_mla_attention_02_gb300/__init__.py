@@ -595,7 +595,9 @@ def smla_cache_fork(parents, children, room, seq_lens, block_table, refcount, bl
     [R,stride], refcount int32 [blocks]; the results go to the ``out_`` tensors
     (None: in place); kv_caches and k_scales as for ``smla_cache_copy``.
     Returns ``missing`` int32 [1]: how many blocks could not be had (a new one shares
-    its memory with the call's workspace, where that is new too)."""
+    its memory with the call's workspace, where that is new too).  Rows without a block
+    for their copy go on sharing their last one, and are not to be appended to before a
+    call has made the copy."""
     import torch
     lib = _lib or load()
     index, raw_stream = _device_stream(children, "children", stream)

@@ -11,7 +11,9 @@
 //   fork      row'[c] = parent's entry for c < ceil(len / B);  ref' = ref - (entries of
 //             the rows replaced) + (entries of the new rows); the last block of a row
 //             that will be written (room > 0) becomes its own where others hold it;
-//             then blocks for the positions [len, len + room)
+//             then blocks for the positions [len, len + room).  Where no block is left
+//             for a row's own last one, it keeps the shared one: what it has written
+//             stays, and a later call finds the copy still to be made
 //   free      entries of blocks that lie in [begin, end) -> -1, ref' = ref - those
 //   compact   L live blocks: the k-th highest of those numbered L or more goes to the
 //             k-th lowest free number below L.  With lr(b) = live blocks below b, that
@@ -512,8 +514,9 @@ smla_fork_take_kernel(const ForkParams p) {
       s.src[m] = q.open;
       s.place[m] = at;
       s.rows[m] = (int)((uint32_t)q.len % (uint32_t)t.block_size);
-      // (a block that is copied keeps a holder: its count was above the copies made)
-      atomicSub(t.ref_out + q.open, 1);
+      // (a block that is copied keeps a holder: its count was above the copies made;
+      // a copy that has no block is not made, and its row goes on holding this one)
+      if (at < base.y) atomicSub(t.ref_out + q.open, 1);
     }
   };
   int wanted;
@@ -608,10 +611,10 @@ __global__ void __launch_bounds__(kCopyThreads) smla_fork_write_kernel(
   const int32_t* stage = s.stage + (int64_t)i * t.width;
   int32_t* row = t.table_out + (int64_t)child * t.width;
   for (int c = threadIdx.x; c < t.width; c += kCopyThreads) {
-    int v = stage[c], k = -1;
+    int v = stage[c], k = -1;                          // (behind the length: -1)
     if (own && c == have - 1) k = first;
     if (c >= have && c < have + fresh) k = first + own + (c - have);
-    if (k >= 0) v = k < got ? s.list[k] : -1;
+    if (k >= 0 && k < got) v = s.list[k];
     row[c] = v;
   }
   if (threadIdx.x == 0) t.lens_out[child] = len;
