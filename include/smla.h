@@ -533,8 +533,9 @@ SMLA_API size_t smla_fwd_window_workspace_size(int num_reqs, int T, int h, int d
  * Every other argument, the results and the errors are those of smla_fwd_window
  * (SMLA_ERR_INVALID_ARG for any other softcap, too).  first_pos and last_pos of tokens
  * behind query_start[num_reqs] are not read.  y_e is within 2^-20 softcap of its value,
- * for a softcap above 256 within 2^-16 |y_e|, the bias within 2^-22 of itself.  With
- * softcap = 0 and the three pointers NULL the call is smla_fwd_window.
+ * for a softcap above 256 within 2^-16 |y_e|, the bias within 2^-22 of itself (2^-21
+ * for distances above 2^24).  With softcap = 0 and the three pointers NULL the call is
+ * smla_fwd_window.
  */
 SMLA_API smla_status smla_fwd_scored(
     const void* q, const void* kv_cache, int kv_dtype, const float* k_scale,

@@ -599,21 +599,26 @@ constexpr float kCapNear = 256.f;
 // is not seen has to be kept from its neighbour.  Error of tanh: rcp 2^-23 and the sum
 // 2^-24 of a quotient of at most 1, ex2 2^-21.5 times at most a quarter, all twice: less
 // than 2^-20.
-// The bias of key k, side * (d0 + k) with side = -+slope, is added up in steps of two
-// from every eighth key's own product: off by at most 2^-22 of itself.
+// The bias of key k is the product of side = -+slope and of d0 + k, which is exact up to
+// 2^24: 0 at the token itself, elsewhere off by its own rounding and the slope's in log2
+// units, 2^-22 of itself.  (Adding the slope up from key to key instead leaves errors of
+// the farthest key of a group at the nearest.)  The distances are counted in steps of two
+// from every eighth key's: above 2^24 they, and the bias, are off by at most 2^-21.
 template <bool kCap>
 __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap, float two_over_cap,
                                             float side, float d0) {
   const float f = cl * two_over_cap, base = kCap ? cap : 0.f;
-  float c0 = base, c1 = base;
+  float a0 = d0, a1 = d0;
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
     if (k % 8 == 0) {
-      c0 = fmaf(side, d0 + (float)k, base);
-      c1 = c0 + side;
+      a0 = d0 + (float)k;
+      a1 = d0 + (float)(k + 1);
     } else {
-      add2(c0, c1, 2.f * side, 2.f * side);
+      add2(a0, a1, 2.f, 2.f);
     }
+    float c0 = a0, c1 = a1;
+    fma2_bcast(c0, c1, side, base);
     if (kCap) {
       float u0 = s[k], u1 = s[k + 1];
       fma2_bcast(u0, u1, f, 0.f);
