@@ -607,7 +607,10 @@ constexpr float kCapNear = 256.f;
 template <bool kCap>
 __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap, float two_over_cap,
                                             float side, float d0) {
-  const float f = cl * two_over_cap, base = kCap ? cap : 0.f;
+  // (a finite factor stays one: a score of 0 under a small cap is 0)
+  float f = cl * two_over_cap;
+  if (kCap && fabsf(cl) < INFINITY) f = fminf(fmaxf(f, -0x1.fffffep127f), 0x1.fffffep127f);
+  const float base = kCap ? cap : 0.f;
   float a0 = d0, a1 = d0;
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
