@@ -104,13 +104,15 @@ __device__ __forceinline__ void copy_block(const CopyParams& c, int layer, int p
 // CTA `id` of the copying ones: a piece of a layer, for every `share`-th move.  A move is
 // read while the one before it is copied (a pool of 6 layers, half free: 142 -> 138 us).
 __device__ __forceinline__ void copy_moves(const CopyParams& c, int id, int share) {
-  const int n = c.n_at ? *c.n_at : c.n, list_n = c.list ? *c.list_n : 0;
+  // (unsigned: the number behind the last move may pass 2^31)
+  const uint32_t n = c.n_at ? *c.n_at : c.n;
+  const int list_n = c.list ? *c.list_n : 0;
   const int piece = id % c.pieces, rest = id / c.pieces;
   const int layer = rest % c.layers;
   struct Move {
     int src, dst, rows;
   };
-  auto read = [&](int m) {
+  auto read = [&](uint32_t m) {
     Move v{-1, -1, 0};
     if (m < n) {
       v.src = c.src[m];
@@ -121,7 +123,7 @@ __device__ __forceinline__ void copy_moves(const CopyParams& c, int id, int shar
     return v;
   };
   Move next = read(rest / c.layers);
-  for (int m = rest / c.layers; m < n; m += share) {
+  for (uint32_t m = rest / c.layers; m < n; m += share) {
     const Move v = next;
     next = read(m + share);
     if (v.src >= c.blocks || v.dst >= c.blocks) {
@@ -131,7 +133,7 @@ __device__ __forceinline__ void copy_moves(const CopyParams& c, int id, int shar
     if (v.src < 0 || v.dst < 0 || v.src == v.dst) continue;
     // (parts of blocks fill the first pieces alone: a CTA takes them in turn; 256 beams:
     // 34.2 -> 32.7 us)
-    const int at = c.rows ? (int)((uint32_t)(piece + m) % (uint32_t)c.pieces) : piece;
+    const int at = c.rows ? (int)((piece + m) % (uint32_t)c.pieces) : piece;
     copy_block(c, layer, at, v.src, v.dst, v.rows);
   }
 }
