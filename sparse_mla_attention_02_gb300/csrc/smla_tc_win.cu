@@ -2210,22 +2210,25 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
 // ---- merge of the partials -------------------------------------------------
 //   LSE = ln sum_s exp(LSE_s),  O = sum_s exp(LSE_s - LSE) O_s
 // One CTA per row, four channels a thread.  Where a tile may have more than 16 parts
-// eight groups of threads share them, and four CTAs a row's channels (eight: the same).
-// A thread's partials are on their way while the weights are made.  One token with 16
-// heads on 20 thousand keys, 76 parts: 22.3 -> 18.5 us with both.  The ranges first ..
-// last hold the row's tile (one: it is written already), the last as its first part and
-// the others as their last.  A part without a visible key has LSE_s = -inf and its O_s,
-// which nothing wrote, is not used.  Rows of no request are left alone.  Launched under
-// the end of the kernel before (launch_early); it waits for it here.
+// eight groups of threads share them, and four CTAs a row's channels (eight: the same),
+// two where there are more than kNarrowRows rows, whose CTAs then come in several waves.
+// A thread's partials are on their way while the weights are made.  A call with one CTA of
+// eight groups a row (1024 threads, the weights first) / two / four, us, 20 thousand keys:
+// 16 rows 22.7 / 20.6 / 18.7, 64 rows 25.2 / 23.2 / 21.2, 96 rows 24.9 / 23.0 / 23.6, 256
+// rows 24.5 / 24.6 / 28.4, 512 rows 33.1 / 31.2 / 39.0.  The ranges first .. last hold the
+// row's tile (one: it is written already), the last as its first part and the others as
+// their last.  A part without a visible key has LSE_s = -inf and its O_s, which nothing
+// wrote, is not used.  Rows of no request are left alone.  Launched under the end of the
+// kernel before (launch_early); it waits for it here.
 constexpr int kMaxParts = 128;
 constexpr int kMergeGroups = 8;
-template <int kGroups>
-__global__ void __launch_bounds__(kGroups == 1 ? 128 : 256)
+constexpr unsigned kNarrowRows = 64;
+template <int kGroups, int kWide>                      // threads over the channels
+__global__ void __launch_bounds__(kGroups * kWide)
 smla_window_merge_kernel(const WinParams p) {
-  constexpr int kWide = kGroups == 1 ? 128 : 32;       // threads over the channels
   constexpr int kCtas = 128 / kWide;
-  constexpr int kAhead = kGroups == 1 ? 8 : 16;        // parts of a thread on their way
-  static_assert(kGroups == 1 || kGroups * kAhead >= kMaxParts, "one turn");
+  // parts of a thread on their way (64 channels: few, for registers)
+  constexpr int kAhead = kWide == 32 ? 16 : kWide == 64 ? 4 : 8;
   __shared__ float weight[kMaxParts];
   __shared__ float red[2][4];
   __shared__ float4 sums[kGroups][kWide];
@@ -2443,11 +2446,14 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   e = p.softcap > 0.f || p.slopes || p.first_pos || p.last_pos ? run(std::true_type())
                                                                : run(std::false_type());
   if (e != cudaSuccess || p.workers == 0) return e;
-  return p.merge_groups > 1
-             ? launch_early(smla_window_merge_kernel<kMergeGroups>, 4u * (unsigned)(p.b.N * p.h),
-                            256, 0, stream, p)
-             : launch_early(smla_window_merge_kernel<1>, (unsigned)(p.b.N * p.h), 128, 0, stream,
-                            p);
+  const unsigned merged = (unsigned)(p.b.N * p.h);
+  if (p.merge_groups == 1)
+    return launch_early(smla_window_merge_kernel<1, 128>, merged, 128, 0, stream, p);
+  return merged <= kNarrowRows
+             ? launch_early(smla_window_merge_kernel<kMergeGroups, 32>, 4 * merged,
+                            kMergeGroups * 32, 0, stream, p)
+             : launch_early(smla_window_merge_kernel<kMergeGroups, 64>, 2 * merged,
+                            kMergeGroups * 64, 0, stream, p);
 }
 
 }  // namespace smla
