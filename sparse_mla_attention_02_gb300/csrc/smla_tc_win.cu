@@ -1563,17 +1563,13 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
           own = (votes & 0xFFu) == 0xFFu ? top : 0.f;
         }
         // The block's rows on their way into L2, two to three blocks before
-        // their copies: a copy then waits for L2, not for HBM.
+        // their copies: a copy then waits for L2, not for HBM.  (By-row copies do
+        // without: a request a row holds up the lookups.  64 decode tokens on 8 thousand
+        // keys in blocks of 16 rows 158 -> 133 us, a prompt of 2048 twice 1375 -> 1135.)
         if (a.box == 64 && (lane & 15) == 0 && id[0] >= 0 && (lane >> 4) == (int)r)
 #pragma unroll 1
           for (int c = 0; c < p.d_qk * C::kElem / 128; c += C::kAtomsPerGroup)
             tma_prefetch_3d(&a.k_map, 0, id[0], c);
-        if (kByRow != 0 && (lane >> 4) == (int)r)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (id[k] >= 0)
-              prefetch_l2(static_cast<const uint8_t*>(p.kv) + (int64_t)id[k] * (p.d_qk * C::kElem),
-                          (uint32_t)(p.d_qk * C::kElem));
         if (J >= kMeta) W.wait(bar(kBarMEmpty + m), mr.ph ^ 1);
         if (stopped()) break;
         __syncwarp();

@@ -22,10 +22,6 @@ template <int n>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
-// `bytes` of global memory (a multiple of 16, 16-byte aligned) into L2.
-__device__ __forceinline__ void prefetch_l2(const void* at, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
-}
 
 // Write a word of a cluster's shared memory (address from mapa).
 __device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
