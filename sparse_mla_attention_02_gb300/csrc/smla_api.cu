@@ -386,6 +386,7 @@ smla_status run_window(const void* q, const void* kv_cache, int kv_dtype,
   p.sinks = sinks;
   p.workers = plan.workers;
   p.merge_groups = plan.merge_groups;
+  p.short_tiles = plan.short_tiles;
   p.sm_scale = sm_scale;
   p.softcap = scoring.softcap;
   p.slopes = scoring.slopes;

@@ -55,6 +55,7 @@ struct WinParams {
   float* lse_part;             // [2 workers, 128]
   int* parts;                  // [N, h] the ranges that hold the row's tile, its row
   int merge_groups;            // thread groups of the merge
+  bool short_tiles;            // many tiles of few key blocks (WindowPlan)
   int* status;
   int* abort_ctr;
   uint64_t wait_limit_ns;
@@ -73,6 +74,7 @@ struct WinParams {
 struct WindowPlan {
   int64_t tiles;
   int workers, merge_groups;
+  bool short_tiles;            // many tiles, none of more than kShortBlocks key blocks
   size_t workspace_bytes;
 };
 WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int window, int sinks,

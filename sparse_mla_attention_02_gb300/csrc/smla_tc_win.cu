@@ -242,11 +242,20 @@ constexpr int kWarpPv = 12;                // issues PV
 // the loaders' threads, the others as boxes by TMA.  A TMA copy of a small box takes 27
 // cycles or more for its 128-byte rows, whoever issues it, and a block of keys is up to
 // 272 of them a CTA; four warps with 16-byte copies bring the same in about half the time.
-// Decode of 64 tokens / documents of 1500 tokens, boxes -> rows: blocks of 1 row 400 ->
-// 185 / 2139 -> 1184 us, of 4 363 -> 171 / 1943 -> 1059, of 16 183 -> 171 / 1087 -> 1060;
-// of 32 156 -> 179 / 974 -> 1134 (boxes), of 64 118 / 844 (boxes).  E4M3 rows, whose
-// softmax is what bounds them, lose by it (blocks of 1 row 763 -> 923 us, of 16 591 -> 856).
+// 64 decode tokens with 128 heads on 4 to 8 thousand keys / a prompt of 2048 twice through
+// a window / scored documents of 1500 tokens, boxes -> rows, us: blocks of 1 row 381 -> 144
+// / 2995 -> 1197 / 2070 -> 1021, of 16 171 -> 133 / 1379 -> 1135 / 1005 -> 960, of 32 145
+// -> 132 / 1196 -> 1135 / 889 -> 961, of 64 108 -> 131 / 909 -> 1147 / 720 -> 961.  E4M3
+// rows, whose softmax is what bounds them, lose by it (blocks of 1 row 763 -> 923 us, of 16
+// 591 -> 856).
 constexpr int kRowsBox = 32;
+// A unit's end waits for its last copies by row, so where units are short and many the
+// boxes of 16 rows are faster: 16 heads, boxes -> rows, blocks of 16, 4000 requests of 100
+// keys 263 -> 345 us, 1000 of 128 77 -> 94, of 257 103 -> 121, of 385 126 -> 127, of 513 159
+// -> 150, 250 of 128 28.2 -> 30.8, 64 of 128 14.3 -> 13.0; blocks of 4, 4000 of 100 357 ->
+// 344, 1000 of 128 107 -> 94.
+constexpr int kRowsBoxShort = 16;
+constexpr int kShortBlocks = 3;            // key blocks of such a unit, at most
 
 template <bool kFp8>
 struct Cfg {
@@ -2390,6 +2399,7 @@ WindowPlan make_window_plan(int T, int h, int num_reqs, int64_t max_len, int win
   if (workers > 1 && std::max<int64_t>(pl.tiles, num_reqs) <= 1024 && ranges < 0.95 * one)
     pl.workers = (int)workers;
   pl.merge_groups = workers > 16 * filled ? kMergeGroups : 1;
+  pl.short_tiles = blocks <= kShortBlocks && filled > 2 * places;
   if (pl.workers > 0)
     pl.workspace_bytes = ((size_t)T * h * sizeof(int) + 255) / 256 * 256 +
                          (size_t)pl.workers * 2 * 128 * (512 + 1) * sizeof(float);
@@ -2431,7 +2441,7 @@ cudaError_t launch_window(WinParams p, cudaStream_t stream) {
   if (ctas > 0x7FFFFFFFll || (int64_t)p.b.N * p.h > 0x7FFFFFFFll)
     return cudaErrorInvalidConfiguration;
   a.p = p;
-  const bool rows = !fp8 && a.box < kRowsBox;
+  const bool rows = !fp8 && a.box < (p.short_tiles ? kRowsBoxShort : kRowsBox);
   const auto run = [&](auto scored) {
     constexpr bool kScored = decltype(scored)::value;
     if (fp8) return launch<true, kScored>(a, (unsigned)ctas, stream);
