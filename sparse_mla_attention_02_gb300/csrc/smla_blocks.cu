@@ -22,11 +22,15 @@
 //
 // Bound: latency for the tables (the launches of a call follow one another, each
 // under the end of the one before), HBM for the rows of a pool.  Measured in a captured
-// graph, on two sets of inputs in turn: 224 bf16 blocks of 64 rows in 24 layers 123 us =
+// graph, on two sets of inputs in turn: 225 bf16 blocks of 64 rows in 24 layers 123 us =
 // 6.4 TB/s read and written (94 % of a copy's rate), one block in 60 layers 2.5 us; eight samples
 // of a prompt 10.9 us, 256 beams in 32 layers of E4M3 blocks 32.7 us (100 MB, of them 17 us
 // the tables); a finished sixteenth of 64 rows 4 us, 1024 rows' windows 11.3 us; half a
-// pool of 4000 blocks in 6 layers 138 us = 6.1 TB/s.
+// pool of 3814 blocks in 6 layers 138 us = 6.1 TB/s.
+// Each pair looks at all the others for a child named again and, in one cluster, for
+// writers of its last block, so many pairs cost their square: rows that go on, 1024 of 16
+// columns 21 us, 4096 119 us, 16384 1.5 ms, 65536 22 ms; as many rows freed 5, 9, 43 and
+// 420 us.
 #include "launch.cuh"
 #include "smla_blocks.h"
 
@@ -257,9 +261,16 @@ cudaError_t launch_carry(const Carry& p, cudaStream_t stream) {
                       kRowThreads, 0, stream, p);
 }
 
-// Tables and pairs of a fork this small are handled by one cluster in one launch, larger
-// ones by a launch for each step that needs the one before it complete.
-constexpr int64_t kSmallWords = 1 << 17;
+// Tables and pairs of a fork this small are handled by one cluster in one launch (a warp
+// per pair), larger ones by a launch for each step that needs the one before it complete.
+// The words are those of the largest array that is carried and of the children's rows.
+// One cluster / a launch a step, us in a graph, rows that go on in place, four samples a
+// row apart, eight new samples apart: 8 rows of 65 columns 7.6 / 8.8, 9.3 / 11.9, 9.4 /
+// 11.9; 256 of 127 (65 thousand words apart) 11.5 / 11.2, 13.8 / 14.1, 10.2 / 11.8; 256 of
+// 400 14.8 / 11.8, 19.2 / 15.7, 14.4 / 12.9; 512 of 127 (66 thousand words for eight) 19.4
+// / 13.7, 24.1 / 17.9, 11.0 / 12.2; 1000 of 100 (101 thousand) 46 / 25, 54 / 32, 13.0 / 13.1.
+constexpr int kSmallPairs = kScanWarps;
+constexpr int64_t kSmallWords = 5 << 14;
 
 // A row is worked on by a CTA, or (kWarp) by each warp of a cluster.
 template <bool kWarp>
@@ -454,7 +465,6 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* sums, long
 // kSmall: the carrying and sharing too, a warp per pair, and each warp counts the pairs
 // before its own instead of a scan over all.  What other CTAs of the cluster wrote is
 // read past L1.
-constexpr int kSmallPairs = 1024;
 template <bool kSmall>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads, 1)
 smla_fork_take_kernel(const ForkParams p) {
@@ -477,7 +487,6 @@ smla_fork_take_kernel(const ForkParams p) {
     };
     if (warp < p.n) mine = share_pair<true>(p, warp, ready);
     ready();
-    for (int i = warp + kScanWarps; i < p.n; i += kScanWarps) share_pair<true>(p, i, ready);
     cluster_sync();
   }
   // A block that is written by some of its holders: of the writers all but the first
@@ -523,26 +532,23 @@ smla_fork_take_kernel(const ForkParams p) {
   };
   int wanted;
   if (kSmall) {
-    wanted = 0;
-    int moves = 0;
-    for (int i = warp; i < p.n || i == warp; i += kScanWarps) {
-      int blocks = 0, copies = 0, at = 0, m = 0, cost = 0;
+    int blocks = 0, copies = 0, at = 0, m = 0, cost = 0;
 #pragma unroll 8
-      for (int j = lane; j < p.n; j += 32) {
-        const int x = __ldcg(s.own + j), need = (x & 1) + (x >> 1);
-        blocks += need;
-        copies += x & 1;
-        at += j < i ? need : 0;
-        m += j < i ? x & 1 : 0;
-        if (j == i) cost = x;
-      }
-      wanted = warp_sum(blocks);
-      moves = warp_sum(copies);
-      if (i >= p.n) break;
+    for (int j = lane; j < p.n; j += 32) {
+      const int x = __ldcg(s.own + j), need = (x & 1) + (x >> 1);
+      blocks += need;
+      copies += x & 1;
+      at += j < warp ? need : 0;
+      m += j < warp ? x & 1 : 0;
+      if (j == warp) cost = x;
+    }
+    wanted = warp_sum(blocks);
+    const int moves = warp_sum(copies);
+    if (warp < p.n) {
       at = warp_sum(at);
       m = warp_sum(m);
       cost = warp_sum(cost);
-      if (lane == 0) place(i, cost, at, m);
+      if (lane == 0) place(warp, cost, at, m);
     }
     if (id == 0) {
       s.head[0] = wanted;
