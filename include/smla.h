@@ -480,6 +480,10 @@ SMLA_API size_t smla_cache_compact_workspace_size(int num_blocks);
  * 2^-17.8 of its row's largest value).  Keys 11 nats below the top one keep their
  * 9 bits, keys 16 nats below may be off by 3 %, keys 20 nats below vanish from O
  * (LSE counts them all).
+ * Scores are fp32, off by 2^-22 |s_e| beside that.  With E4M3 caches the logarithm of
+ * a key's scale is rounded with its score, so even a row that one key carries is off by
+ * that much of V, and rows whose largest |s_e| is 2^23 or more are not served: O may be
+ * off by a factor, from about 2^27 on NaN.
  * Rows of tokens behind query_start[num_reqs] are left alone.  A position past
  * the block table or a row past the cache is not seen and sets the
  * SMLA_ERR_BAD_INDEX device status.  Asynchronous on `stream`, no allocation.
