@@ -2072,10 +2072,15 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
         }
       }
       if (live && seg == 0) {
-        int up = 0;                                      // (scored bf16 rows: l may be 2^32)
-        if (kScored && !kFp8 && l >= 256.f && l < INFINITY) up = (__float_as_int(l) >> 23) - 127;
-        const float log2l = log2f(__int_as_float(__float_as_int(l) - (up << 23)));
-        const float v = empty ? -INFINITY : (m_run + (float)up + log2l) * 0.69314718055994530942f;
+        float whole = m_run, rest = l;                   // (scored bf16 rows: l may be 2^32)
+        if constexpr (kScored && !kFp8) {
+          if (l >= 256.f && l < INFINITY) {
+            const int up = (__float_as_int(l) >> 23) - 127;
+            rest = __int_as_float(__float_as_int(l) - (up << 23));
+            whole += (float)up;
+          }
+        }
+        const float v = empty ? -INFINITY : (whole + log2f(rest)) * 0.69314718055994530942f;
         if (partial)
           p.lse_part[prow_g] = v;
         else if (p.lse)
