@@ -15,11 +15,12 @@
 // <= last[t], in the window, or e < sinks }.  A tile's keys run from its first token's
 // first position to its last token's last, in blocks that begin at a multiple of 64; a
 // segment of 32 keys costs a thread two more steps of the special function unit a key for
-// the cap, and half a packed product for the bias (near_scores).  That is hidden behind
-// the MMAs of bf16 rows but for 5 % (packed documents of 1500 tokens, 64 heads, 728 us,
-// uncapped 695; 64 capped decode tokens of 4 to 8 thousand keys, 128 heads, 112 us); E4M3
-// rows, whose softmax is as long as their MMAs, pay for it (a mixed batch 361 -> 386 us
-// with a bias, 417 with a cap, 428 with both).
+// the cap, and half a packed product and sum for the bias (near_scores).  That is hidden
+// behind the MMAs of bf16 rows but for 4 % (packed documents of 1500 tokens, 64 heads, 734
+// to 749 us, uncapped 706; 64 capped decode tokens of 4 to 8 thousand keys, 128 heads, 113
+// us); E4M3 rows, whose softmax is as long as their MMAs, pay for it (a mixed batch 363 us
+// with neither, 394 with a bias, 424 with a cap, 436 with both; 32 decode tokens of 8 to 16
+// thousand keys, 128 heads, 113, 116, 125 and 128).
 //
 // Tile.  All heads share the key rows, and neighbouring tokens of a request
 // share most of them, so a tile is 128 consecutive rows of the flattened
