@@ -155,8 +155,8 @@ enum {
   kBarCFull = kBarTEmpty + 2,              // [2] own: an answer of the launch control
   kBarCEmpty = kBarCFull + 2,              // [2] even CTA: both have read it
   kBarDrain = kBarCEmpty + 2,              // [2] even CTA: QK's and PV's last MMAs
-  kBarQScale = kBarDrain + 2,              // own, E4M3: the Q rows' scales are written
-  kNumBars
+  kBarQScale = kBarDrain + 2,              // [2] own, E4M3: the Q rows' scales are written
+  kNumBars = kBarQScale + 2
 };
 
 // The bounded waits of tc_common.cuh with everything but the first try out of
@@ -892,7 +892,8 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       mbar_init(bar(kBarPEmpty + i), 1);
     }
     mbar_init(bar(kBarQFull), kFp8 ? 6 : 1);         // E4M3: three warps of both CTAs write Q
-    if (kFp8) mbar_init(bar(kBarQScale), 3);
+    if (kFp8)
+      for (int i = 0; i < 2; ++i) mbar_init(bar(kBarQScale + i), 3);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(bar(kBarMFull + i), 1);
       mbar_init(bar(kBarMEmpty + i), kByRow != 0 ? 12 : 10); // softmax, loaders
@@ -1677,7 +1678,10 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       const bool idle = t->row0 + 64 * (int)r + (row & 32) >= t->row1;
       float qs = 1.f;
       if (kFp8 && nb > 0) {
-        W.wait(bar(kBarQScale), q & 1);
+        // (A unit of up to two blocks has its QK done, and the next one's Q may be split,
+        // before the softmax comes to it: a barrier for every other unit, whose next phase
+        // needs a unit that is described only once this one is let go.)
+        W.wait(bar(kBarQScale + (q & 1)), (q >> 1) & 1);
         qs = reinterpret_cast<const float*>(sm + C::kOffQScale)[kRows * (q & 1) + row];
         ++q;
       }
@@ -2183,7 +2187,7 @@ smla_window_kernel(const __grid_constant__ WinArgs a) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(kBarQScale));
+        mbar_arrive(bar(kBarQScale + (q & 1)));
         mbar_signal_remote(bar0(kBarQFull));
       }
       ++q;

@@ -20,7 +20,7 @@ def test_short_requests(cuda_lib, block, d, new):
     b = P.Batch(rows, block, seed=block, pad=3, holes=9)
     more = 700 // block                                    # (a table that bounds no length here)
     b.table = torch.nn.functional.pad(b.table, (0, more), value=-1)
-    n, h = int(b.start[-1]), 120
+    n, h = int(b.start[-1]), 24
     kw = dict(cap=9.0, slopes=slopes_of(h))
     want = want_scored = None
     for limit in (300, 384, 385, 600):
