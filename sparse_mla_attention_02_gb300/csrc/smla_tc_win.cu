@@ -603,15 +603,15 @@ constexpr float kCapNear = 256.f;
 
 // Scores s * cl (log2 units) capped, cap tanh(s cl / cap), and lowered by the distance.
 // With u = 2^(two_over_cap s cl) = exp(2 y), tanh(y) = 1 - 2 / (1 + u): two steps of the
-// special function unit, the sums and products packed, the bias on the way (a form of its
+// special function unit, the sums and products packed, the bias with them (a form of its
 // own for a cap without a bias made a longer kernel: 439 -> 450 us).  One reciprocal for
 // two keys, 1 / a = b / (a b), saves 1 % on bf16 rows and gives it back where a key that
 // is not seen has to be kept from its neighbour.  Error of tanh: rcp 2^-23 and the sum
 // 2^-24 of a quotient of at most 1, ex2 2^-21.5 times at most a quarter, all twice: less
 // than 2^-20.
 // The bias of key k is the product of side = -+slope and of d0 + k, which is exact up to
-// 2^24: 0 at the token itself, elsewhere off by its own rounding and the slope's in log2
-// units, 2^-22 of itself.  (Adding the slope up from key to key instead leaves errors of
+// 2^24, added unrounded: 0 at the token itself, elsewhere off by the slope's rounding in
+// log2 units and the sum's, 2^-22 of itself.  (Adding the slope up from key to key instead leaves errors of
 // the farthest key of a group at the nearest.)  The distances are counted in steps of two
 // from every eighth key's: above 2^24 they, and the bias, are off by at most 2^-21.
 template <bool kCap>
@@ -630,8 +630,6 @@ __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap,
     } else {
       add2(a0, a1, 2.f, 2.f);
     }
-    float c0 = a0, c1 = a1;
-    fma2_bcast(c0, c1, side, base);
     if (kCap) {
       float u0 = s[k], u1 = s[k + 1];
       fma2_bcast(u0, u1, f, 0.f);
@@ -641,7 +639,11 @@ __device__ __forceinline__ void near_scores(float (&s)[32], float cl, float cap,
       s[k] = rcp_approx(u0);
       s[k + 1] = rcp_approx(u1);
     }
-    fma2(s[k], s[k + 1], kCap ? -2.f * cap : cl, c0, c1);
+    fma2_bcast(s[k], s[k + 1], kCap ? -2.f * cap : cl, base);
+    float c0 = a0, c1 = a1;
+    fma2(c0, c1, side, s[k], s[k + 1]);                // (behind the score: 452 -> 446 us)
+    s[k] = c0;
+    s[k + 1] = c1;
   }
 }
 
