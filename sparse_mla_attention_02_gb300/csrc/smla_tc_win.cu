@@ -16,11 +16,11 @@
 // first position to its last token's last, in blocks that begin at a multiple of 64; a
 // segment of 32 keys costs a thread two more steps of the special function unit a key for
 // the cap, and half a packed product and sum for the bias (near_scores).  That is hidden
-// behind the MMAs of bf16 rows but for 4 % (packed documents of 1500 tokens, 64 heads, 734
-// to 749 us, uncapped 706; 64 capped decode tokens of 4 to 8 thousand keys, 128 heads, 113
-// us); E4M3 rows, whose softmax is as long as their MMAs, pay for it (a mixed batch 363 us
-// with neither, 394 with a bias, 424 with a cap, 436 with both; 32 decode tokens of 8 to 16
-// thousand keys, 128 heads, 113, 116, 125 and 128).
+// behind the MMAs of bf16 rows but for 5 % (packed documents of 1500 tokens, 64 heads, 735
+// to 758 us, uncapped 704; 64 capped decode tokens of 4 to 8 thousand keys, 128 heads, 114
+// us); E4M3 rows, whose softmax is as long as their MMAs, pay for it (a mixed batch 360 us
+// with neither, 395 with a bias, 430 with a cap, 443 with both; 32 decode tokens of 8 to 16
+// thousand keys, 128 heads, 113, 116, 128 and 132).
 //
 // Tile.  All heads share the key rows, and neighbouring tokens of a request
 // share most of them, so a tile is 128 consecutive rows of the flattened
